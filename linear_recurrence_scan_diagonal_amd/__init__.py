@@ -15,7 +15,11 @@ _BINDING_NAMES = ("scan_fwd", "scan_bwd", "scan_fwd_bwd", "sru_fwd", "sru_bwd", 
                   "sru_deer_fwd", "rnn_seq", "scan_workspace_bytes", "plan_options",
                   "LrsError", "load")
 
-__all__ = ["DEER_DEFAULT_EPS", "DEER_DEFAULT_KMAX", *_BINDING_NAMES]
+# operators of recurrent language models (include/lrs_lm.h)
+_LM_NAMES = ("glr_checkpoints", "glr_fwd", "glr_bwd", "glr_step", "layernorm_fwd", "layernorm_bwd",
+             "linear_ce_fwd", "linear_ce_bwd", "linear_ce_fwd_bwd")
+
+__all__ = ["DEER_DEFAULT_EPS", "DEER_DEFAULT_KMAX", *_BINDING_NAMES, *_LM_NAMES]
 
 
 def __getattr__(name):
@@ -23,4 +27,7 @@ def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import binding
         return getattr(binding, name)
+    if name in _LM_NAMES:
+        from . import lm
+        return getattr(lm, name)
     raise AttributeError(name)

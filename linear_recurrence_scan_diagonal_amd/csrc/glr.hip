@@ -1,0 +1,556 @@
+// glr.hip -- gated linear recurrence with a learned decay, [T, B, D] layout:
+// forward, backward with recomputed states, and single tokens over a pool of
+// states.
+//
+//   r = sigmoid(z_r + bias_r),  i = sigmoid(z_i + bias_i),
+//   la = -c softplus(decay) r,  a = exp(la),  m = sqrt(1 - a^2) = sqrt(-expm1(2 la)),
+//   h_t = a h_{t-1} + m i x;    a reset sets a = 0, m = 1.
+//
+// The recurrence is an affine map a step, so the tiles, the look-back and the
+// persistent walk are those of the other [T, B, D] layers (lrs_tbd.hpp); the
+// gates are evaluated once an element next to their loads.  With resets the
+// maps compose through affine<true>, which lets a factor of 0 replace the state
+// rather than multiply it: a NaN or an infinity of one document stays there.
+//
+// Inputs are rows of a wider projection (pitch ld): a lane's channels are at
+// b * ld + d of a row, computed once a thread.
+//
+// The backward pass reads no h: the forward leaves the states that enter each
+// tile of kGlrRows steps (4 / 64 of a byte an element and byte of state), and
+// the tile runs its own forward maps again from there, which is exact in fp32
+// where a saved bf16 h would add its rounding to dL/dz_r.
+#include "lrs_tbd.hpp"
+
+namespace lrs {
+
+namespace {
+
+// One row of a strided input: the lane's channels at offsets zo (FULL: all in
+// one aligned group at zo[0]).
+template <int CPT, bool FULL, bool NT>
+__device__ __forceinline__ void glr_ld(const uint16_t* p, const uint32_t (&zo)[CPT], int nv,
+                                       IoRow<uint16_t, CPT>& r) {
+  if constexpr (FULL) {
+    r.template load<true, NT>(p, zo[0], CPT);
+  } else {
+#pragma unroll
+    for (int k = 0; k < CPT / 2; ++k) {
+      const uint32_t lo = 2 * k < nv ? p[zo[2 * k]] : 0u;
+      const uint32_t hi = 2 * k + 1 < nv ? p[zo[2 * k + 1]] : 0u;
+      r.w[k] = lo | (hi << 16);
+    }
+  }
+}
+template <int CPT, bool FULL, bool NT>
+__device__ __forceinline__ void glr_ld(const float* p, const uint32_t (&zo)[CPT], int nv,
+                                       IoRow<float, CPT>& r) {
+  if constexpr (FULL) {
+    r.template load<true, NT>(p, zo[0], CPT);
+  } else {
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) r.v[k] = k < nv ? p[zo[k]] : 0.0f;
+  }
+}
+template <int CPT, bool FULL, bool NT, typename IO>
+__device__ __forceinline__ void glr_st(IO* p, const uint32_t (&zo)[CPT], int nv,
+                                       const float (&v)[CPT]) {
+  if constexpr (FULL) {
+    IoRow<IO, CPT>::template store<true, NT>(p, zo[0], CPT, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < CPT; ++k)
+      if (k < nv) io_st(p, zo[k], v[k]);
+  }
+}
+
+// softplus(v) = max(v, 0) + log(1 + exp(-|v|)), once a channel.
+__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))); }
+
+// What a channel's parameters become: biases in the sigmoid's log2 units and
+// the exponent of a fully open gate, k = c softplus(decay).
+template <int CPT>
+struct GlrChan {
+  float br[CPT], bi[CPT], k[CPT];
+  uint32_t zo[CPT];  // offsets in a row of the inputs
+  uint32_t b[CPT], d[CPT];
+  __device__ __forceinline__ void set(const GlrArgs& g, int64_t c0, int nvc) {
+#pragma unroll
+    for (int j = 0; j < CPT; ++j) {
+      const uint32_t c = j < nvc ? (uint32_t)(c0 + j) : 0u;
+      b[j] = c / (uint32_t)g.D;
+      d[j] = c - b[j] * (uint32_t)g.D;
+      zo[j] = b[j] * (uint32_t)g.ld + d[j];
+      br[j] = -kLog2e * g.bias_r[d[j]];
+      bi[j] = -kLog2e * g.bias_i[d[j]];
+      k[j] = g.c * softplus(g.decay[d[j]]);
+    }
+  }
+};
+
+// a = exp(-t) and m^2 = 1 - a^2 for t = c softplus(decay) r >= 0.  For a long
+// memory (t < 1/8) 1 - a comes from the series of -expm1(-t), cut after the
+// fifth term (t^5 / 720 = 4e-8 of it there), and a and 1 - a^2 = (1 - a)(1 + a)
+// from that: subtracting a^2 from 1 would lose the digits of 1 - a, and the
+// exponential instruction's last bit, which does not round to nearest, would
+// add up over the steps that the state survives (2e-5 of h over 640 of them).
+__device__ __forceinline__ void glr_decay(float t, float& a, float& m2) {
+  float p = __builtin_fmaf(t, 1.0f / 120.0f, -1.0f / 24.0f);
+  p = __builtin_fmaf(t, p, 1.0f / 6.0f);
+  p = __builtin_fmaf(t, p, -0.5f);
+  p = __builtin_fmaf(t, p, 1.0f);
+  const float e = t * p;
+  const float far = __builtin_amdgcn_exp2f(-kLog2e * t);
+  const bool near = t < 0.125f;
+  a = near ? 1.0f - e : far;
+  m2 = near ? e * (2.0f - e) : __builtin_fmaf(-far, far, 1.0f);
+}
+
+struct GlrGate {
+  float r, i, a, m;
+};
+__device__ __forceinline__ GlrGate glr_gate(float zr, float zi, float br, float bi, float k,
+                                            bool cut) {
+  GlrGate g;
+  g.r = fast_sigmoid(zr, br);
+  g.i = fast_sigmoid(zi, bi);
+  float m2;
+  glr_decay(k * g.r, g.a, m2);
+  g.m = __builtin_amdgcn_sqrtf(m2);
+  if (cut) {
+    g.a = 0.0f;
+    g.m = 1.0f;
+  }
+  return g;
+}
+
+// The reset bytes of a row for the lane's channels (FULL: one sequence a lane).
+template <int CPT, bool FULL, bool RST>
+__device__ __forceinline__ void glr_cut(const uint8_t* reset, int64_t row, const GlrArgs& g,
+                                        const GlrChan<CPT>& ch, int nv, uint32_t (&cut)[CPT]) {
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) cut[k] = 0;
+  if constexpr (RST) {
+    if constexpr (FULL) {
+      cut[0] = reset[row * g.B + ch.b[0]];
+#pragma unroll
+      for (int k = 1; k < CPT; ++k) cut[k] = cut[0];
+    } else {
+#pragma unroll
+      for (int k = 0; k < CPT; ++k)
+        if (k < nv) cut[k] = reset[row * g.B + ch.b[k]];
+    }
+  }
+}
+
+template <typename IO, int L, int CPT>
+struct GlrRows {
+  IoRow<IO, CPT> zr[L], zi[L], x[L];
+  uint32_t cut[L][CPT];
+};
+
+template <typename IO, int L, int CPT, bool FULL, bool NT, bool RST>
+__device__ __forceinline__ void glr_load(const GlrArgs& g, const GlrChan<CPT>& ch, int64_t row0,
+                                         int nvc, GlrRows<IO, L, CPT>& rows) {
+  const int64_t pitch = g.B * g.ld;
+  const IO* rp = (const IO*)g.z_r + row0 * pitch;
+  const IO* ip = (const IO*)g.z_i + row0 * pitch;
+  const IO* xp = (const IO*)g.x + row0 * pitch;
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int nv = (FULL || row0 + i < g.T) ? nvc : 0;
+    glr_ld<CPT, FULL, NT>(rp, ch.zo, nv, rows.zr[i]);
+    glr_ld<CPT, FULL, NT>(ip, ch.zo, nv, rows.zi[i]);
+    glr_ld<CPT, FULL, NT>(xp, ch.zo, nv, rows.x[i]);
+    glr_cut<CPT, FULL, RST>(g.reset, row0 + i, g, ch, nv, rows.cut[i]);
+    rp += pitch;
+    ip += pitch;
+    xp += pitch;
+  }
+}
+
+// The step maps (a, m i x) of the loaded rows; identity past the end.
+template <typename IO, int L, int CPT, bool FULL>
+__device__ __forceinline__ void glr_maps(const GlrArgs& g, const GlrChan<CPT>& ch, int64_t row0,
+                                         int nvc, const GlrRows<IO, L, CPT>& rows,
+                                         float (&av)[L][CPT], float (&bv)[L][CPT]) {
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const bool row_ok = FULL || row0 + i < g.T;
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) {
+      if (FULL || (row_ok && k < nvc)) {
+        const GlrGate q = glr_gate(rows.zr[i].get(k), rows.zi[i].get(k), ch.br[k], ch.bi[k],
+                                   ch.k[k], rows.cut[i][k] != 0);
+        av[i][k] = q.a;
+        bv[i][k] = q.m * q.i * rows.x[i].get(k);
+      } else {
+        av[i][k] = 1.0f;
+        bv[i][k] = 0.0f;
+      }
+    }
+  }
+}
+
+template <int L, int CPT, bool SEL>
+__device__ __forceinline__ void glr_fold(const float (&av)[L][CPT], const float (&bv)[L][CPT],
+                                         float (&A)[CPT], float (&B)[CPT]) {
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) {
+    A[k] = av[0][k];
+    B[k] = bv[0][k];
+#pragma unroll
+    for (int i = 1; i < L; ++i) {
+      B[k] = affine<SEL>(av[i][k], B[k], bv[i][k]);
+      A[k] = A[k] * av[i][k];
+    }
+  }
+}
+
+// The wave's steps from its entering state x, h written on the way; x ends as
+// the state after the wave's last row.
+template <typename IO, int L, int CPT, bool FULL, bool NT, bool SEL>
+__device__ __forceinline__ void glr_walk(const GlrArgs& g, int64_t row0, int64_t cbase,
+                                         uint32_t off, int nvc, const float (&av)[L][CPT],
+                                         const float (&bv)[L][CPT], float (&x)[CPT]) {
+  const int64_t C = g.B * g.D;
+  IO* hp = (IO*)g.h + row0 * C + cbase;
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) x[k] = affine<SEL>(av[i][k], x[k], bv[i][k]);
+    const int nv = (FULL || row0 + i < g.T) ? nvc : 0;
+    IoRow<IO, CPT>::template store<FULL, NT>(hp, off, nv, x);
+    hp += C;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// forward, look-back tiles
+// ---------------------------------------------------------------------------
+template <typename IO, int NW, int L, int CPT, bool FULL, bool NT, bool RST>
+__device__ __forceinline__ void glr_tile(const GlrArgs& g, int tb, int cb, bool multi,
+                                         uint64_t* st, ColShared<NW, CPT>& s) {
+  const int64_t C = g.B * g.D;
+  const ColPos q = col_pos<NW, L, CPT>(tb, cb, C);
+  const int64_t cbase = (int64_t)cb * (kWave * CPT);
+  GlrChan<CPT> ch;
+  ch.set(g, q.c0, q.nvc);
+  GlrRows<IO, L, CPT> rows;
+  glr_load<IO, L, CPT, FULL, NT, RST>(g, ch, q.row0, q.nvc, rows);
+  float av[L][CPT], bv[L][CPT], A[CPT], B[CPT], x0[CPT], x[CPT];
+  glr_maps<IO, L, CPT, FULL>(g, ch, q.row0, q.nvc, rows, av, bv);
+  glr_fold<L, CPT, RST>(av, bv, A, B);
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) x0[k] = (g.h0 && k < q.nvc) ? g.h0[q.c0 + k] : 0.0f;
+  col_enter_state<NW, CPT, RST>(A, B, multi, tb, x0, g.h0, cbase,
+                                clamp_valid(C - cbase, kWave * CPT), st, s, x);
+  if (g.checkpoints && q.row0 == (int64_t)tb * (NW * L))  // wave 0: the state entering the tile
+    store_row<CPT, FULL, false>(g.checkpoints + (int64_t)tb * C + cbase, q.off, q.nvc, x);
+  glr_walk<IO, L, CPT, FULL, NT, RST>(g, q.row0, cbase, q.off, q.nvc, av, bv, x);
+  // rows past the end keep the state, so the wave that holds row T-1 ends with h_T
+  if (g.h_last && q.row0 < g.T && q.row0 + L >= g.T) {
+#pragma unroll
+    for (int k = 0; k < CPT; ++k)
+      if (k < q.nvc) g.h_last[q.c0 + k] = x[k];
+  }
+}
+
+template <typename IO, int NW, int L, int CPT, bool NT, bool RST>
+__global__ __launch_bounds__(NW* kWave) void k_glr_fwd(GlrArgs g, int ncb, int ntb, int vec,
+                                                       uint64_t* __restrict__ status,
+                                                       unsigned* __restrict__ tickets) {
+  constexpr int CW = kWave * CPT, TW = NW * L;
+  static_assert(TW == kGlrRows, "a tile is a checkpoint's stretch");
+  __shared__ ColShared<NW, CPT> s;
+  const bool multi = ntb > 1;
+  const int cb = (int)(blockIdx.x % (unsigned)ncb);
+  const int tb = col_ticket<NW, CPT>(multi, tickets, cb, s);
+  uint64_t* st = status + (int64_t)cb * ntb * CW;
+  const bool full = vec && (int64_t)(tb + 1) * TW <= g.T && (int64_t)(cb + 1) * CW <= g.B * g.D;
+  if (full)
+    glr_tile<IO, NW, L, CPT, true, NT, RST>(g, tb, cb, multi, st, s);
+  else
+    glr_tile<IO, NW, L, CPT, false, NT, RST>(g, tb, cb, multi, st, s);
+}
+
+// ---------------------------------------------------------------------------
+// backward: logical time block 0 is the last physical one, wave 0 takes its
+// latest steps (as the other layers' backward passes).  Two chains run through
+// a tile: forward, the states from the tile's checkpoint (within the tile
+// only), and in reverse time the gradient y_t = a_t lam_t, tiles joined by the
+// look-back.
+// ---------------------------------------------------------------------------
+template <int NW, int CPT>
+struct GlrBwdShared {
+  float fA[NW][kWave * CPT], fB[NW][kWave * CPT];  // forward maps of the waves
+  float red[3][NW][kWave * CPT];                   // parameter gradients of the waves
+};
+
+template <typename IO, int NW, int L, int CPT, bool FULL, bool NT, bool RST>
+__device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, int cb, bool multi,
+                                             uint64_t* st, ColShared<NW, CPT>& s,
+                                             GlrBwdShared<NW, CPT>& f) {
+  constexpr int CW = kWave * CPT;
+  const int64_t C = g.B * g.D;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int ptb = ntb - 1 - tb;
+  const uint32_t off = (uint32_t)(lane * CPT);
+  const int64_t cbase = (int64_t)cb * CW;
+  const int64_t c0 = cbase + off;
+  const int nvc = FULL ? CPT : clamp_valid(C - c0, CPT);
+  const int64_t row0 = (int64_t)ptb * (NW * L) + (int64_t)(NW - 1 - wid) * L;
+  GlrChan<CPT> ch;
+  ch.set(g, c0, nvc);
+  GlrRows<IO, L, CPT> rows;
+  glr_load<IO, L, CPT, FULL, NT, RST>(g, ch, row0, nvc, rows);
+  IoRow<IO, CPT> gh[L];
+  {
+    const IO* gp = (const IO*)g.grad_h + row0 * C + cbase;
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      gh[i].template load<FULL, NT>(gp, off, (FULL || row0 + i < g.T) ? nvc : 0);
+      gp += C;
+    }
+  }
+  float r[L][CPT], gi[L][CPT], av[L][CPT], m[L][CPT];
+  float FA[CPT], FB[CPT], A[CPT], B[CPT];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const bool row_ok = FULL || row0 + i < g.T;
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) {
+      GlrGate q;
+      if (FULL || (row_ok && k < nvc)) {
+        q = glr_gate(rows.zr[i].get(k), rows.zi[i].get(k), ch.br[k], ch.bi[k], ch.k[k],
+                     rows.cut[i][k] != 0);
+      } else {
+        q.r = q.i = q.m = 0.0f;
+        q.a = 1.0f;
+      }
+      r[i][k] = q.r;
+      gi[i][k] = q.i;
+      av[i][k] = q.a;
+      m[i][k] = q.m;
+      const float b = q.m * q.i * rows.x[i].get(k);  // 0 past the end (x reads as 0 there)
+      FB[k] = i == 0 ? b : affine<RST>(q.a, FB[k], b);
+      FA[k] = i == 0 ? q.a : FA[k] * q.a;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) {
+    f.fA[wid][off + k] = FA[k];
+    f.fB[wid][off + k] = FB[k];
+    // y passed on: lam_{L-1} = gh_{L-1} + y_in, lam_i = gh_i + a_{i+1} lam_{i+1},
+    // y_out = a_0 lam_0 (gh and a are 0 and 1 past the end)
+    A[k] = 1.0f;
+    B[k] = gh[L - 1].get(k);
+#pragma unroll
+    for (int i = L - 2; i >= 0; --i) {
+      B[k] = affine<RST>(av[i + 1][k], B[k], gh[i].get(k));
+      A[k] = A[k] * av[i + 1][k];
+    }
+    A[k] = A[k] * av[0][k];
+    B[k] = affine<RST>(av[0][k], B[k], 0.0f);
+  }
+  float x0[CPT], y[CPT], hs[CPT];
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) {
+    x0[k] = (g.grad_h_last && k < nvc) ? g.grad_h_last[c0 + k] : 0.0f;
+    hs[k] = k < nvc ? g.checkpoints[(int64_t)ptb * C + c0 + k] : 0.0f;
+  }
+  col_enter_state<NW, CPT, RST>(A, B, multi, tb, x0, g.grad_h_last, cbase, clamp_valid(C - cbase, CW),
+                                st, s, y);
+  // past a barrier: the states before each of the wave's rows
+  for (int w = NW - 1; w > wid; --w) {
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) hs[k] = affine<RST>(f.fA[w][off + k], hs[k], f.fB[w][off + k]);
+  }
+  float hp[L][CPT];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) {
+      hp[i][k] = hs[k];
+      hs[k] = affine<RST>(av[i][k], hs[k], m[i][k] * gi[i][k] * rows.x[i].get(k));
+    }
+  }
+  uint32_t go[CPT];
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) go[k] = ch.b[k] * (uint32_t)g.ld_grad + ch.d[k];
+  const int64_t gpitch = g.B * g.ld_grad;
+  IO* qr = (IO*)g.grad_zr + (row0 + L - 1) * gpitch;
+  IO* qi = (IO*)g.grad_zi + (row0 + L - 1) * gpitch;
+  IO* qx = (IO*)g.grad_x + (row0 + L - 1) * gpitch;
+  float sr[CPT], si[CPT], sd[CPT];
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) sr[k] = si[k] = sd[k] = 0.0f;
+#pragma unroll
+  for (int i = L - 1; i >= 0; --i) {
+    float dr[CPT], di[CPT], dx[CPT];
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) {
+      y[k] = i == L - 1 ? y[k] + gh[i].get(k) : affine<RST>(av[i + 1][k], y[k], gh[i].get(k));  // lam_t
+      const float u = gi[i][k] * rows.x[i].get(k), a = av[i][k], mm = m[i][k], lam = y[k];
+      const float dgx = lam * mm;
+      dx[k] = dgx * gi[i][k];
+      di[k] = dgx * u * (1.0f - gi[i][k]);
+      const float rm = mm > 0.0f ? __builtin_amdgcn_rcpf(mm) : 0.0f;
+      float dla = lam * a * __builtin_fmaf(-a * rm, u, hp[i][k]);
+      if (RST && a == 0.0f) dla = 0.0f;  // whatever the state before was
+      const float dlr = dla * r[i][k];
+      dr[k] = -dlr * ch.k[k] * (1.0f - r[i][k]);  // la = -k r
+      sr[k] += dr[k];
+      si[k] += di[k];
+      sd[k] += dlr;
+    }
+    const int nv = (FULL || row0 + i < g.T) ? nvc : 0;
+    glr_st<CPT, FULL, NT>(qr, go, nv, dr);
+    glr_st<CPT, FULL, NT>(qi, go, nv, di);
+    glr_st<CPT, FULL, NT>(qx, go, nv, dx);
+    qr -= gpitch;
+    qi -= gpitch;
+    qx -= gpitch;
+  }
+  if (g.grad_h0 && row0 == 0) {
+#pragma unroll
+    for (int k = 0; k < CPT; ++k)
+      if (k < nvc) g.grad_h0[c0 + k] = affine<RST>(av[0][k], y[k], 0.0f);
+  }
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) {
+    f.red[0][wid][off + k] = sr[k];
+    f.red[1][wid][off + k] = si[k];
+    // d softplus / d decay = sigmoid(decay)
+    f.red[2][wid][off + k] = sd[k] * (-g.c * fast_sigmoid(g.decay[ch.d[k]], 0.0f));
+  }
+  __syncthreads();
+  for (int j = threadIdx.x; j < 3 * CW; j += NW * kWave) {
+    const int which = j / CW, c = j % CW;
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) t += f.red[which][w][c];
+    if (cbase + c < C) g.part[((int64_t)which * ntb + ptb) * C + cbase + c] = t;
+  }
+}
+
+template <typename IO, int NW, int L, int CPT, bool NT, bool RST>
+__global__ __launch_bounds__(NW* kWave) void k_glr_bwd(GlrArgs g, int ncb, int ntb, int vec,
+                                                       uint64_t* __restrict__ status,
+                                                       unsigned* __restrict__ tickets) {
+  constexpr int CW = kWave * CPT, TW = NW * L;
+  static_assert(TW == kGlrRows, "a tile is a checkpoint's stretch");
+  __shared__ ColShared<NW, CPT> s;
+  __shared__ GlrBwdShared<NW, CPT> f;
+  const bool multi = ntb > 1;
+  const int cb = (int)(blockIdx.x % (unsigned)ncb);
+  const int tb = col_ticket<NW, CPT>(multi, tickets, cb, s);
+  uint64_t* st = status + (int64_t)cb * ntb * CW;
+  const int ptb = ntb - 1 - tb;
+  const bool full = vec && (int64_t)(ptb + 1) * TW <= g.T && (int64_t)(cb + 1) * CW <= g.B * g.D;
+  if (full)
+    glr_bwd_tile<IO, NW, L, CPT, true, NT, RST>(g, tb, ntb, cb, multi, st, s, f);
+  else
+    glr_bwd_tile<IO, NW, L, CPT, false, NT, RST>(g, tb, ntb, cb, multi, st, s, f);
+}
+
+// ---------------------------------------------------------------------------
+// single tokens: element-wise over [B, D], the state's row by its slot
+// ---------------------------------------------------------------------------
+template <typename IO>
+__global__ __launch_bounds__(256) void k_glr_step(GlrArgs g, const int32_t* __restrict__ slots,
+                                                  float* __restrict__ state, int64_t S) {
+  const int64_t n = g.B * g.D;
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= n) return;
+  const uint32_t b = (uint32_t)e / (uint32_t)g.D, d = (uint32_t)e - b * (uint32_t)g.D;
+  const int64_t slot = slots ? slots[b] : (int64_t)b;
+  const int64_t z = (int64_t)b * g.ld + d;
+  float h = 0.0f;
+  if (slot >= 0 && slot < S) {
+    const GlrGate q = glr_gate(io_ld((const IO*)g.z_r, z), io_ld((const IO*)g.z_i, z),
+                               -kLog2e * g.bias_r[d], -kLog2e * g.bias_i[d],
+                               g.c * softplus(g.decay[d]), false);
+    float* p = state + slot * g.D + d;
+    h = __builtin_fmaf(q.a, *p, q.m * q.i * io_ld((const IO*)g.x, z));
+    *p = h;
+  }
+  io_st((IO*)g.h, e, h);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+ColPlan plan_glr(int64_t C, int64_t T, int io) {
+  ColPlan p = plan_cols(C, T, 8, 8, 2);
+  p.stream = C * T * 4 * io_bytes(io) >= kStreamFootprint;
+  return p;
+}
+
+ColPlan plan_glr_bwd(int64_t C, int64_t T, int io) {
+  ColPlan p = plan_cols(C, T, 8, 8, 2);
+  p.stream = C * T * 7 * io_bytes(io) >= kStreamFootprint;
+  return p;
+}
+
+#define LRS_GLR_PICK(LAUNCH)                                    \
+  if (io == kIoBf16) {                                          \
+    if (p.stream) {                                             \
+      if (g.reset) LAUNCH(uint16_t, true, true);                \
+      else LAUNCH(uint16_t, true, false);                       \
+    } else {                                                    \
+      if (g.reset) LAUNCH(uint16_t, false, true);               \
+      else LAUNCH(uint16_t, false, false);                      \
+    }                                                           \
+  } else {                                                      \
+    if (p.stream) {                                             \
+      if (g.reset) LAUNCH(float, true, true);                   \
+      else LAUNCH(float, true, false);                          \
+    } else {                                                    \
+      if (g.reset) LAUNCH(float, false, true);                  \
+      else LAUNCH(float, false, false);                         \
+    }                                                           \
+  }
+
+hipError_t launch_glr_fwd(const GlrArgs& g, int io, const ColPlan& p, int vec, uint64_t* status,
+                          unsigned* tickets, hipStream_t stream) {
+  const dim3 grid((unsigned)(p.ncb * p.ntb));
+#define LRS_GLR_F(IO, NTF, RSTF)                                                               \
+  hipLaunchKernelGGL((k_glr_fwd<IO, 8, 8, 2, NTF, RSTF>), grid, dim3(512), 0, stream, g,       \
+                     (int)p.ncb, (int)p.ntb, vec, status, tickets)
+  LRS_GLR_PICK(LRS_GLR_F)
+#undef LRS_GLR_F
+  return hipGetLastError();
+}
+
+hipError_t launch_glr_bwd(const GlrArgs& g, int io, const ColPlan& p, int vec, uint64_t* status,
+                          unsigned* tickets, double* acc, float* grad_bias_r, float* grad_bias_i,
+                          float* grad_decay, hipStream_t stream) {
+  const dim3 grid((unsigned)(p.ncb * p.ntb));
+#define LRS_GLR_B(IO, NTF, RSTF)                                                               \
+  hipLaunchKernelGGL((k_glr_bwd<IO, 8, 8, 2, NTF, RSTF>), grid, dim3(512), 0, stream, g,       \
+                     (int)p.ncb, (int)p.ntb, vec, status, tickets)
+  LRS_GLR_PICK(LRS_GLR_B)
+#undef LRS_GLR_B
+  hipError_t e = hipGetLastError();
+  const int64_t R = p.ntb * g.B;
+  if (e == hipSuccess)
+    e = launch_col_sums(g.part, 2, R, g.D, acc, grad_bias_r, grad_bias_i, stream);
+  if (e == hipSuccess)
+    e = launch_col_sums(g.part + 2 * R * g.D, 1, R, g.D, acc, grad_decay, nullptr, stream);
+  return e;
+}
+
+hipError_t launch_glr_step(const GlrArgs& g, int io, const int32_t* slots, float* state, int64_t S,
+                           hipStream_t stream) {
+  const dim3 grid((unsigned)((g.B * g.D + 255) / 256));
+  if (io == kIoBf16)
+    hipLaunchKernelGGL(k_glr_step<uint16_t>, grid, dim3(256), 0, stream, g, slots, state, S);
+  else
+    hipLaunchKernelGGL(k_glr_step<float>, grid, dim3(256), 0, stream, g, slots, state, S);
+  return hipGetLastError();
+}
+
+}  // namespace lrs

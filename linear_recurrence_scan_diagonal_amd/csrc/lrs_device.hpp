@@ -206,6 +206,15 @@ __device__ __forceinline__ float lookback_group_wave(const uint64_t* st, int c, 
   return __builtin_fmaf(PA, xs, PB);
 }
 
+// The state after an affine map, a*x + b.  SEL: a factor of exactly 0 replaces
+// the state by b whatever the state was (0 * inf and 0 * NaN would be NaN), so
+// that a restart cuts off what came before it.
+template <bool SEL>
+__device__ __forceinline__ float affine(float a, float x, float b) {
+  const float y = __builtin_fmaf(a, x, b);
+  return SEL && a == 0.0f ? b : y;
+}
+
 // Lane-parallel form for the feature-contiguous kernels: each lane resolves
 // one channel of its own, groups of G blocks.  The lane loads every word it
 // needs at once (v[i], i < j: aggregate of block g0 + i; v[G-1]: inclusive
@@ -213,7 +222,7 @@ __device__ __forceinline__ float lookback_group_wave(const uint64_t* st, int c, 
 // aggregates in ascending block order to the previous group's end state.
 // st points at block 0 of the lane's channel, consecutive blocks `stride`
 // words apart; x0 is the channel's initial state.
-template <int G>
+template <int G, bool SEL = false>
 __device__ __forceinline__ float lookback_group_lane(const uint64_t* st, int64_t stride, int c,
                                                      float x0) {
   const int g0 = c - c % G;
@@ -240,7 +249,7 @@ __device__ __forceinline__ float lookback_group_lane(const uint64_t* st, int64_t
     x = ((uint32_t)v[G - 1] == kIncTag) ? as_f32((uint32_t)(v[G - 1] >> 32)) : __builtin_nanf("");
 #pragma unroll
   for (int i = 0; i < G - 1; ++i)
-    if (i < j) x = __builtin_fmaf(as_f32((uint32_t)v[i]), x, as_f32((uint32_t)(v[i] >> 32)));
+    if (i < j) x = affine<SEL>(as_f32((uint32_t)v[i]), x, as_f32((uint32_t)(v[i] >> 32)));
   return x;
 }
 

@@ -224,4 +224,76 @@ hipError_t launch_sru_deer_out(const void* zr, const void* zx, const float* bias
                                const float* c, void* h, float* c_last, int64_t N, int64_t C,
                                int64_t D, int io_dtype, int vec, hipStream_t stream);
 
+// Gated linear recurrence (glr.hip).  Arrays as in lrs_lm.h; the forward reads
+// and writes the first group, the backward also the second.
+constexpr int kGlrRows = 64;  // time steps a tile, and between two checkpoints
+struct GlrArgs {
+  const void *z_r, *z_i, *x;
+  const float *bias_r, *bias_i, *decay;
+  const uint8_t* reset;
+  const float* h0;
+  void* h;
+  float *h_last, *checkpoints;
+  int64_t T, B, D, ld;
+  float c;
+  const void* grad_h;
+  const float* grad_h_last;
+  void *grad_zr, *grad_zi, *grad_x;
+  int64_t ld_grad;
+  float* grad_h0;
+  float* part;  // [3][ntb * B][D]: the tiles' sums for bias_r, bias_i and decay
+};
+ColPlan plan_glr(int64_t C, int64_t T, int io);
+ColPlan plan_glr_bwd(int64_t C, int64_t T, int io);
+hipError_t launch_glr_fwd(const GlrArgs& g, int io, const ColPlan& p, int vec, uint64_t* status,
+                          unsigned* tickets, hipStream_t stream);
+hipError_t launch_glr_bwd(const GlrArgs& g, int io, const ColPlan& p, int vec, uint64_t* status,
+                          unsigned* tickets, double* acc, float* grad_bias_r, float* grad_bias_i,
+                          float* grad_decay, hipStream_t stream);
+hipError_t launch_glr_step(const GlrArgs& g, int io, const int32_t* slots, float* state, int64_t S,
+                           hipStream_t stream);
+
+// Layer norm (layernorm.hip).  ln_bwd_blocks: row blocks of the backward, each
+// leaving one partial sum a feature in part ([2][blocks][D]).
+hipError_t launch_layernorm_fwd(const void* x, const void* residual, const float* gamma,
+                                const float* beta, void* y, void* sum, float* mean, float* rstd,
+                                int64_t R, int64_t D, float eps, int io, hipStream_t stream);
+int64_t ln_bwd_blocks(int64_t R, int64_t D);
+hipError_t launch_layernorm_bwd(const void* s, const float* gamma, const float* mean,
+                                const float* rstd, const void* grad_y, const void* grad_sum,
+                                void* grad_x, float* grad_gamma, float* grad_beta, int64_t R,
+                                int64_t D, int io, float* part, double* acc, hipStream_t stream);
+
+// Cross entropy of a linear head (linear_ce.hip).  The plan of a shape, and the
+// arrays of a call; the workspace's own are bf16 (uint16_t) or fp32.
+struct CePlan {
+  int parts = 1;        // bf16 parts of an operand's element
+  int64_t Dp = 0;       // features rounded up to whole k steps
+  int64_t Np = 0;       // rows rounded up to whole tiles
+  int64_t piece = 0, pieces = 0;  // classes of a piece (whole tiles), and how many
+  int64_t tiles = 0;    // class tiles (the forward's partial sums a row)
+  bool big_l = false, big_x = false, big_w = false;  // tile shapes: logits, the gradients
+  int64_t split_x = 1, split_w = 1;        // shares of their k loops
+  bool slots_x = false, slots_w = false;   // fp32 partial results are kept and joined
+};
+struct CeArgs {
+  const void *x, *w;
+  const int64_t* target;
+  const float* grad_loss;
+  float *loss, *lse;
+  void *grad_x, *grad_w;
+  int64_t N, V, D;
+  bool forward, backward;
+  uint16_t *x_rows, *w_rows;  // [N][parts Dp], [piece][parts Dp]
+  uint16_t *x_cols, *w_cols;  // [D][parts Np], [D][parts piece]
+  uint16_t *g, *gt;           // [N][parts piece], [piece][parts Np]
+  float2* part;               // [N][tiles]
+  float *tlogit, *ratio, *row_scale, *top;  // [N], [N], [N], 1
+  float *slots_x, *slots_w;   // [split_x][N][D], [split_w][piece][D]
+};
+CePlan plan_ce(int64_t N, int64_t V, int64_t D, int io);
+hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_t stream);
+// Fill with zero bytes (p aligned to 4, an even number of bytes).
+hipError_t launch_zero(void* p, int64_t bytes, hipStream_t stream);
+
 }  // namespace lrs

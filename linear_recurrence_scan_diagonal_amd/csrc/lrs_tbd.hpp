@@ -181,8 +181,8 @@ constexpr int kColGroup = 8;
 // per-channel maps, run the look-back (multi-block) and share the carries; every
 // wave then composes the maps of the waves before it (wave order = scan order).
 // st points at this channel block's status row for time block 0; time blocks
-// are CW words apart.
-template <int NW, int CPT>
+// are CW words apart.  SEL: maps with a factor of 0 replace the state (affine).
+template <int NW, int CPT, bool SEL = false>
 __device__ __forceinline__ void col_enter_state(const float (&A)[CPT], const float (&B)[CPT],
                                                 bool multi, int tb, const float (&x0)[CPT],
                                                 const float* x0p, int64_t cbase, int cvalid,
@@ -209,7 +209,7 @@ __device__ __forceinline__ void col_enter_state(const float (&A)[CPT], const flo
       float TA = 1.0f, TB = 0.0f;
       for (int w = 0; w < NW; ++w) {
         const float wa = s.A[w][j], wb = s.B[w][j];
-        TB = __builtin_fmaf(wa, TB, wb);
+        TB = affine<SEL>(wa, TB, wb);
         TA = TA * wa;
       }
       float x_in = 0.0f;
@@ -217,8 +217,8 @@ __device__ __forceinline__ void col_enter_state(const float (&A)[CPT], const flo
         const bool gend = group_end(tb, kColGroup);
         if (!gend) status_store(st + (int64_t)tb * CW + j, pack_agg(TA, TB));
         const float xs = x0p ? x0p[cbase + j] : 0.0f;
-        x_in = lookback_group_lane<kColGroup>(st + j, CW, tb, xs);
-        if (gend) status_store(st + (int64_t)tb * CW + j, pack_inc(__builtin_fmaf(TA, x_in, TB)));
+        x_in = lookback_group_lane<kColGroup, SEL>(st + j, CW, tb, xs);
+        if (gend) status_store(st + (int64_t)tb * CW + j, pack_inc(affine<SEL>(TA, x_in, TB)));
       }
       s.carry[j] = x_in;
     }
@@ -236,12 +236,12 @@ __device__ __forceinline__ void col_enter_state(const float (&A)[CPT], const flo
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
       const float wa = s.A[w][j0 + k], wb = s.B[w][j0 + k];
-      PB[k] = __builtin_fmaf(wa, PB[k], wb);
+      PB[k] = affine<SEL>(wa, PB[k], wb);
       PA[k] = PA[k] * wa;
     }
   }
 #pragma unroll
-  for (int k = 0; k < CPT; ++k) x[k] = __builtin_fmaf(PA[k], carry[k], PB[k]);
+  for (int k = 0; k < CPT; ++k) x[k] = affine<SEL>(PA[k], carry[k], PB[k]);
 }
 
 template <int NW, int CPT>
@@ -273,8 +273,8 @@ struct PersistShared {
 
 // Publish this wave's per-channel maps (A, B) and return in x the state
 // entering this wave's first step: the maps of the earlier waves of the tile,
-// in order, applied to the carry.  par: the tile's parity.
-template <int NW, int CPT>
+// in order, applied to the carry.  par: the tile's parity.  SEL as in affine.
+template <int NW, int CPT, bool SEL = false>
 __device__ __forceinline__ void persist_enter(const float (&A)[CPT], const float (&B)[CPT],
                                               PersistShared<NW, CPT>& s, int wid, uint32_t off,
                                               float (&x)[CPT], int par) {
@@ -288,10 +288,10 @@ __device__ __forceinline__ void persist_enter(const float (&A)[CPT], const float
   for (int k = 0; k < CPT; ++k) {
     float PA = 1.0f, PB = 0.0f;
     for (int w = 0; w < wid; ++w) {
-      PB = __builtin_fmaf(s.A[par][w][off + k], PB, s.B[par][w][off + k]);
+      PB = affine<SEL>(s.A[par][w][off + k], PB, s.B[par][w][off + k]);
       PA = PA * s.A[par][w][off + k];
     }
-    x[k] = __builtin_fmaf(PA, s.carry[par][off + k], PB);
+    x[k] = affine<SEL>(PA, s.carry[par][off + k], PB);
   }
 }
 
