@@ -120,18 +120,21 @@ LRS_API int lrs_layernorm_bwd(const void *s, const float *gamma, const float *me
  * its x reaches no gradient of w (lse is written all the same).  The logits are
  * made tile by tile on the matrix cores and never stored.
  * x: [N,D], w: [V,D], I/O type.  target: [N] int64.  loss, lse: [N] fp32.
- * fp32 operands are split into three bf16 parts and multiplied in six products
- * (the neglected ones are 2^-24 of the result); inputs must be finite.
- * Supported while N, V and D stay below 2^21. */
-LRS_API size_t lrs_linear_ce_workspace_bytes(int64_t N, int64_t V, int64_t D, int io_dtype);
+ * fp32 operands are split into two scaled fp16 parts and multiplied in three
+ * products, which neglects 2^-22 of the result.
+ * Supported while N, V and D stay below 2^21.
+ * The workspace query takes whether the call makes the gradient. */
+LRS_API size_t lrs_linear_ce_workspace_bytes(int64_t N, int64_t V, int64_t D, int io_dtype,
+                                             int backward);
 LRS_API int lrs_linear_ce_fwd(const void *x, const void *w, const int64_t *target, float *loss,
                               float *lse, int64_t N, int64_t V, int64_t D, int io_dtype,
                               void *workspace, size_t workspace_bytes, void *stream);
 
 /* Its gradient for given dL/dloss: with G = (exp(l - lse) - onehot) grad_loss
  * (rows of 0 where ignored), grad_x = G w and grad_w = G^T x, I/O type.  The
- * logits are made again for one piece of the vocabulary after the other; G of
- * the piece is kept in the workspace, rounded to the I/O type.
+ * rows are taken in pieces: the exponentials of a piece's logits (made again
+ * here) and its G are kept in the workspace, at most 2 GiB of it whatever the
+ * vocabulary and the number of rows.  G is rounded to bf16 for bf16 inputs.
  * lse: as lrs_linear_ce_fwd wrote it.  grad_loss: [N] fp32. */
 LRS_API int lrs_linear_ce_bwd(const void *x, const void *w, const int64_t *target,
                               const float *lse, const float *grad_loss, void *grad_x,
@@ -140,7 +143,7 @@ LRS_API int lrs_linear_ce_bwd(const void *x, const void *w, const int64_t *targe
 
 /* Both in one call, for a grad_loss that is known before the loss is (a mean
  * over the rows that count): the results of lrs_linear_ce_fwd and then
- * lrs_linear_ce_bwd. */
+ * lrs_linear_ce_bwd, with the logits made once instead of twice. */
 LRS_API int lrs_linear_ce_fwd_bwd(const void *x, const void *w, const int64_t *target,
                                   const float *grad_loss, float *loss, float *lse, void *grad_x,
                                   void *grad_w, int64_t N, int64_t V, int64_t D, int io_dtype,

@@ -7,31 +7,36 @@
 //
 // Three products carry the work, all of the form C[m][n] = sum_k A[m][k] B[n][k]
 // with both operands contiguous along k (one matrix-core kernel, k_gemm, with
-// three epilogues):
+// two epilogues):
 //   logits  m = class, n = row, k = feature, A = w, B = x.  A lane of the
 //           32x32 product holds one n and 16 values of m, so the softmax's
-//           maximum and sum over classes run inside a lane.  The forward leaves
-//           (maximum, sum) of each 256-class tile and row, joined afterwards;
-//           the backward makes the logits again and writes G and G^T of one
-//           piece of the vocabulary, rounded to bf16, through LDS;
+//           maximum and sum over classes run inside a lane.  Each tile leaves
+//           its (maximum, sum) a row, joined afterwards;
 //   grad_w  m = class, n = feature, k = row, A = G^T, B = x^T;
 //   grad_x  m = row, n = feature, k = class, A = G, B = w^T.
+// For the gradient the rows are taken in pieces, whose e = exp(l - tile maximum)
+// is kept (fp16 for bf16 inputs, fp32 for fp32) until lse is known, turned into
+// G and G^T by one pass, and used up by the two gradient products; the piece is
+// chosen so that this stays within a fixed number of bytes.
 // Operands that are not laid out like that (x^T, w^T, rows that are not a whole
-// number of 32-wide steps or not 16-byte aligned) are copied once into the
-// workspace.
+// number of k steps or not 16-byte aligned) are copied once into the workspace.
 //
-// fp32 operands are three bf16 parts, hi + mid + lo = x to 2^-24, side by side
-// along k, and a product is the six part products of order up to 2^-16 (a loop
-// of the same kernel over pairs of parts): the vector fp32 rate of the matrix
-// cores is 1/16 of the bf16 rate, so six bf16 products cost less than half.
+// fp32 operands are two fp16 parts, hi + lo = x to 2^-22, scaled by a power of
+// two that brings the row's (x and w as rows) or the array's (transposed) largest
+// value near fp16's largest, so that the parts' range is no limit: what is lost
+// is 2^-22 of an element or 2^-39 of the largest.  A product is the three part
+// products hi hi + hi lo + lo hi (a loop of the same kernel over pairs of parts),
+// about as exact as fp32 and, at the matrix cores' fp16 rate, five times as fast
+// as their fp32 rate.
 //
-// Rounding.  G is rounded to bf16 before the second and third product (its
-// error, 2^-9 an element with random sign, adds to that of the rounded
-// gradient).  It is rounded unscaled, where the entries that dominate, p - 1 at
-// the target, lie next to -1: scaled by a common grad_loss, they would all be
-// rounded the same way.  grad_x is scaled by row in fp32 afterwards.  grad_w's
-// sum runs over rows, so G^T carries grad_loss / max |grad_loss| (exactly 1 for
-// a mean) and the maximum is applied in fp32 at the end.
+// Rounding.  G is rounded to bf16 (two fp16 parts for fp32 inputs) before the
+// second and third product: an error of 2^-9 an element with random sign, which
+// adds to that of the rounded gradient.  It is rounded unscaled, where the
+// entries that dominate, p - 1 at the target, lie next to -1: scaled by a common
+// grad_loss, they would all be rounded the same way.  grad_x is scaled by row in
+// fp32 afterwards.  grad_w's sum runs over rows, so G^T carries grad_loss / max
+// |grad_loss| (exactly 1 for a mean) and the maximum is applied in fp32 at the
+// end.  Keeping e in fp16 (2^-12) adds 1% to the error of G in bf16.
 #include "lrs_device.hpp"
 #include "lrs_internal.hpp"
 
@@ -40,41 +45,42 @@ namespace lrs {
 namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2eF = 1.4426950408889634f;
-constexpr int kBK = 32;  // k a step: rows of 64 bytes in LDS
-constexpr int kMaxPairs = 6;
+constexpr int kMaxPairs = 3;
+// fp32 inputs: G's parts are of G * 2^14.
+constexpr float kGScale = 16384.0f;
 
-enum { kEpiLse = 0, kEpiGrad = 1, kEpiOut = 2 };
+// What a logits tile leaves besides its maximum and sum.
+enum { kKeepNone = 0, kKeepF16 = 1, kKeepF32 = 2 };
+enum { kEpiLogits = 0, kEpiOut = 1 };
 
 struct GemmArgs {
-  const uint16_t *a, *b;  // [M][lda], [N][ldb], bf16
+  const uint16_t *a, *b;  // [M][lda], [N][ldb], bf16 or fp16
   int64_t lda, ldb;
   int64_t M, N;
-  int kt;                         // steps of 32 along k, of one part
-  int npair;                      // part products: 1, or 6 for fp32
-  int pa[kMaxPairs], pb[kMaxPairs];  // where the pair's parts begin along k
-  int tm, tn, splits;             // tiles, and contiguous shares of the k loop
-  // logits (m = class v0 + m, n = row)
+  int64_t k;                         // of one part, a multiple of 64
+  int npair;                         // part products: 1, or 3 for fp32
+  int64_t pa[kMaxPairs], pb[kMaxPairs];  // where the pair's parts begin along k
+  int tm, tn, splits;                // tiles, and contiguous shares of the k loop
+  // logits (m = class, n = row)
   const int64_t* target;
-  int64_t v0, V;
-  float2* part;     // [N][part_ld]: maximum and sum of each class tile
-  int64_t part_ld, part0;
+  float2* part;     // [N][tm]: maximum and sum of each class tile
   float* tlogit;    // [N]: the target's logit
-  const float* lse;
-  const float* ratio;  // [N]: grad_loss / max |grad_loss|, 0 where ignored
-  uint16_t *g, *gt;    // G [N][ldg], G^T [M][ldgt], parts side by side
-  int64_t ldg, ldgt;
-  int nparts;
-  int64_t part_k, part_kt;  // a part's length along k in g and gt
+  const float *a_unscale, *b_unscale;  // [M to a whole tile], [N]: powers of two (fp32 operands)
+  void* e;          // [N][lde]: exp(l - tile maximum), fp16 or fp32
+  int64_t lde;
   // products
-  float* slots;        // [splits][M][N] fp32, or null: straight to out
-  int accumulate;      // add to the slots
+  float* slots;        // [splits][M][N] fp32, or null
+  int add;             // the slots hold what earlier pieces left: add to it
+  int last;            // write out (from the slots too, if add)
   void* out;           // [M][N], I/O type
   int out_bf16;
   const float* row_scale;  // [M] or null
-  const float* scale;      // one value, or null
+  const float *scale, *unscale;  // one value each, or null
 };
 
 // One 16-byte piece a lane from global memory straight to LDS (lane l's piece
@@ -92,13 +98,6 @@ __device__ __forceinline__ void dma16(uint32_t dst, uint32_t off, const uint16_t
       :
       : "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(off), "s"(ub)
       : "memory");
-}
-
-// Where a row's target lies from the lane's first class on (m = class v0 + m);
-// out of the lane's reach: -1.  An ignored target never matches.
-__device__ __forceinline__ int class_at(int64_t t, const GemmArgs& g, int64_t mb) {
-  const int64_t d = t - g.v0 - mb;
-  return t >= 0 && t < g.V && d >= 0 && d < 1024 ? (int)d : -1;
 }
 
 template <int N>
@@ -126,26 +125,52 @@ __device__ __forceinline__ void tile_of(const GemmArgs& g, int& tm, int& tn, int
   tn = (int)(in / gm);
 }
 
-template <int TM, int TN, int WM, int WN, int NST, int EPI>
-struct GemmCfg {
-  static constexpr int kThreads = WM * WN * kWave;
-  static constexpr int kRows = TM + TN;
-  static constexpr int kStage = kRows * kBK * 2;  // bytes
-  static constexpr int kIssue = kRows / 16 / (WM * WN);
-  static constexpr int MT = TM / WM / 32, NT = TN / WN / 32;
-  static constexpr int kStageG = TN * (TM + 8) * 2, kStageGt = TM * (TN + 8) * 2;
-  static constexpr int kLds =
-      NST * kStage > (kStageG > kStageGt ? kStageG : kStageGt)
-          ? NST * kStage
-          : (kStageG > kStageGt ? kStageG : kStageGt);
-  static_assert(kRows % (16 * WM * WN) == 0, "whole loads");
+// The piece of 16 bytes at which piece p of row r is kept in LDS is p ^ f(r):
+// the 8 (or 16) rows that a fragment read touches at once then fall on
+// different banks, for rows of 64 and of 128 bytes.
+template <int BK>
+__device__ __forceinline__ int swizzle(int r) {
+  return BK == 32 ? ((r >> 1) & 3) ^ ((r >> 3) & 1) : (r & 7) ^ ((r >> 3) & 1);
+}
+
+template <bool F16>
+struct Frag;
+template <>
+struct Frag<false> {
+  typedef bf16x8_t V;
+  static __device__ __forceinline__ f32x16_t mma(V a, V b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Frag<true> {
+  typedef f16x8_t V;
+  static __device__ __forceinline__ f32x16_t mma(V a, V b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
 };
 
-template <int TM, int TN, int WM, int WN, int NST, int EPI>
-__global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm(GemmArgs g) {
-  using Cfg = GemmCfg<TM, TN, WM, WN, NST, EPI>;
-  constexpr int MT = Cfg::MT, NT = Cfg::NT, NI = Cfg::kIssue;
-  __shared__ __align__(128) char lds[Cfg::kLds];
+// Tile TM x TN by WM x WN waves, k in steps of BK, NST buffers.
+template <int TM_, int TN_, int WM_, int WN_, int BK_, int NST_, int MINW_>
+struct Shape {
+  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, BK = BK_, NST = NST_, MINW = MINW_;
+  static constexpr int kThreads = WM * WN * kWave;
+  static constexpr int kRowBytes = BK * 2;
+  static constexpr int kStage = (TM + TN) * kRowBytes;
+  static constexpr int kRowsPerLoad = 1024 / kRowBytes;
+  static constexpr int kIssue = (TM + TN) / kRowsPerLoad / (WM * WN);
+  static constexpr int MT = TM / WM / 32, NT = TN / WN / 32;
+  static constexpr int kKeep = TN * (TM + 8) * 2 + WM * TN * 8;  // an fp16 tile, and the rows' sums
+  static constexpr int kLds = NST * kStage > kKeep ? NST * kStage : kKeep;
+  static_assert((TM + TN) % (kRowsPerLoad * WM * WN) == 0 && TM % (16 * WM) == 0, "whole loads");
+};
+
+template <class S, int EPI, int KEEP, bool F16>
+__global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
+  constexpr int TM = S::TM, TN = S::TN, WM = S::WM, WN = S::WN, BK = S::BK, NST = S::NST;
+  constexpr int MT = S::MT, NT = S::NT, NI = S::kIssue, RB = S::kRowBytes, RPL = S::kRowsPerLoad;
+  typedef typename Frag<F16>::V frag_t;
+  __shared__ __align__(128) char lds[S::kLds];
   const int lane = threadIdx.x & (kWave - 1);
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wid / WN, wn = wid % WN;
@@ -156,40 +181,39 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm(GemmArgs g) {
   const uint16_t* bbase = g.b + n0 * g.ldb;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
 
-  // This lane's global piece of each of the wave's loads.  A load fills 16 rows
-  // of 64 bytes; the four 16-byte pieces of row r are stored in the order
-  // piece ^ f(r), f(r) = ((r >> 1) & 3) ^ ((r >> 3) & 1), so that the 8 (or 16)
-  // rows that a fragment read touches at once fall on different banks.  Rows
-  // past the end read the last row (their results are not used).
+  // This lane's global piece of each of the wave's loads (a load fills RPL
+  // rows).  Rows past the end read the last row (their results are not used).
   uint32_t voff[NI];
   {
-    const int r = lane >> 2;
-    const uint32_t piece = (uint32_t)((lane & 3) ^ ((r >> 1) & 3) ^ ((r >> 3) & 1));
+    constexpr int PPR = RB / 16;  // pieces a row
+    const int r = lane / PPR;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-      const int row = (wid * NI + j) * 16 + r;
-      const bool isb = (wid * NI + j) * 16 >= TM;
+      const int row = (wid * NI + j) * RPL + r;
+      const bool isb = (wid * NI + j) * RPL >= TM;
       const int64_t last = (isb ? g.N - n0 : g.M - m0) - 1;
       int64_t rr = isb ? row - TM : row;
       rr = rr < last ? rr : last;
-      voff[j] = (uint32_t)(rr * (isb ? g.ldb : g.lda) * 2) + piece * 16u;
+      voff[j] = (uint32_t)(rr * (isb ? g.ldb : g.lda) * 2) +
+                (uint32_t)((lane % PPR) ^ swizzle<BK>(row & 15)) * 16u;
     }
   }
-  const int total = g.kt * g.npair;
+  const int kt = (int)(g.k / BK);
+  const int total = kt * g.npair;
   const int it0 = (int)((int64_t)total * split / g.splits);
   const int nk = (int)((int64_t)total * (split + 1) / g.splits) - it0;
 
-  int ipair = it0 / g.kt, ik = it0 % g.kt;  // the next step to load
+  int ipair = it0 / kt, ik = it0 % kt;  // the next step to load
   auto issue = [&](int stage) {
-    const uint16_t* ap = abase + g.pa[ipair] + ik * kBK;
-    const uint16_t* bp = bbase + g.pb[ipair] + ik * kBK;
-    const uint32_t dst = lds0 + (uint32_t)(stage * Cfg::kStage);
+    const uint16_t* ap = abase + g.pa[ipair] + ik * BK;
+    const uint16_t* bp = bbase + g.pb[ipair] + ik * BK;
+    const uint32_t dst = lds0 + (uint32_t)(stage * S::kStage);
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int idx = wid * NI + j;
-      dma16(dst + (uint32_t)idx * 1024u, voff[j], idx * 16 >= TM ? bp : ap);
+      dma16(dst + (uint32_t)idx * 1024u, voff[j], idx * RPL >= TM ? bp : ap);
     }
-    if (++ik == g.kt) {
+    if (++ik == kt) {
       ik = 0;
       ++ipair;
     }
@@ -205,8 +229,8 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm(GemmArgs g) {
 
   // fragment addresses: row lane % 32 of a 32-row block, piece 2 kk + lane / 32
   const int fr = lane & 31;
-  const int fsw = ((fr >> 1) & 3) ^ ((fr >> 3) & 1);
-  const int fa = (wm * (TM / WM) + fr) * 64, fb = (TM + wn * (TN / WN) + fr) * 64;
+  const int fsw = swizzle<BK>(fr & 15);
+  const int fa = (wm * (TM / WM) + fr) * RB, fb = (TM + wn * (TN / WN) + fr) * RB;
 
 #pragma unroll
   for (int s = 0; s < NST - 1; ++s)
@@ -220,22 +244,21 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm(GemmArgs g) {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     if (i + NST - 1 < nk) issue(stage == 0 ? NST - 1 : stage - 1);
-    const char* st = lds + stage * Cfg::kStage;
+    const char* st = lds + stage * S::kStage;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
+    for (int kk = 0; kk < BK / 16; ++kk) {
       const int pc = ((kk * 2 + (lane >> 5)) ^ fsw) * 16;
-      bf16x8_t af[MT], bf[NT];
+      frag_t af[MT], bf[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        bf[j] = *reinterpret_cast<const bf16x8_t*>(st + fb + j * 32 * 64 + pc);
+        bf[j] = *reinterpret_cast<const frag_t*>(st + fb + j * 32 * RB + pc);
 #pragma unroll
       for (int j = 0; j < MT; ++j)
-        af[j] = *reinterpret_cast<const bf16x8_t*>(st + fa + j * 32 * 64 + pc);
+        af[j] = *reinterpret_cast<const frag_t*>(st + fa + j * 32 * RB + pc);
 #pragma unroll
       for (int j = 0; j < MT; ++j)
 #pragma unroll
-        for (int q = 0; q < NT; ++q)
-          acc[j][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[j], bf[q], acc[j][q], 0, 0, 0);
+        for (int q = 0; q < NT; ++q) acc[j][q] = Frag<F16>::mma(af[j], bf[q], acc[j][q]);
     }
     stage = stage == NST - 1 ? 0 : stage + 1;
   }
@@ -245,14 +268,37 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm(GemmArgs g) {
   const int ln = wn * (TN / WN) + (lane & 31);
   const int lm = wm * (TM / WM) + 4 * (lane >> 5);
   const int64_t nb = n0 + ln, mb = m0 + lm;
-  const int mleft = (int)(g.M - mb < 32 * MT ? g.M - mb : 32 * MT);  // classes left (<= 0: none)
+  const int mleft = (int)(g.M - mb < 32 * MT ? g.M - mb : 32 * MT);  // <= 0: none
 
-  if constexpr (EPI == kEpiLse) {
-    float2* red = reinterpret_cast<float2*>(lds);  // [WM][TN]
+  if constexpr (EPI == kEpiLogits) {
+    constexpr int PG = TM + 8;  // a padded row of e in LDS
+    float* red = reinterpret_cast<float*>(lds);         // [2][WM][TN]: maxima, sums
+    uint16_t* keep = reinterpret_cast<uint16_t*>(lds + WM * TN * 8);
+    if constexpr (F16) {
+      float bu[NT];
+#pragma unroll
+      for (int q = 0; q < NT; ++q) bu[q] = nb + 32 * q < g.N ? g.b_unscale[nb + 32 * q] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+          // past the last class: room of the workspace, masked below
+          const f32x4_t au =
+              *reinterpret_cast<const f32x4_t*>(g.a_unscale + mb + 32 * j + 8 * e4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+              acc[j][q][4 * e4 + e] = acc[j][q][4 * e4 + e] * bu[q] * au[e];
+          asm volatile("" ::: "memory");  // one load's values at a time
+        }
+    }
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
       const int64_t n = nb + 32 * q;
-      const int at = class_at(n < g.N ? g.target[n] : -1, g, mb);
+      // the target's place among the lane's classes (it has those with bit 2 clear)
+      const int64_t d = (n < g.N ? g.target[n] : -1) - mb;
+      const int at = d >= 0 && d < 32 * MT && d < mleft && (d & 4) == 0 ? (int)d : -1;
       float mx = -__builtin_inff(), tl = 0.0f;
 #pragma unroll
       for (int j = 0; j < MT; ++j)
@@ -263,152 +309,98 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm(GemmArgs g) {
           mx = fmaxf(mx, acc[j][q][e]);
           if (m == at) tl = acc[j][q][e];
         }
-      if (at >= 0 && at < 32 * MT && (at & 4) == 0) g.tlogit[n] = tl;
-      float sum = 0.0f;
-      if (mx > -__builtin_inff()) {
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            sum += __builtin_amdgcn_exp2f((acc[j][q][e] - mx) * kLog2eF);
-      }
-      const float mx2 = __shfl_xor(mx, 32), sum2 = __shfl_xor(sum, 32);
-      const float top = fmaxf(mx, mx2);
-      float all = 0.0f;
-      if (sum > 0.0f || sum != sum) all += sum * __builtin_amdgcn_exp2f((mx - top) * kLog2eF);
-      if (sum2 > 0.0f || sum2 != sum2) all += sum2 * __builtin_amdgcn_exp2f((mx2 - top) * kLog2eF);
-      if (lane < 32) red[wm * TN + ln + 32 * q] = make_float2(top, all);
+      if (at >= 0) g.tlogit[n] = tl;
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      if (lane < 32) red[wm * TN + ln + 32 * q] = mx;
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < TN; c += Cfg::kThreads) {
-      if (n0 + c >= g.N) continue;
-      float top = -__builtin_inff(), all = 0.0f;
-#pragma unroll
-      for (int w = 0; w < WM; ++w) top = fmaxf(top, red[w * TN + c].x);
-#pragma unroll
-      for (int w = 0; w < WM; ++w) {
-        const float2 v = red[w * TN + c];
-        if (v.y > 0.0f || v.y != v.y) all += v.y * __builtin_amdgcn_exp2f((v.x - top) * kLog2eF);
-      }
-      g.part[(n0 + c) * g.part_ld + g.part0 + tm] = make_float2(top, all);
-    }
-  }
-
-  if constexpr (EPI == kEpiGrad) {
-    constexpr int PG = TM + 8, PT = TN + 8;  // padded rows in LDS
-    uint16_t* sg = reinterpret_cast<uint16_t*>(lds);
-    float ratio[NT];
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
-      const int64_t n = nb + 32 * q;
-      const bool in = n < g.N;
-      const int64_t t = in ? g.target[n] : -1;
-      const bool counts = t >= 0 && t < g.V;
-      const float l2 = counts ? g.lse[n] * kLog2eF : 0.0f;
-      const int at = class_at(t, g, mb), mend = counts ? mleft : 0;
-      ratio[q] = in ? g.ratio[n] : 0.0f;
+      float top = red[ln + 32 * q];
+#pragma unroll
+      for (int w = 1; w < WM; ++w) top = fmaxf(top, red[w * TN + ln + 32 * q]);
+      const float top2 = top * kLog2eF;
+      float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < MT; ++j)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int m = 32 * j + 8 * (e / 4) + e % 4;
-          float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[j][q][e], kLog2eF, -l2));
-          if (m == at) p -= 1.0f;
-          acc[j][q][e] = m < mend ? p : 0.0f;
+          const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[j][q][e], kLog2eF, -top2));
+          sum += v;
+          if constexpr (KEEP != kKeepNone) acc[j][q][e] = v;
         }
-    }
-    for (int part = 0; part < g.nparts; ++part) {
-      // G: rows of n, TM classes each.  The residue of this part stays in acc.
-#pragma unroll
-      for (int q = 0; q < NT; ++q)
+      sum += __shfl_xor(sum, 32);
+      if (lane < 32) red[WM * TN + wm * TN + ln + 32 * q] = sum;
+      if constexpr (KEEP == kKeepF16) {
 #pragma unroll
         for (int j = 0; j < MT; ++j)
 #pragma unroll
           for (int e4 = 0; e4 < 4; ++e4) {
-            const u32x2_t w = {pack_bf16x2(acc[j][q][4 * e4], acc[j][q][4 * e4 + 1]),
-                               pack_bf16x2(acc[j][q][4 * e4 + 2], acc[j][q][4 * e4 + 3])};
-            *reinterpret_cast<u32x2_t*>(sg + (ln + 32 * q) * PG + lm + 32 * j + 8 * e4) = w;
+            const f16x2_t lo = {(_Float16)acc[j][q][4 * e4], (_Float16)acc[j][q][4 * e4 + 1]};
+            const f16x2_t hi = {(_Float16)acc[j][q][4 * e4 + 2], (_Float16)acc[j][q][4 * e4 + 3]};
+            *reinterpret_cast<u32x2_t*>(keep + (ln + 32 * q) * PG + lm + 32 * j + 8 * e4) =
+                u32x2_t{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
           }
-      __syncthreads();
-      for (int c = threadIdx.x; c < TN * (TM / 8); c += Cfg::kThreads) {
-        const int r = c / (TM / 8), k = c % (TM / 8) * 8;
-        if (n0 + r < g.N)
-          *reinterpret_cast<u32x4_t*>(g.g + (n0 + r) * g.ldg + part * g.part_k + m0 + k) =
-              *reinterpret_cast<const u32x4_t*>(sg + r * PG + k);
       }
-      if (g.nparts > 1) {
-#pragma unroll
-        for (int q = 0; q < NT; ++q)
+      if constexpr (KEEP == kKeepF32) {
+        if (nb + 32 * q < g.N) {
+          float* o = (float*)g.e + (nb + 32 * q) * g.lde + mb;
 #pragma unroll
           for (int j = 0; j < MT; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              acc[j][q][e] -= bf16_lo(pack_bf16x2(acc[j][q][e], 0.0f));
-      }
-      __syncthreads();
-    }
-    if (g.nparts > 1) {
-      // the residue is spent: p once more from what was written would round
-      // twice, so the parts of G^T are split from the sum of G's three
-      // parts (exact in fp32)
-      for (int c = threadIdx.x; c < TM * TN; c += Cfg::kThreads) {
-        const int n = c / TM, m = c % TM;
-        if (n0 + n < g.N && m0 + m < g.M) {
-          const uint16_t* p = g.g + (n0 + n) * g.ldg + m0 + m;
-          float v = io_ld(p, 0) + io_ld(p, g.part_k) + io_ld(p, 2 * g.part_k);
-          v *= g.ratio[n0 + n];
-          uint16_t* o = g.gt + (m0 + m) * g.ldgt + n0 + n;
-          for (int part = 0; part < 3; ++part) {
-            io_st(o, part * g.part_kt, v);
-            v -= bf16_lo(pack_bf16x2(v, 0.0f));
-          }
-        } else if (m0 + m < g.M) {
-          uint16_t* o = g.gt + (m0 + m) * g.ldgt + n0 + n;
-          for (int part = 0; part < 3; ++part) o[part * g.part_kt] = 0;
+            for (int e4 = 0; e4 < 4; ++e4)
+              *reinterpret_cast<f32x4_t*>(o + 32 * j + 8 * e4) =
+                  f32x4_t{acc[j][q][4 * e4], acc[j][q][4 * e4 + 1], acc[j][q][4 * e4 + 2],
+                          acc[j][q][4 * e4 + 3]};
         }
       }
-    } else {
-      // G^T: rows of m, TN rows of x each
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < TN; c += S::kThreads) {
+      if (n0 + c >= g.N) continue;
+      float top = red[c], sum = red[WM * TN + c];
 #pragma unroll
-      for (int q = 0; q < NT; ++q)
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            io_st(sg, (lm + 32 * j + 8 * (e / 4) + e % 4) * PT + ln + 32 * q,
-                  acc[j][q][e] * ratio[q]);
-      __syncthreads();
-      for (int c = threadIdx.x; c < TM * (TN / 8); c += Cfg::kThreads) {
-        const int r = c / (TN / 8), k = c % (TN / 8) * 8;
-        if (m0 + r < g.M)
-          *reinterpret_cast<u32x4_t*>(g.gt + (m0 + r) * g.ldgt + n0 + k) =
-              *reinterpret_cast<const u32x4_t*>(sg + r * PT + k);
+      for (int w = 1; w < WM; ++w) {
+        top = fmaxf(top, red[w * TN + c]);
+        sum += red[WM * TN + w * TN + c];
+      }
+      g.part[(n0 + c) * g.tm + tm] = make_float2(top, sum);
+    }
+    if constexpr (KEEP == kKeepF16) {
+      for (int c = threadIdx.x; c < TN * (TM / 8); c += S::kThreads) {
+        const int r = c / (TM / 8), k = c % (TM / 8) * 8;
+        if (n0 + r < g.N)
+          *reinterpret_cast<u32x4_t*>((uint16_t*)g.e + (n0 + r) * g.lde + m0 + k) =
+              *reinterpret_cast<const u32x4_t*>(keep + r * PG + k);
       }
     }
   }
 
   if constexpr (EPI == kEpiOut) {
-    const float sc = g.scale ? *g.scale : 1.0f;
+    const float sc = (g.scale ? *g.scale : 1.0f), un = g.unscale ? *g.unscale : 1.0f;
+    const bool slot = g.slots != nullptr;
 #pragma unroll
     for (int j = 0; j < MT; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const int64_t m = mb + 32 * j + 8 * (e / 4) + e % 4;
-        if (m >= g.M) continue;
-        const float rs = g.slots ? 1.0f : g.row_scale ? g.row_scale[m] : sc;
+        const int dm = 32 * j + 8 * (e / 4) + e % 4;
+        if (dm >= mleft) continue;
+        const int64_t m = mb + dm;
+        const float rs = g.row_scale ? g.row_scale[m] : sc;
 #pragma unroll
         for (int q = 0; q < NT; ++q) {
           const int64_t n = nb + 32 * q;
           if (n >= g.N) continue;
-          float v = acc[j][q][e];
-          if (g.slots) {
-            float* p = g.slots + ((int64_t)split * g.M + m) * g.N + n;
-            *p = g.accumulate ? *p + v : v;
-          } else {
+          float v = acc[j][q][e] * un;
+          float* p = g.slots + ((int64_t)split * g.M + m) * g.N + n;
+          if (slot && g.add) v += *p;
+          if (g.last) {
             // a scale of 0 (an ignored row) is a gradient of 0 whatever v is
             v = rs == 0.0f ? 0.0f : v * rs;
             if (g.out_bf16) io_st((uint16_t*)g.out, m * g.N + n, v);
             else ((float*)g.out)[m * g.N + n] = v;
+          } else {
+            *p = v;
           }
         }
       }
@@ -417,46 +409,117 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void k_gemm(GemmArgs g) {
 
 // ---- small kernels -----------------------------------------------------------
 
-// bf16 parts of v, most significant first.
+__device__ __forceinline__ bool row_counts(int64_t t, int64_t V) { return t >= 0 && t < V; }
+
+// A value as the products take it: bf16 unchanged, fp32 as two fp16 parts.
+__device__ __forceinline__ uint16_t f16_bits(float v) {
+  return __builtin_bit_cast(uint16_t, (_Float16)v);
+}
 template <int P>
 __device__ __forceinline__ void split_parts(float v, uint16_t (&p)[P]) {
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    p[i] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
-    v -= as_f32((uint32_t)p[i] << 16);
+  if constexpr (P == 1) {
+    p[0] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+  } else {
+    p[0] = f16_bits(v);
+    p[1] = f16_bits(v - (float)__builtin_bit_cast(_Float16, p[0]));
   }
 }
 
-// [rows][D] -> bf16 [rows][P * Dp], zero past D.
-template <typename IO, int P>
-__global__ __launch_bounds__(256) void k_ce_pack(const IO* __restrict__ src,
-                                                 uint16_t* __restrict__ dst, int64_t rows,
-                                                 int64_t D, int64_t Dp) {
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
-    for (int64_t d = threadIdx.x; d < Dp; d += 256) {
-      uint16_t p[P];
-      split_parts<P>(d < D ? io_ld(src, row * D + d) : 0.0f, p);
-#pragma unroll
-      for (int i = 0; i < P; ++i) dst[(row * P + i) * Dp + d] = p[i];
-    }
+// The power of two that brings values up to `top` to at most 2^14, and its
+// inverse (1 for 0, infinities and NaN).
+__device__ __forceinline__ float scale_for(float top, float& inverse) {
+  int e = (int)((as_u32(top) >> 23) & 255) - 127;  // top = 1.x * 2^e
+  const bool ok = top > 0.0f && e < 128;
+  e = ok ? 13 - e : 0;
+  e = e < -126 ? -126 : e > 126 ? 126 : e;
+  inverse = as_f32((uint32_t)(127 - e) << 23);
+  return as_f32((uint32_t)(127 + e) << 23);
 }
 
-// [rows][D] -> bf16 [D][P * Rp], zero past `rows` and in ignored rows (whatever
-// they hold).
+__device__ __forceinline__ float wave_top(float v) {
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+  return v;
+}
+
+// bf16 [rows][D] -> [rows][Dp], zero past D; one wave a row.  With `target`,
+// rows that do not count become 0, whatever they hold.
+__global__ __launch_bounds__(256) void k_ce_rows_bf16(const uint16_t* __restrict__ src,
+                                                      uint16_t* __restrict__ dst, int64_t rows,
+                                                      int64_t D, int64_t Dp) {
+  const int lane = threadIdx.x & (kWave - 1);
+  for (int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; row < rows;
+       row += (int64_t)gridDim.x * 4)
+    for (int64_t d = lane; d < Dp; d += kWave) dst[row * Dp + d] = d < D ? src[row * D + d] : 0;
+}
+
+// fp32 [rows][D] -> two fp16 parts [rows][2][Dp] scaled by the row's power of
+// two; unscale[row] undoes it and top[row] is the row's largest value (0 in rows
+// that do not count).  One wave a row.
+__global__ __launch_bounds__(256) void k_ce_rows_f32(const float* __restrict__ src,
+                                                     const int64_t* __restrict__ target, int64_t V,
+                                                     uint16_t* __restrict__ dst,
+                                                     float* __restrict__ unscale,
+                                                     float* __restrict__ top_out, int64_t rows,
+                                                     int64_t D, int64_t Dp) {
+  const int lane = threadIdx.x & (kWave - 1);
+  for (int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; row < rows;
+       row += (int64_t)gridDim.x * 4) {
+    float top = 0.0f;
+    for (int64_t d = lane; d < D; d += kWave) top = fmaxf(top, fabsf(src[row * D + d]));
+    top = wave_top(top);
+    float inv;
+    const float sc = scale_for(top, inv);
+    for (int64_t d = lane; d < Dp; d += kWave) {
+      uint16_t p[2];
+      split_parts<2>(d < D ? src[row * D + d] * sc : 0.0f, p);
+      dst[row * 2 * Dp + d] = p[0];
+      dst[(row * 2 + 1) * Dp + d] = p[1];
+    }
+    if (lane == 0) {
+      unscale[row] = inv;
+      top_out[row] = !target || row_counts(target[row], V) ? top : 0.0f;
+    }
+  }
+}
+
+// The largest of top[0 .. n), as a scale for a whole array: scale[0] and
+// scale[1] / kGScale, which undoes it and G's.  One workgroup.
+__global__ __launch_bounds__(1024) void k_ce_top(const float* __restrict__ top, int64_t n,
+                                                 float* __restrict__ scale) {
+  __shared__ float red[16];
+  float v = 0.0f;
+  for (int64_t i = threadIdx.x; i < n; i += 1024) v = fmaxf(v, top[i]);
+  v = wave_top(v);
+  if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    v = red[0];
+    for (int w = 1; w < 16; ++w) v = fmaxf(v, red[w]);
+    float inv;
+    scale[0] = scale_for(v, inv);
+    scale[1] = inv / kGScale;
+  }
+}
+
+// [rows][D] -> [D][P][Rp] (row pitch ld), zero past `rows` and in rows that do
+// not count, whatever they hold.
 template <typename IO, int P>
-__global__ __launch_bounds__(256) void k_ce_pack_t(const IO* __restrict__ src,
-                                                   const int64_t* __restrict__ target, int64_t V,
-                                                   uint16_t* __restrict__ dst, int64_t rows,
-                                                   int64_t D, int64_t Rp) {
+__global__ __launch_bounds__(256) void k_ce_cols(const IO* __restrict__ src,
+                                                 const int64_t* __restrict__ target, int64_t V,
+                                                 const float* __restrict__ scale,
+                                                 uint16_t* __restrict__ dst, int64_t rows,
+                                                 int64_t D, int64_t Rp, int64_t ld) {
   __shared__ float tile[64][65];
   const int64_t r0 = (int64_t)blockIdx.x * 64, d0 = (int64_t)blockIdx.y * 64;
   const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+  const float sc = P == 1 ? 1.0f : *scale;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int64_t r = r0 + ty + 4 * i, d = d0 + tx;
     bool ok = r < rows && d < D;
-    if (ok && target) ok = target[r] >= 0 && target[r] < V;
-    tile[ty + 4 * i][tx] = ok ? io_ld(src, r * D + d) : 0.0f;
+    if (ok && target) ok = row_counts(target[r], V);
+    tile[ty + 4 * i][tx] = ok ? io_ld(src, r * D + d) * sc : 0.0f;
   }
   __syncthreads();
 #pragma unroll
@@ -466,7 +529,7 @@ __global__ __launch_bounds__(256) void k_ce_pack_t(const IO* __restrict__ src,
       uint16_t p[P];
       split_parts<P>(tile[tx][ty + 4 * i], p);
 #pragma unroll
-      for (int k = 0; k < P; ++k) dst[(d * P + k) * Rp + r] = p[k];
+      for (int k = 0; k < P; ++k) dst[d * ld + k * Rp + r] = p[k];
     }
   }
 }
@@ -483,8 +546,7 @@ __global__ __launch_bounds__(256) void k_ce_join(const float2* __restrict__ part
   const float2* p = part + n * tiles;
   float top = -__builtin_inff(), sum = 0.0f;
   for (int64_t t = lane; t < tiles; t += kWave) top = fmaxf(top, p[t].x);
-#pragma unroll
-  for (int o = kWave / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  top = wave_top(top);
   for (int64_t t = lane; t < tiles; t += kWave)
     sum += p[t].y * __builtin_amdgcn_exp2f((p[t].x - top) * kLog2eF);
 #pragma unroll
@@ -492,8 +554,7 @@ __global__ __launch_bounds__(256) void k_ce_join(const float2* __restrict__ part
   if (lane == 0) {
     const float l = top + logf(sum);
     lse[n] = l;
-    const int64_t t = target[n];
-    loss[n] = t >= 0 && t < V ? l - tlogit[n] : 0.0f;
+    loss[n] = row_counts(target[n], V) ? l - tlogit[n] : 0.0f;
   }
 }
 
@@ -506,24 +567,90 @@ __global__ __launch_bounds__(1024) void k_ce_scale(const float* __restrict__ gra
                                                    float* __restrict__ top_out) {
   __shared__ float red[16];
   float top = 0.0f;
-  for (int64_t n = threadIdx.x; n < N; n += 1024) {
-    const bool ok = target[n] >= 0 && target[n] < V;
-    if (ok) top = fmaxf(top, fabsf(grad_loss[n]));
-  }
-#pragma unroll
-  for (int o = kWave / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  for (int64_t n = threadIdx.x; n < N; n += 1024)
+    if (row_counts(target[n], V)) top = fmaxf(top, fabsf(grad_loss[n]));
+  top = wave_top(top);
   if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = top;
   __syncthreads();
   top = red[0];
 #pragma unroll
   for (int w = 1; w < 16; ++w) top = fmaxf(top, red[w]);
   for (int64_t n = threadIdx.x; n < N; n += 1024) {
-    const bool ok = target[n] >= 0 && target[n] < V;
-    const float v = ok ? grad_loss[n] : 0.0f;
+    const float v = row_counts(target[n], V) ? grad_loss[n] : 0.0f;
     row_scale[n] = v;
     ratio[n] = v == 0.0f ? 0.0f : v / top;
   }
   if (threadIdx.x == 0) *top_out = top;
+}
+
+// e -> G [rows][P][Vp] (row pitch ldg; bf16 over e's own fp16 values) and G^T
+// [classes][P][Np] (ldgt), 64 x 64 values a workgroup.  Columns of padding hold
+// 0: e is 0 past the last class, and rows past the last one are written as 0.
+template <typename E, int P>
+__global__ __launch_bounds__(256) void k_ce_g(const E* e, int64_t lde, const float2* __restrict__ part,
+                                              int64_t tiles, int tile_m,
+                                              const float* __restrict__ lse,
+                                              const int64_t* __restrict__ target,
+                                              const float* __restrict__ ratio, uint16_t* g,
+                                              int64_t ldg, uint16_t* __restrict__ gt, int64_t ldgt,
+                                              int64_t rows, int64_t V, int64_t Vp, int64_t Np) {
+  __shared__ float tile[64][65];
+  const int64_t n0 = (int64_t)blockIdx.y * 64, v0 = (int64_t)blockIdx.x * 64;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // four classes a thread, 16 rows a pass
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t n = n0 + ty + 16 * i, v = v0 + 4 * tx;
+    float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float share = 0.0f;
+    if (n < rows) {
+      const int64_t t = target[n];
+      if (row_counts(t, V)) {
+        share = ratio[n];
+        // v0's tile of 64 lies inside one tile of the logits
+        const float f =
+            __builtin_amdgcn_exp2f((part[n * tiles + v0 / tile_m].x - lse[n]) * kLog2eF);
+        const int at = (int)(t - v);
+        float ev[4];
+        if constexpr (sizeof(E) == 2) {
+          const u32x2_t w = *reinterpret_cast<const u32x2_t*>(e + n * lde + v);
+          const uint32_t w0 = w.x, w1 = w.y;  // a bit cast of an element takes the vector's first
+          const f16x2_t a = __builtin_bit_cast(f16x2_t, w0), b = __builtin_bit_cast(f16x2_t, w1);
+          ev[0] = (float)a.x; ev[1] = (float)a.y; ev[2] = (float)b.x; ev[3] = (float)b.y;
+        } else {
+          const f32x4_t w = *reinterpret_cast<const f32x4_t*>(e + n * lde + v);
+          ev[0] = w.x; ev[1] = w.y; ev[2] = w.z; ev[3] = w.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j] = __builtin_fmaf(ev[j], f, j == at ? -1.0f : 0.0f);
+      }
+      const float gs = P == 1 ? 1.0f : kGScale;
+      uint16_t q[4][P];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split_parts<P>(p[j] * gs, q[j]);
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+        *reinterpret_cast<u32x2_t*>(g + n * ldg + k * Vp + v) =
+            u32x2_t{(uint32_t)q[0][k] | (uint32_t)q[1][k] << 16,
+                    (uint32_t)q[2][k] | (uint32_t)q[3][k] << 16};
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) tile[ty + 16 * i][4 * tx + j] = p[j] * share;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t v = v0 + ty + 16 * i, n = n0 + 4 * tx;
+    if (v >= V) continue;
+    const float gs = P == 1 ? 1.0f : kGScale;
+    uint16_t q[4][P];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split_parts<P>(tile[4 * tx + j][ty + 16 * i] * gs, q[j]);
+#pragma unroll
+    for (int k = 0; k < P; ++k)
+      *reinterpret_cast<u32x2_t*>(gt + v * ldgt + k * Np + n) =
+          u32x2_t{(uint32_t)q[0][k] | (uint32_t)q[1][k] << 16,
+                  (uint32_t)q[2][k] | (uint32_t)q[3][k] << 16};
+  }
 }
 
 // out[m][n] = scale of the row (or of all) times the sum of the slots, in order.
@@ -558,73 +685,76 @@ unsigned blocks_for(int64_t n, int64_t per) {
   return (unsigned)(b < 1 ? 1 : b > 65536 ? 65536 : b);
 }
 
-// The two tile shapes: 256 x 128 with four waves of 128 x 64, three buffers,
-// two workgroups a compute unit; and 128 x 64 for products with few tiles.
-constexpr int kBigM = 256, kBigN = 128, kSmallM = 128, kSmallN = 64;
+// The tile shapes: 256 x 128 with four waves of 128 x 64, three buffers, two
+// workgroups a compute unit (one's epilogue runs beside the other's products);
+// and 128 x 64 for products with few tiles.
+typedef Shape<256, 128, 2, 2, 32, 3, 2> Big;
+typedef Shape<128, 64, 4, 1, 32, 6, 2> Small;
+typedef Shape<256, 256, 2, 4, 64, 2, 2> Huge;
 
 int64_t tiles_of(int64_t M, int64_t N, bool big) {
-  return big ? up(M, kBigM) / kBigM * (up(N, kBigN) / kBigN)
-             : up(M, kSmallM) / kSmallM * (up(N, kSmallN) / kSmallN);
+  return big ? up(M, Big::TM) / Big::TM * (up(N, Big::TN) / Big::TN)
+             : up(M, Small::TM) / Small::TM * (up(N, Small::TN) / Small::TN);
 }
 bool use_big(int64_t M, int64_t N) { return tiles_of(M, N, true) >= 256; }
 
-template <int EPI>
-hipError_t run_gemm(GemmArgs& g, bool big, hipStream_t stream) {
-  g.tm = (int)(up(g.M, big ? kBigM : kSmallM) / (big ? kBigM : kSmallM));
-  g.tn = (int)(up(g.N, big ? kBigN : kSmallN) / (big ? kBigN : kSmallN));
-  const dim3 grid((unsigned)((int64_t)g.tm * g.tn * g.splits));
-  if (big)
-    hipLaunchKernelGGL((k_gemm<kBigM, kBigN, 2, 2, 3, EPI>), grid, dim3(256), 0, stream, g);
-  else
-    hipLaunchKernelGGL((k_gemm<kSmallM, kSmallN, 4, 1, 6, EPI>), grid, dim3(256), 0, stream, g);
+template <class S, int EPI, int KEEP, bool F16>
+hipError_t run_gemm(GemmArgs& g, hipStream_t stream) {
+  g.tm = (int)(up(g.M, S::TM) / S::TM);
+  g.tn = (int)(up(g.N, S::TN) / S::TN);
+  hipLaunchKernelGGL((k_gemm<S, EPI, KEEP, F16>), dim3((unsigned)((int64_t)g.tm * g.tn * g.splits)),
+                     dim3(S::kThreads), 0, stream, g);
   return hipGetLastError();
 }
 
-template <typename IO, int P>
-hipError_t pack(const void* src, uint16_t* dst, int64_t rows, int64_t D, int64_t Dp,
-                hipStream_t stream) {
-  hipLaunchKernelGGL((k_ce_pack<IO, P>), dim3(blocks_for(rows, 1)), dim3(256), 0, stream,
-                     (const IO*)src, dst, rows, D, Dp);
-  return hipGetLastError();
-}
-template <typename IO, int P>
-hipError_t pack_t(const void* src, const int64_t* target, int64_t V, uint16_t* dst, int64_t rows,
-                  int64_t D, int64_t Rp, hipStream_t stream) {
-  hipLaunchKernelGGL((k_ce_pack_t<IO, P>),
-                     dim3((unsigned)(up(Rp, 64) / 64), (unsigned)(up(D, 64) / 64)), dim3(256), 0,
-                     stream, (const IO*)src, target, V, dst, rows, D, Rp);
-  return hipGetLastError();
+template <int EPI, int KEEP>
+hipError_t run(GemmArgs& g, bool big, bool f16, hipStream_t stream) {
+  if (big)
+    return f16 ? run_gemm<Big, EPI, KEEP, true>(g, stream)
+               : run_gemm<Big, EPI, KEEP, false>(g, stream);
+  return f16 ? run_gemm<Small, EPI, KEEP, true>(g, stream)
+             : run_gemm<Small, EPI, KEEP, false>(g, stream);
 }
 
 }  // namespace
 
-// Pieces of the vocabulary whose G takes at most this many bytes.
+// Pieces of the rows whose G takes at most this many bytes.
 constexpr int64_t kCePieceBytes = (int64_t)512 << 20;
 
 CePlan plan_ce(int64_t N, int64_t V, int64_t D, int io) {
   CePlan p;
-  p.parts = io == kIoBf16 ? 1 : 3;
-  p.Dp = up(D, kBK);
-  p.Np = up(N, kBigN);
-  const int64_t most = kCePieceBytes / (p.Np * 2 * p.parts) / kBigM * kBigM;
-  const int64_t pieces = (V + (most < kBigM ? kBigM : most) - 1) / (most < kBigM ? kBigM : most);
-  p.piece = up((V + pieces - 1) / pieces, kBigM);
-  p.pieces = (V + p.piece - 1) / p.piece;
-  p.big_l = use_big(p.piece, N);
-  p.tiles = p.big_l ? up(V, kBigM) / kBigM : up(V, kSmallM) / kSmallM;
+  p.parts = io == kIoBf16 ? 1 : 2;
+  p.Dp = up(D, 64);
+  p.Vp = up(V, Big::TM);
+  const int64_t most = kCePieceBytes / (p.Vp * 2 * p.parts) / Big::TM * Big::TM;
+  const int64_t cap = most < Big::TM ? Big::TM : most;
+  const int64_t pieces = (N + cap - 1) / cap;
+  p.piece = up((N + pieces - 1) / pieces, Big::TN);
+  p.pieces = (N + p.piece - 1) / p.piece;
+  // 128 bytes past a power of two: rows a power of two apart would meet in few
+  // of the cache's channels
+  p.ldg = p.parts * p.Vp + 64;
+  p.ldgt = p.parts * p.piece + 64;
+  // the forward's only growing array is (maximum, sum) of each tile and row:
+  // pieces of rows for it too (128 MiB; each still fills the GPU)
+  const int64_t most_f = (kCePieceBytes / 4) / (up(V, Small::TM) / Small::TM * 8) / Big::TN * Big::TN;
+  p.piece_f = most_f < Big::TN ? Big::TN : most_f > N ? N : most_f;
+  p.big_f = use_big(V, p.piece_f);
+  p.big_l = use_big(V, p.piece);
+  p.tiles_f = up(V, p.big_f ? Big::TM : Small::TM) / (p.big_f ? Big::TM : Small::TM);
+  p.tiles_l = up(V, p.big_l ? Big::TM : Small::TM) / (p.big_l ? Big::TM : Small::TM);
   auto splits = [](int64_t M, int64_t N_, int64_t K, bool big) -> int64_t {
-    // enough workgroups for two a compute unit, each with 16 steps at least
+    // enough workgroups for two a compute unit, each with 512 of k at least
     int64_t s = 512 / tiles_of(M, N_, big);
-    const int64_t most_s = K / (16 * kBK);
-    s = s > most_s ? most_s : s;
+    s = s > K / 512 ? K / 512 : s;
     return s < 1 ? 1 : s > 16 ? 16 : s;
   };
-  p.big_x = use_big(N, D) || tiles_of(N, D, true) * 8 >= 256;
-  p.big_w = use_big(p.piece, D) || tiles_of(p.piece, D, true) * 8 >= 256;
-  p.split_x = splits(N, D, p.piece, p.big_x);
-  p.split_w = splits(p.piece, D, p.Np, p.big_w);
-  p.slots_x = p.split_x > 1 || p.pieces > 1;
-  p.slots_w = p.split_w > 1;
+  p.big_x = tiles_of(p.piece, D, true) * 8 >= 256;
+  p.big_w = tiles_of(V, D, true) * 8 >= 256;
+  p.split_x = splits(p.piece, D, p.Vp, p.big_x);
+  p.split_w = splits(V, D, p.piece, p.big_w);
+  p.slots_x = p.split_x > 1;
+  p.slots_w = p.split_w > 1 || p.pieces > 1;
   return p;
 }
 
@@ -632,142 +762,156 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
   const bool bf = io == kIoBf16;
   const int64_t es = bf ? 2 : 4;
   hipError_t e = hipSuccess;
-#define LRS_CE(call)                 \
-  do {                               \
-    e = (call);                      \
-    if (e != hipSuccess) return e;   \
+#define LRS_CE(call)               \
+  do {                             \
+    e = (call);                    \
+    if (e != hipSuccess) return e; \
   } while (0)
   GemmArgs base = {};
-  base.npair = p.parts == 1 ? 1 : 6;
-  // smallest products first: lo hi, hi lo, mid mid, mid hi, hi mid, hi hi
-  const int ia[6] = {2, 0, 1, 1, 0, 0}, ib[6] = {0, 2, 1, 0, 1, 0};
+  base.npair = bf ? 1 : 3;
+  // smallest products first: lo hi, hi lo, hi hi
   auto pairs = [&](GemmArgs& g, int64_t ka, int64_t kb, int64_t k) {
-    for (int i = 0; i < base.npair; ++i) {
-      g.pa[i] = p.parts == 1 ? 0 : (int)(ia[i] * ka);
-      g.pb[i] = p.parts == 1 ? 0 : (int)(ib[i] * kb);
+    if (!bf) {
+      g.pa[0] = ka;
+      g.pb[1] = kb;
     }
-    g.kt = (int)(k / kBK);
+    g.k = k;
   };
   base.splits = 1;
-  base.target = a.target;
-  base.V = a.V;
-  base.lse = a.lse;
   // rows of x and w as the logits' product takes them
-  const bool raw_x = bf && p.Dp == a.D && ((uintptr_t)a.x & 15) == 0;
-  const bool raw_w = bf && p.Dp == a.D && ((uintptr_t)a.w & 15) == 0;
-  const uint16_t* xr = raw_x ? (const uint16_t*)a.x : a.x_rows;
-  if (!raw_x)
-    LRS_CE(bf ? (pack<uint16_t, 1>(a.x, a.x_rows, a.N, a.D, p.Dp, stream))
-              : (pack<float, 3>(a.x, a.x_rows, a.N, a.D, p.Dp, stream)));
-  auto w_rows = [&](int64_t v0, int64_t n, const uint16_t** out) -> hipError_t {
-    const char* src = (const char*)a.w + v0 * a.D * es;
-    if (raw_w) {
-      *out = (const uint16_t*)src;
-      return hipSuccess;
-    }
-    *out = a.w_rows;
-    return bf ? pack<uint16_t, 1>(src, a.w_rows, n, a.D, p.Dp, stream)
-              : pack<float, 3>(src, a.w_rows, n, a.D, p.Dp, stream);
+  const uint16_t *xr = (const uint16_t*)a.x, *wr = (const uint16_t*)a.w;
+  auto rows = [&](const void* src, uint16_t* dst, int64_t n, const int64_t* target, float* unscale,
+                  float* top, const uint16_t** out) -> hipError_t {
+    if (bf && p.Dp == a.D && ((uintptr_t)src & 15) == 0) return hipSuccess;
+    *out = dst;
+    if (bf)
+      hipLaunchKernelGGL(k_ce_rows_bf16, dim3(blocks_for(n, 4)), dim3(256), 0, stream,
+                         (const uint16_t*)src, dst, n, a.D, p.Dp);
+    else
+      hipLaunchKernelGGL(k_ce_rows_f32, dim3(blocks_for(n, 4)), dim3(256), 0, stream,
+                         (const float*)src, target, a.V, dst, unscale, top, n, a.D, p.Dp);
+    return hipGetLastError();
   };
-  auto logits = [&](GemmArgs& g, const uint16_t* wr, int64_t v0, int64_t n) {
+  LRS_CE(rows(a.x, a.x_rows, a.N, a.target, a.x_unscale, a.x_top, &xr));
+  LRS_CE(rows(a.w, a.w_rows, a.V, nullptr, a.w_unscale, a.w_top, &wr));
+  auto logits = [&](int64_t n0, int64_t n) {
+    GemmArgs g = base;
     g.a = wr;
-    g.b = xr;
+    g.b = xr + n0 * p.parts * p.Dp;
     g.lda = g.ldb = p.parts * p.Dp;
-    g.M = n;
-    g.N = a.N;
-    g.v0 = v0;
+    g.M = a.V;
+    g.N = n;
+    g.target = a.target + n0;
+    g.part = a.part;
+    g.tlogit = a.tlogit;  // of this piece's rows
+    g.a_unscale = a.w_unscale;
+    g.b_unscale = a.x_unscale + n0;
+    g.e = a.e;
+    g.lde = a.lde;
     pairs(g, p.Dp, p.Dp, p.Dp);
+    return g;
   };
-  bool packed_whole = false;  // a.w_rows holds the only piece
-  if (a.forward) {
-    for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
-      const int64_t n = a.V - v0 < p.piece ? a.V - v0 : p.piece;
-      const uint16_t* wr;
-      LRS_CE(w_rows(v0, n, &wr));
-      GemmArgs g = base;
-      logits(g, wr, v0, n);
-      g.part = a.part;
-      g.part0 = v0 / (p.big_l ? kBigM : kSmallM);
-      g.part_ld = p.tiles;
-      g.tlogit = a.tlogit;
-      LRS_CE(run_gemm<kEpiLse>(g, p.big_l, stream));
-      if (v0 + p.piece >= a.V) {
-        hipLaunchKernelGGL(k_ce_join, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, stream, a.part,
-                           a.tlogit, a.target, a.loss, a.lse, a.N, a.V, p.tiles);
-        LRS_CE(hipGetLastError());
-      }
+  auto join = [&](int64_t n0, int64_t n, int64_t tiles) {
+    hipLaunchKernelGGL(k_ce_join, dim3((unsigned)((n + 3) / 4)), dim3(256), 0, stream, a.part,
+                       a.tlogit, a.target + n0, a.loss + n0, a.lse + n0, n, a.V, tiles);
+    return hipGetLastError();
+  };
+  if (!a.backward) {
+    for (int64_t n0 = 0; n0 < a.N; n0 += p.piece_f) {
+      const int64_t n = a.N - n0 < p.piece_f ? a.N - n0 : p.piece_f;
+      GemmArgs g = logits(n0, n);
+      LRS_CE((run<kEpiLogits, kKeepNone>(g, p.big_f, !bf, stream)));
+      LRS_CE(join(n0, n, p.tiles_f));
     }
-    packed_whole = p.pieces == 1;
+    return hipSuccess;
   }
-  if (!a.backward) return hipSuccess;
   hipLaunchKernelGGL(k_ce_scale, dim3(1), dim3(1024), 0, stream, a.grad_loss, a.target, a.N, a.V,
                      a.ratio, a.row_scale, a.top);
   LRS_CE(hipGetLastError());
-  LRS_CE(bf ? (pack_t<uint16_t, 1>(a.x, a.target, a.V, a.x_cols, a.N, a.D, p.Np, stream))
-            : (pack_t<float, 3>(a.x, a.target, a.V, a.x_cols, a.N, a.D, p.Np, stream)));
-  for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
-    const int64_t n = a.V - v0 < p.piece ? a.V - v0 : p.piece;
-    const char* src = (const char*)a.w + v0 * a.D * es;
-    const uint16_t* wr = a.w_rows;
-    if (!packed_whole || raw_w) LRS_CE(w_rows(v0, n, &wr));
-    LRS_CE(bf ? (pack_t<uint16_t, 1>(src, nullptr, 0, a.w_cols, n, a.D, p.piece, stream))
-              : (pack_t<float, 3>(src, nullptr, 0, a.w_cols, n, a.D, p.piece, stream)));
-    {
-      GemmArgs g = base;
-      logits(g, wr, v0, n);
-      g.ratio = a.ratio;
-      g.g = a.g;
-      g.gt = a.gt;
-      g.nparts = p.parts;
-      g.part_k = p.piece;
-      g.part_kt = p.Np;
-      g.ldg = p.parts * p.piece;
-      g.ldgt = p.parts * p.Np;
-      // a whole number of tiles writes all of G's padded columns: the last
-      // piece's k loop below stops at its own whole number of tiles
-      LRS_CE(run_gemm<kEpiGrad>(g, p.big_l, stream));
-    }
+  if (!bf) {
+    hipLaunchKernelGGL(k_ce_top, dim3(1), dim3(1024), 0, stream, a.x_top, a.N, a.x_scale);
+    LRS_CE(hipGetLastError());
+    hipLaunchKernelGGL(k_ce_top, dim3(1), dim3(1024), 0, stream, a.w_top, a.V, a.w_scale);
+    LRS_CE(hipGetLastError());
+  }
+  auto cols = [&](const void* src, const int64_t* target, const float* scale, uint16_t* dst,
+                  int64_t n, int64_t np, int64_t ld) -> hipError_t {
+    const dim3 grid((unsigned)(up(np, 64) / 64), (unsigned)(up(a.D, 64) / 64));
+    if (bf)
+      hipLaunchKernelGGL((k_ce_cols<uint16_t, 1>), grid, dim3(256), 0, stream, (const uint16_t*)src,
+                         target, a.V, scale, dst, n, a.D, np, ld);
+    else
+      hipLaunchKernelGGL((k_ce_cols<float, 2>), grid, dim3(256), 0, stream, (const float*)src,
+                         target, a.V, scale, dst, n, a.D, np, ld);
+    return hipGetLastError();
+  };
+  LRS_CE(cols(a.w, nullptr, a.w_scale, a.w_cols, a.V, p.Vp, p.ldg));
+  for (int64_t n0 = 0; n0 < a.N; n0 += p.piece) {
+    const int64_t n = a.N - n0 < p.piece ? a.N - n0 : p.piece;
+    const bool last = n0 + n == a.N;
+    GemmArgs l = logits(n0, n);
+    LRS_CE(bf ? (run<kEpiLogits, kKeepF16>(l, p.big_l, false, stream))
+              : (run<kEpiLogits, kKeepF32>(l, p.big_l, true, stream)));
+    if (a.forward) LRS_CE(join(n0, n, p.tiles_l));
+    const int tile_m = p.big_l ? Big::TM : Small::TM;
+    // the classes that the tiles cover
+    const dim3 gg((unsigned)(p.tiles_l * tile_m / 64), (unsigned)(p.piece / 64));
+    if (bf)
+      hipLaunchKernelGGL((k_ce_g<uint16_t, 1>), gg, dim3(256), 0, stream, (const uint16_t*)a.e,
+                         a.lde, a.part, p.tiles_l, tile_m, a.lse + n0, a.target + n0, a.ratio + n0,
+                         a.g, p.ldg, a.gt, p.ldgt, n, a.V, p.Vp, p.piece);
+    else
+      hipLaunchKernelGGL((k_ce_g<float, 2>), gg, dim3(256), 0, stream, (const float*)a.e, a.lde,
+                         a.part, p.tiles_l, tile_m, a.lse + n0, a.target + n0, a.ratio + n0, a.g,
+                         p.ldg, a.gt, p.ldgt, n, a.V, p.Vp, p.piece);
+    LRS_CE(hipGetLastError());
+    LRS_CE(cols((const char*)a.x + n0 * a.D * es, a.target + n0, a.x_scale, a.x_cols, n, p.piece,
+                p.ldgt));
     {
       GemmArgs g = base;
       g.a = a.gt;
       g.b = a.x_cols;
-      g.lda = g.ldb = p.parts * p.Np;
-      g.M = n;
+      g.lda = g.ldb = p.ldgt;
+      g.M = a.V;
       g.N = a.D;
-      pairs(g, p.Np, p.Np, up(a.N, kSmallN));
+      pairs(g, p.piece, p.piece, up(n, 64));
       g.splits = (int)p.split_w;
       g.slots = p.slots_w ? a.slots_w : nullptr;
-      g.out = (char*)a.grad_w + v0 * a.D * es;
+      g.add = n0 > 0;
+      g.last = last && p.split_w == 1;
+      g.out = a.grad_w;
       g.out_bf16 = bf;
       g.scale = a.top;
-      LRS_CE(run_gemm<kEpiOut>(g, p.big_w, stream));
-      if (p.slots_w) {
-        hipLaunchKernelGGL(k_ce_join_slots, dim3(blocks_for(n * a.D, 1024)), dim3(256), 0, stream,
-                           a.slots_w, (int)p.split_w, n, a.D, nullptr, a.top, g.out, bf ? 1 : 0);
-        LRS_CE(hipGetLastError());
-      }
+      g.unscale = bf ? nullptr : a.x_scale + 1;
+      LRS_CE((run<kEpiOut, kKeepNone>(g, p.big_w, !bf, stream)));
     }
     {
       GemmArgs g = base;
       g.a = a.g;
       g.b = a.w_cols;
-      g.lda = g.ldb = p.parts * p.piece;
-      g.M = a.N;
+      g.lda = g.ldb = p.ldg;
+      g.M = n;
       g.N = a.D;
-      pairs(g, p.piece, p.piece, up(n, kSmallM));
+      pairs(g, p.Vp, p.Vp, up(a.V, 64));
       g.splits = (int)p.split_x;
       g.slots = p.slots_x ? a.slots_x : nullptr;
-      g.accumulate = v0 > 0;
-      g.out = a.grad_x;
+      g.last = p.split_x == 1;
+      g.out = (char*)a.grad_x + n0 * a.D * es;
       g.out_bf16 = bf;
-      g.row_scale = a.row_scale;
-      LRS_CE(run_gemm<kEpiOut>(g, p.big_x, stream));
+      g.row_scale = a.row_scale + n0;
+      g.unscale = bf ? nullptr : a.w_scale + 1;
+      LRS_CE((run<kEpiOut, kKeepNone>(g, p.big_x, !bf, stream)));
+      if (p.split_x > 1) {
+        hipLaunchKernelGGL(k_ce_join_slots, dim3(blocks_for(n * a.D, 1024)), dim3(256), 0, stream,
+                           a.slots_x, (int)p.split_x, n, a.D, a.row_scale + n0, nullptr, g.out,
+                           bf ? 1 : 0);
+        LRS_CE(hipGetLastError());
+      }
     }
   }
-  if (p.slots_x) {
-    hipLaunchKernelGGL(k_ce_join_slots, dim3(blocks_for(a.N * a.D, 1024)), dim3(256), 0, stream,
-                       a.slots_x, (int)p.split_x, a.N, a.D, a.row_scale, nullptr, a.grad_x,
-                       bf ? 1 : 0);
+  if (p.split_w > 1) {
+    hipLaunchKernelGGL(k_ce_join_slots, dim3(blocks_for(a.V * a.D, 1024)), dim3(256), 0, stream,
+                       a.slots_w, (int)p.split_w, a.V, a.D, nullptr, a.top, a.grad_w, bf ? 1 : 0);
     LRS_CE(hipGetLastError());
   }
 #undef LRS_CE

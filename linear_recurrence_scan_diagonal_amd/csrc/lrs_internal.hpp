@@ -265,16 +265,17 @@ hipError_t launch_layernorm_bwd(const void* s, const float* gamma, const float* 
                                 int64_t D, int io, float* part, double* acc, hipStream_t stream);
 
 // Cross entropy of a linear head (linear_ce.hip).  The plan of a shape, and the
-// arrays of a call; the workspace's own are bf16 (uint16_t) or fp32.
+// arrays of a call; the workspace's own are bf16 or fp16 (uint16_t) or fp32.
 struct CePlan {
-  int parts = 1;        // bf16 parts of an operand's element
-  int64_t Dp = 0;       // features rounded up to whole k steps
-  int64_t Np = 0;       // rows rounded up to whole tiles
-  int64_t piece = 0, pieces = 0;  // classes of a piece (whole tiles), and how many
-  int64_t tiles = 0;    // class tiles (the forward's partial sums a row)
-  bool big_l = false, big_x = false, big_w = false;  // tile shapes: logits, the gradients
-  int64_t split_x = 1, split_w = 1;        // shares of their k loops
-  bool slots_x = false, slots_w = false;   // fp32 partial results are kept and joined
+  int parts = 1;        // 16-bit parts of an operand's element
+  int64_t Dp = 0, Vp = 0;           // features and classes, rounded up
+  int64_t piece = 0, pieces = 0;    // rows of a piece of the gradient, and how many
+  int64_t piece_f = 0;              // rows of a piece of the forward alone
+  int64_t ldg = 0, ldgt = 0;        // row pitch of G and w^T, of G^T and x^T
+  int64_t tiles_f = 0, tiles_l = 0; // class tiles, forward alone and a piece's
+  bool big_f = false, big_l = false, big_x = false, big_w = false;  // tile shapes
+  int64_t split_x = 1, split_w = 1;        // shares of the gradients' k loops
+  bool slots_x = false, slots_w = false;   // fp32 partial results are kept
 };
 struct CeArgs {
   const void *x, *w;
@@ -284,12 +285,18 @@ struct CeArgs {
   void *grad_x, *grad_w;
   int64_t N, V, D;
   bool forward, backward;
-  uint16_t *x_rows, *w_rows;  // [N][parts Dp], [piece][parts Dp]
-  uint16_t *x_cols, *w_cols;  // [D][parts Np], [D][parts piece]
-  uint16_t *g, *gt;           // [N][parts piece], [piece][parts Np]
-  float2* part;               // [N][tiles]
-  float *tlogit, *ratio, *row_scale, *top;  // [N], [N], [N], 1
-  float *slots_x, *slots_w;   // [split_x][N][D], [split_w][piece][D]
+  uint16_t *x_rows, *w_rows;  // [N][parts Dp], [V][parts Dp]
+  float *x_unscale, *w_unscale, *x_top, *w_top;  // [N], [Vp], [N], [V] (fp32 inputs)
+  float *x_scale, *w_scale;   // 2 each (fp32 inputs)
+  float2* part;               // [piece][class tiles]
+  float* tlogit;              // [piece]
+  // the gradient's
+  uint16_t *x_cols, *w_cols;  // [D][ldgt], [D][ldg]
+  void* e;                    // [piece][lde]; bf16 inputs: G's own memory
+  int64_t lde;
+  uint16_t *g, *gt;           // [piece][ldg], [V][ldgt]
+  float *ratio, *row_scale, *top;  // [N], [N], 1
+  float *slots_x, *slots_w;   // [split_x][piece][D], [split_w][V][D]
 };
 CePlan plan_ce(int64_t N, int64_t V, int64_t D, int io);
 hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_t stream);

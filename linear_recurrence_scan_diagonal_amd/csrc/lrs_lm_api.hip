@@ -369,23 +369,34 @@ namespace {
 
 constexpr int64_t kCeMost = (int64_t)1 << 21;
 
-// Carves the workspace of one call; with a null base it only counts.
-size_t ce_carve(const lrs::CePlan& p, int64_t N, int64_t V, int64_t D, void* ws, lrs::CeArgs* a) {
+// Carves the workspace of one call; with a null base it only counts.  A call
+// without the gradient uses the first part only.
+size_t ce_carve(const lrs::CePlan& p, int64_t N, int64_t V, int64_t D, bool backward, void* ws,
+                lrs::CeArgs* a) {
   Carve cv(ws);
-  a->part = (float2*)cv.take<uint64_t>(N * p.tiles);
-  a->tlogit = cv.take<float>(N);
+  const bool f32 = p.parts > 1;
+  a->part = (float2*)cv.take<uint64_t>(backward ? p.piece * p.tiles_l : p.piece_f * p.tiles_f);
+  a->tlogit = cv.take<float>(backward ? p.piece : p.piece_f);
+  a->x_rows = cv.take<uint16_t>(N * p.parts * p.Dp);
+  a->w_rows = cv.take<uint16_t>(V * p.parts * p.Dp);
+  a->x_unscale = cv.take<float>(f32 ? N : 0);
+  a->w_unscale = cv.take<float>(f32 ? p.Vp : 0);
+  a->x_top = cv.take<float>(f32 ? N : 0);
+  a->w_top = cv.take<float>(f32 ? V : 0);
+  a->x_scale = cv.take<float>(f32 ? 2 : 0);
+  a->w_scale = cv.take<float>(f32 ? 2 : 0);
+  if (!backward) return cv.used;
   a->ratio = cv.take<float>(N);
   a->row_scale = cv.take<float>(N);
   a->top = cv.take<float>(1);
-  a->x_rows = cv.take<uint16_t>(N * p.parts * p.Dp);
-  a->w_rows = cv.take<uint16_t>(p.piece * p.parts * p.Dp);
-  a->x_cols = cv.take<uint16_t>(D * p.parts * p.Np);
-  a->w_cols = cv.take<uint16_t>(D * p.parts * p.piece);
-  a->g = cv.take<uint16_t>(N * p.parts * p.piece);
-  a->gt = cv.take<uint16_t>(p.piece * p.parts * p.Np);
-  a->slots_x = cv.take<float>(p.slots_x ? p.split_x * N * D : 0);
-  a->slots_w = cv.take<float>(p.slots_w ? p.split_w * p.piece * D : 0);
-  (void)V;
+  a->x_cols = cv.take<uint16_t>(D * p.ldgt);
+  a->w_cols = cv.take<uint16_t>(D * p.ldg);
+  a->g = cv.take<uint16_t>(p.piece * p.ldg);
+  a->gt = cv.take<uint16_t>(V * p.ldgt);
+  a->e = f32 ? (void*)cv.take<float>(p.piece * (p.Vp + 32)) : (void*)a->g;
+  a->lde = f32 ? p.Vp + 32 : p.ldg;
+  a->slots_x = cv.take<float>(p.slots_x ? p.split_x * p.piece * D : 0);
+  a->slots_w = cv.take<float>(p.slots_w ? p.split_w * V * D : 0);
   return cv.used;
 }
 
@@ -421,9 +432,9 @@ int ce_call(const void* x, const void* w, const int64_t* target, const float* gr
   if (any_overlap(outs, 4, ins, 5)) return LRS_ERR_INVALID_ARG;
   const lrs::CePlan p = lrs::plan_ce(N, V, D, io);
   lrs::CeArgs a = {};
-  if (!workspace || workspace_bytes < lrs_linear_ce_workspace_bytes(N, V, D, io))
-    return LRS_ERR_WORKSPACE;
-  ce_carve(p, N, V, D, align_ptr(workspace), &a);
+  const size_t need = kAlign + ce_carve(p, N, V, D, backward, nullptr, &a);
+  if (!workspace || workspace_bytes < need) return LRS_ERR_WORKSPACE;
+  ce_carve(p, N, V, D, backward, align_ptr(workspace), &a);
   a.x = x;
   a.w = w;
   a.target = target;
@@ -444,10 +455,11 @@ int ce_call(const void* x, const void* w, const int64_t* target, const float* gr
 
 extern "C" {
 
-size_t lrs_linear_ce_workspace_bytes(int64_t N, int64_t V, int64_t D, int io_dtype) {
+size_t lrs_linear_ce_workspace_bytes(int64_t N, int64_t V, int64_t D, int io_dtype, int backward) {
   if (!ce_sizes(N, V, D, io_dtype) || !ce_fits(N, V, D) || N == 0) return 0;
   lrs::CeArgs a = {};
-  return kAlign + ce_carve(lrs::plan_ce(N, V, D, io_dtype), N, V, D, nullptr, &a);
+  return kAlign +
+         ce_carve(lrs::plan_ce(N, V, D, io_dtype), N, V, D, backward != 0, nullptr, &a);
 }
 
 int lrs_linear_ce_fwd(const void* x, const void* w, const int64_t* target, float* loss, float* lse,

@@ -42,7 +42,7 @@ def load():
     lib.lrs_layernorm_bwd_workspace_bytes.argtypes = [_i64] * 2
     lib.lrs_layernorm_bwd_workspace_bytes.restype = _sz
     lib.lrs_layernorm_bwd.argtypes = [_vp] * 9 + [_i64] * 2 + [_int, _vp, _sz, _vp]
-    lib.lrs_linear_ce_workspace_bytes.argtypes = [_i64] * 3 + [_int]
+    lib.lrs_linear_ce_workspace_bytes.argtypes = [_i64] * 3 + [_int, _int]
     lib.lrs_linear_ce_workspace_bytes.restype = _sz
     lib.lrs_linear_ce_fwd.argtypes = [_vp] * 5 + [_i64] * 3 + [_int, _vp, _sz, _vp]
     lib.lrs_linear_ce_bwd.argtypes = [_vp] * 7 + [_i64] * 3 + [_int, _vp, _sz, _vp]
@@ -272,7 +272,7 @@ def layernorm_bwd(s, gamma, mean, rstd, grad_y, grad_sum=None, want_grad_beta: b
     return gx, gg, gb
 
 
-def _ce_args(x, w, target):
+def _ce_args(x, w, target, backward):
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(w, torch.Tensor) \
             or w.dim() != 2:
         raise ValueError("x must be [N,D] and w [V,D]")
@@ -283,7 +283,8 @@ def _ce_args(x, w, target):
     _check_dev("x", x, x.dtype, (N, D))
     _check_dev("w", w, x.dtype, (V, D))
     _check_dev("target", target, torch.int64, (N,))
-    return N, V, D, load().lrs_linear_ce_workspace_bytes(N, V, D, DTYPES[x.dtype])
+    return N, V, D, load().lrs_linear_ce_workspace_bytes(N, V, D, DTYPES[x.dtype],
+                                                                int(backward))
 
 
 def linear_ce_fwd(x, w, target, workspace=None):
@@ -291,7 +292,7 @@ def linear_ce_fwd(x, w, target, workspace=None):
     target [N] int64; a target outside [0, V) is ignored.  Returns (loss, lse),
     [N] fp32 each."""
     lib = load()
-    N, V, D, nbytes = _ce_args(x, w, target)
+    N, V, D, nbytes = _ce_args(x, w, target, False)
     loss, lse = (torch.empty(N, dtype=torch.float32, device=x.device) for _ in range(2))
     ws = _workspace(nbytes, x.device, workspace)
     _call(lib.lrs_linear_ce_fwd(_ptr(x), _ptr(w), _ptr(target), _ptr(loss), _ptr(lse), N, V, D,
@@ -304,7 +305,7 @@ def linear_ce_bwd(x, w, target, lse, grad_loss, out=None, workspace=None):
     """Gradient of linear_ce_fwd for dL/dloss = grad_loss [N] fp32, with the lse
     it returned.  Returns (grad_x, grad_w)."""
     lib = load()
-    N, V, D, nbytes = _ce_args(x, w, target)
+    N, V, D, nbytes = _ce_args(x, w, target, True)
     _check_dev("lse", lse, torch.float32, (N,))
     _check_dev("grad_loss", grad_loss, torch.float32, (N,))
     gx, gw = (torch.empty_like(x), torch.empty_like(w)) if out is None else out
@@ -321,7 +322,7 @@ def linear_ce_fwd_bwd(x, w, target, grad_loss, out=None, workspace=None):
     """linear_ce_fwd and linear_ce_bwd in one call, for a grad_loss known before
     the loss.  Returns (loss, lse, grad_x, grad_w)."""
     lib = load()
-    N, V, D, nbytes = _ce_args(x, w, target)
+    N, V, D, nbytes = _ce_args(x, w, target, True)
     _check_dev("grad_loss", grad_loss, torch.float32, (N,))
     loss, lse = (torch.empty(N, dtype=torch.float32, device=x.device) for _ in range(2))
     gx, gw = (torch.empty_like(x), torch.empty_like(w)) if out is None else out

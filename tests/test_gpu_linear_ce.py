@@ -164,7 +164,7 @@ def test_repeatable():
 def test_other_stream_and_given_workspace():
     args = make(200, 1000, 64, torch.bfloat16)
     want = lrs.linear_ce_fwd_bwd(*args)
-    nbytes = lrs.load().lrs_linear_ce_workspace_bytes(200, 1000, 64, 1)
+    nbytes = lrs.load().lrs_linear_ce_workspace_bytes(200, 1000, 64, 1, 1)
     ws = torch.full((nbytes,), 255, dtype=torch.uint8, device=DEV)  # whatever was there before
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
