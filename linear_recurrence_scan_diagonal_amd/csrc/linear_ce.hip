@@ -47,7 +47,6 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2eF = 1.4426950408889634f;
 constexpr int kMaxPairs = 3;
@@ -127,48 +126,56 @@ __device__ __forceinline__ void tile_of(const GemmArgs& g, int& tm, int& tn, int
 
 // The piece of 16 bytes at which piece p of row r is kept in LDS is p ^ f(r):
 // the 8 (or 16) rows that a fragment read touches at once then fall on
-// different banks, for rows of 64 and of 128 bytes.
-template <int BK>
+// different banks (rows of 128 bytes).
 __device__ __forceinline__ int swizzle(int r) {
-  return BK == 32 ? ((r >> 1) & 3) ^ ((r >> 3) & 1) : (r & 7) ^ ((r >> 3) & 1);
+  return (r & 7) ^ ((r >> 3) & 1);
 }
 
+// The 16x16x32 product: lane l gives 8 values along k of row l % 16, from k =
+// 8 (l / 16) on, and holds n = l % 16, m = 4 (l / 16) + 0..3 of the result.
+// Written as an instruction that adds in place: through the builtin the register
+// allocator rotates hundreds of accumulators by copies in the loop.  Volatile,
+// so that products and the loads to LDS keep the order they are written in.
+// settle() has to come between the last product and the first use of a result
+// (the wait states that the compiler would count for the builtin).
 template <bool F16>
 struct Frag;
 template <>
 struct Frag<false> {
   typedef bf16x8_t V;
-  static __device__ __forceinline__ f32x16_t mma(V a, V b, f32x16_t c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  static __device__ __forceinline__ void mma(V a, V b, f32x4_t& c) {
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
   }
 };
 template <>
 struct Frag<true> {
   typedef f16x8_t V;
-  static __device__ __forceinline__ f32x16_t mma(V a, V b, f32x16_t c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  static __device__ __forceinline__ void mma(V a, V b, f32x4_t& c) {
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
   }
 };
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
-// Tile TM x TN by WM x WN waves, k in steps of BK, NST buffers.
-template <int TM_, int TN_, int WM_, int WN_, int BK_, int NST_, int MINW_>
+// Tile TM x TN by WM x WN waves, k in stages of 64 (rows of 128 bytes: whole
+// cache lines), NA buffers of A's part of a stage and NB of B's.
+template <int TM_, int TN_, int WM_, int WN_, int NA_, int NB_, int MINW_>
 struct Shape {
-  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, BK = BK_, NST = NST_, MINW = MINW_;
+  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, NA = NA_, NB = NB_, MINW = MINW_;
   static constexpr int kThreads = WM * WN * kWave;
-  static constexpr int kRowBytes = BK * 2;
-  static constexpr int kStage = (TM + TN) * kRowBytes;
-  static constexpr int kRowsPerLoad = 1024 / kRowBytes;
-  static constexpr int kIssue = (TM + TN) / kRowsPerLoad / (WM * WN);
-  static constexpr int MT = TM / WM / 32, NT = TN / WN / 32;
+  static constexpr int kStageA = TM * 128, kStageB = TN * 128;
+  static constexpr int kLoadsA = TM / 8 / (WM * WN), kLoadsB = TN / 8 / (WM * WN);
+  static constexpr int MT = TM / WM / 16, NT = TN / WN / 16;
   static constexpr int kKeep = TN * (TM + 8) * 2 + WM * TN * 8;  // an fp16 tile, and the rows' sums
-  static constexpr int kLds = NST * kStage > kKeep ? NST * kStage : kKeep;
-  static_assert((TM + TN) % (kRowsPerLoad * WM * WN) == 0 && TM % (16 * WM) == 0, "whole loads");
+  static constexpr int kBuffers = NA * kStageA + NB * kStageB;
+  static constexpr int kLds = kBuffers > kKeep ? kBuffers : kKeep;
+  static_assert(TM % (8 * WM * WN) == 0 && TN % (8 * WM * WN) == 0 && NB >= 2 && NA == NB + 1,
+                "whole loads, and the order of the waits");
 };
 
 template <class S, int EPI, int KEEP, bool F16>
 __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
-  constexpr int TM = S::TM, TN = S::TN, WM = S::WM, WN = S::WN, BK = S::BK, NST = S::NST;
-  constexpr int MT = S::MT, NT = S::NT, NI = S::kIssue, RB = S::kRowBytes, RPL = S::kRowsPerLoad;
+  constexpr int TM = S::TM, TN = S::TN, WM = S::WM, WN = S::WN, NA = S::NA, NB = S::NB;
+  constexpr int MT = S::MT, NT = S::NT, LA = S::kLoadsA, LB = S::kLoadsB;
   typedef typename Frag<F16>::V frag_t;
   __shared__ __align__(128) char lds[S::kLds];
   const int lane = threadIdx.x & (kWave - 1);
@@ -181,94 +188,167 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
   const uint16_t* bbase = g.b + n0 * g.ldb;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
 
-  // This lane's global piece of each of the wave's loads (a load fills RPL
+  // This lane's global piece of each of the wave's loads (a load fills eight
   // rows).  Rows past the end read the last row (their results are not used).
-  uint32_t voff[NI];
+  uint32_t offa[LA], offb[LB];
   {
-    constexpr int PPR = RB / 16;  // pieces a row
-    const int r = lane / PPR;
+    const int r = lane >> 3, p = lane & 7;
+    const int64_t lasta = g.M - m0 - 1, lastb = g.N - n0 - 1;
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int row = (wid * NI + j) * RPL + r;
-      const bool isb = (wid * NI + j) * RPL >= TM;
-      const int64_t last = (isb ? g.N - n0 : g.M - m0) - 1;
-      int64_t rr = isb ? row - TM : row;
-      rr = rr < last ? rr : last;
-      voff[j] = (uint32_t)(rr * (isb ? g.ldb : g.lda) * 2) +
-                (uint32_t)((lane % PPR) ^ swizzle<BK>(row & 15)) * 16u;
+    for (int j = 0; j < LA; ++j) {
+      const int row = (wid * LA + j) * 8 + r;
+      const int64_t rr = row < lasta ? row : lasta;
+      offa[j] = (uint32_t)(rr * g.lda * 2) + (uint32_t)(p ^ swizzle(row & 15)) * 16u;
+    }
+#pragma unroll
+    for (int j = 0; j < LB; ++j) {
+      const int row = (wid * LB + j) * 8 + r;
+      const int64_t rr = row < lastb ? row : lastb;
+      offb[j] = (uint32_t)(rr * g.ldb * 2) + (uint32_t)(p ^ swizzle(row & 15)) * 16u;
     }
   }
-  const int kt = (int)(g.k / BK);
+  const int kt = (int)(g.k / 64);
   const int total = kt * g.npair;
   const int it0 = (int)((int64_t)total * split / g.splits);
   const int nk = (int)((int64_t)total * (split + 1) / g.splits) - it0;
 
-  int ipair = it0 / kt, ik = it0 % kt;  // the next step to load
-  auto issue = [&](int stage) {
-    const uint16_t* ap = abase + g.pa[ipair] + ik * BK;
-    const uint16_t* bp = bbase + g.pb[ipair] + ik * BK;
-    const uint32_t dst = lds0 + (uint32_t)(stage * S::kStage);
-#pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int idx = wid * NI + j;
-      dma16(dst + (uint32_t)idx * 1024u, voff[j], idx * RPL >= TM ? bp : ap);
-    }
-    if (++ik == kt) {
-      ik = 0;
-      ++ipair;
+  // One operand's walk along k: the address of the next stage to load.
+  struct Walk {
+    const uint16_t *base, *p;
+    int pair, k;
+  };
+  Walk wa = {abase, abase + g.pa[it0 / kt] + (int64_t)(it0 % kt) * 64, it0 / kt, it0 % kt};
+  Walk wb = {bbase, bbase + g.pb[it0 / kt] + (int64_t)(it0 % kt) * 64, it0 / kt, it0 % kt};
+  auto advance = [&](Walk& w, const int64_t* parts) __attribute__((always_inline)) {
+    w.p += 64;
+    if (++w.k == kt && ++w.pair < g.npair) {
+      w.k = 0;
+      w.p = w.base + parts[w.pair];
     }
   };
+  auto load_a = [&](int buf, int j) __attribute__((always_inline)) {
+    dma16(lds0 + (uint32_t)(buf * S::kStageA + (wid * LA + j) * 1024), offa[j], wa.p);
+  };
+  auto load_b = [&](int buf, int j) __attribute__((always_inline)) {
+    dma16(lds0 + (uint32_t)(NA * S::kStageA + buf * S::kStageB + (wid * LB + j) * 1024), offb[j],
+          wb.p);
+  };
 
-  f32x16_t acc[MT][NT];
+  f32x4_t acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // fragment addresses: row lane % 32 of a 32-row block, piece 2 kk + lane / 32
-  const int fr = lane & 31;
-  const int fsw = swizzle<BK>(fr & 15);
-  const int fa = (wm * (TM / WM) + fr) * RB, fb = (TM + wn * (TN / WN) + fr) * RB;
-
+  // Pipeline.  A stage is two steps of 32 along k.  The fragments of a step are
+  // read while the step before it is multiplied, also across the border of two
+  // stages: before a stage's second step its own reads are complete and the next
+  // stage has landed; one barrier makes both true for all waves, its buffers are
+  // filled again and the products go on from registers.  B's loads are begun
+  // right after the barrier, A's in the first step of the stage after it: A has
+  // one buffer more, because it is the operand that streams from memory (B's
+  // rows are shared by all tiles of m and come from the caches).
+  // A step is MT chunks of NT products, each with its share of the fragment
+  // reads and of the loads; the compiler is kept from moving anything between
+  // chunks (it would put the reads next to their use, and the loads in front of
+  // all products, where their addresses queue up).
+  frag_t af[2][MT], bf[2][NT];
+  // fragment addresses: row lane % 16 of a block of 16, piece 4 kk + lane / 16
+  const int fr = lane & 15, fsw = swizzle(fr);
+  const int fa = (wm * (TM / WM) + fr) * 128;
+  const int fb = NA * S::kStageA + (wn * (TN / WN) + fr) * 128;
+  // Fragment reads of a chunk: all of B come first, since the first chunk of the
+  // next step needs every one of them; A's are needed one a chunk.
+  auto read_share = [&](int bufa, int bufb, int kk, int set, int j) __attribute__((always_inline)) {
+    constexpr int R = MT + NT;
+    const int pc = ((kk * 4 + (lane >> 4)) ^ fsw) * 16;
+    const char* sa = lds + bufa * S::kStageA + fa + pc;
+    const char* sb = lds + bufb * S::kStageB + fb + pc;
 #pragma unroll
-  for (int s = 0; s < NST - 1; ++s)
-    if (s < nk) issue(s);
-  int stage = 0;
-  for (int i = 0; i < nk; ++i) {
-    // this step's loads have landed (the later steps' may be in flight), and
-    // every wave has finished reading the buffer that is filled next
-    if (i + NST - 2 < nk) wait_vm<NI*(NST - 2)>();
+    for (int r = R * j / MT; r < R * (j + 1) / MT; ++r) {
+      if (r < NT) bf[set][r] = *reinterpret_cast<const frag_t*>(sb + r * 2048);
+      else af[set][r - NT] = *reinterpret_cast<const frag_t*>(sa + (r - NT) * 2048);
+    }
+  };
+  auto multiply = [&](int set, int j) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < NT; ++q) Frag<F16>::mma(af[set][j], bf[set][q], acc[j][q]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // B's loads go into the first chunks of their step
+  constexpr int CB = MT > 2 ? MT / 2 : MT;
+  // buffers of the current stage, and A's of the one before it
+  int ca = 0, cb = 0, oa = NA - 1;
+  // one stage; `fill`: the buffers that are freed are filled again (A's with the
+  // stage NA after the one before, B's with the stage NB after this one: the
+  // same stage, since NA = NB + 1)
+  auto body = [&](auto fill) __attribute__((always_inline)) {
+    const int na = ca == NA - 1 ? 0 : ca + 1, nb = cb == NB - 1 ? 0 : cb + 1;
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      read_share(ca, cb, 1, 1, j);
+      if (fill) {
+#pragma unroll
+        for (int l = LA * j / MT; l < LA * (j + 1) / MT; ++l) load_a(oa, l);
+      }
+      multiply(0, j);
+    }
+    // the next stage has landed; begun after its last load: an A, and NB - 2 stages
+    if (fill) wait_vm<LA + (NB - 2) * (LA + LB)>();
     else wait_vm<0>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (i + NST - 1 < nk) issue(stage == 0 ? NST - 1 : stage - 1);
-    const char* st = lds + stage * S::kStage;
 #pragma unroll
-    for (int kk = 0; kk < BK / 16; ++kk) {
-      const int pc = ((kk * 2 + (lane >> 5)) ^ fsw) * 16;
-      frag_t af[MT], bf[NT];
+    for (int j = 0; j < MT; ++j) {
+      read_share(na, nb, 0, 0, j);  // past the last stage: read and not used
+      if (fill && j < CB) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        bf[j] = *reinterpret_cast<const frag_t*>(st + fb + j * 32 * RB + pc);
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-        af[j] = *reinterpret_cast<const frag_t*>(st + fa + j * 32 * RB + pc);
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int q = 0; q < NT; ++q) acc[j][q] = Frag<F16>::mma(af[j], bf[q], acc[j][q]);
+        for (int l = LB * j / CB; l < LB * (j + 1) / CB; ++l) load_b(cb, l);
+      }
+      multiply(1, j);
     }
-    stage = stage == NST - 1 ? 0 : stage + 1;
+    if (fill) {
+      advance(wa, g.pa);
+      advance(wb, g.pb);
+    }
+    oa = ca;
+    ca = na;
+    cb = nb;
+  };
+  // Before the first stage, in the order in which the stages before it would
+  // have begun them: A 0; B 0, A 1; B 1, A 2; ...; B NB-1 (A NB follows in the
+  // first step).
+#pragma unroll
+  for (int s = 0; s < NB; ++s) {
+    if (s < nk) {
+#pragma unroll
+      for (int j = 0; j < LA; ++j) load_a(s, j);
+      advance(wa, g.pa);
+#pragma unroll
+      for (int j = 0; j < LB; ++j) load_b(s, j);
+      advance(wb, g.pb);
+    }
   }
+  // stage 0 has landed: begun after it, NB - 1 stages
+  if (nk >= NB) wait_vm<(NB - 1) * (LA + LB)>();
+  else wait_vm<0>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int j = 0; j < MT; ++j) read_share(0, 0, 0, 0, j);
+  struct Yes { __device__ constexpr operator bool() const { return true; } };
+  struct No { __device__ constexpr operator bool() const { return false; } };
+  int i = 0;
+  for (; i + NB < nk; ++i) body(Yes());
+  for (; i < nk; ++i) body(No());
+  settle();
   __syncthreads();  // the epilogues reuse the buffers
 
-  // The lane's values: n = nb + 32 q, m = mb + 32 j + 8 (e / 4) + e % 4.
-  const int ln = wn * (TN / WN) + (lane & 31);
-  const int lm = wm * (TM / WM) + 4 * (lane >> 5);
+  // The lane's values: n = nb + 16 q, m = mb + 16 j + e.
+  const int ln = wn * (TN / WN) + (lane & 15);
+  const int lm = wm * (TM / WM) + 4 * (lane >> 4);
   const int64_t nb = n0 + ln, mb = m0 + lm;
-  const int mleft = (int)(g.M - mb < 32 * MT ? g.M - mb : 32 * MT);  // <= 0: none
+  const int mleft = (int)(g.M - mb < 16 * MT ? g.M - mb : 16 * MT);  // <= 0: none
 
   if constexpr (EPI == kEpiLogits) {
     constexpr int PG = TM + 8;  // a padded row of e in LDS
@@ -277,81 +357,71 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
     if constexpr (F16) {
       float bu[NT];
 #pragma unroll
-      for (int q = 0; q < NT; ++q) bu[q] = nb + 32 * q < g.N ? g.b_unscale[nb + 32 * q] : 0.0f;
+      for (int q = 0; q < NT; ++q) bu[q] = nb + 16 * q < g.N ? g.b_unscale[nb + 16 * q] : 0.0f;
 #pragma unroll
       for (int j = 0; j < MT; ++j)
+      {
+        // past the last class: room of the workspace, masked below
+        const f32x4_t au = *reinterpret_cast<const f32x4_t*>(g.a_unscale + mb + 16 * j);
 #pragma unroll
-        for (int e4 = 0; e4 < 4; ++e4) {
-          // past the last class: room of the workspace, masked below
-          const f32x4_t au =
-              *reinterpret_cast<const f32x4_t*>(g.a_unscale + mb + 32 * j + 8 * e4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int q = 0; q < NT; ++q)
-              acc[j][q][4 * e4 + e] = acc[j][q][4 * e4 + e] * bu[q] * au[e];
-          asm volatile("" ::: "memory");  // one load's values at a time
-        }
+        for (int q = 0; q < NT; ++q) acc[j][q] = acc[j][q] * bu[q] * au;
+      }
     }
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
-      const int64_t n = nb + 32 * q;
-      // the target's place among the lane's classes (it has those with bit 2 clear)
+      const int64_t n = nb + 16 * q;
+      // the target's place among the lane's classes (it has those with bits 2 and 3 clear)
       const int64_t d = (n < g.N ? g.target[n] : -1) - mb;
-      const int at = d >= 0 && d < 32 * MT && d < mleft && (d & 4) == 0 ? (int)d : -1;
+      const int at = d >= 0 && d < mleft && (d & 12) == 0 ? (int)d : -1;
       float mx = -__builtin_inff(), tl = 0.0f;
 #pragma unroll
       for (int j = 0; j < MT; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int m = 32 * j + 8 * (e / 4) + e % 4;
+        for (int e = 0; e < 4; ++e) {
+          const int m = 16 * j + e;
           if (m >= mleft) acc[j][q][e] = -__builtin_inff();
           mx = fmaxf(mx, acc[j][q][e]);
           if (m == at) tl = acc[j][q][e];
         }
       if (at >= 0) g.tlogit[n] = tl;
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
-      if (lane < 32) red[wm * TN + ln + 32 * q] = mx;
+      if (lane < 16) red[wm * TN + ln + 16 * q] = mx;
     }
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
-      float top = red[ln + 32 * q];
+      float top = red[ln + 16 * q];
 #pragma unroll
-      for (int w = 1; w < WM; ++w) top = fmaxf(top, red[w * TN + ln + 32 * q]);
+      for (int w = 1; w < WM; ++w) top = fmaxf(top, red[w * TN + ln + 16 * q]);
       const float top2 = top * kLog2eF;
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < MT; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
+        for (int e = 0; e < 4; ++e) {
           const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[j][q][e], kLog2eF, -top2));
           sum += v;
           if constexpr (KEEP != kKeepNone) acc[j][q][e] = v;
         }
+      sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
-      if (lane < 32) red[WM * TN + wm * TN + ln + 32 * q] = sum;
+      if (lane < 16) red[WM * TN + wm * TN + ln + 16 * q] = sum;
       if constexpr (KEEP == kKeepF16) {
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-          for (int e4 = 0; e4 < 4; ++e4) {
-            const f16x2_t lo = {(_Float16)acc[j][q][4 * e4], (_Float16)acc[j][q][4 * e4 + 1]};
-            const f16x2_t hi = {(_Float16)acc[j][q][4 * e4 + 2], (_Float16)acc[j][q][4 * e4 + 3]};
-            *reinterpret_cast<u32x2_t*>(keep + (ln + 32 * q) * PG + lm + 32 * j + 8 * e4) =
-                u32x2_t{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
-          }
+        for (int j = 0; j < MT; ++j) {
+          const f16x2_t lo = {(_Float16)acc[j][q][0], (_Float16)acc[j][q][1]};
+          const f16x2_t hi = {(_Float16)acc[j][q][2], (_Float16)acc[j][q][3]};
+          *reinterpret_cast<u32x2_t*>(keep + (ln + 16 * q) * PG + lm + 16 * j) =
+              u32x2_t{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+        }
       }
       if constexpr (KEEP == kKeepF32) {
-        if (nb + 32 * q < g.N) {
-          float* o = (float*)g.e + (nb + 32 * q) * g.lde + mb;
+        if (nb + 16 * q < g.N) {
+          float* o = (float*)g.e + (nb + 16 * q) * g.lde + mb;
 #pragma unroll
           for (int j = 0; j < MT; ++j)
-#pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4)
-              *reinterpret_cast<f32x4_t*>(o + 32 * j + 8 * e4) =
-                  f32x4_t{acc[j][q][4 * e4], acc[j][q][4 * e4 + 1], acc[j][q][4 * e4 + 2],
-                          acc[j][q][4 * e4 + 3]};
+            *reinterpret_cast<f32x4_t*>(o + 16 * j) = acc[j][q];
         }
       }
     }
@@ -382,14 +452,14 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
 #pragma unroll
     for (int j = 0; j < MT; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int dm = 32 * j + 8 * (e / 4) + e % 4;
+      for (int e = 0; e < 4; ++e) {
+        const int dm = 16 * j + e;
         if (dm >= mleft) continue;
         const int64_t m = mb + dm;
         const float rs = g.row_scale ? g.row_scale[m] : sc;
 #pragma unroll
         for (int q = 0; q < NT; ++q) {
-          const int64_t n = nb + 32 * q;
+          const int64_t n = nb + 16 * q;
           if (n >= g.N) continue;
           float v = acc[j][q][e] * un;
           float* p = g.slots + ((int64_t)split * g.M + m) * g.N + n;
@@ -685,18 +755,46 @@ unsigned blocks_for(int64_t n, int64_t per) {
   return (unsigned)(b < 1 ? 1 : b > 65536 ? 65536 : b);
 }
 
-// The tile shapes: 256 x 128 with four waves of 128 x 64, three buffers, two
-// workgroups a compute unit (one's epilogue runs beside the other's products);
-// and 128 x 64 for products with few tiles.
-typedef Shape<256, 128, 2, 2, 32, 3, 2> Big;
-typedef Shape<128, 64, 4, 1, 32, 6, 2> Small;
-typedef Shape<256, 256, 2, 4, 64, 2, 2> Huge;
+// The tile shapes, with what a product of many tiles of it reaches (TFLOP/s,
+// measured at 8192 x 1024 x 32768) and the workgroups a compute unit holds: 256
+// x 256 by eight waves of 128 x 64 fills the LDS alone; the others are for
+// products with few tiles, where the largest would leave compute units idle.
+typedef Shape<256, 256, 2, 4, 3, 2, 2> Large;
+typedef Shape<128, 128, 2, 2, 3, 2, 2> Medium;
+typedef Shape<128, 64, 4, 1, 3, 2, 2> Small;
+struct ShapeInfo {
+  int tm, tn, wgs;
+  double tflops;
+};
+constexpr ShapeInfo kShapes[3] = {{Large::TM, Large::TN, 1, 1150.0},
+                                  {Medium::TM, Medium::TN, 2, 880.0},
+                                  {Small::TM, Small::TN, 2, 600.0}};
 
-int64_t tiles_of(int64_t M, int64_t N, bool big) {
-  return big ? up(M, Big::TM) / Big::TM * (up(N, Big::TN) / Big::TN)
-             : up(M, Small::TM) / Small::TM * (up(N, Small::TN) / Small::TN);
+int64_t tiles_of(int64_t M, int64_t N, const ShapeInfo& s) {
+  return up(M, s.tm) / s.tm * (up(N, s.tn) / s.tn);
 }
-bool use_big(int64_t M, int64_t N) { return tiles_of(M, N, true) >= 256; }
+
+// The shape, and for the gradients the number of shares of the k loop, with the
+// least estimated time: rounds of workgroups at the shape's rate, and 8 bytes of
+// every fp32 partial result at the memory's.
+void choose(int64_t M, int64_t N, int64_t K, int most_splits, int* shape, int64_t* splits) {
+  double best = 0.0;
+  for (int i = 0; i < 3; ++i) {
+    const ShapeInfo& s = kShapes[i];
+    const int64_t tiles = tiles_of(M, N, s), slots = 256 * s.wgs;
+    for (int64_t n = 1; n <= most_splits && (n == 1 || K / n >= 512); n *= 2) {
+      const int64_t rounds = (tiles * n + slots - 1) / slots;
+      const double k = (double)((K + n - 1) / n + 192);  // and the pipeline's start
+      double t = rounds * s.wgs * 2.0 * s.tm * s.tn * k / (s.tflops * 1e12 / 256);
+      if (n > 1) t += 8.0 * n * M * N / 4e12 + 3e-6;
+      if (best == 0.0 || t < best) {
+        best = t;
+        *shape = i;
+        *splits = n;
+      }
+    }
+  }
+}
 
 template <class S, int EPI, int KEEP, bool F16>
 hipError_t run_gemm(GemmArgs& g, hipStream_t stream) {
@@ -708,12 +806,18 @@ hipError_t run_gemm(GemmArgs& g, hipStream_t stream) {
 }
 
 template <int EPI, int KEEP>
-hipError_t run(GemmArgs& g, bool big, bool f16, hipStream_t stream) {
-  if (big)
-    return f16 ? run_gemm<Big, EPI, KEEP, true>(g, stream)
-               : run_gemm<Big, EPI, KEEP, false>(g, stream);
-  return f16 ? run_gemm<Small, EPI, KEEP, true>(g, stream)
-             : run_gemm<Small, EPI, KEEP, false>(g, stream);
+hipError_t run(GemmArgs& g, int shape, bool f16, hipStream_t stream) {
+  switch (shape) {
+    case 0:
+      return f16 ? run_gemm<Large, EPI, KEEP, true>(g, stream)
+                 : run_gemm<Large, EPI, KEEP, false>(g, stream);
+    case 1:
+      return f16 ? run_gemm<Medium, EPI, KEEP, true>(g, stream)
+                 : run_gemm<Medium, EPI, KEEP, false>(g, stream);
+    default:
+      return f16 ? run_gemm<Small, EPI, KEEP, true>(g, stream)
+                 : run_gemm<Small, EPI, KEEP, false>(g, stream);
+  }
 }
 
 }  // namespace
@@ -725,11 +829,11 @@ CePlan plan_ce(int64_t N, int64_t V, int64_t D, int io) {
   CePlan p;
   p.parts = io == kIoBf16 ? 1 : 2;
   p.Dp = up(D, 64);
-  p.Vp = up(V, Big::TM);
-  const int64_t most = kCePieceBytes / (p.Vp * 2 * p.parts) / Big::TM * Big::TM;
-  const int64_t cap = most < Big::TM ? Big::TM : most;
+  p.Vp = up(V, 256);
+  const int64_t most = kCePieceBytes / (p.Vp * 2 * p.parts) / 256 * 256;
+  const int64_t cap = most < 256 ? 256 : most;
   const int64_t pieces = (N + cap - 1) / cap;
-  p.piece = up((N + pieces - 1) / pieces, Big::TN);
+  p.piece = up((N + pieces - 1) / pieces, 256);
   p.pieces = (N + p.piece - 1) / p.piece;
   // 128 bytes past a power of two: rows a power of two apart would meet in few
   // of the cache's channels
@@ -737,22 +841,19 @@ CePlan plan_ce(int64_t N, int64_t V, int64_t D, int io) {
   p.ldgt = p.parts * p.piece + 64;
   // the forward's only growing array is (maximum, sum) of each tile and row:
   // pieces of rows for it too (128 MiB; each still fills the GPU)
-  const int64_t most_f = (kCePieceBytes / 4) / (up(V, Small::TM) / Small::TM * 8) / Big::TN * Big::TN;
-  p.piece_f = most_f < Big::TN ? Big::TN : most_f > N ? N : most_f;
-  p.big_f = use_big(V, p.piece_f);
-  p.big_l = use_big(V, p.piece);
-  p.tiles_f = up(V, p.big_f ? Big::TM : Small::TM) / (p.big_f ? Big::TM : Small::TM);
-  p.tiles_l = up(V, p.big_l ? Big::TM : Small::TM) / (p.big_l ? Big::TM : Small::TM);
-  auto splits = [](int64_t M, int64_t N_, int64_t K, bool big) -> int64_t {
-    // enough workgroups for two a compute unit, each with 512 of k at least
-    int64_t s = 512 / tiles_of(M, N_, big);
-    s = s > K / 512 ? K / 512 : s;
-    return s < 1 ? 1 : s > 16 ? 16 : s;
-  };
-  p.big_x = tiles_of(p.piece, D, true) * 8 >= 256;
-  p.big_w = tiles_of(V, D, true) * 8 >= 256;
-  p.split_x = splits(p.piece, D, p.Vp, p.big_x);
-  p.split_w = splits(V, D, p.piece, p.big_w);
+  const int64_t most_f = (kCePieceBytes / 4) / (p.Vp / 128 * 8) / 256 * 256;
+  p.piece_f = most_f < 256 ? 256 : most_f > N ? N : most_f;
+  int64_t one;
+  const int64_t K = p.Dp * (p.parts == 1 ? 1 : 3);
+  choose(V, p.piece_f < N ? p.piece_f : N, K, 1, &p.shape_f, &one);
+  choose(V, p.piece < N ? p.piece : N, K, 1, &p.shape_l, &one);
+  p.tm_f = kShapes[p.shape_f].tm;
+  p.tm_l = kShapes[p.shape_l].tm;
+  p.tiles_f = up(V, p.tm_f) / p.tm_f;
+  p.tiles_l = up(V, p.tm_l) / p.tm_l;
+  const int64_t n = p.piece < N ? p.piece : N, f = p.parts == 1 ? 1 : 3;
+  choose(n, D, up(V, 64) * f, 16, &p.shape_x, &p.split_x);
+  choose(V, D, up(n, 64) * f, 16, &p.shape_w, &p.split_w);
   p.slots_x = p.split_x > 1;
   p.slots_w = p.split_w > 1 || p.pieces > 1;
   return p;
@@ -820,7 +921,7 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
     for (int64_t n0 = 0; n0 < a.N; n0 += p.piece_f) {
       const int64_t n = a.N - n0 < p.piece_f ? a.N - n0 : p.piece_f;
       GemmArgs g = logits(n0, n);
-      LRS_CE((run<kEpiLogits, kKeepNone>(g, p.big_f, !bf, stream)));
+      LRS_CE((run<kEpiLogits, kKeepNone>(g, p.shape_f, !bf, stream)));
       LRS_CE(join(n0, n, p.tiles_f));
     }
     return hipSuccess;
@@ -850,10 +951,10 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
     const int64_t n = a.N - n0 < p.piece ? a.N - n0 : p.piece;
     const bool last = n0 + n == a.N;
     GemmArgs l = logits(n0, n);
-    LRS_CE(bf ? (run<kEpiLogits, kKeepF16>(l, p.big_l, false, stream))
-              : (run<kEpiLogits, kKeepF32>(l, p.big_l, true, stream)));
+    LRS_CE(bf ? (run<kEpiLogits, kKeepF16>(l, p.shape_l, false, stream))
+              : (run<kEpiLogits, kKeepF32>(l, p.shape_l, true, stream)));
     if (a.forward) LRS_CE(join(n0, n, p.tiles_l));
-    const int tile_m = p.big_l ? Big::TM : Small::TM;
+    const int tile_m = p.tm_l;
     // the classes that the tiles cover
     const dim3 gg((unsigned)(p.tiles_l * tile_m / 64), (unsigned)(p.piece / 64));
     if (bf)
@@ -883,7 +984,7 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
       g.out_bf16 = bf;
       g.scale = a.top;
       g.unscale = bf ? nullptr : a.x_scale + 1;
-      LRS_CE((run<kEpiOut, kKeepNone>(g, p.big_w, !bf, stream)));
+      LRS_CE((run<kEpiOut, kKeepNone>(g, p.shape_w, !bf, stream)));
     }
     {
       GemmArgs g = base;
@@ -900,7 +1001,7 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
       g.out_bf16 = bf;
       g.row_scale = a.row_scale + n0;
       g.unscale = bf ? nullptr : a.w_scale + 1;
-      LRS_CE((run<kEpiOut, kKeepNone>(g, p.big_x, !bf, stream)));
+      LRS_CE((run<kEpiOut, kKeepNone>(g, p.shape_x, !bf, stream)));
       if (p.split_x > 1) {
         hipLaunchKernelGGL(k_ce_join_slots, dim3(blocks_for(n * a.D, 1024)), dim3(256), 0, stream,
                            a.slots_x, (int)p.split_x, n, a.D, a.row_scale + n0, nullptr, g.out,
