@@ -354,6 +354,7 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
     constexpr int PG = TM + 8;  // a padded row of e in LDS
     float* red = reinterpret_cast<float*>(lds);         // [2][WM][TN]: maxima, sums
     uint16_t* keep = reinterpret_cast<uint16_t*>(lds + WM * TN * 8);
+    const bool whole = m0 + TM <= g.M;
     if constexpr (F16) {
       float bu[NT];
 #pragma unroll
@@ -373,17 +374,27 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
       // the target's place among the lane's classes (it has those with bits 2 and 3 clear)
       const int64_t d = (n < g.N ? g.target[n] : -1) - mb;
       const int at = d >= 0 && d < mleft && (d & 12) == 0 ? (int)d : -1;
-      float mx = -__builtin_inff(), tl = 0.0f;
+      if (!whole) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * j + e >= mleft) acc[j][q][e] = -__builtin_inff();
+      }
+      if (__ballot(at >= 0)) {  // few tiles hold the target of one of 16 rows
+        float tl = 0.0f;
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * j + e == at) tl = acc[j][q][e];
+        if (at >= 0) g.tlogit[n] = tl;
+      }
+      float mx = -__builtin_inff();
 #pragma unroll
       for (int j = 0; j < MT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int m = 16 * j + e;
-          if (m >= mleft) acc[j][q][e] = -__builtin_inff();
-          mx = fmaxf(mx, acc[j][q][e]);
-          if (m == at) tl = acc[j][q][e];
-        }
-      if (at >= 0) g.tlogit[n] = tl;
+        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, acc[j][q][e]);
       mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
       if (lane < 16) red[wm * TN + ln + 16 * q] = mx;

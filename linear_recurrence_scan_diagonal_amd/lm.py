@@ -11,7 +11,8 @@ import ctypes
 import torch
 
 from . import binding
-from .binding import DTYPES, _call, _check_dev, _i64, _int, _ptr, _stream, _sz, _vp, _workspace
+from .binding import DTYPES, LrsError, _i64, _int, _sz, _vp
+from .binding import _check_dev as _refuse
 
 EXPORTS = ("lrs_glr_checkpoint_rows", "lrs_glr_workspace_bytes", "lrs_glr_fwd",
            "lrs_glr_bwd_workspace_bytes", "lrs_glr_bwd", "lrs_glr_step", "lrs_layernorm_fwd",
@@ -54,51 +55,98 @@ def load():
     return lib
 
 
-def _rows(name, t, like=None):
+# The smallest calls take a few microseconds on the device, so the checks below
+# first ask one cheap question and look for the reason only if the answer is no;
+# pointers go to ctypes as plain integers.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(dev):
+    return _raw_stream(dev.index)
+
+
+def _call(rc, where):
+    if rc:
+        raise LrsError(rc, where)
+
+
+def _check_dev(name, t, dtype, shape):
+    """A contiguous device tensor of this type and shape, or None."""
+    if t is None:
+        return
+    try:
+        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _refuse(name, t, dtype, shape)
+
+
+def _workspace(nbytes, dev, workspace):
+    if nbytes == 0:
+        return None
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
+        raise TypeError("workspace must be a device tensor")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError(f"workspace needs {nbytes} bytes")
+    return workspace
+
+
+def _pitch(name, t, like=None):
     """Row pitch of a tensor [..., D] whose last axis is contiguous and whose
     leading axes are evenly spaced rows (contiguous, or one slice of a wider
-    array's last axis)."""
+    array's last axis); None if it has at most one row."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a device tensor")
     if t.dtype not in DTYPES:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     if like is not None:
-        if t.dtype != like.dtype:
+        if t.dtype is not like.dtype:
             raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
         if t.shape != like.shape:
             raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
-    D = int(t.shape[-1])
-    if t.numel() == 0:
-        return D
-    if D > 1 and t.stride(-1) != 1:
+    shape, stride = t.shape, t.stride()
+    D = shape[-1]
+    if stride[-1] != 1 and D > 1 and t.numel():
         raise ValueError(f"{name}: the last axis must be contiguous")
-    ld, expect = None, None  # pitch of a row, stride that the next axis must have
-    for axis in range(t.dim() - 2, -1, -1):
-        if t.shape[axis] == 1:
+    ld = expect = None  # pitch of a row, stride that the next axis must have
+    for axis in range(len(shape) - 2, -1, -1):
+        if shape[axis] == 1:
             continue
         if ld is None:
-            ld = expect = t.stride(axis)
-        elif t.stride(axis) != expect:
+            ld = expect = stride[axis]
+        elif stride[axis] != expect and t.numel():
             raise ValueError(f"{name}: rows must be evenly spaced")
-        expect *= int(t.shape[axis])
-    if ld is None:
-        ld = D
-    if ld < D:
+        expect *= shape[axis]
+    if ld is not None and ld < D and t.numel():
         raise ValueError(f"{name}: rows must not overlap")
     return ld
 
 
-def _same_pitch(*named):
-    lds = [_rows(n, t, named[0][1]) for n, t in named]
-    # a single row has no pitch of its own
-    if named[0][1].numel() and len(set(lds)) > 1:
-        raise ValueError("%s must have the same row pitch" % ", ".join(n for n, _ in named))
-    return lds[0]
+def _same_pitch(n0, t0, n1, t1, n2, t2, like=None):
+    """The common row pitch of three tensors of one shape and type."""
+    ld = _pitch(n0, t0, like)
+    if _pitch(n1, t1, t0) != ld or _pitch(n2, t2, t0) != ld:
+        if t0.numel():
+            raise ValueError(f"{n0}, {n1} and {n2} must have the same row pitch")
+    return int(t0.shape[-1]) if ld is None or not t0.numel() else ld
 
 
 def _glr_params(D, bias_r, bias_i, decay):
+    shape = (D,)
     for name, t in (("bias_r", bias_r), ("bias_i", bias_i), ("decay", decay)):
-        _check_dev(name, t, torch.float32, (D,))
+        if t is None:
+            raise TypeError(f"{name} must be a device tensor")
+        _check_dev(name, t, torch.float32, shape)
 
 
 def glr_checkpoints(z_r):
@@ -122,7 +170,7 @@ def glr_fwd(z_r, z_i, x, bias_r, bias_i, decay, c: float = 8.0, reset=None, h0=N
     if z_r.dim() != 3:
         raise ValueError("z_r must be [T,B,D]")
     T, B, D = (int(v) for v in z_r.shape)
-    ld = _same_pitch(("z_r", z_r), ("z_i", z_i), ("x", x))
+    ld = _same_pitch("z_r", z_r, "z_i", z_i, "x", x)
     _glr_params(D, bias_r, bias_i, decay)
     reset = _reset(reset, T, B)
     _check_dev("h0", h0, torch.float32, (B, D))
@@ -158,7 +206,7 @@ def glr_bwd(z_r, z_i, x, bias_r, bias_i, decay, checkpoints, grad_h, c: float = 
     if z_r.dim() != 3:
         raise ValueError("z_r must be [T,B,D]")
     T, B, D = (int(v) for v in z_r.shape)
-    ld = _same_pitch(("z_r", z_r), ("z_i", z_i), ("x", x))
+    ld = _same_pitch("z_r", z_r, "z_i", z_i, "x", x)
     _glr_params(D, bias_r, bias_i, decay)
     reset = _reset(reset, T, B)
     _check_dev("checkpoints", checkpoints, torch.float32, (lib.lrs_glr_checkpoint_rows(T), B, D))
@@ -170,8 +218,7 @@ def glr_bwd(z_r, z_i, x, bias_r, bias_i, decay, checkpoints, grad_h, c: float = 
     if grad_z is None:
         grad_z = tuple(torch.empty((T, B, D), dtype=z_r.dtype, device=dev) for _ in range(3))
     gr, gi, gx = grad_z
-    _rows("grad_zr", gr, z_r)
-    ldg = _same_pitch(("grad_zr", gr), ("grad_zi", gi), ("grad_x", gx))
+    ldg = _same_pitch("grad_zr", gr, "grad_zi", gi, "grad_x", gx, like=z_r)
     gbr, gbi, gd = (torch.empty(D, dtype=torch.float32, device=dev) for _ in range(3))
     gh0 = torch.empty((B, D), dtype=torch.float32, device=dev)
     nbytes = lib.lrs_glr_bwd_workspace_bytes(T, B, D)
@@ -192,11 +239,11 @@ def glr_step(z_r, z_i, x, bias_r, bias_i, decay, state, slots=None, c: float = 8
     if z_r.dim() != 2:
         raise ValueError("z_r must be [B,D]")
     B, D = (int(v) for v in z_r.shape)
-    ld = _same_pitch(("z_r", z_r), ("z_i", z_i), ("x", x))
+    ld = _same_pitch("z_r", z_r, "z_i", z_i, "x", x)
     _glr_params(D, bias_r, bias_i, decay)
-    _check_dev("state", state, torch.float32)
-    if state is None or state.dim() != 2 or state.shape[1] != D:
+    if not isinstance(state, torch.Tensor) or state.dim() != 2 or state.shape[1] != D:
         raise ValueError(f"state must be [S,{D}]")
+    _check_dev("state", state, torch.float32, state.shape)
     _check_dev("slots", slots, torch.int32, (B,))
     if slots is None and state.shape[0] < B:
         raise ValueError("state needs a row for every sequence")
