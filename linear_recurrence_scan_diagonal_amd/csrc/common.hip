@@ -141,6 +141,52 @@ hipError_t launch_col_sums(const float* part, int nmat, int64_t R, int64_t D, do
   return hipGetLastError();
 }
 
+struct ParamOuts {
+  float* p[3];
+};
+
+// Column sums of gridDim.y matrices [R, D] in one launch: sixteen waves a
+// workgroup take every sixteenth row of 64 columns, summed in fp64 in that
+// order, and their sums are added in wave order.
+__global__ __launch_bounds__(1024) void k_param_sums(const float* __restrict__ part, ParamOuts outs,
+                                                     int64_t R, int64_t D) {
+  __shared__ double red[16][kWave];
+  const int lane = threadIdx.x & (kWave - 1), wid = threadIdx.x / kWave;
+  const int64_t d = (int64_t)blockIdx.x * kWave + lane;
+  const float* m = part + (int64_t)blockIdx.y * R * D;
+  double s = 0.0;
+  if (d < D) {
+#pragma unroll 8
+    for (int64_t r = wid; r < R; r += 16) s += (double)m[r * D + d];
+  }
+  red[wid][lane] = s;
+  __syncthreads();
+  if (wid == 0 && d < D) {
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s += red[w][lane];
+    outs.p[blockIdx.y][d] = (float)s;
+  }
+}
+
+// One launch up to 1024 rows: 8 us against 2 x (4.8 + 4.8) us for three matrices
+// of 1024 x 1024.  Beyond, a column's rows in one workgroup take longer than two
+// stages.
+hipError_t launch_param_sums(const float* part, int nmat, int64_t R, int64_t D, double* acc,
+                             float* const* outs, hipStream_t stream) {
+  if (R <= 0 || D <= 0) return hipSuccess;
+  if (R <= 1024) {
+    ParamOuts o = {{outs[0], nmat > 1 ? outs[1] : nullptr, nmat > 2 ? outs[2] : nullptr}};
+    hipLaunchKernelGGL(k_param_sums, dim3((unsigned)((D + kWave - 1) / kWave), (unsigned)nmat),
+                       dim3(1024), 0, stream, part, o, R, D);
+    return hipGetLastError();
+  }
+  hipError_t e = launch_col_sums(part, nmat > 1 ? 2 : 1, R, D, acc, outs[0],
+                                 nmat > 1 ? outs[1] : nullptr, stream);
+  if (e == hipSuccess && nmat > 2)
+    e = launch_col_sums(part + 2 * R * D, 1, R, D, acc, outs[2], nullptr, stream);
+  return e;
+}
+
 int device_cus() {
   static int cache[64] = {0};
   int dev = 0;

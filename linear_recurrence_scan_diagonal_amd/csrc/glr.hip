@@ -25,6 +25,11 @@ namespace lrs {
 
 namespace {
 
+// Time tiles of a look-back group.  The end states of the groups form a chain,
+// about 1.2 us a link: with 16 tiles a group instead of the other layers' 8 a
+// prompt of 16384 steps has 8 links of 128 x 16 steps (bf16).
+constexpr int kGlrGroup = 16;
+
 // One row of a strided input: the lane's channels at offsets zo (FULL: all in
 // one aligned group at zo[0]).
 template <int CPT, bool FULL, bool NT>
@@ -224,6 +229,14 @@ __device__ __forceinline__ void glr_walk(const GlrArgs& g, int64_t row0, int64_t
   }
 }
 
+// The state entering row0, where a checkpoint's stretch begins there.
+template <int CPT, bool FULL>
+__device__ __forceinline__ void glr_checkpoint(const GlrArgs& g, int64_t row0, int64_t cbase,
+                                               uint32_t off, int nvc, const float (&x)[CPT]) {
+  if (g.checkpoints && row0 % kGlrRows == 0 && row0 < g.T)
+    store_row<CPT, FULL, false>(g.checkpoints + row0 / kGlrRows * (g.B * g.D) + cbase, off, nvc, x);
+}
+
 // ---------------------------------------------------------------------------
 // forward, look-back tiles
 // ---------------------------------------------------------------------------
@@ -242,10 +255,9 @@ __device__ __forceinline__ void glr_tile(const GlrArgs& g, int tb, int cb, bool 
   glr_fold<L, CPT, RST>(av, bv, A, B);
 #pragma unroll
   for (int k = 0; k < CPT; ++k) x0[k] = (g.h0 && k < q.nvc) ? g.h0[q.c0 + k] : 0.0f;
-  col_enter_state<NW, CPT, RST>(A, B, multi, tb, x0, g.h0, cbase,
-                                clamp_valid(C - cbase, kWave * CPT), st, s, x);
-  if (g.checkpoints && q.row0 == (int64_t)tb * (NW * L))  // wave 0: the state entering the tile
-    store_row<CPT, FULL, false>(g.checkpoints + (int64_t)tb * C + cbase, q.off, q.nvc, x);
+  col_enter_state<NW, CPT, RST, kGlrGroup>(A, B, multi, tb, x0, g.h0, cbase,
+                                           clamp_valid(C - cbase, kWave * CPT), st, s, x);
+  glr_checkpoint<CPT, FULL>(g, q.row0, cbase, q.off, q.nvc, x);
   glr_walk<IO, L, CPT, FULL, NT, RST>(g, q.row0, cbase, q.off, q.nvc, av, bv, x);
   // rows past the end keep the state, so the wave that holds row T-1 ends with h_T
   if (g.h_last && q.row0 < g.T && q.row0 + L >= g.T) {
@@ -260,7 +272,7 @@ __global__ __launch_bounds__(NW* kWave) void k_glr_fwd(GlrArgs g, int ncb, int n
                                                        uint64_t* __restrict__ status,
                                                        unsigned* __restrict__ tickets) {
   constexpr int CW = kWave * CPT, TW = NW * L;
-  static_assert(TW == kGlrRows, "a tile is a checkpoint's stretch");
+  static_assert(TW % kGlrRows == 0 && kGlrRows % L == 0, "stretches begin with a wave's rows");
   __shared__ ColShared<NW, CPT> s;
   const bool multi = ntb > 1;
   const int cb = (int)(blockIdx.x % (unsigned)ncb);
@@ -271,6 +283,73 @@ __global__ __launch_bounds__(NW* kWave) void k_glr_fwd(GlrArgs g, int ncb, int n
     glr_tile<IO, NW, L, CPT, true, NT, RST>(g, tb, cb, multi, st, s);
   else
     glr_tile<IO, NW, L, CPT, false, NT, RST>(g, tb, cb, multi, st, s);
+}
+
+// ---------------------------------------------------------------------------
+// persistent forward: one workgroup per channel block visits every time tile in
+// order, the state entering the tile carried in LDS, the next tile's rows loaded
+// into registers while the current one is processed; no look-back state and no
+// kernel that resets it.  Used when the channel blocks alone fill the GPU.
+// ---------------------------------------------------------------------------
+template <typename IO, int NW, int L, int CPT, bool FULL, int PF, bool NT, bool RST>
+__device__ __forceinline__ void glr_persist_tile(const GlrArgs& g, const GlrChan<CPT>& ch,
+                                                 int64_t row0, int64_t cbase, uint32_t off, int nvc,
+                                                 GlrRows<IO, L, CPT>& rows,
+                                                 PersistShared<NW, CPT>& s, int wid, int par) {
+  float av[L][CPT], bv[L][CPT], A[CPT], B[CPT], x[CPT];
+  glr_maps<IO, L, CPT, FULL>(g, ch, row0, nvc, rows, av, bv);
+  if (PF == 1) glr_load<IO, L, CPT, true, NT, RST>(g, ch, row0 + NW * L, nvc, rows);
+  else if (PF == 2) glr_load<IO, L, CPT, false, NT, RST>(g, ch, row0 + NW * L, nvc, rows);
+  glr_fold<L, CPT, RST>(av, bv, A, B);
+  persist_enter<NW, CPT, RST>(A, B, s, wid, off, x, par);
+  glr_checkpoint<CPT, FULL>(g, row0, cbase, off, nvc, x);
+  glr_walk<IO, L, CPT, FULL, NT, RST>(g, row0, cbase, off, nvc, av, bv, x);
+  persist_advance<NW, CPT>(x, s, wid, off, par);
+}
+
+template <typename IO, int NW, int L, int CPT, bool NT, bool RST>
+__global__ __launch_bounds__(NW* kWave) void k_glr_fwd_persist(GlrArgs g, int vec) {
+  constexpr int CW = kWave * CPT, TW = NW * L;
+  __shared__ PersistShared<NW, CPT> s;
+  const int64_t C = g.B * g.D;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t cbase = (int64_t)blockIdx.x * CW;
+  const uint32_t off = (uint32_t)(lane * CPT);
+  const int nvc = clamp_valid(C - (cbase + off), CPT);
+  const bool cfull = vec && cbase + CW <= C;
+  for (int j = threadIdx.x; j < CW; j += NW * kWave)
+    s.carry[0][j] = (g.h0 && cbase + j < C) ? g.h0[cbase + j] : 0.0f;
+  GlrChan<CPT> ch;
+  ch.set(g, cbase + off, nvc);
+  const int64_t ntb = (g.T + TW - 1) / TW, nfull = g.T / TW;
+  const int64_t w0 = (int64_t)wid * L;
+  GlrRows<IO, L, CPT> rows;
+#define LRS_TILE(FULLT, PFT, TB)                                                                \
+  glr_persist_tile<IO, NW, L, CPT, FULLT, PFT, NT, RST>(g, ch, (TB) * TW + w0, cbase, off, nvc, \
+                                                        rows, s, wid, (int)((TB) & 1))
+  if (cfull && nfull > 0) {
+    glr_load<IO, L, CPT, true, NT, RST>(g, ch, w0, nvc, rows);
+    for (int64_t tb = 0; tb + 1 < nfull; ++tb) LRS_TILE(true, 1, tb);
+    if (ntb > nfull) {
+      LRS_TILE(true, 2, nfull - 1);
+      LRS_TILE(false, 0, nfull);
+    } else {
+      LRS_TILE(true, 0, nfull - 1);
+    }
+  } else {
+    glr_load<IO, L, CPT, false, NT, RST>(g, ch, w0, nvc, rows);
+    for (int64_t tb = 0; tb < ntb; ++tb) {
+      if (tb + 1 < ntb) LRS_TILE(false, 2, tb);
+      else LRS_TILE(false, 0, tb);
+    }
+  }
+#undef LRS_TILE
+  if (g.h_last) {  // rows past the end keep the state
+    __syncthreads();
+    for (int j = threadIdx.x; j < CW; j += NW * kWave)
+      if (cbase + j < C) g.h_last[cbase + j] = s.carry[ntb & 1][j];
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -359,8 +438,17 @@ __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, 
     x0[k] = (g.grad_h_last && k < nvc) ? g.grad_h_last[c0 + k] : 0.0f;
     hs[k] = k < nvc ? g.checkpoints[(int64_t)ptb * C + c0 + k] : 0.0f;
   }
-  col_enter_state<NW, CPT, RST>(A, B, multi, tb, x0, g.grad_h_last, cbase, clamp_valid(C - cbase, CW),
-                                st, s, y);
+  col_enter_state<NW, CPT, RST>(A, B, multi, tb, x0, g.grad_h_last, cbase,
+                                clamp_valid(C - cbase, CW), st, s, y);
+  // x and grad_h stay packed across the barriers: unpacked copies kept by the
+  // compiler would cost half the waves a compute unit can hold
+  if constexpr (sizeof(IO) == 2) {
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+#pragma unroll
+      for (int k = 0; k < CPT / 2; ++k)
+        asm("" : "+v"(rows.x[i].w[k]), "+v"(gh[i].w[k]));
+  }
   // past a barrier: the states before each of the wave's rows
   for (int w = NW - 1; w > wid; --w) {
 #pragma unroll
@@ -435,7 +523,7 @@ __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, 
 }
 
 template <typename IO, int NW, int L, int CPT, bool NT, bool RST>
-__global__ __launch_bounds__(NW* kWave) void k_glr_bwd(GlrArgs g, int ncb, int ntb, int vec,
+__global__ __launch_bounds__(NW* kWave, 4) void k_glr_bwd(GlrArgs g, int ncb, int ntb, int vec,
                                                        uint64_t* __restrict__ status,
                                                        unsigned* __restrict__ tickets) {
   constexpr int CW = kWave * CPT, TW = NW * L;
@@ -483,14 +571,18 @@ __global__ __launch_bounds__(256) void k_glr_step(GlrArgs g, const int32_t* __re
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-ColPlan plan_glr(int64_t C, int64_t T, int io) {
-  ColPlan p = plan_cols(C, T, 8, 8, 2);
+ColPlan plan_glr(int64_t C, int64_t T, int io, bool allow_persist) {
+  ColPlan p = plan_cols(C, T, 8, io == kIoBf16 ? 16 : 8, 2);
+  if (allow_persist && p.ncb >= persist_min_blocks()) {
+    p = plan_cols(C, T, 8, 8, 2);
+    p.persist = true;
+  }
   p.stream = C * T * 4 * io_bytes(io) >= kStreamFootprint;
   return p;
 }
 
 ColPlan plan_glr_bwd(int64_t C, int64_t T, int io) {
-  ColPlan p = plan_cols(C, T, 8, 8, 2);
+  ColPlan p = plan_cols(C, T, 16, 4, 2);
   p.stream = C * T * 7 * io_bytes(io) >= kStreamFootprint;
   return p;
 }
@@ -516,10 +608,18 @@ ColPlan plan_glr_bwd(int64_t C, int64_t T, int io) {
 
 hipError_t launch_glr_fwd(const GlrArgs& g, int io, const ColPlan& p, int vec, uint64_t* status,
                           unsigned* tickets, hipStream_t stream) {
+  if (p.persist) {
+#define LRS_GLR_P(IO, NTF, RSTF)                                                              \
+  hipLaunchKernelGGL((k_glr_fwd_persist<IO, 8, 8, 2, NTF, RSTF>), dim3((unsigned)p.ncb),      \
+                     dim3(512), 0, stream, g, vec)
+    LRS_GLR_PICK(LRS_GLR_P)
+#undef LRS_GLR_P
+    return hipGetLastError();
+  }
   const dim3 grid((unsigned)(p.ncb * p.ntb));
-#define LRS_GLR_F(IO, NTF, RSTF)                                                               \
-  hipLaunchKernelGGL((k_glr_fwd<IO, 8, 8, 2, NTF, RSTF>), grid, dim3(512), 0, stream, g,       \
-                     (int)p.ncb, (int)p.ntb, vec, status, tickets)
+#define LRS_GLR_F(IO, NTF, RSTF)                                                                \
+  hipLaunchKernelGGL((k_glr_fwd<IO, 8, sizeof(IO) == 2 ? 16 : 8, 2, NTF, RSTF>), grid,          \
+                     dim3(512), 0, stream, g, (int)p.ncb, (int)p.ntb, vec, status, tickets)
   LRS_GLR_PICK(LRS_GLR_F)
 #undef LRS_GLR_F
   return hipGetLastError();
@@ -530,17 +630,14 @@ hipError_t launch_glr_bwd(const GlrArgs& g, int io, const ColPlan& p, int vec, u
                           float* grad_decay, hipStream_t stream) {
   const dim3 grid((unsigned)(p.ncb * p.ntb));
 #define LRS_GLR_B(IO, NTF, RSTF)                                                               \
-  hipLaunchKernelGGL((k_glr_bwd<IO, 8, 8, 2, NTF, RSTF>), grid, dim3(512), 0, stream, g,       \
+  hipLaunchKernelGGL((k_glr_bwd<IO, 16, 4, 2, NTF, RSTF>), grid, dim3(1024), 0, stream, g,       \
                      (int)p.ncb, (int)p.ntb, vec, status, tickets)
   LRS_GLR_PICK(LRS_GLR_B)
 #undef LRS_GLR_B
-  hipError_t e = hipGetLastError();
-  const int64_t R = p.ntb * g.B;
-  if (e == hipSuccess)
-    e = launch_col_sums(g.part, 2, R, g.D, acc, grad_bias_r, grad_bias_i, stream);
-  if (e == hipSuccess)
-    e = launch_col_sums(g.part + 2 * R * g.D, 1, R, g.D, acc, grad_decay, nullptr, stream);
-  return e;
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  float* const outs[3] = {grad_bias_r, grad_bias_i, grad_decay};
+  return launch_param_sums(g.part, 3, p.ntb * g.B, g.D, acc, outs, stream);
 }
 
 hipError_t launch_glr_step(const GlrArgs& g, int io, const int32_t* slots, float* state, int64_t S,

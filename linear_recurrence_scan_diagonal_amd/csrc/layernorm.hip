@@ -488,7 +488,8 @@ static hipError_t ln_bwd(const IO* s, const float* gamma, const float* mean, con
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return launch_col_sums(part, grad_beta ? 2 : 1, nb, D, acc, grad_gamma, grad_beta, stream);
+  float* const outs[2] = {grad_gamma, grad_beta};
+  return launch_param_sums(part, grad_beta ? 2 : 1, nb, D, acc, outs, stream);
 }
 
 hipError_t launch_layernorm_bwd(const void* s, const float* gamma, const float* mean,

@@ -178,6 +178,12 @@ int64_t col_sum_blocks(int64_t R);
 hipError_t launch_col_sums(const float* part, int nmat, int64_t R, int64_t D, double* acc,
                            float* out0, float* out1, hipStream_t stream);
 
+// The same for up to three matrices and as many outputs, for the operators of
+// lrs_lm.h: one launch while R is small (any D at the same speed), the two
+// stages above otherwise.  `acc` as above for nmat matrices.
+hipError_t launch_param_sums(const float* part, int nmat, int64_t R, int64_t D, double* acc,
+                             float* const* outs, hipStream_t stream);
+
 // Launches the SRU backward kernel and the bias-gradient reduction; `part`
 // holds 2 * ntb * B * D floats of per-tile partial sums.
 hipError_t launch_sru_bwd(const void* zf, const void* zr, const void* zx, const float* bias_f,
@@ -243,7 +249,8 @@ struct GlrArgs {
   float* grad_h0;
   float* part;  // [3][ntb * B][D]: the tiles' sums for bias_r, bias_i and decay
 };
-ColPlan plan_glr(int64_t C, int64_t T, int io);
+// allow_persist = false: the look-back tile plan (workspace queries size for it).
+ColPlan plan_glr(int64_t C, int64_t T, int io, bool allow_persist = true);
 ColPlan plan_glr_bwd(int64_t C, int64_t T, int io);
 hipError_t launch_glr_fwd(const GlrArgs& g, int io, const ColPlan& p, int vec, uint64_t* status,
                           unsigned* tickets, hipStream_t stream);

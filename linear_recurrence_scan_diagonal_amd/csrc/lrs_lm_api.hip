@@ -77,7 +77,8 @@ int64_t lrs_glr_checkpoint_rows(int64_t T) {
 size_t lrs_glr_workspace_bytes(int64_t T, int64_t B, int64_t D) {
   int64_t C, N;
   if (!glr_shape(T, B, D, &C, &N) || N == 0) return 0;
-  const lrs::ColPlan p = lrs::plan_glr(C, T, LRS_F32);
+  // the fp32 tiles are the shorter ones
+  const lrs::ColPlan p = lrs::plan_glr(C, T, LRS_F32, false);
   return lookback_bytes(lrs::col_status_words(p), p.ncb);
 }
 
@@ -107,7 +108,8 @@ int lrs_glr_fwd(const void* z_r, const void* z_i, const void* x, int64_t ld, con
                        {checkpoints, (size_t)lrs_glr_checkpoint_rows(T) * cb}};
   if (any_overlap(outs, 3, ins, 8)) return LRS_ERR_INVALID_ARG;
   const lrs::ColPlan p = lrs::plan_glr(C, T, io_dtype);
-  if (!glr_step_fits(B, C, ld) || !grid_ok(p.ncb * p.ntb, p.nw * 64)) return LRS_ERR_UNSUPPORTED;
+  if (!glr_step_fits(B, C, ld) || !grid_ok(p.persist ? p.ncb : p.ncb * p.ntb, p.nw * 64))
+    return LRS_ERR_UNSUPPORTED;
   const int64_t nst = lrs::col_status_words(p);
   const size_t need = lookback_bytes(nst, p.ncb);
   if (need && (!workspace || workspace_bytes < need)) return LRS_ERR_WORKSPACE;

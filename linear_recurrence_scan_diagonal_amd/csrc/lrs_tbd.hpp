@@ -182,7 +182,8 @@ constexpr int kColGroup = 8;
 // wave then composes the maps of the waves before it (wave order = scan order).
 // st points at this channel block's status row for time block 0; time blocks
 // are CW words apart.  SEL: maps with a factor of 0 replace the state (affine).
-template <int NW, int CPT, bool SEL = false>
+// G: time blocks of a look-back group.
+template <int NW, int CPT, bool SEL = false, int G = kColGroup>
 __device__ __forceinline__ void col_enter_state(const float (&A)[CPT], const float (&B)[CPT],
                                                 bool multi, int tb, const float (&x0)[CPT],
                                                 const float* x0p, int64_t cbase, int cvalid,
@@ -214,10 +215,10 @@ __device__ __forceinline__ void col_enter_state(const float (&A)[CPT], const flo
       }
       float x_in = 0.0f;
       if (j < cvalid) {
-        const bool gend = group_end(tb, kColGroup);
+        const bool gend = group_end(tb, G);
         if (!gend) status_store(st + (int64_t)tb * CW + j, pack_agg(TA, TB));
         const float xs = x0p ? x0p[cbase + j] : 0.0f;
-        x_in = lookback_group_lane<kColGroup, SEL>(st + j, CW, tb, xs);
+        x_in = lookback_group_lane<G, SEL>(st + j, CW, tb, xs);
         if (gend) status_store(st + (int64_t)tb * CW + j, pack_inc(affine<SEL>(TA, x_in, TB)));
       }
       s.carry[j] = x_in;
