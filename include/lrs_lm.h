@@ -40,7 +40,7 @@ extern "C" {
  *               enter each stretch of time steps, which lrs_glr_bwd reads (it
  *               recomputes the states between them); or NULL.
  * c           : positive and finite.
- * Supported while B*D and B*ld stay below 2^31. */
+ * Supported while B*D stays below 2^31 and B*ld below 2^30. */
 LRS_API int64_t lrs_glr_checkpoint_rows(int64_t T);
 LRS_API size_t lrs_glr_workspace_bytes(int64_t T, int64_t B, int64_t D);
 LRS_API int lrs_glr_fwd(const void *z_r, const void *z_i, const void *x, int64_t ld,

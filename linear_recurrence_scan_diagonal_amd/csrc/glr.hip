@@ -28,20 +28,45 @@ namespace {
 // Time tiles of a look-back group.  The end states of the groups form a chain,
 // about 1.2 us a link: with 16 tiles a group instead of the other layers' 8 a
 // prompt of 16384 steps has 8 links of 128 x 16 steps (bf16).
-constexpr int kGlrGroup = 16;
+#ifndef VG
+#define VG 16
+#endif
+#ifndef VL
+#define VL 16
+#endif
+#ifndef VNW
+#define VNW 8
+#endif
+#ifndef VBNW
+#define VBNW 8
+#define VBL 8
+#endif
+#ifndef VOCC
+#define VOCC 1
+#endif
+constexpr int kGlrGroup = VG;
 
-// One row of a strided input: the lane's channels at offsets zo (FULL: all in
-// one aligned group at zo[0]).
+// One row of a strided array: the lane's channels at byte offsets zo from a
+// wave-uniform pointer (32 bits: no address arithmetic a row); FULL: all in one
+// aligned group at zo[0].
+template <typename IO>
+__device__ __forceinline__ const IO* at(const IO* p, uint32_t bytes) {
+  return reinterpret_cast<const IO*>(reinterpret_cast<const char*>(p) + bytes);
+}
+template <typename IO>
+__device__ __forceinline__ IO* at(IO* p, uint32_t bytes) {
+  return reinterpret_cast<IO*>(reinterpret_cast<char*>(p) + bytes);
+}
 template <int CPT, bool FULL, bool NT>
 __device__ __forceinline__ void glr_ld(const uint16_t* p, const uint32_t (&zo)[CPT], int nv,
                                        IoRow<uint16_t, CPT>& r) {
   if constexpr (FULL) {
-    r.template load<true, NT>(p, zo[0], CPT);
+    r.template load<true, NT>(at(p, zo[0]), 0, CPT);
   } else {
 #pragma unroll
     for (int k = 0; k < CPT / 2; ++k) {
-      const uint32_t lo = 2 * k < nv ? p[zo[2 * k]] : 0u;
-      const uint32_t hi = 2 * k + 1 < nv ? p[zo[2 * k + 1]] : 0u;
+      const uint32_t lo = 2 * k < nv ? *at(p, zo[2 * k]) : 0u;
+      const uint32_t hi = 2 * k + 1 < nv ? *at(p, zo[2 * k + 1]) : 0u;
       r.w[k] = lo | (hi << 16);
     }
   }
@@ -50,45 +75,74 @@ template <int CPT, bool FULL, bool NT>
 __device__ __forceinline__ void glr_ld(const float* p, const uint32_t (&zo)[CPT], int nv,
                                        IoRow<float, CPT>& r) {
   if constexpr (FULL) {
-    r.template load<true, NT>(p, zo[0], CPT);
+    r.template load<true, NT>(at(p, zo[0]), 0, CPT);
   } else {
 #pragma unroll
-    for (int k = 0; k < CPT; ++k) r.v[k] = k < nv ? p[zo[k]] : 0.0f;
+    for (int k = 0; k < CPT; ++k) r.v[k] = k < nv ? *at(p, zo[k]) : 0.0f;
   }
 }
 template <int CPT, bool FULL, bool NT, typename IO>
 __device__ __forceinline__ void glr_st(IO* p, const uint32_t (&zo)[CPT], int nv,
                                        const float (&v)[CPT]) {
   if constexpr (FULL) {
-    IoRow<IO, CPT>::template store<true, NT>(p, zo[0], CPT, v);
+    IoRow<IO, CPT>::template store<true, NT>(at(p, zo[0]), 0, CPT, v);
   } else {
 #pragma unroll
     for (int k = 0; k < CPT; ++k)
-      if (k < nv) io_st(p, zo[k], v[k]);
+      if (k < nv) io_st(at(p, zo[k]), 0, v[k]);
   }
 }
 
-// softplus(v) = max(v, 0) + log(1 + exp(-|v|)), once a channel.
+// softplus(v) = max(v, 0) + log(1 + exp(-|v|)).
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))); }
 
-// What a channel's parameters become: biases in the sigmoid's log2 units and
-// the exponent of a fully open gate, k = c softplus(decay).
+// The exponent of a fully open gate, k = c softplus(decay), and -c times the
+// derivative of softplus: computed once a call (k_glr_prep) where a tile is one
+// of many, because with its 32 elements a thread the library functions and the
+// division below would be a seventh of the backward's instructions.
+__device__ __forceinline__ void glr_rates(const GlrArgs& g, uint32_t d, float& k, float& dk) {
+  const float v = g.decay[d];
+  k = g.c * softplus(v);
+  dk = -g.c * fast_sigmoid(v, 0.0f);
+}
+
+// What a channel's parameters become: biases in the sigmoid's log2 units, and k.
 template <int CPT>
 struct GlrChan {
   float br[CPT], bi[CPT], k[CPT];
-  uint32_t zo[CPT];  // offsets in a row of the inputs
+  uint32_t zo[CPT];  // byte offsets in a row of the inputs
   uint32_t b[CPT], d[CPT];
-  __device__ __forceinline__ void set(const GlrArgs& g, int64_t c0, int nvc) {
+  bool near;  // k < 1/8 in every channel of the wave
+  // off: the lane's first channel in its block, which begins at cbase
+  __device__ __forceinline__ void set(const GlrArgs& g, int64_t cbase, uint32_t off, int nvc,
+                                      uint32_t es) {
+    const uint32_t D = (uint32_t)g.D;
+    const uint32_t b0 = __builtin_amdgcn_readfirstlane((uint32_t)cbase / D);
+    const uint32_t d0 = (uint32_t)cbase - b0 * D;
+    bool low = true;
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
-      const uint32_t c = j < nvc ? (uint32_t)(c0 + j) : 0u;
-      b[j] = c / (uint32_t)g.D;
-      d[j] = c - b[j] * (uint32_t)g.D;
-      zo[j] = b[j] * (uint32_t)g.ld + d[j];
+      const uint32_t e = j < nvc ? d0 + off + j : d0;
+      if (D >= kWave * CPT) {  // a block meets at most one border of two sequences
+        b[j] = e >= D ? b0 + 1 : b0;
+        d[j] = e >= D ? e - D : e;
+      } else {
+        const uint32_t q = e / D;
+        b[j] = b0 + q;
+        d[j] = e - q * D;
+      }
+      zo[j] = (b[j] * (uint32_t)g.ld + d[j]) * es;
       br[j] = -kLog2e * g.bias_r[d[j]];
       bi[j] = -kLog2e * g.bias_i[d[j]];
-      k[j] = g.c * softplus(g.decay[d[j]]);
+      if (g.rates) {
+        k[j] = g.rates[d[j]];
+      } else {
+        float dk;
+        glr_rates(g, d[j], k[j], dk);
+      }
+      low = low && k[j] < 0.125f;
     }
+    near = __all(low);
   }
 };
 
@@ -98,12 +152,19 @@ struct GlrChan {
 // from that: subtracting a^2 from 1 would lose the digits of 1 - a, and the
 // exponential instruction's last bit, which does not round to nearest, would
 // add up over the steps that the state survives (2e-5 of h over 640 of them).
+// NEAR: every t is below 1/8 (k is, and r is at most 1), and the rest is left out.
+template <bool NEAR>
 __device__ __forceinline__ void glr_decay(float t, float& a, float& m2) {
   float p = __builtin_fmaf(t, 1.0f / 120.0f, -1.0f / 24.0f);
   p = __builtin_fmaf(t, p, 1.0f / 6.0f);
   p = __builtin_fmaf(t, p, -0.5f);
   p = __builtin_fmaf(t, p, 1.0f);
   const float e = t * p;
+  if constexpr (NEAR) {
+    a = 1.0f - e;
+    m2 = e * (2.0f - e);
+    return;
+  }
   const float far = __builtin_amdgcn_exp2f(-kLog2e * t);
   const bool near = t < 0.125f;
   a = near ? 1.0f - e : far;
@@ -113,13 +174,14 @@ __device__ __forceinline__ void glr_decay(float t, float& a, float& m2) {
 struct GlrGate {
   float r, i, a, m;
 };
+template <bool NEAR>
 __device__ __forceinline__ GlrGate glr_gate(float zr, float zi, float br, float bi, float k,
                                             bool cut) {
   GlrGate g;
   g.r = fast_sigmoid(zr, br);
   g.i = fast_sigmoid(zi, bi);
   float m2;
-  glr_decay(k * g.r, g.a, m2);
+  glr_decay<NEAR>(k * g.r, g.a, m2);
   g.m = __builtin_amdgcn_sqrtf(m2);
   if (cut) {
     g.a = 0.0f;
@@ -145,6 +207,23 @@ __device__ __forceinline__ void glr_cut(const uint8_t* reset, int64_t row, const
         if (k < nv) cut[k] = reset[row * g.B + ch.b[k]];
     }
   }
+}
+
+// a * x, and one step a * x + b, where with SEL a factor of 0 gives 0 whatever x
+// is (the "legacy" product's rule: two instructions a step, where affine's
+// compare and select make three).
+template <bool SEL>
+__device__ __forceinline__ float scale(float a, float x) {
+  if constexpr (SEL) {
+    float r;
+    asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(x));
+    return r;
+  }
+  return a * x;
+}
+template <bool SEL>
+__device__ __forceinline__ float step(float a, float x, float b) {
+  return SEL ? scale<SEL>(a, x) + b : __builtin_fmaf(a, x, b);
 }
 
 template <typename IO, int L, int CPT>
@@ -174,7 +253,7 @@ __device__ __forceinline__ void glr_load(const GlrArgs& g, const GlrChan<CPT>& c
 }
 
 // The step maps (a, m i x) of the loaded rows; identity past the end.
-template <typename IO, int L, int CPT, bool FULL>
+template <bool NEAR, typename IO, int L, int CPT, bool FULL>
 __device__ __forceinline__ void glr_maps(const GlrArgs& g, const GlrChan<CPT>& ch, int64_t row0,
                                          int nvc, const GlrRows<IO, L, CPT>& rows,
                                          float (&av)[L][CPT], float (&bv)[L][CPT]) {
@@ -184,8 +263,8 @@ __device__ __forceinline__ void glr_maps(const GlrArgs& g, const GlrChan<CPT>& c
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
       if (FULL || (row_ok && k < nvc)) {
-        const GlrGate q = glr_gate(rows.zr[i].get(k), rows.zi[i].get(k), ch.br[k], ch.bi[k],
-                                   ch.k[k], rows.cut[i][k] != 0);
+        const GlrGate q = glr_gate<NEAR>(rows.zr[i].get(k), rows.zi[i].get(k), ch.br[k],
+                                         ch.bi[k], ch.k[k], rows.cut[i][k] != 0);
         av[i][k] = q.a;
         bv[i][k] = q.m * q.i * rows.x[i].get(k);
       } else {
@@ -194,6 +273,16 @@ __device__ __forceinline__ void glr_maps(const GlrArgs& g, const GlrChan<CPT>& c
       }
     }
   }
+}
+
+// Both forms, chosen once a wave: an open gate keeps more than 0.88 of the state
+// (k < 1/8) in all of its channels, or not.
+template <typename IO, int L, int CPT, bool FULL>
+__device__ __forceinline__ void glr_maps(const GlrArgs& g, const GlrChan<CPT>& ch, int64_t row0,
+                                         int nvc, const GlrRows<IO, L, CPT>& rows,
+                                         float (&av)[L][CPT], float (&bv)[L][CPT]) {
+  if (ch.near) glr_maps<true, IO, L, CPT, FULL>(g, ch, row0, nvc, rows, av, bv);
+  else glr_maps<false, IO, L, CPT, FULL>(g, ch, row0, nvc, rows, av, bv);
 }
 
 template <int L, int CPT, bool SEL>
@@ -205,7 +294,7 @@ __device__ __forceinline__ void glr_fold(const float (&av)[L][CPT], const float 
     B[k] = bv[0][k];
 #pragma unroll
     for (int i = 1; i < L; ++i) {
-      B[k] = affine<SEL>(av[i][k], B[k], bv[i][k]);
+      B[k] = step<SEL>(av[i][k], B[k], bv[i][k]);
       A[k] = A[k] * av[i][k];
     }
   }
@@ -222,9 +311,9 @@ __device__ __forceinline__ void glr_walk(const GlrArgs& g, int64_t row0, int64_t
 #pragma unroll
   for (int i = 0; i < L; ++i) {
 #pragma unroll
-    for (int k = 0; k < CPT; ++k) x[k] = affine<SEL>(av[i][k], x[k], bv[i][k]);
+    for (int k = 0; k < CPT; ++k) x[k] = step<SEL>(av[i][k], x[k], bv[i][k]);
     const int nv = (FULL || row0 + i < g.T) ? nvc : 0;
-    IoRow<IO, CPT>::template store<FULL, NT>(hp, off, nv, x);
+    IoRow<IO, CPT>::template store<FULL, NT>(at(hp, off * (uint32_t)sizeof(IO)), 0, nv, x);
     hp += C;
   }
 }
@@ -247,7 +336,7 @@ __device__ __forceinline__ void glr_tile(const GlrArgs& g, int tb, int cb, bool 
   const ColPos q = col_pos<NW, L, CPT>(tb, cb, C);
   const int64_t cbase = (int64_t)cb * (kWave * CPT);
   GlrChan<CPT> ch;
-  ch.set(g, q.c0, q.nvc);
+  ch.set(g, cbase, q.off, q.nvc, sizeof(IO));
   GlrRows<IO, L, CPT> rows;
   glr_load<IO, L, CPT, FULL, NT, RST>(g, ch, q.row0, q.nvc, rows);
   float av[L][CPT], bv[L][CPT], A[CPT], B[CPT], x0[CPT], x[CPT];
@@ -321,7 +410,7 @@ __global__ __launch_bounds__(NW* kWave) void k_glr_fwd_persist(GlrArgs g, int ve
   for (int j = threadIdx.x; j < CW; j += NW * kWave)
     s.carry[0][j] = (g.h0 && cbase + j < C) ? g.h0[cbase + j] : 0.0f;
   GlrChan<CPT> ch;
-  ch.set(g, cbase + off, nvc);
+  ch.set(g, cbase, off, nvc, sizeof(IO));
   const int64_t ntb = (g.T + TW - 1) / TW, nfull = g.T / TW;
   const int64_t w0 = (int64_t)wid * L;
   GlrRows<IO, L, CPT> rows;
@@ -365,6 +454,32 @@ struct GlrBwdShared {
   float red[3][NW][kWave * CPT];                   // parameter gradients of the waves
 };
 
+template <bool NEAR, typename IO, int L, int CPT, bool FULL>
+__device__ __forceinline__ void glr_gates(const GlrArgs& g, const GlrChan<CPT>& ch, int64_t row0,
+                                          int nvc, const GlrRows<IO, L, CPT>& rows,
+                                          float (&r)[L][CPT], float (&gi)[L][CPT],
+                                          float (&av)[L][CPT], float (&m)[L][CPT]) {
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const bool row_ok = FULL || row0 + i < g.T;
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) {
+      GlrGate q;
+      if (FULL || (row_ok && k < nvc)) {
+        q = glr_gate<NEAR>(rows.zr[i].get(k), rows.zi[i].get(k), ch.br[k], ch.bi[k], ch.k[k],
+                           rows.cut[i][k] != 0);
+      } else {
+        q.r = q.i = q.m = 0.0f;
+        q.a = 1.0f;
+      }
+      r[i][k] = q.r;
+      gi[i][k] = q.i;
+      av[i][k] = q.a;
+      m[i][k] = q.m;
+    }
+  }
+}
+
 template <typename IO, int NW, int L, int CPT, bool FULL, bool NT, bool RST>
 __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, int cb, bool multi,
                                              uint64_t* st, ColShared<NW, CPT>& s,
@@ -380,7 +495,7 @@ __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, 
   const int nvc = FULL ? CPT : clamp_valid(C - c0, CPT);
   const int64_t row0 = (int64_t)ptb * (NW * L) + (int64_t)(NW - 1 - wid) * L;
   GlrChan<CPT> ch;
-  ch.set(g, c0, nvc);
+  ch.set(g, cbase, off, nvc, sizeof(IO));
   GlrRows<IO, L, CPT> rows;
   glr_load<IO, L, CPT, FULL, NT, RST>(g, ch, row0, nvc, rows);
   IoRow<IO, CPT> gh[L];
@@ -388,32 +503,22 @@ __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, 
     const IO* gp = (const IO*)g.grad_h + row0 * C + cbase;
 #pragma unroll
     for (int i = 0; i < L; ++i) {
-      gh[i].template load<FULL, NT>(gp, off, (FULL || row0 + i < g.T) ? nvc : 0);
+      gh[i].template load<FULL, NT>(at(gp, off * (uint32_t)sizeof(IO)), 0,
+                                    (FULL || row0 + i < g.T) ? nvc : 0);
       gp += C;
     }
   }
   float r[L][CPT], gi[L][CPT], av[L][CPT], m[L][CPT];
   float FA[CPT], FB[CPT], A[CPT], B[CPT];
+  if (ch.near) glr_gates<true, IO, L, CPT, FULL>(g, ch, row0, nvc, rows, r, gi, av, m);
+  else glr_gates<false, IO, L, CPT, FULL>(g, ch, row0, nvc, rows, r, gi, av, m);
 #pragma unroll
   for (int i = 0; i < L; ++i) {
-    const bool row_ok = FULL || row0 + i < g.T;
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
-      GlrGate q;
-      if (FULL || (row_ok && k < nvc)) {
-        q = glr_gate(rows.zr[i].get(k), rows.zi[i].get(k), ch.br[k], ch.bi[k], ch.k[k],
-                     rows.cut[i][k] != 0);
-      } else {
-        q.r = q.i = q.m = 0.0f;
-        q.a = 1.0f;
-      }
-      r[i][k] = q.r;
-      gi[i][k] = q.i;
-      av[i][k] = q.a;
-      m[i][k] = q.m;
-      const float b = q.m * q.i * rows.x[i].get(k);  // 0 past the end (x reads as 0 there)
-      FB[k] = i == 0 ? b : affine<RST>(q.a, FB[k], b);
-      FA[k] = i == 0 ? q.a : FA[k] * q.a;
+      const float b = m[i][k] * gi[i][k] * rows.x[i].get(k);  // 0 past the end (x reads as 0 there)
+      FB[k] = i == 0 ? b : step<RST>(av[i][k], FB[k], b);
+      FA[k] = i == 0 ? av[i][k] : FA[k] * av[i][k];
     }
   }
 #pragma unroll
@@ -426,11 +531,11 @@ __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, 
     B[k] = gh[L - 1].get(k);
 #pragma unroll
     for (int i = L - 2; i >= 0; --i) {
-      B[k] = affine<RST>(av[i + 1][k], B[k], gh[i].get(k));
+      B[k] = step<RST>(av[i + 1][k], B[k], gh[i].get(k));
       A[k] = A[k] * av[i + 1][k];
     }
     A[k] = A[k] * av[0][k];
-    B[k] = affine<RST>(av[0][k], B[k], 0.0f);
+    B[k] = scale<RST>(av[0][k], B[k]);
   }
   float x0[CPT], y[CPT], hs[CPT];
 #pragma unroll
@@ -460,12 +565,12 @@ __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, 
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
       hp[i][k] = hs[k];
-      hs[k] = affine<RST>(av[i][k], hs[k], m[i][k] * gi[i][k] * rows.x[i].get(k));
+      hs[k] = step<RST>(av[i][k], hs[k], m[i][k] * gi[i][k] * rows.x[i].get(k));
     }
   }
   uint32_t go[CPT];
 #pragma unroll
-  for (int k = 0; k < CPT; ++k) go[k] = ch.b[k] * (uint32_t)g.ld_grad + ch.d[k];
+  for (int k = 0; k < CPT; ++k) go[k] = (ch.b[k] * (uint32_t)g.ld_grad + ch.d[k]) * (uint32_t)sizeof(IO);
   const int64_t gpitch = g.B * g.ld_grad;
   IO* qr = (IO*)g.grad_zr + (row0 + L - 1) * gpitch;
   IO* qi = (IO*)g.grad_zi + (row0 + L - 1) * gpitch;
@@ -478,14 +583,13 @@ __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, 
     float dr[CPT], di[CPT], dx[CPT];
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
-      y[k] = i == L - 1 ? y[k] + gh[i].get(k) : affine<RST>(av[i + 1][k], y[k], gh[i].get(k));  // lam_t
+      y[k] = i == L - 1 ? y[k] + gh[i].get(k) : step<RST>(av[i + 1][k], y[k], gh[i].get(k));  // lam_t
       const float u = gi[i][k] * rows.x[i].get(k), a = av[i][k], mm = m[i][k], lam = y[k];
       const float dgx = lam * mm;
       dx[k] = dgx * gi[i][k];
       di[k] = dgx * u * (1.0f - gi[i][k]);
-      const float rm = mm > 0.0f ? __builtin_amdgcn_rcpf(mm) : 0.0f;
-      float dla = lam * a * __builtin_fmaf(-a * rm, u, hp[i][k]);
-      if (RST && a == 0.0f) dla = 0.0f;  // whatever the state before was
+      const float rm = __builtin_amdgcn_rcpf(fmaxf(mm, 1e-30f));  // m = 0: with r = 0 below
+      const float dla = scale<RST>(a, lam * __builtin_fmaf(-a * rm, u, hp[i][k]));
       const float dlr = dla * r[i][k];
       dr[k] = -dlr * ch.k[k] * (1.0f - r[i][k]);  // la = -k r
       sr[k] += dr[k];
@@ -503,14 +607,14 @@ __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, 
   if (g.grad_h0 && row0 == 0) {
 #pragma unroll
     for (int k = 0; k < CPT; ++k)
-      if (k < nvc) g.grad_h0[c0 + k] = affine<RST>(av[0][k], y[k], 0.0f);
+      if (k < nvc) g.grad_h0[c0 + k] = scale<RST>(av[0][k], y[k]);
   }
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
     f.red[0][wid][off + k] = sr[k];
     f.red[1][wid][off + k] = si[k];
-    // d softplus / d decay = sigmoid(decay)
-    f.red[2][wid][off + k] = sd[k] * (-g.c * fast_sigmoid(g.decay[ch.d[k]], 0.0f));
+    // with d k / d decay
+    f.red[2][wid][off + k] = sd[k] * g.rates[g.D + ch.d[k]];
   }
   __syncthreads();
   for (int j = threadIdx.x; j < 3 * CW; j += NW * kWave) {
@@ -523,7 +627,7 @@ __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, 
 }
 
 template <typename IO, int NW, int L, int CPT, bool NT, bool RST>
-__global__ __launch_bounds__(NW* kWave, 4) void k_glr_bwd(GlrArgs g, int ncb, int ntb, int vec,
+__global__ __launch_bounds__(NW* kWave, VOCC) void k_glr_bwd(GlrArgs g, int ncb, int ntb, int vec,
                                                        uint64_t* __restrict__ status,
                                                        unsigned* __restrict__ tickets) {
   constexpr int CW = kWave * CPT, TW = NW * L;
@@ -542,6 +646,20 @@ __global__ __launch_bounds__(NW* kWave, 4) void k_glr_bwd(GlrArgs g, int ncb, in
     glr_bwd_tile<IO, NW, L, CPT, false, NT, RST>(g, tb, ntb, cb, multi, st, s, f);
 }
 
+// Before the tiles of a call: k and dk of every feature, and the look-back state
+// reset (one launch for both).
+__global__ __launch_bounds__(256) void k_glr_prep(GlrArgs g, float* __restrict__ rates,
+                                                  uint4* __restrict__ status, int64_t npairs,
+                                                  unsigned* __restrict__ tickets,
+                                                  int64_t ntickets) {
+  const int64_t stride = (int64_t)gridDim.x * 256;
+  const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  for (int64_t d = i0; d < g.D; d += stride) glr_rates(g, (uint32_t)d, rates[d], rates[g.D + d]);
+  const uint4 empty = make_uint4(~0u, ~0u, ~0u, ~0u);  // two status words, not ready
+  for (int64_t i = i0; i < npairs; i += stride) status[i] = empty;
+  for (int64_t i = i0; i < ntickets; i += stride) tickets[i] = 0u;
+}
+
 // ---------------------------------------------------------------------------
 // single tokens: element-wise over [B, D], the state's row by its slot
 // ---------------------------------------------------------------------------
@@ -556,7 +674,7 @@ __global__ __launch_bounds__(256) void k_glr_step(GlrArgs g, const int32_t* __re
   const int64_t z = (int64_t)b * g.ld + d;
   float h = 0.0f;
   if (slot >= 0 && slot < S) {
-    const GlrGate q = glr_gate(io_ld((const IO*)g.z_r, z), io_ld((const IO*)g.z_i, z),
+    const GlrGate q = glr_gate<false>(io_ld((const IO*)g.z_r, z), io_ld((const IO*)g.z_i, z),
                                -kLog2e * g.bias_r[d], -kLog2e * g.bias_i[d],
                                g.c * softplus(g.decay[d]), false);
     float* p = state + slot * g.D + d;
@@ -572,7 +690,7 @@ __global__ __launch_bounds__(256) void k_glr_step(GlrArgs g, const int32_t* __re
 // host side
 // ---------------------------------------------------------------------------
 ColPlan plan_glr(int64_t C, int64_t T, int io, bool allow_persist) {
-  ColPlan p = plan_cols(C, T, 8, io == kIoBf16 ? 16 : 8, 2);
+  ColPlan p = plan_cols(C, T, VNW, io == kIoBf16 ? VL : 8, 2);
   if (allow_persist && p.ncb >= persist_min_blocks()) {
     p = plan_cols(C, T, 8, 8, 2);
     p.persist = true;
@@ -582,7 +700,7 @@ ColPlan plan_glr(int64_t C, int64_t T, int io, bool allow_persist) {
 }
 
 ColPlan plan_glr_bwd(int64_t C, int64_t T, int io) {
-  ColPlan p = plan_cols(C, T, 16, 4, 2);
+  ColPlan p = plan_cols(C, T, VBNW, VBL, 2);
   p.stream = C * T * 7 * io_bytes(io) >= kStreamFootprint;
   return p;
 }
@@ -606,8 +724,26 @@ ColPlan plan_glr_bwd(int64_t C, int64_t T, int io) {
     }                                                           \
   }
 
-hipError_t launch_glr_fwd(const GlrArgs& g, int io, const ColPlan& p, int vec, uint64_t* status,
-                          unsigned* tickets, hipStream_t stream) {
+// status: whole pairs of words, 16-byte aligned.
+static hipError_t glr_prep(const GlrArgs& g, const ColPlan& p, float* rates, uint64_t* status,
+                           unsigned* tickets, hipStream_t stream) {
+  const int64_t npairs = col_status_words(p) / 2;
+  int64_t n = npairs > g.D ? npairs : g.D;
+  if (p.ncb > n) n = p.ncb;
+  int64_t blocks = (n + 255) / 256;
+  if (blocks > 2048) blocks = 2048;
+  hipLaunchKernelGGL(k_glr_prep, dim3((unsigned)blocks), dim3(256), 0, stream, g, rates,
+                     (uint4*)status, npairs, tickets, npairs > 0 ? p.ncb : 0);
+  return hipGetLastError();
+}
+
+hipError_t launch_glr_fwd(GlrArgs& g, int io, const ColPlan& p, int vec, float* rates,
+                          uint64_t* status, unsigned* tickets, hipStream_t stream) {
+  if (status) {
+    const hipError_t e = glr_prep(g, p, rates, status, tickets, stream);
+    if (e != hipSuccess) return e;
+    g.rates = rates;
+  }
   if (p.persist) {
 #define LRS_GLR_P(IO, NTF, RSTF)                                                              \
   hipLaunchKernelGGL((k_glr_fwd_persist<IO, 8, 8, 2, NTF, RSTF>), dim3((unsigned)p.ncb),      \
@@ -618,19 +754,22 @@ hipError_t launch_glr_fwd(const GlrArgs& g, int io, const ColPlan& p, int vec, u
   }
   const dim3 grid((unsigned)(p.ncb * p.ntb));
 #define LRS_GLR_F(IO, NTF, RSTF)                                                                \
-  hipLaunchKernelGGL((k_glr_fwd<IO, 8, sizeof(IO) == 2 ? 16 : 8, 2, NTF, RSTF>), grid,          \
-                     dim3(512), 0, stream, g, (int)p.ncb, (int)p.ntb, vec, status, tickets)
+  hipLaunchKernelGGL((k_glr_fwd<IO, VNW, sizeof(IO) == 2 ? VL : 8, 2, NTF, RSTF>), grid,          \
+                     dim3(VNW * 64), 0, stream, g, (int)p.ncb, (int)p.ntb, vec, status, tickets)
   LRS_GLR_PICK(LRS_GLR_F)
 #undef LRS_GLR_F
   return hipGetLastError();
 }
 
-hipError_t launch_glr_bwd(const GlrArgs& g, int io, const ColPlan& p, int vec, uint64_t* status,
-                          unsigned* tickets, double* acc, float* grad_bias_r, float* grad_bias_i,
-                          float* grad_decay, hipStream_t stream) {
+hipError_t launch_glr_bwd(GlrArgs& g, int io, const ColPlan& p, int vec, float* rates,
+                          uint64_t* status, unsigned* tickets, double* acc, float* grad_bias_r,
+                          float* grad_bias_i, float* grad_decay, hipStream_t stream) {
+  const hipError_t e0 = glr_prep(g, p, rates, status, tickets, stream);
+  if (e0 != hipSuccess) return e0;
+  g.rates = rates;
   const dim3 grid((unsigned)(p.ncb * p.ntb));
 #define LRS_GLR_B(IO, NTF, RSTF)                                                               \
-  hipLaunchKernelGGL((k_glr_bwd<IO, 16, 4, 2, NTF, RSTF>), grid, dim3(1024), 0, stream, g,       \
+  hipLaunchKernelGGL((k_glr_bwd<IO, VBNW, VBL, 2, NTF, RSTF>), grid, dim3(VBNW * 64), 0, stream, g,       \
                      (int)p.ncb, (int)p.ntb, vec, status, tickets)
   LRS_GLR_PICK(LRS_GLR_B)
 #undef LRS_GLR_B

@@ -248,15 +248,18 @@ struct GlrArgs {
   int64_t ld_grad;
   float* grad_h0;
   float* part;  // [3][ntb * B][D]: the tiles' sums for bias_r, bias_i and decay
+  const float* rates;  // [2][D]: k and dk of every feature (glr_rates), or null
 };
 // allow_persist = false: the look-back tile plan (workspace queries size for it).
 ColPlan plan_glr(int64_t C, int64_t T, int io, bool allow_persist = true);
 ColPlan plan_glr_bwd(int64_t C, int64_t T, int io);
-hipError_t launch_glr_fwd(const GlrArgs& g, int io, const ColPlan& p, int vec, uint64_t* status,
-                          unsigned* tickets, hipStream_t stream);
-hipError_t launch_glr_bwd(const GlrArgs& g, int io, const ColPlan& p, int vec, uint64_t* status,
-                          unsigned* tickets, double* acc, float* grad_bias_r, float* grad_bias_i,
-                          float* grad_decay, hipStream_t stream);
+// rates: [2][D] fp32 of workspace; status and tickets (reset here) null where the
+// plan needs no look-back.
+hipError_t launch_glr_fwd(GlrArgs& g, int io, const ColPlan& p, int vec, float* rates,
+                          uint64_t* status, unsigned* tickets, hipStream_t stream);
+hipError_t launch_glr_bwd(GlrArgs& g, int io, const ColPlan& p, int vec, float* rates,
+                          uint64_t* status, unsigned* tickets, double* acc, float* grad_bias_r,
+                          float* grad_bias_i, float* grad_decay, hipStream_t stream);
 hipError_t launch_glr_step(const GlrArgs& g, int io, const int32_t* slots, float* state, int64_t S,
                            hipStream_t stream);
 

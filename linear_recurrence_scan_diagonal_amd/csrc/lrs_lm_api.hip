@@ -54,8 +54,15 @@ bool glr_shape(int64_t T, int64_t B, int64_t D, int64_t* C, int64_t* N) {
   return shape_ok(B, D, T, C, N);
 }
 bool glr_step_fits(int64_t B, int64_t C, int64_t ld) {
-  int64_t row;
-  return C < ((int64_t)1 << 31) && mul_ok(B, ld, &row) && row < ((int64_t)1 << 31);
+  int64_t row;  // 32-bit byte offsets inside a time step
+  return C < ((int64_t)1 << 31) && mul_ok(B, ld, &row) && row < ((int64_t)1 << 30);
+}
+
+// Workspace of a plan with look-back: the rates of every feature, the status
+// words and the tickets.
+size_t glr_lookback_bytes(const lrs::ColPlan& p, int64_t D) {
+  const int64_t nst = lrs::col_status_words(p);
+  return nst > 0 ? lookback_bytes(nst, p.ncb) + align_up((size_t)(2 * D) * 4) : 0;
 }
 
 // Pitched extents inside int64 bytes.
@@ -79,7 +86,7 @@ size_t lrs_glr_workspace_bytes(int64_t T, int64_t B, int64_t D) {
   if (!glr_shape(T, B, D, &C, &N) || N == 0) return 0;
   // the fp32 tiles are the shorter ones
   const lrs::ColPlan p = lrs::plan_glr(C, T, LRS_F32, false);
-  return lookback_bytes(lrs::col_status_words(p), p.ncb);
+  return glr_lookback_bytes(p, D);
 }
 
 int lrs_glr_fwd(const void* z_r, const void* z_i, const void* x, int64_t ld, const float* bias_r,
@@ -110,17 +117,16 @@ int lrs_glr_fwd(const void* z_r, const void* z_i, const void* x, int64_t ld, con
   const lrs::ColPlan p = lrs::plan_glr(C, T, io_dtype);
   if (!glr_step_fits(B, C, ld) || !grid_ok(p.persist ? p.ncb : p.ncb * p.ntb, p.nw * 64))
     return LRS_ERR_UNSUPPORTED;
-  const int64_t nst = lrs::col_status_words(p);
-  const size_t need = lookback_bytes(nst, p.ncb);
+  const size_t need = glr_lookback_bytes(p, D);
   if (need && (!workspace || workspace_bytes < need)) return LRS_ERR_WORKSPACE;
   uint64_t* status = nullptr;
   unsigned* tickets = nullptr;
-  if (nst > 0) {
+  float* rates = nullptr;
+  if (need) {
     Carve cv(align_ptr(workspace));
-    status = cv.take<uint64_t>(nst);
+    status = cv.take<uint64_t>(lrs::col_status_words(p));
     tickets = cv.take<unsigned>(p.ncb);
-    const int rc = hip_status(lrs::launch_reset(status, nst, tickets, p.ncb, nullptr, 0, s));
-    if (rc != LRS_OK) return rc;
+    rates = cv.take<float>(2 * D);
   }
   const size_t rb = (size_t)p.cpt * es;
   const int vec = D % p.cpt == 0 && ld % p.cpt == 0 && aligned(z_r, rb) && aligned(z_i, rb) &&
@@ -142,12 +148,12 @@ int lrs_glr_fwd(const void* z_r, const void* z_i, const void* x, int64_t ld, con
   g.D = D;
   g.ld = ld;
   g.c = c;
-  return hip_status(lrs::launch_glr_fwd(g, io_dtype, p, vec, status, tickets, s));
+  return hip_status(lrs::launch_glr_fwd(g, io_dtype, p, vec, rates, status, tickets, s));
 }
 
 static size_t glr_bwd_ws(const lrs::ColPlan& p, int64_t B, int64_t D) {
   return kAlign + lookback_bytes(lrs::col_status_words(p), p.ncb) +
-         align_up((size_t)(3 * p.ntb * B * D) * 4) +
+         align_up((size_t)(3 * p.ntb * B * D) * 4) + align_up((size_t)(2 * D) * 4) +
          align_up((size_t)(2 * lrs::col_sum_blocks(p.ntb * B) * D) * 8);
 }
 
@@ -220,9 +226,8 @@ int lrs_glr_bwd(const void* z_r, const void* z_i, const void* x, int64_t ld, con
   if (nst > 0) {
     status = cv.take<uint64_t>(nst);
     tickets = cv.take<unsigned>(p.ncb);
-    const int rc = hip_status(lrs::launch_reset(status, nst, tickets, p.ncb, nullptr, 0, s));
-    if (rc != LRS_OK) return rc;
   }
+  float* rates = cv.take<float>(2 * D);
   const size_t rb = (size_t)p.cpt * es;
   int vec = D % p.cpt == 0 && ld % p.cpt == 0 && ld_grad % p.cpt == 0;
   for (const void* q : io) vec = vec && aligned(q, rb);
@@ -246,8 +251,8 @@ int lrs_glr_bwd(const void* z_r, const void* z_i, const void* x, int64_t ld, con
   g.grad_x = grad_x;
   g.ld_grad = ld_grad;
   g.grad_h0 = grad_h0;
-  return hip_status(lrs::launch_glr_bwd(g, io_dtype, p, vec, status, tickets, acc, grad_bias_r,
-                                        grad_bias_i, grad_decay, s));
+  return hip_status(lrs::launch_glr_bwd(g, io_dtype, p, vec, rates, status, tickets, acc,
+                                        grad_bias_r, grad_bias_i, grad_decay, s));
 }
 
 int lrs_glr_step(const void* z_r, const void* z_i, const void* x, int64_t ld, const float* bias_r,
