@@ -28,23 +28,7 @@ namespace {
 // Time tiles of a look-back group.  The end states of the groups form a chain,
 // about 1.2 us a link: with 16 tiles a group instead of the other layers' 8 a
 // prompt of 16384 steps has 8 links of 128 x 16 steps (bf16).
-#ifndef VG
-#define VG 16
-#endif
-#ifndef VL
-#define VL 16
-#endif
-#ifndef VNW
-#define VNW 8
-#endif
-#ifndef VBNW
-#define VBNW 8
-#define VBL 8
-#endif
-#ifndef VOCC
-#define VOCC 1
-#endif
-constexpr int kGlrGroup = VG;
+constexpr int kGlrGroup = 16;
 
 // One row of a strided array: the lane's channels at byte offsets zo from a
 // wave-uniform pointer (32 bits: no address arithmetic a row); FULL: all in one
@@ -480,6 +464,159 @@ __device__ __forceinline__ void glr_gates(const GlrArgs& g, const GlrChan<CPT>& 
   }
 }
 
+// A wave's rows of one tile: the packed inputs and what the gates make of them.
+template <typename IO, int L, int CPT>
+struct GlrBwdRows {
+  GlrRows<IO, L, CPT> in;
+  IoRow<IO, CPT> gh[L];
+};
+
+template <typename IO, int L, int CPT, bool FULL, bool NT, bool RST>
+__device__ __forceinline__ void glr_bwd_load(const GlrArgs& g, const GlrChan<CPT>& ch, int64_t row0,
+                                             int64_t cbase, uint32_t off, int nvc,
+                                             GlrBwdRows<IO, L, CPT>& w) {
+  const int64_t C = g.B * g.D;
+  glr_load<IO, L, CPT, FULL, NT, RST>(g, ch, row0, nvc, w.in);
+  const IO* gp = (const IO*)g.grad_h + row0 * C + cbase;
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    w.gh[i].template load<FULL, NT>(at(gp, off * (uint32_t)sizeof(IO)), 0,
+                                    (FULL || row0 + i < g.T) ? nvc : 0);
+    gp += C;
+  }
+}
+
+// The wave's maps of both chains: forward (FA, FB) for the states, reverse (A, B)
+// for y.
+template <int L, int CPT, bool RST, typename IO>
+__device__ __forceinline__ void glr_bwd_fold(const IoRow<IO, CPT> (&x)[L],
+                                             const IoRow<IO, CPT> (&gh)[L],
+                                             const float (&gi)[L][CPT], const float (&av)[L][CPT],
+                                             const float (&m)[L][CPT], float (&FA)[CPT],
+                                             float (&FB)[CPT], float (&A)[CPT], float (&B)[CPT]) {
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const float b = m[i][k] * gi[i][k] * x[i].get(k);  // 0 past the end (x reads as 0 there)
+      FB[k] = i == 0 ? b : step<RST>(av[i][k], FB[k], b);
+      FA[k] = i == 0 ? av[i][k] : FA[k] * av[i][k];
+    }
+    // y passed on: lam_{L-1} = gh_{L-1} + y_in, lam_i = gh_i + a_{i+1} lam_{i+1},
+    // y_out = a_0 lam_0 (gh and a are 0 and 1 past the end)
+    A[k] = 1.0f;
+    B[k] = gh[L - 1].get(k);
+#pragma unroll
+    for (int i = L - 2; i >= 0; --i) {
+      B[k] = step<RST>(av[i + 1][k], B[k], gh[i].get(k));
+      A[k] = A[k] * av[i + 1][k];
+    }
+    A[k] = A[k] * av[0][k];
+    B[k] = scale<RST>(av[0][k], B[k]);
+  }
+}
+
+// x and grad_h stay packed across the barriers: unpacked copies kept by the
+// compiler would cost registers that the waves of a compute unit do not have.
+template <int L, int CPT>
+__device__ __forceinline__ void keep_packed(IoRow<uint16_t, CPT> (&x)[L],
+                                            IoRow<uint16_t, CPT> (&gh)[L]) {
+#pragma unroll
+  for (int i = 0; i < L; ++i)
+#pragma unroll
+    for (int k = 0; k < CPT / 2; ++k) asm("" : "+v"(x[i].w[k]), "+v"(gh[i].w[k]));
+}
+template <int L, int CPT>
+__device__ __forceinline__ void keep_packed(IoRow<float, CPT> (&)[L], IoRow<float, CPT> (&)[L]) {}
+
+template <int CPT>
+struct GlrSums {
+  float r[CPT], i[CPT], d[CPT];  // for bias_r, bias_i and k
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) r[k] = i[k] = d[k] = 0.0f;
+  }
+};
+
+// The wave's rows from the state hs before them and y after them: the gradients,
+// and y before them.
+template <typename IO, int L, int CPT, bool FULL, bool NT, bool RST>
+__device__ __forceinline__ void glr_bwd_walk(const GlrArgs& g, const GlrChan<CPT>& ch,
+                                             const uint32_t (&go)[CPT], int64_t row0, int nvc,
+                                             const IoRow<IO, CPT> (&x)[L],
+                                             const IoRow<IO, CPT> (&gh)[L],
+                                             const float (&r)[L][CPT], const float (&gi)[L][CPT],
+                                             const float (&av)[L][CPT], const float (&m)[L][CPT],
+                                             float (&hs)[CPT], float (&y)[CPT],
+                                             GlrSums<CPT>& sum) {
+  float hp[L][CPT];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) {
+      hp[i][k] = hs[k];
+      hs[k] = step<RST>(av[i][k], hs[k], m[i][k] * gi[i][k] * x[i].get(k));
+    }
+  }
+  const int64_t gpitch = g.B * g.ld_grad;
+  IO* qr = (IO*)g.grad_zr + (row0 + L - 1) * gpitch;
+  IO* qi = (IO*)g.grad_zi + (row0 + L - 1) * gpitch;
+  IO* qx = (IO*)g.grad_x + (row0 + L - 1) * gpitch;
+#pragma unroll
+  for (int i = L - 1; i >= 0; --i) {
+    float dr[CPT], di[CPT], dx[CPT];
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) {
+      y[k] = i == L - 1 ? y[k] + gh[i].get(k) : step<RST>(av[i + 1][k], y[k], gh[i].get(k));  // lam_t
+      const float u = gi[i][k] * x[i].get(k), a = av[i][k], mm = m[i][k], lam = y[k];
+      const float dgx = lam * mm;
+      dx[k] = dgx * gi[i][k];
+      di[k] = dgx * u * (1.0f - gi[i][k]);
+      const float rm = __builtin_amdgcn_rcpf(fmaxf(mm, 1e-30f));  // m = 0: with r = 0 below
+      const float dla = scale<RST>(a, lam * __builtin_fmaf(-a * rm, u, hp[i][k]));
+      const float dlr = dla * r[i][k];
+      dr[k] = -dlr * ch.k[k] * (1.0f - r[i][k]);  // la = -k r
+      sum.r[k] += dr[k];
+      sum.i[k] += di[k];
+      sum.d[k] += dlr;
+    }
+    const int nv = (FULL || row0 + i < g.T) ? nvc : 0;
+    glr_st<CPT, FULL, NT>(qr, go, nv, dr);
+    glr_st<CPT, FULL, NT>(qi, go, nv, di);
+    glr_st<CPT, FULL, NT>(qx, go, nv, dx);
+    qr -= gpitch;
+    qi -= gpitch;
+    qx -= gpitch;
+  }
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) y[k] = scale<RST>(av[0][k], y[k]);
+}
+
+// The waves' sums of a workgroup, added in wave order, to row `slot` of the
+// partial sums' `slots` rows.
+template <int NW, int CPT>
+__device__ __forceinline__ void glr_bwd_sums(const GlrArgs& g, const GlrChan<CPT>& ch,
+                                             const GlrSums<CPT>& sum,
+                                             float (&red)[3][NW][kWave * CPT], int wid, uint32_t off,
+                                             int64_t cbase, int64_t slot, int64_t slots) {
+  constexpr int CW = kWave * CPT;
+  const int64_t C = g.B * g.D;
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) {
+    red[0][wid][off + k] = sum.r[k];
+    red[1][wid][off + k] = sum.i[k];
+    red[2][wid][off + k] = sum.d[k] * g.rates[g.D + ch.d[k]];  // with d k / d decay
+  }
+  __syncthreads();
+  for (int j = threadIdx.x; j < 3 * CW; j += NW * kWave) {
+    const int which = j / CW, c = j % CW;
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) t += red[which][w][c];
+    if (cbase + c < C) g.part[((int64_t)which * slots + slot) * C + cbase + c] = t;
+  }
+}
+
 template <typename IO, int NW, int L, int CPT, bool FULL, bool NT, bool RST>
 __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, int cb, bool multi,
                                              uint64_t* st, ColShared<NW, CPT>& s,
@@ -496,138 +633,47 @@ __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, 
   const int64_t row0 = (int64_t)ptb * (NW * L) + (int64_t)(NW - 1 - wid) * L;
   GlrChan<CPT> ch;
   ch.set(g, cbase, off, nvc, sizeof(IO));
-  GlrRows<IO, L, CPT> rows;
-  glr_load<IO, L, CPT, FULL, NT, RST>(g, ch, row0, nvc, rows);
-  IoRow<IO, CPT> gh[L];
-  {
-    const IO* gp = (const IO*)g.grad_h + row0 * C + cbase;
-#pragma unroll
-    for (int i = 0; i < L; ++i) {
-      gh[i].template load<FULL, NT>(at(gp, off * (uint32_t)sizeof(IO)), 0,
-                                    (FULL || row0 + i < g.T) ? nvc : 0);
-      gp += C;
-    }
-  }
+  GlrBwdRows<IO, L, CPT> w;
+  glr_bwd_load<IO, L, CPT, FULL, NT, RST>(g, ch, row0, cbase, off, nvc, w);
   float r[L][CPT], gi[L][CPT], av[L][CPT], m[L][CPT];
   float FA[CPT], FB[CPT], A[CPT], B[CPT];
-  if (ch.near) glr_gates<true, IO, L, CPT, FULL>(g, ch, row0, nvc, rows, r, gi, av, m);
-  else glr_gates<false, IO, L, CPT, FULL>(g, ch, row0, nvc, rows, r, gi, av, m);
-#pragma unroll
-  for (int i = 0; i < L; ++i) {
-#pragma unroll
-    for (int k = 0; k < CPT; ++k) {
-      const float b = m[i][k] * gi[i][k] * rows.x[i].get(k);  // 0 past the end (x reads as 0 there)
-      FB[k] = i == 0 ? b : step<RST>(av[i][k], FB[k], b);
-      FA[k] = i == 0 ? av[i][k] : FA[k] * av[i][k];
-    }
-  }
+  if (ch.near) glr_gates<true, IO, L, CPT, FULL>(g, ch, row0, nvc, w.in, r, gi, av, m);
+  else glr_gates<false, IO, L, CPT, FULL>(g, ch, row0, nvc, w.in, r, gi, av, m);
+  glr_bwd_fold<L, CPT, RST>(w.in.x, w.gh, gi, av, m, FA, FB, A, B);
+  float x0[CPT], y[CPT], hs[CPT];
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
     f.fA[wid][off + k] = FA[k];
     f.fB[wid][off + k] = FB[k];
-    // y passed on: lam_{L-1} = gh_{L-1} + y_in, lam_i = gh_i + a_{i+1} lam_{i+1},
-    // y_out = a_0 lam_0 (gh and a are 0 and 1 past the end)
-    A[k] = 1.0f;
-    B[k] = gh[L - 1].get(k);
-#pragma unroll
-    for (int i = L - 2; i >= 0; --i) {
-      B[k] = step<RST>(av[i + 1][k], B[k], gh[i].get(k));
-      A[k] = A[k] * av[i + 1][k];
-    }
-    A[k] = A[k] * av[0][k];
-    B[k] = scale<RST>(av[0][k], B[k]);
-  }
-  float x0[CPT], y[CPT], hs[CPT];
-#pragma unroll
-  for (int k = 0; k < CPT; ++k) {
     x0[k] = (g.grad_h_last && k < nvc) ? g.grad_h_last[c0 + k] : 0.0f;
     hs[k] = k < nvc ? g.checkpoints[(int64_t)ptb * C + c0 + k] : 0.0f;
   }
   col_enter_state<NW, CPT, RST>(A, B, multi, tb, x0, g.grad_h_last, cbase,
                                 clamp_valid(C - cbase, CW), st, s, y);
-  // x and grad_h stay packed across the barriers: unpacked copies kept by the
-  // compiler would cost half the waves a compute unit can hold
-  if constexpr (sizeof(IO) == 2) {
-#pragma unroll
-    for (int i = 0; i < L; ++i)
-#pragma unroll
-      for (int k = 0; k < CPT / 2; ++k)
-        asm("" : "+v"(rows.x[i].w[k]), "+v"(gh[i].w[k]));
-  }
+  keep_packed<L, CPT>(w.in.x, w.gh);
   // past a barrier: the states before each of the wave's rows
-  for (int w = NW - 1; w > wid; --w) {
+  for (int v = NW - 1; v > wid; --v) {
 #pragma unroll
-    for (int k = 0; k < CPT; ++k) hs[k] = affine<RST>(f.fA[w][off + k], hs[k], f.fB[w][off + k]);
-  }
-  float hp[L][CPT];
-#pragma unroll
-  for (int i = 0; i < L; ++i) {
-#pragma unroll
-    for (int k = 0; k < CPT; ++k) {
-      hp[i][k] = hs[k];
-      hs[k] = step<RST>(av[i][k], hs[k], m[i][k] * gi[i][k] * rows.x[i].get(k));
-    }
+    for (int k = 0; k < CPT; ++k) hs[k] = affine<RST>(f.fA[v][off + k], hs[k], f.fB[v][off + k]);
   }
   uint32_t go[CPT];
 #pragma unroll
-  for (int k = 0; k < CPT; ++k) go[k] = (ch.b[k] * (uint32_t)g.ld_grad + ch.d[k]) * (uint32_t)sizeof(IO);
-  const int64_t gpitch = g.B * g.ld_grad;
-  IO* qr = (IO*)g.grad_zr + (row0 + L - 1) * gpitch;
-  IO* qi = (IO*)g.grad_zi + (row0 + L - 1) * gpitch;
-  IO* qx = (IO*)g.grad_x + (row0 + L - 1) * gpitch;
-  float sr[CPT], si[CPT], sd[CPT];
-#pragma unroll
-  for (int k = 0; k < CPT; ++k) sr[k] = si[k] = sd[k] = 0.0f;
-#pragma unroll
-  for (int i = L - 1; i >= 0; --i) {
-    float dr[CPT], di[CPT], dx[CPT];
-#pragma unroll
-    for (int k = 0; k < CPT; ++k) {
-      y[k] = i == L - 1 ? y[k] + gh[i].get(k) : step<RST>(av[i + 1][k], y[k], gh[i].get(k));  // lam_t
-      const float u = gi[i][k] * rows.x[i].get(k), a = av[i][k], mm = m[i][k], lam = y[k];
-      const float dgx = lam * mm;
-      dx[k] = dgx * gi[i][k];
-      di[k] = dgx * u * (1.0f - gi[i][k]);
-      const float rm = __builtin_amdgcn_rcpf(fmaxf(mm, 1e-30f));  // m = 0: with r = 0 below
-      const float dla = scale<RST>(a, lam * __builtin_fmaf(-a * rm, u, hp[i][k]));
-      const float dlr = dla * r[i][k];
-      dr[k] = -dlr * ch.k[k] * (1.0f - r[i][k]);  // la = -k r
-      sr[k] += dr[k];
-      si[k] += di[k];
-      sd[k] += dlr;
-    }
-    const int nv = (FULL || row0 + i < g.T) ? nvc : 0;
-    glr_st<CPT, FULL, NT>(qr, go, nv, dr);
-    glr_st<CPT, FULL, NT>(qi, go, nv, di);
-    glr_st<CPT, FULL, NT>(qx, go, nv, dx);
-    qr -= gpitch;
-    qi -= gpitch;
-    qx -= gpitch;
-  }
+  for (int k = 0; k < CPT; ++k)
+    go[k] = (ch.b[k] * (uint32_t)g.ld_grad + ch.d[k]) * (uint32_t)sizeof(IO);
+  GlrSums<CPT> sum;
+  sum.clear();
+  glr_bwd_walk<IO, L, CPT, FULL, NT, RST>(g, ch, go, row0, nvc, w.in.x, w.gh, r, gi, av, m, hs, y,
+                                          sum);
   if (g.grad_h0 && row0 == 0) {
 #pragma unroll
     for (int k = 0; k < CPT; ++k)
-      if (k < nvc) g.grad_h0[c0 + k] = scale<RST>(av[0][k], y[k]);
+      if (k < nvc) g.grad_h0[c0 + k] = y[k];
   }
-#pragma unroll
-  for (int k = 0; k < CPT; ++k) {
-    f.red[0][wid][off + k] = sr[k];
-    f.red[1][wid][off + k] = si[k];
-    // with d k / d decay
-    f.red[2][wid][off + k] = sd[k] * g.rates[g.D + ch.d[k]];
-  }
-  __syncthreads();
-  for (int j = threadIdx.x; j < 3 * CW; j += NW * kWave) {
-    const int which = j / CW, c = j % CW;
-    float t = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) t += f.red[which][w][c];
-    if (cbase + c < C) g.part[((int64_t)which * ntb + ptb) * C + cbase + c] = t;
-  }
+  glr_bwd_sums<NW, CPT>(g, ch, sum, f.red, wid, off, cbase, ptb, ntb);
 }
 
 template <typename IO, int NW, int L, int CPT, bool NT, bool RST>
-__global__ __launch_bounds__(NW* kWave, VOCC) void k_glr_bwd(GlrArgs g, int ncb, int ntb, int vec,
+__global__ __launch_bounds__(NW* kWave) void k_glr_bwd(GlrArgs g, int ncb, int ntb, int vec,
                                                        uint64_t* __restrict__ status,
                                                        unsigned* __restrict__ tickets) {
   constexpr int CW = kWave * CPT, TW = NW * L;
@@ -644,6 +690,119 @@ __global__ __launch_bounds__(NW* kWave, VOCC) void k_glr_bwd(GlrArgs g, int ncb,
     glr_bwd_tile<IO, NW, L, CPT, true, NT, RST>(g, tb, ntb, cb, multi, st, s, f);
   else
     glr_bwd_tile<IO, NW, L, CPT, false, NT, RST>(g, tb, ntb, cb, multi, st, s, f);
+}
+
+// ---------------------------------------------------------------------------
+// persistent backward: one workgroup per channel block walks the tiles from the
+// last to the first, y in LDS, the next tile's rows and checkpoint in flight
+// while the current one is processed, the parameters' sums in registers until
+// the end.  As the forward, where the channel blocks alone fill the GPU: a tile's
+// rows and gates take 170 registers, so that a compute unit holds one workgroup
+// either way, and without the prefetch its loads and its arithmetic take turns.
+// ---------------------------------------------------------------------------
+template <int NW, int CPT>
+struct GlrWalkShared {
+  PersistShared<NW, CPT> y;
+  float fA[2][NW][kWave * CPT], fB[2][NW][kWave * CPT];
+};
+
+template <typename IO, int NW, int L, int CPT, bool FULL, int PF, bool NT, bool RST>
+__device__ __forceinline__ void glr_bwd_persist_tile(
+    const GlrArgs& g, const GlrChan<CPT>& ch, const uint32_t (&go)[CPT], int64_t row0, int64_t cbase,
+    uint32_t off, int nvc, GlrBwdRows<IO, L, CPT>& w, float (&ck)[CPT], GlrSums<CPT>& sum,
+    GlrWalkShared<NW, CPT>& s, int wid, int par) {
+  float r[L][CPT], gi[L][CPT], av[L][CPT], m[L][CPT];
+  float FA[CPT], FB[CPT], A[CPT], B[CPT], y[CPT], hs[CPT];
+  if (ch.near) glr_gates<true, IO, L, CPT, FULL>(g, ch, row0, nvc, w.in, r, gi, av, m);
+  else glr_gates<false, IO, L, CPT, FULL>(g, ch, row0, nvc, w.in, r, gi, av, m);
+  IoRow<IO, CPT> x[L], gh[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    x[i] = w.in.x[i];
+    gh[i] = w.gh[i];
+  }
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) hs[k] = ck[k];
+  if (PF != 0) {  // the tile before this one: whole rows
+    glr_bwd_load<IO, L, CPT, PF == 1, NT, RST>(g, ch, row0 - NW * L, cbase, off, nvc, w);
+    const float* p = g.checkpoints + (row0 / kGlrRows - 1) * (g.B * g.D) + cbase + off;
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) ck[k] = k < nvc ? p[k] : 0.0f;
+  }
+  glr_bwd_fold<L, CPT, RST>(x, gh, gi, av, m, FA, FB, A, B);
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) {
+    s.fA[par][wid][off + k] = FA[k];
+    s.fB[par][wid][off + k] = FB[k];
+  }
+  persist_enter<NW, CPT, RST>(A, B, s.y, wid, off, y, par);  // its barrier covers fA and fB
+  keep_packed<L, CPT>(x, gh);
+  for (int v = NW - 1; v > wid; --v) {
+#pragma unroll
+    for (int k = 0; k < CPT; ++k)
+      hs[k] = affine<RST>(s.fA[par][v][off + k], hs[k], s.fB[par][v][off + k]);
+  }
+  glr_bwd_walk<IO, L, CPT, FULL, NT, RST>(g, ch, go, row0, nvc, x, gh, r, gi, av, m, hs, y, sum);
+  persist_advance<NW, CPT>(y, s.y, wid, off, par);
+}
+
+template <typename IO, int NW, int L, int CPT, bool NT, bool RST>
+__global__ __launch_bounds__(NW* kWave) void k_glr_bwd_persist(GlrArgs g, int vec) {
+  constexpr int CW = kWave * CPT, TW = NW * L;
+  static_assert(TW == kGlrRows, "a tile is a checkpoint's stretch");
+  __shared__ GlrWalkShared<NW, CPT> s;
+  __shared__ float red[3][NW][CW];
+  const int64_t C = g.B * g.D;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t cbase = (int64_t)blockIdx.x * CW;
+  const uint32_t off = (uint32_t)(lane * CPT);
+  const int nvc = clamp_valid(C - (cbase + off), CPT);
+  const bool cfull = vec && cbase + CW <= C;
+  for (int j = threadIdx.x; j < CW; j += NW * kWave)
+    s.y.carry[0][j] = (g.grad_h_last && cbase + j < C) ? g.grad_h_last[cbase + j] : 0.0f;
+  GlrChan<CPT> ch;
+  ch.set(g, cbase, off, nvc, sizeof(IO));
+  uint32_t go[CPT];
+#pragma unroll
+  for (int k = 0; k < CPT; ++k)
+    go[k] = (ch.b[k] * (uint32_t)g.ld_grad + ch.d[k]) * (uint32_t)sizeof(IO);
+  const int64_t ntb = (g.T + TW - 1) / TW;
+  const int64_t w0 = (int64_t)(NW - 1 - wid) * L;
+  GlrSums<CPT> sum;
+  sum.clear();
+  GlrBwdRows<IO, L, CPT> w;
+  float ck[CPT];
+#pragma unroll
+  for (int k = 0; k < CPT; ++k)
+    ck[k] = k < nvc ? g.checkpoints[(ntb - 1) * C + cbase + off + k] : 0.0f;
+  // tile tb of the walk is the physical one ntb - 1 - tb; the first may be ragged
+#define LRS_TILE(FULLT, PFT, TB)                                                               \
+  glr_bwd_persist_tile<IO, NW, L, CPT, FULLT, PFT, NT, RST>(g, ch, go, (ntb - 1 - (TB)) * TW + w0, \
+                                                            cbase, off, nvc, w, ck, sum, s, wid, \
+                                                            (int)((TB) & 1))
+  int64_t tb = 0;
+  if (cfull) {
+    if (g.T % TW) {
+      glr_bwd_load<IO, L, CPT, false, NT, RST>(g, ch, (ntb - 1) * TW + w0, cbase, off, nvc, w);
+      if (ntb > 1) LRS_TILE(false, 1, 0);
+      else LRS_TILE(false, 0, 0);
+      tb = 1;
+    } else {
+      glr_bwd_load<IO, L, CPT, true, NT, RST>(g, ch, (ntb - 1) * TW + w0, cbase, off, nvc, w);
+    }
+    for (; tb + 1 < ntb; ++tb) LRS_TILE(true, 1, tb);
+    if (tb < ntb) LRS_TILE(true, 0, tb);
+  } else {
+    glr_bwd_load<IO, L, CPT, false, NT, RST>(g, ch, (ntb - 1) * TW + w0, cbase, off, nvc, w);
+    for (; tb + 1 < ntb; ++tb) LRS_TILE(false, 2, tb);
+    LRS_TILE(false, 0, tb);
+  }
+#undef LRS_TILE
+  glr_bwd_sums<NW, CPT>(g, ch, sum, red, wid, off, cbase, 0, 1);
+  if (g.grad_h0)  // past a barrier
+    for (int j = threadIdx.x; j < CW; j += NW * kWave)
+      if (cbase + j < C) g.grad_h0[cbase + j] = s.y.carry[ntb & 1][j];
 }
 
 // Before the tiles of a call: k and dk of every feature, and the look-back state
@@ -690,7 +849,7 @@ __global__ __launch_bounds__(256) void k_glr_step(GlrArgs g, const int32_t* __re
 // host side
 // ---------------------------------------------------------------------------
 ColPlan plan_glr(int64_t C, int64_t T, int io, bool allow_persist) {
-  ColPlan p = plan_cols(C, T, VNW, io == kIoBf16 ? VL : 8, 2);
+  ColPlan p = plan_cols(C, T, 8, io == kIoBf16 ? 16 : 8, 2);
   if (allow_persist && p.ncb >= persist_min_blocks()) {
     p = plan_cols(C, T, 8, 8, 2);
     p.persist = true;
@@ -699,8 +858,9 @@ ColPlan plan_glr(int64_t C, int64_t T, int io, bool allow_persist) {
   return p;
 }
 
-ColPlan plan_glr_bwd(int64_t C, int64_t T, int io) {
-  ColPlan p = plan_cols(C, T, VBNW, VBL, 2);
+ColPlan plan_glr_bwd(int64_t C, int64_t T, int io, bool allow_persist) {
+  ColPlan p = plan_cols(C, T, 8, 8, 2);
+  p.persist = allow_persist && p.ncb >= persist_min_blocks();
   p.stream = C * T * 7 * io_bytes(io) >= kStreamFootprint;
   return p;
 }
@@ -754,8 +914,8 @@ hipError_t launch_glr_fwd(GlrArgs& g, int io, const ColPlan& p, int vec, float* 
   }
   const dim3 grid((unsigned)(p.ncb * p.ntb));
 #define LRS_GLR_F(IO, NTF, RSTF)                                                                \
-  hipLaunchKernelGGL((k_glr_fwd<IO, VNW, sizeof(IO) == 2 ? VL : 8, 2, NTF, RSTF>), grid,          \
-                     dim3(VNW * 64), 0, stream, g, (int)p.ncb, (int)p.ntb, vec, status, tickets)
+  hipLaunchKernelGGL((k_glr_fwd<IO, 8, sizeof(IO) == 2 ? 16 : 8, 2, NTF, RSTF>), grid,             \
+                     dim3(512), 0, stream, g, (int)p.ncb, (int)p.ntb, vec, status, tickets)
   LRS_GLR_PICK(LRS_GLR_F)
 #undef LRS_GLR_F
   return hipGetLastError();
@@ -767,16 +927,24 @@ hipError_t launch_glr_bwd(GlrArgs& g, int io, const ColPlan& p, int vec, float* 
   const hipError_t e0 = glr_prep(g, p, rates, status, tickets, stream);
   if (e0 != hipSuccess) return e0;
   g.rates = rates;
-  const dim3 grid((unsigned)(p.ncb * p.ntb));
-#define LRS_GLR_B(IO, NTF, RSTF)                                                               \
-  hipLaunchKernelGGL((k_glr_bwd<IO, VBNW, VBL, 2, NTF, RSTF>), grid, dim3(VBNW * 64), 0, stream, g,       \
+  if (p.persist) {
+#define LRS_GLR_Q(IO, NTF, RSTF)                                                               \
+  hipLaunchKernelGGL((k_glr_bwd_persist<IO, 8, 8, 2, NTF, RSTF>), dim3((unsigned)p.ncb),       \
+                     dim3(512), 0, stream, g, vec)
+    LRS_GLR_PICK(LRS_GLR_Q)
+#undef LRS_GLR_Q
+  } else {
+    const dim3 grid((unsigned)(p.ncb * p.ntb));
+#define LRS_GLR_B(IO, NTF, RSTF)                                                              \
+  hipLaunchKernelGGL((k_glr_bwd<IO, 8, 8, 2, NTF, RSTF>), grid, dim3(512), 0, stream, g,      \
                      (int)p.ncb, (int)p.ntb, vec, status, tickets)
-  LRS_GLR_PICK(LRS_GLR_B)
+    LRS_GLR_PICK(LRS_GLR_B)
 #undef LRS_GLR_B
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   float* const outs[3] = {grad_bias_r, grad_bias_i, grad_decay};
-  return launch_param_sums(g.part, 3, p.ntb * g.B, g.D, acc, outs, stream);
+  return launch_param_sums(g.part, 3, (p.persist ? 1 : p.ntb) * g.B, g.D, acc, outs, stream);
 }
 
 hipError_t launch_glr_step(const GlrArgs& g, int io, const int32_t* slots, float* state, int64_t S,

@@ -252,7 +252,7 @@ struct GlrArgs {
 };
 // allow_persist = false: the look-back tile plan (workspace queries size for it).
 ColPlan plan_glr(int64_t C, int64_t T, int io, bool allow_persist = true);
-ColPlan plan_glr_bwd(int64_t C, int64_t T, int io);
+ColPlan plan_glr_bwd(int64_t C, int64_t T, int io, bool allow_persist = true);
 // rates: [2][D] fp32 of workspace; status and tickets (reset here) null where the
 // plan needs no look-back.
 hipError_t launch_glr_fwd(GlrArgs& g, int io, const ColPlan& p, int vec, float* rates,

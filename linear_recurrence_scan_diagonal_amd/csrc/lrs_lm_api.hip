@@ -160,7 +160,7 @@ static size_t glr_bwd_ws(const lrs::ColPlan& p, int64_t B, int64_t D) {
 size_t lrs_glr_bwd_workspace_bytes(int64_t T, int64_t B, int64_t D) {
   int64_t C, N;
   if (!glr_shape(T, B, D, &C, &N) || N == 0) return 0;
-  return glr_bwd_ws(lrs::plan_glr_bwd(C, T, LRS_F32), B, D);
+  return glr_bwd_ws(lrs::plan_glr_bwd(C, T, LRS_F32, false), B, D);
 }
 
 int lrs_glr_bwd(const void* z_r, const void* z_i, const void* x, int64_t ld, const float* bias_r,
@@ -212,7 +212,7 @@ int lrs_glr_bwd(const void* z_r, const void* z_i, const void* x, int64_t ld, con
   }
   const lrs::ColPlan p = lrs::plan_glr_bwd(C, T, io_dtype);
   if (!glr_step_fits(B, C, ld) || !glr_step_fits(B, C, ld_grad) ||
-      !grid_ok(p.ncb * p.ntb, p.nw * 64))
+      !grid_ok(p.persist ? p.ncb : p.ncb * p.ntb, p.nw * 64))
     return LRS_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < lrs_glr_bwd_workspace_bytes(T, B, D))
     return LRS_ERR_WORKSPACE;
