@@ -13,7 +13,9 @@
 // rather than multiply it: a NaN or an infinity of one document stays there.
 //
 // Inputs are rows of a wider projection (pitch ld): a lane's channels are at
-// b * ld + d of a row, computed once a thread.
+// b * ld + d of a row, computed once a thread.  A lane has two channels, read as
+// one pair (the caller has seen to it that pairs are aligned and do not cross
+// two sequences), or one.
 //
 // The backward pass reads no h: the forward leaves the states that enter each
 // tile of kGlrRows steps (4 / 64 of a byte an element and byte of state), and
@@ -46,6 +48,8 @@ __device__ __forceinline__ void glr_ld(const uint16_t* p, const uint32_t (&zo)[C
                                        IoRow<uint16_t, CPT>& r) {
   if constexpr (FULL) {
     r.template load<true, NT>(at(p, zo[0]), 0, CPT);
+  } else if constexpr (CPT == 1) {
+    r.w = nv > 0 ? *at(p, zo[0]) : 0u;
   } else {
 #pragma unroll
     for (int k = 0; k < CPT / 2; ++k) {
@@ -341,7 +345,7 @@ __device__ __forceinline__ void glr_tile(const GlrArgs& g, int tb, int cb, bool 
 }
 
 template <typename IO, int NW, int L, int CPT, bool NT, bool RST>
-__global__ __launch_bounds__(NW* kWave) void k_glr_fwd(GlrArgs g, int ncb, int ntb, int vec,
+__global__ __launch_bounds__(NW* kWave) void k_glr_fwd(GlrArgs g, int ncb, int ntb,
                                                        uint64_t* __restrict__ status,
                                                        unsigned* __restrict__ tickets) {
   constexpr int CW = kWave * CPT, TW = NW * L;
@@ -351,7 +355,7 @@ __global__ __launch_bounds__(NW* kWave) void k_glr_fwd(GlrArgs g, int ncb, int n
   const int cb = (int)(blockIdx.x % (unsigned)ncb);
   const int tb = col_ticket<NW, CPT>(multi, tickets, cb, s);
   uint64_t* st = status + (int64_t)cb * ntb * CW;
-  const bool full = vec && (int64_t)(tb + 1) * TW <= g.T && (int64_t)(cb + 1) * CW <= g.B * g.D;
+  const bool full = (int64_t)(tb + 1) * TW <= g.T && (int64_t)(cb + 1) * CW <= g.B * g.D;
   if (full)
     glr_tile<IO, NW, L, CPT, true, NT, RST>(g, tb, cb, multi, st, s);
   else
@@ -381,7 +385,7 @@ __device__ __forceinline__ void glr_persist_tile(const GlrArgs& g, const GlrChan
 }
 
 template <typename IO, int NW, int L, int CPT, bool NT, bool RST>
-__global__ __launch_bounds__(NW* kWave) void k_glr_fwd_persist(GlrArgs g, int vec) {
+__global__ __launch_bounds__(NW* kWave) void k_glr_fwd_persist(GlrArgs g) {
   constexpr int CW = kWave * CPT, TW = NW * L;
   __shared__ PersistShared<NW, CPT> s;
   const int64_t C = g.B * g.D;
@@ -390,7 +394,7 @@ __global__ __launch_bounds__(NW* kWave) void k_glr_fwd_persist(GlrArgs g, int ve
   const int64_t cbase = (int64_t)blockIdx.x * CW;
   const uint32_t off = (uint32_t)(lane * CPT);
   const int nvc = clamp_valid(C - (cbase + off), CPT);
-  const bool cfull = vec && cbase + CW <= C;
+  const bool cfull = cbase + CW <= C;
   for (int j = threadIdx.x; j < CW; j += NW * kWave)
     s.carry[0][j] = (g.h0 && cbase + j < C) ? g.h0[cbase + j] : 0.0f;
   GlrChan<CPT> ch;
@@ -526,6 +530,11 @@ __device__ __forceinline__ void keep_packed(IoRow<uint16_t, CPT> (&x)[L],
 #pragma unroll
     for (int k = 0; k < CPT / 2; ++k) asm("" : "+v"(x[i].w[k]), "+v"(gh[i].w[k]));
 }
+template <int L>
+__device__ __forceinline__ void keep_packed(IoRow<uint16_t, 1> (&x)[L], IoRow<uint16_t, 1> (&gh)[L]) {
+#pragma unroll
+  for (int i = 0; i < L; ++i) asm("" : "+v"(x[i].w), "+v"(gh[i].w));
+}
 template <int L, int CPT>
 __device__ __forceinline__ void keep_packed(IoRow<float, CPT> (&)[L], IoRow<float, CPT> (&)[L]) {}
 
@@ -650,7 +659,7 @@ __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, 
   }
   col_enter_state<NW, CPT, RST>(A, B, multi, tb, x0, g.grad_h_last, cbase,
                                 clamp_valid(C - cbase, CW), st, s, y);
-  keep_packed<L, CPT>(w.in.x, w.gh);
+  keep_packed(w.in.x, w.gh);
   // past a barrier: the states before each of the wave's rows
   for (int v = NW - 1; v > wid; --v) {
 #pragma unroll
@@ -673,7 +682,7 @@ __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, 
 }
 
 template <typename IO, int NW, int L, int CPT, bool NT, bool RST>
-__global__ __launch_bounds__(NW* kWave) void k_glr_bwd(GlrArgs g, int ncb, int ntb, int vec,
+__global__ __launch_bounds__(NW* kWave) void k_glr_bwd(GlrArgs g, int ncb, int ntb,
                                                        uint64_t* __restrict__ status,
                                                        unsigned* __restrict__ tickets) {
   constexpr int CW = kWave * CPT, TW = NW * L;
@@ -685,7 +694,7 @@ __global__ __launch_bounds__(NW* kWave) void k_glr_bwd(GlrArgs g, int ncb, int n
   const int tb = col_ticket<NW, CPT>(multi, tickets, cb, s);
   uint64_t* st = status + (int64_t)cb * ntb * CW;
   const int ptb = ntb - 1 - tb;
-  const bool full = vec && (int64_t)(ptb + 1) * TW <= g.T && (int64_t)(cb + 1) * CW <= g.B * g.D;
+  const bool full = (int64_t)(ptb + 1) * TW <= g.T && (int64_t)(cb + 1) * CW <= g.B * g.D;
   if (full)
     glr_bwd_tile<IO, NW, L, CPT, true, NT, RST>(g, tb, ntb, cb, multi, st, s, f);
   else
@@ -736,7 +745,7 @@ __device__ __forceinline__ void glr_bwd_persist_tile(
     s.fB[par][wid][off + k] = FB[k];
   }
   persist_enter<NW, CPT, RST>(A, B, s.y, wid, off, y, par);  // its barrier covers fA and fB
-  keep_packed<L, CPT>(x, gh);
+  keep_packed(x, gh);
   for (int v = NW - 1; v > wid; --v) {
 #pragma unroll
     for (int k = 0; k < CPT; ++k)
@@ -747,7 +756,7 @@ __device__ __forceinline__ void glr_bwd_persist_tile(
 }
 
 template <typename IO, int NW, int L, int CPT, bool NT, bool RST>
-__global__ __launch_bounds__(NW* kWave) void k_glr_bwd_persist(GlrArgs g, int vec) {
+__global__ __launch_bounds__(NW* kWave) void k_glr_bwd_persist(GlrArgs g) {
   constexpr int CW = kWave * CPT, TW = NW * L;
   static_assert(TW == kGlrRows, "a tile is a checkpoint's stretch");
   __shared__ GlrWalkShared<NW, CPT> s;
@@ -758,7 +767,7 @@ __global__ __launch_bounds__(NW* kWave) void k_glr_bwd_persist(GlrArgs g, int ve
   const int64_t cbase = (int64_t)blockIdx.x * CW;
   const uint32_t off = (uint32_t)(lane * CPT);
   const int nvc = clamp_valid(C - (cbase + off), CPT);
-  const bool cfull = vec && cbase + CW <= C;
+  const bool cfull = cbase + CW <= C;
   for (int j = threadIdx.x; j < CW; j += NW * kWave)
     s.y.carry[0][j] = (g.grad_h_last && cbase + j < C) ? g.grad_h_last[cbase + j] : 0.0f;
   GlrChan<CPT> ch;
@@ -848,40 +857,48 @@ __global__ __launch_bounds__(256) void k_glr_step(GlrArgs g, const int32_t* __re
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-ColPlan plan_glr(int64_t C, int64_t T, int io, bool allow_persist) {
-  ColPlan p = plan_cols(C, T, 8, io == kIoBf16 ? 16 : 8, 2);
-  if (allow_persist && p.ncb >= persist_min_blocks()) {
-    p = plan_cols(C, T, 8, 8, 2);
-    p.persist = true;
-  }
+// Two channels a lane where rows and pointers allow pairs; one otherwise (odd
+// widths, odd pitches, views that begin at an odd element), which keeps full
+// rows of 64 elements: predicated pairs took 26 and 42 us (forward, backward) at
+// 1531 x 5 x 517 fp32 against 23 and 35.
+// The rows a wave takes, and whether the walk is persistent, do not depend on it:
+// a result has the same bits whatever its arrays' alignment.
+static bool glr_persist(int64_t C, bool allow) {
+  return allow && (C + 2 * kWave - 1) / (2 * kWave) >= persist_min_blocks();
+}
+
+ColPlan plan_glr(int64_t C, int64_t T, int io, int cpt, bool allow_persist) {
+  const bool persist = glr_persist(C, allow_persist);
+  ColPlan p = plan_cols(C, T, 8, io == kIoBf16 && !persist ? 16 : 8, cpt);
+  p.persist = persist;
   p.stream = C * T * 4 * io_bytes(io) >= kStreamFootprint;
   return p;
 }
 
-ColPlan plan_glr_bwd(int64_t C, int64_t T, int io, bool allow_persist) {
-  ColPlan p = plan_cols(C, T, 8, 8, 2);
-  p.persist = allow_persist && p.ncb >= persist_min_blocks();
+ColPlan plan_glr_bwd(int64_t C, int64_t T, int io, int cpt, bool allow_persist) {
+  ColPlan p = plan_cols(C, T, 8, 8, cpt);
+  p.persist = glr_persist(C, allow_persist);
   p.stream = C * T * 7 * io_bytes(io) >= kStreamFootprint;
   return p;
 }
 
-#define LRS_GLR_PICK(LAUNCH)                                    \
-  if (io == kIoBf16) {                                          \
-    if (p.stream) {                                             \
-      if (g.reset) LAUNCH(uint16_t, true, true);                \
-      else LAUNCH(uint16_t, true, false);                       \
-    } else {                                                    \
-      if (g.reset) LAUNCH(uint16_t, false, true);               \
-      else LAUNCH(uint16_t, false, false);                      \
-    }                                                           \
-  } else {                                                      \
-    if (p.stream) {                                             \
-      if (g.reset) LAUNCH(float, true, true);                   \
-      else LAUNCH(float, true, false);                          \
-    } else {                                                    \
-      if (g.reset) LAUNCH(float, false, true);                  \
-      else LAUNCH(float, false, false);                         \
-    }                                                           \
+#define LRS_GLR_PICK(LAUNCH)                        \
+  if (io == kIoBf16) {                              \
+    if (p.stream) {                                 \
+      if (g.reset) LAUNCH(uint16_t, true, true)     \
+      else LAUNCH(uint16_t, true, false)            \
+    } else {                                        \
+      if (g.reset) LAUNCH(uint16_t, false, true)    \
+      else LAUNCH(uint16_t, false, false)           \
+    }                                               \
+  } else {                                          \
+    if (p.stream) {                                 \
+      if (g.reset) LAUNCH(float, true, true)        \
+      else LAUNCH(float, true, false)               \
+    } else {                                        \
+      if (g.reset) LAUNCH(float, false, true)       \
+      else LAUNCH(float, false, false)              \
+    }                                               \
   }
 
 // status: whole pairs of words, 16-byte aligned.
@@ -897,7 +914,7 @@ static hipError_t glr_prep(const GlrArgs& g, const ColPlan& p, float* rates, uin
   return hipGetLastError();
 }
 
-hipError_t launch_glr_fwd(GlrArgs& g, int io, const ColPlan& p, int vec, float* rates,
+hipError_t launch_glr_fwd(GlrArgs& g, int io, const ColPlan& p, float* rates,
                           uint64_t* status, unsigned* tickets, hipStream_t stream) {
   if (status) {
     const hipError_t e = glr_prep(g, p, rates, status, tickets, stream);
@@ -906,38 +923,63 @@ hipError_t launch_glr_fwd(GlrArgs& g, int io, const ColPlan& p, int vec, float* 
   }
   if (p.persist) {
 #define LRS_GLR_P(IO, NTF, RSTF)                                                              \
-  hipLaunchKernelGGL((k_glr_fwd_persist<IO, 8, 8, 2, NTF, RSTF>), dim3((unsigned)p.ncb),      \
-                     dim3(512), 0, stream, g, vec)
+  {                                                                                           \
+    if (p.cpt == 2)                                                                           \
+      hipLaunchKernelGGL((k_glr_fwd_persist<IO, 8, 8, 2, NTF, RSTF>), dim3((unsigned)p.ncb),  \
+                         dim3(512), 0, stream, g);                                            \
+    else                                                                                      \
+      hipLaunchKernelGGL((k_glr_fwd_persist<IO, 8, 8, 1, NTF, RSTF>), dim3((unsigned)p.ncb),  \
+                         dim3(512), 0, stream, g);                                            \
+  }
     LRS_GLR_PICK(LRS_GLR_P)
 #undef LRS_GLR_P
     return hipGetLastError();
   }
   const dim3 grid((unsigned)(p.ncb * p.ntb));
-#define LRS_GLR_F(IO, NTF, RSTF)                                                                \
-  hipLaunchKernelGGL((k_glr_fwd<IO, 8, sizeof(IO) == 2 ? 16 : 8, 2, NTF, RSTF>), grid,             \
-                     dim3(512), 0, stream, g, (int)p.ncb, (int)p.ntb, vec, status, tickets)
+#define LRS_GLR_F(IO, NTF, RSTF)                                                            \
+  {                                                                                         \
+    constexpr int L = sizeof(IO) == 2 ? 16 : 8;                                             \
+    if (p.cpt == 2)                                                                         \
+      hipLaunchKernelGGL((k_glr_fwd<IO, 8, L, 2, NTF, RSTF>), grid, dim3(512), 0, stream,   \
+                         g, (int)p.ncb, (int)p.ntb, status, tickets);                       \
+    else                                                                                    \
+      hipLaunchKernelGGL((k_glr_fwd<IO, 8, L, 1, NTF, RSTF>), grid, dim3(512), 0, stream,   \
+                         g, (int)p.ncb, (int)p.ntb, status, tickets);                       \
+  }
   LRS_GLR_PICK(LRS_GLR_F)
 #undef LRS_GLR_F
   return hipGetLastError();
 }
 
-hipError_t launch_glr_bwd(GlrArgs& g, int io, const ColPlan& p, int vec, float* rates,
+hipError_t launch_glr_bwd(GlrArgs& g, int io, const ColPlan& p, float* rates,
                           uint64_t* status, unsigned* tickets, double* acc, float* grad_bias_r,
                           float* grad_bias_i, float* grad_decay, hipStream_t stream) {
   const hipError_t e0 = glr_prep(g, p, rates, status, tickets, stream);
   if (e0 != hipSuccess) return e0;
   g.rates = rates;
   if (p.persist) {
-#define LRS_GLR_Q(IO, NTF, RSTF)                                                               \
-  hipLaunchKernelGGL((k_glr_bwd_persist<IO, 8, 8, 2, NTF, RSTF>), dim3((unsigned)p.ncb),       \
-                     dim3(512), 0, stream, g, vec)
+#define LRS_GLR_Q(IO, NTF, RSTF)                                                              \
+  {                                                                                           \
+    if (p.cpt == 2)                                                                           \
+      hipLaunchKernelGGL((k_glr_bwd_persist<IO, 8, 8, 2, NTF, RSTF>), dim3((unsigned)p.ncb),  \
+                         dim3(512), 0, stream, g);                                            \
+    else                                                                                      \
+      hipLaunchKernelGGL((k_glr_bwd_persist<IO, 8, 8, 1, NTF, RSTF>), dim3((unsigned)p.ncb),  \
+                         dim3(512), 0, stream, g);                                            \
+  }
     LRS_GLR_PICK(LRS_GLR_Q)
 #undef LRS_GLR_Q
   } else {
     const dim3 grid((unsigned)(p.ncb * p.ntb));
-#define LRS_GLR_B(IO, NTF, RSTF)                                                              \
-  hipLaunchKernelGGL((k_glr_bwd<IO, 8, 8, 2, NTF, RSTF>), grid, dim3(512), 0, stream, g,      \
-                     (int)p.ncb, (int)p.ntb, vec, status, tickets)
+#define LRS_GLR_B(IO, NTF, RSTF)                                                             \
+  {                                                                                          \
+    if (p.cpt == 2)                                                                          \
+      hipLaunchKernelGGL((k_glr_bwd<IO, 8, 8, 2, NTF, RSTF>), grid, dim3(512), 0, stream, g, \
+                         (int)p.ncb, (int)p.ntb, status, tickets);                           \
+    else                                                                                     \
+      hipLaunchKernelGGL((k_glr_bwd<IO, 8, 8, 1, NTF, RSTF>), grid, dim3(512), 0, stream, g, \
+                         (int)p.ncb, (int)p.ntb, status, tickets);                           \
+  }
     LRS_GLR_PICK(LRS_GLR_B)
 #undef LRS_GLR_B
   }

@@ -251,13 +251,15 @@ struct GlrArgs {
   const float* rates;  // [2][D]: k and dk of every feature (glr_rates), or null
 };
 // allow_persist = false: the look-back tile plan (workspace queries size for it).
-ColPlan plan_glr(int64_t C, int64_t T, int io, bool allow_persist = true);
-ColPlan plan_glr_bwd(int64_t C, int64_t T, int io, bool allow_persist = true);
+// cpt: channels a lane, 2 where every row of every array can be read in aligned
+// pairs, else 1.
+ColPlan plan_glr(int64_t C, int64_t T, int io, int cpt, bool allow_persist = true);
+ColPlan plan_glr_bwd(int64_t C, int64_t T, int io, int cpt, bool allow_persist = true);
 // rates: [2][D] fp32 of workspace; status and tickets (reset here) null where the
 // plan needs no look-back.
-hipError_t launch_glr_fwd(GlrArgs& g, int io, const ColPlan& p, int vec, float* rates,
+hipError_t launch_glr_fwd(GlrArgs& g, int io, const ColPlan& p, float* rates,
                           uint64_t* status, unsigned* tickets, hipStream_t stream);
-hipError_t launch_glr_bwd(GlrArgs& g, int io, const ColPlan& p, int vec, float* rates,
+hipError_t launch_glr_bwd(GlrArgs& g, int io, const ColPlan& p, float* rates,
                           uint64_t* status, unsigned* tickets, double* acc, float* grad_bias_r,
                           float* grad_bias_i, float* grad_decay, hipStream_t stream);
 hipError_t launch_glr_step(const GlrArgs& g, int io, const int32_t* slots, float* state, int64_t S,

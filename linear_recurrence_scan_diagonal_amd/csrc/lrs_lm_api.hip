@@ -85,8 +85,9 @@ size_t lrs_glr_workspace_bytes(int64_t T, int64_t B, int64_t D) {
   int64_t C, N;
   if (!glr_shape(T, B, D, &C, &N) || N == 0) return 0;
   // the fp32 tiles are the shorter ones
-  const lrs::ColPlan p = lrs::plan_glr(C, T, LRS_F32, false);
-  return glr_lookback_bytes(p, D);
+  const size_t a = glr_lookback_bytes(lrs::plan_glr(C, T, LRS_F32, 1, false), D);
+  const size_t b = glr_lookback_bytes(lrs::plan_glr(C, T, LRS_F32, 2, false), D);
+  return a > b ? a : b;
 }
 
 int lrs_glr_fwd(const void* z_r, const void* z_i, const void* x, int64_t ld, const float* bias_r,
@@ -114,7 +115,10 @@ int lrs_glr_fwd(const void* z_r, const void* z_i, const void* x, int64_t ld, con
   const Span outs[] = {{h, (size_t)N * es}, {h_last, cb},
                        {checkpoints, (size_t)lrs_glr_checkpoint_rows(T) * cb}};
   if (any_overlap(outs, 3, ins, 8)) return LRS_ERR_INVALID_ARG;
-  const lrs::ColPlan p = lrs::plan_glr(C, T, io_dtype);
+  const size_t pair = 2 * es;
+  const bool pairs = D % 2 == 0 && ld % 2 == 0 && aligned(z_r, pair) && aligned(z_i, pair) &&
+                     aligned(x, pair) && aligned(h, pair) && aligned(checkpoints, 8);
+  const lrs::ColPlan p = lrs::plan_glr(C, T, io_dtype, pairs ? 2 : 1);
   if (!glr_step_fits(B, C, ld) || !grid_ok(p.persist ? p.ncb : p.ncb * p.ntb, p.nw * 64))
     return LRS_ERR_UNSUPPORTED;
   const size_t need = glr_lookback_bytes(p, D);
@@ -128,9 +132,6 @@ int lrs_glr_fwd(const void* z_r, const void* z_i, const void* x, int64_t ld, con
     tickets = cv.take<unsigned>(p.ncb);
     rates = cv.take<float>(2 * D);
   }
-  const size_t rb = (size_t)p.cpt * es;
-  const int vec = D % p.cpt == 0 && ld % p.cpt == 0 && aligned(z_r, rb) && aligned(z_i, rb) &&
-                  aligned(x, rb) && aligned(h, rb) && aligned(checkpoints, (size_t)p.cpt * 4);
   lrs::GlrArgs g = {};
   g.z_r = z_r;
   g.z_i = z_i;
@@ -148,7 +149,7 @@ int lrs_glr_fwd(const void* z_r, const void* z_i, const void* x, int64_t ld, con
   g.D = D;
   g.ld = ld;
   g.c = c;
-  return hip_status(lrs::launch_glr_fwd(g, io_dtype, p, vec, rates, status, tickets, s));
+  return hip_status(lrs::launch_glr_fwd(g, io_dtype, p, rates, status, tickets, s));
 }
 
 static size_t glr_bwd_ws(const lrs::ColPlan& p, int64_t B, int64_t D) {
@@ -160,7 +161,9 @@ static size_t glr_bwd_ws(const lrs::ColPlan& p, int64_t B, int64_t D) {
 size_t lrs_glr_bwd_workspace_bytes(int64_t T, int64_t B, int64_t D) {
   int64_t C, N;
   if (!glr_shape(T, B, D, &C, &N) || N == 0) return 0;
-  return glr_bwd_ws(lrs::plan_glr_bwd(C, T, LRS_F32, false), B, D);
+  const size_t a = glr_bwd_ws(lrs::plan_glr_bwd(C, T, LRS_F32, 1, false), B, D);
+  const size_t b = glr_bwd_ws(lrs::plan_glr_bwd(C, T, LRS_F32, 2, false), B, D);
+  return a > b ? a : b;
 }
 
 int lrs_glr_bwd(const void* z_r, const void* z_i, const void* x, int64_t ld, const float* bias_r,
@@ -210,7 +213,9 @@ int lrs_glr_bwd(const void* z_r, const void* z_i, const void* x, int64_t ld, con
     if (any_overlap(one, 1, ins, 10) || any_overlap(one, 1, sums, 4)) return LRS_ERR_INVALID_ARG;
     if (rows_overlap(gz[i], gz[(i + 1) % 3], T * B, ld_grad, D, es)) return LRS_ERR_INVALID_ARG;
   }
-  const lrs::ColPlan p = lrs::plan_glr_bwd(C, T, io_dtype);
+  bool pairs = D % 2 == 0 && ld % 2 == 0 && ld_grad % 2 == 0;
+  for (const void* q : io) pairs = pairs && aligned(q, 2 * es);
+  const lrs::ColPlan p = lrs::plan_glr_bwd(C, T, io_dtype, pairs ? 2 : 1);
   if (!glr_step_fits(B, C, ld) || !glr_step_fits(B, C, ld_grad) ||
       !grid_ok(p.persist ? p.ncb : p.ncb * p.ntb, p.nw * 64))
     return LRS_ERR_UNSUPPORTED;
@@ -228,9 +233,6 @@ int lrs_glr_bwd(const void* z_r, const void* z_i, const void* x, int64_t ld, con
     tickets = cv.take<unsigned>(p.ncb);
   }
   float* rates = cv.take<float>(2 * D);
-  const size_t rb = (size_t)p.cpt * es;
-  int vec = D % p.cpt == 0 && ld % p.cpt == 0 && ld_grad % p.cpt == 0;
-  for (const void* q : io) vec = vec && aligned(q, rb);
   g.z_r = z_r;
   g.z_i = z_i;
   g.x = x;
@@ -251,7 +253,7 @@ int lrs_glr_bwd(const void* z_r, const void* z_i, const void* x, int64_t ld, con
   g.grad_x = grad_x;
   g.ld_grad = ld_grad;
   g.grad_h0 = grad_h0;
-  return hip_status(lrs::launch_glr_bwd(g, io_dtype, p, vec, rates, status, tickets, acc,
+  return hip_status(lrs::launch_glr_bwd(g, io_dtype, p, rates, status, tickets, acc,
                                         grad_bias_r, grad_bias_i, grad_decay, s));
 }
 
