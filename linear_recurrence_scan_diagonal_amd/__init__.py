@@ -23,11 +23,13 @@ __all__ = ["DEER_DEFAULT_EPS", "DEER_DEFAULT_KMAX", *_BINDING_NAMES, *_LM_NAMES]
 
 
 def __getattr__(name):
-    # the binding imports torch; load it only when a device entry point is used
+    # the bindings import torch; load them only when a device entry point is used,
+    # and look each name up once
     if name in _BINDING_NAMES:
-        from . import binding
-        return getattr(binding, name)
-    if name in _LM_NAMES:
-        from . import lm
-        return getattr(lm, name)
-    raise AttributeError(name)
+        from . import binding as module
+    elif name in _LM_NAMES:
+        from . import lm as module
+    else:
+        raise AttributeError(name)
+    globals()[name] = value = getattr(module, name)
+    return value

@@ -30,44 +30,64 @@ constexpr int kGroup = 16 / (int)sizeof(IO);
 typedef f32x4_t f32x4_any __attribute__((aligned(4)));
 typedef u32x4_t u32x4_any __attribute__((aligned(2)));
 
-// The group at element e of a row of D elements; 0 past the end.
-__device__ __forceinline__ void ld_group(const float* row, int64_t e, int64_t D, float (&v)[4]) {
-  if (e + 4 <= D) {
-    const f32x4_t q = *reinterpret_cast<const f32x4_any*>(row + e);
-    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = e + j < D ? row[e + j] : 0.0f;
+// The group at element e of a row of D elements, as it is in memory; 0 past the
+// end.  NT: nontemporal (see kStreamFootprint).
+template <bool NT, typename IO>
+__device__ __forceinline__ u32x4_t ld_raw(const IO* row, int64_t e, int64_t D) {
+  u32x4_t q = {0u, 0u, 0u, 0u};
+  if (e + kGroup<IO> <= D) {
+    const u32x4_any* p = reinterpret_cast<const u32x4_any*>(row + e);
+    if constexpr (NT) return __builtin_nontemporal_load(p);
+    else return *p;
   }
-}
-__device__ __forceinline__ void ld_group(const uint16_t* row, int64_t e, int64_t D, float (&v)[8]) {
-  if (e + 8 <= D) {
-    const u32x4_t q = *reinterpret_cast<const u32x4_any*>(row + e);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = bf16_lo(q[j]);
-      v[2 * j + 1] = bf16_hi(q[j]);
+  for (int j = 0; j < kGroup<IO>; ++j) {
+    if constexpr (sizeof(IO) == 4) {
+      if (e + j < D) q[j] = as_u32(row[e + j]);
+    } else {
+      if (e + j < D) q[j / 2] |= (uint32_t)row[e + j] << (16 * (j % 2));
     }
-  } else {
+  }
+  return q;
+}
+__device__ __forceinline__ void unpack(u32x4_t q, float (&v)[4]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = e + j < D ? io_ld(row, e + j) : 0.0f;
+  for (int j = 0; j < 4; ++j) v[j] = as_f32(q[j]);
+}
+__device__ __forceinline__ void unpack(u32x4_t q, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = bf16_lo(q[j]);
+    v[2 * j + 1] = bf16_hi(q[j]);
   }
 }
+template <bool NT, typename IO>
+__device__ __forceinline__ void ld_group(const IO* row, int64_t e, int64_t D,
+                                         float (&v)[kGroup<IO>]) {
+  unpack(ld_raw<NT>(row, e, D), v);
+}
+template <bool NT>
 __device__ __forceinline__ void st_group(float* row, int64_t e, int64_t D, const float (&v)[4]) {
   if (e + 4 <= D) {
-    *reinterpret_cast<f32x4_any*>(row + e) = f32x4_t{v[0], v[1], v[2], v[3]};
+    f32x4_any* p = reinterpret_cast<f32x4_any*>(row + e);
+    const f32x4_t q = {v[0], v[1], v[2], v[3]};
+    if constexpr (NT) __builtin_nontemporal_store(q, p);
+    else *p = q;
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (e + j < D) row[e + j] = v[j];
   }
 }
+template <bool NT>
 __device__ __forceinline__ void st_group(uint16_t* row, int64_t e, int64_t D, const float (&v)[8]) {
   if (e + 8 <= D) {
     u32x4_t q;
 #pragma unroll
     for (int j = 0; j < 4; ++j) q[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-    *reinterpret_cast<u32x4_any*>(row + e) = q;
+    u32x4_any* p = reinterpret_cast<u32x4_any*>(row + e);
+    if constexpr (NT) __builtin_nontemporal_store(q, p);
+    else *p = q;
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -119,7 +139,7 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-template <typename IO, int TPR, int NV>
+template <typename IO, int TPR, int NV, bool NT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_ln_fwd(
     const IO* x, const IO* residual, const float* __restrict__ gamma,
     const float* __restrict__ beta, IO* __restrict__ y, IO* sum, float* __restrict__ mean_out,
@@ -132,17 +152,17 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_ln_fwd(
   const IO* xr = x + row * D;
   float v[NV][G];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) ld_group(xr, ((int64_t)i * TPR + t) * G, D, v[i]);
+  for (int i = 0; i < NV; ++i) ld_group<NT>(xr, ((int64_t)i * TPR + t) * G, D, v[i]);
   if (residual) {
     const IO* rr = residual + row * D;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t e = ((int64_t)i * TPR + t) * G;
       float a[G];
-      ld_group(rr, e, D, a);
+      ld_group<NT>(rr, e, D, a);
 #pragma unroll
       for (int j = 0; j < G; ++j) v[i][j] = round_io(v[i][j] + a[j], x);
-      st_group(sum + row * D, e, D, v[i]);
+      st_group<NT>(sum + row * D, e, D, v[i]);
     }
   }
   float part = 0.0f;
@@ -178,7 +198,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_ln_fwd(
 #pragma unroll
       for (int j = 0; j < G; ++j)
         o[j] = __builtin_fmaf(v[i][j] * rstd, ga[j], beta ? be[j] : 0.0f);
-      st_group(yr, e, D, o);
+      st_group<NT>(yr, e, D, o);
     }
   }
   if (mean_out && t == 0) {
@@ -201,13 +221,13 @@ __global__ __launch_bounds__(1024) void k_ln_fwd_wide(
   float part = 0.0f;
   for (int64_t e = (int64_t)threadIdx.x * G; e < D; e += 1024 * G) {
     float v[G];
-    ld_group(xr, e, D, v);
+    ld_group<false>(xr, e, D, v);
     if (residual) {
       float a[G];
-      ld_group(residual + row * D, e, D, a);
+      ld_group<false>(residual + row * D, e, D, a);
 #pragma unroll
       for (int j = 0; j < G; ++j) v[j] = round_io(v[j] + a[j], x);
-      st_group(sum + row * D, e, D, v);
+      st_group<false>(sum + row * D, e, D, v);
     }
 #pragma unroll
     for (int j = 0; j < G; ++j) part += v[j];
@@ -219,7 +239,7 @@ __global__ __launch_bounds__(1024) void k_ln_fwd_wide(
   part = 0.0f;
   for (int64_t e = (int64_t)threadIdx.x * G; e < D; e += 1024 * G) {
     float v[G];
-    ld_group(sr, e, D, v);
+    ld_group<false>(sr, e, D, v);
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       const float c = e + j < D ? v[j] - mean : 0.0f;
@@ -229,13 +249,13 @@ __global__ __launch_bounds__(1024) void k_ln_fwd_wide(
   const float rstd = 1.0f / sqrtf(row_sum<1024>(part, red[1]) / n + eps);
   for (int64_t e = (int64_t)threadIdx.x * G; e < D; e += 1024 * G) {
     float v[G], ga[G], be[G];
-    ld_group(sr, e, D, v);
+    ld_group<false>(sr, e, D, v);
     ld_param<G>(gamma, e, D, ga);
     if (beta) ld_param<G>(beta, e, D, be);
 #pragma unroll
     for (int j = 0; j < G; ++j)
       v[j] = __builtin_fmaf((v[j] - mean) * rstd, ga[j], beta ? be[j] : 0.0f);
-    st_group(y + row * D, e, D, v);
+    st_group<false>(y + row * D, e, D, v);
   }
   if (mean_out && threadIdx.x == 0) {
     mean_out[row] = mean;
@@ -249,7 +269,7 @@ __global__ __launch_bounds__(1024) void k_ln_fwd_wide(
 // to part[0][block][d] (dgamma) and part[1][block][d] (dbeta), which the column
 // sums (common.hip) add up in a fixed order.
 // ---------------------------------------------------------------------------
-template <typename IO, int TPR, int NV>
+template <typename IO, int TPR, int NV, bool NT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_ln_bwd(
     const IO* s, const float* __restrict__ gamma, const float* __restrict__ mean_in,
     const float* __restrict__ rstd_in, const IO* grad_y, const IO* grad_sum, IO* grad_x,
@@ -266,18 +286,35 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_ln_bwd(
 #pragma unroll
     for (int j = 0; j < G; ++j) dg[i][j] = db[i][j] = 0.0f;
   }
-  int par = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < R;
-       row += (int64_t)gridDim.x * RPB, par ^= 1) {
-    const float mean = mean_in[row], rstd = rstd_in[row];
-    float xh[NV][G], q[NV][G];
-    float s1 = 0.0f, s2 = 0.0f;
+  // the next row is in flight, packed, while the current one is summed and written
+  u32x4_t ns[NV], ng[NV], na[NV];
+  float nmean = 0.0f, nrstd = 0.0f;
+  auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+    nmean = mean_in[row];
+    nrstd = rstd_in[row];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t e = ((int64_t)i * TPR + t) * G;
-      ld_group(s + row * D, e, D, xh[i]);
-      ld_group(grad_y + row * D, e, D, q[i]);
+      ns[i] = ld_raw<NT>(s + row * D, e, D);
+      ng[i] = ld_raw<NT>(grad_y + row * D, e, D);
+      if (grad_sum) na[i] = ld_raw<NT>(grad_sum + row * D, e, D);
     }
+  };
+  const int64_t stride = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + sub;
+  if (row < R) fetch(row);
+  for (int par = 0; row < R; row += stride, par ^= 1) {
+    const float mean = nmean, rstd = nrstd;
+    float xh[NV][G], q[NV][G];
+    u32x4_t add[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      unpack(ns[i], xh[i]);
+      unpack(ng[i], q[i]);
+      add[i] = na[i];
+    }
+    if (row + stride < R) fetch(row + stride);
+    float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
@@ -298,13 +335,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_ln_bwd(
       const int64_t e = ((int64_t)i * TPR + t) * G;
       if (e < D) {
         float o[G];
-        if (grad_sum) ld_group(grad_sum + row * D, e, D, o);
+        if (grad_sum) unpack(add[i], o);
 #pragma unroll
         for (int j = 0; j < G; ++j) {
           const float d = rstd * (q[i][j] - __builtin_fmaf(xh[i][j], s2, s1));
           o[j] = grad_sum ? d + o[j] : d;
         }
-        st_group(grad_x + row * D, e, D, o);
+        st_group<NT>(grad_x + row * D, e, D, o);
       }
     }
   }
@@ -351,8 +388,8 @@ __global__ __launch_bounds__(1024) void k_ln_bwd_wide(
   float s1 = 0.0f, s2 = 0.0f;
   for (int64_t e = (int64_t)threadIdx.x * G; e < D; e += 1024 * G) {
     float x[G], g[G], ga[G];
-    ld_group(s + row * D, e, D, x);
-    ld_group(grad_y + row * D, e, D, g);
+    ld_group<false>(s + row * D, e, D, x);
+    ld_group<false>(grad_y + row * D, e, D, g);
     ld_param<G>(gamma, e, D, ga);
 #pragma unroll
     for (int j = 0; j < G; ++j) {
@@ -365,16 +402,16 @@ __global__ __launch_bounds__(1024) void k_ln_bwd_wide(
   s2 = row_sum<1024>(s2, red[1]) * inv;
   for (int64_t e = (int64_t)threadIdx.x * G; e < D; e += 1024 * G) {
     float x[G], g[G], ga[G], o[G];
-    ld_group(s + row * D, e, D, x);
-    ld_group(grad_y + row * D, e, D, g);
+    ld_group<false>(s + row * D, e, D, x);
+    ld_group<false>(grad_y + row * D, e, D, g);
     ld_param<G>(gamma, e, D, ga);
-    if (grad_sum) ld_group(grad_sum + row * D, e, D, o);
+    if (grad_sum) ld_group<false>(grad_sum + row * D, e, D, o);
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       const float d = rstd * (g[j] * ga[j] - __builtin_fmaf((x[j] - mean) * rstd, s2, s1));
       o[j] = grad_sum ? d + o[j] : d;
     }
-    st_group(grad_x + row * D, e, D, o);
+    st_group<false>(grad_x + row * D, e, D, o);
   }
 }
 
@@ -439,9 +476,17 @@ static hipError_t ln_fwd(const IO* x, const IO* residual, const float* gamma, co
   }
   const int rpb = sh.tpr < 256 ? 256 / sh.tpr : 1;
   const dim3 grid((unsigned)((R + rpb - 1) / rpb));
-#define LRS_LN_F(IO_, TPR, NV)                                                                  \
-  hipLaunchKernelGGL((k_ln_fwd<IO_, TPR, NV>), grid, dim3(TPR < 256 ? 256 : TPR), 0, stream, x, \
-                     residual, gamma, beta, y, sum, mean, rstd, R, D, eps)
+  const bool nt = R * D * (residual ? 4 : 2) * (int64_t)sizeof(IO) >= kStreamFootprint;
+#define LRS_LN_F(IO_, TPR, NV)                                                                \
+  do {                                                                                        \
+    const dim3 wg(TPR < 256 ? 256 : TPR);                                                     \
+    if (nt)                                                                                   \
+      hipLaunchKernelGGL((k_ln_fwd<IO_, TPR, NV, true>), grid, wg, 0, stream, x, residual,    \
+                         gamma, beta, y, sum, mean, rstd, R, D, eps);                         \
+    else                                                                                      \
+      hipLaunchKernelGGL((k_ln_fwd<IO_, TPR, NV, false>), grid, wg, 0, stream, x, residual,   \
+                         gamma, beta, y, sum, mean, rstd, R, D, eps);                         \
+  } while (0)
   LRS_LN_PICK(LRS_LN_F, IO)
   else if (sh.nv <= 2) LRS_LN_F(IO, 1024, 2);
   else LRS_LN_F(IO, 1024, 4);
@@ -480,9 +525,17 @@ static hipError_t ln_bwd(const IO* s, const float* gamma, const float* mean, con
     hipLaunchKernelGGL(k_ln_bwd_wide<IO>, dim3((unsigned)R), dim3(1024), 0, stream, s, gamma, mean,
                        rstd, grad_y, grad_sum, grad_x, D);
   } else {
-#define LRS_LN_B(IO_, TPR, NV)                                                                    \
-  hipLaunchKernelGGL((k_ln_bwd<IO_, TPR, NV>), grid, dim3(TPR < 256 ? 256 : TPR), 0, stream, s,   \
-                     gamma, mean, rstd, grad_y, grad_sum, grad_x, part, R, D)
+    const bool nt = R * D * (grad_sum ? 4 : 3) * (int64_t)sizeof(IO) >= kStreamFootprint;
+#define LRS_LN_B(IO_, TPR, NV)                                                                \
+  do {                                                                                        \
+    const dim3 wg(TPR < 256 ? 256 : TPR);                                                     \
+    if (nt)                                                                                   \
+      hipLaunchKernelGGL((k_ln_bwd<IO_, TPR, NV, true>), grid, wg, 0, stream, s, gamma, mean, \
+                         rstd, grad_y, grad_sum, grad_x, part, R, D);                         \
+    else                                                                                      \
+      hipLaunchKernelGGL((k_ln_bwd<IO_, TPR, NV, false>), grid, wg, 0, stream, s, gamma,      \
+                         mean, rstd, grad_y, grad_sum, grad_x, part, R, D);                   \
+  } while (0)
     LRS_LN_PICK(LRS_LN_B, IO)
 #undef LRS_LN_B
   }

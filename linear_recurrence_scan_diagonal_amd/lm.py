@@ -135,7 +135,15 @@ def _pitch(name, t, like=None):
 def _same_pitch(n0, t0, n1, t1, n2, t2, like=None):
     """The common row pitch of three tensors of one shape and type."""
     ld = _pitch(n0, t0, like)
-    if _pitch(n1, t1, t0) != ld or _pitch(n2, t2, t0) != ld:
+    alike = False
+    try:
+        st = t0.stride()
+        alike = (t1.stride() == st and t2.stride() == st and t1.shape == t0.shape and
+                 t2.shape == t0.shape and t1.dtype is t0.dtype and t2.dtype is t0.dtype and
+                 t1.is_cuda and t2.is_cuda)
+    except AttributeError:
+        pass
+    if not alike and (_pitch(n1, t1, t0) != ld or _pitch(n2, t2, t0) != ld):
         if t0.numel():
             raise ValueError(f"{n0}, {n1} and {n2} must have the same row pitch")
     return int(t0.shape[-1]) if ld is None or not t0.numel() else ld
