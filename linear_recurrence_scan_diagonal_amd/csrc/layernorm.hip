@@ -135,6 +135,26 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   }
   return v;
 }
+// Two sums behind one barrier.
+template <int TPR>
+__device__ __forceinline__ void row_sums(float& a, float& b, float (*red)[2]) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if constexpr (TPR > kWave) {
+    constexpr int NWR = TPR / kWave;
+    if ((threadIdx.x & (kWave - 1)) == 0) {
+      red[threadIdx.x / kWave][0] = a;
+      red[threadIdx.x / kWave][1] = b;
+    }
+    __syncthreads();
+    a = b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NWR; ++w) {
+      a += red[w][0];
+      b += red[w][1];
+    }
+  }
+}
 
 // ---------------------------------------------------------------------------
 // forward
@@ -275,7 +295,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_ln_bwd(
     const float* __restrict__ rstd_in, const IO* grad_y, const IO* grad_sum, IO* grad_x,
     float* __restrict__ part, int64_t R, int64_t D) {
   constexpr int G = kGroup<IO>, BT = TPR < 256 ? 256 : TPR, RPB = BT / TPR;
-  __shared__ float red[2][2][BT / kWave];
+  __shared__ float red[2][BT / kWave][2];
   __shared__ float comb[RPB > 1 ? RPB * TPR * G : 1];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const float inv = 1.0f / (float)D;
@@ -328,8 +348,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_ln_bwd(
         s2 = __builtin_fmaf(q[i][j], h, s2);
       }
     }
-    s1 = row_sum<TPR>(s1, red[par][0]) * inv;
-    s2 = row_sum<TPR>(s2, red[par][1]) * inv;
+    row_sums<TPR>(s1, s2, red[par]);
+    s1 *= inv;
+    s2 *= inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t e = ((int64_t)i * TPR + t) * G;
