@@ -47,6 +47,8 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2eF = 1.4426950408889634f;
 constexpr int kMaxPairs = 3;
@@ -56,9 +58,11 @@ constexpr float kGScale = 16384.0f;
 // What a logits tile leaves besides its maximum and sum.
 enum { kKeepNone = 0, kKeepF16 = 1, kKeepF32 = 2 };
 enum { kEpiLogits = 0, kEpiOut = 1 };
+// How A is stored: [m][k], or [k][m].
+enum { kRowsM = 0, kRowsK = 1 };
 
 struct GemmArgs {
-  const uint16_t *a, *b;  // [M][lda], [N][ldb], bf16 or fp16
+  const uint16_t *a, *b;  // [M][lda] (kRowsK: [k][lda]), [N][ldb], bf16 or fp16
   int64_t lda, ldb;
   int64_t M, N;
   int64_t k;                         // of one part, a multiple of 64
@@ -131,6 +135,19 @@ __device__ __forceinline__ int swizzle(int r) {
   return (r & 7) ^ ((r >> 3) & 1);
 }
 
+// A stored as [k][m]: a stage is 64 rows of TM values, in LDS as rows of TM / 16
+// blocks of 32 bytes, block c of row r at c ^ swizzle_k(r).  The transposing read
+// gives each of 16 lanes one column of four rows that the lanes address together
+// (32 bytes of each); two such groups go through the banks at once, rows 0..3 and
+// 8..11 or the like, which the swizzle puts on eight different blocks.
+__device__ __forceinline__ int swizzle_k(int r) {
+  return (r & 3) | ((r >> 3) & 1) << 2;
+}
+__device__ __forceinline__ s16x4_t read_columns(const char* p) {
+  typedef __attribute__((address_space(3))) s16x4_t lds_t;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)p);
+}
+
 // The 16x16x32 product: lane l gives 8 values along k of row l % 16, from k =
 // 8 (l / 16) on, and holds n = l % 16, m = 4 (l / 16) + 0..3 of the result.
 // Written as an instruction that adds in place: through the builtin the register
@@ -172,7 +189,7 @@ struct Shape {
                 "whole loads, and the order of the waits");
 };
 
-template <class S, int EPI, int KEEP, bool F16>
+template <class S, int EPI, int KEEP, bool F16, int ROWS>
 __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
   constexpr int TM = S::TM, TN = S::TN, WM = S::WM, WN = S::WN, NA = S::NA, NB = S::NB;
   constexpr int MT = S::MT, NT = S::NT, LA = S::kLoadsA, LB = S::kLoadsB;
@@ -184,18 +201,27 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
   int tm, tn, split;
   tile_of(g, tm, tn, split);
   const int64_t m0 = (int64_t)tm * TM, n0 = (int64_t)tn * TN;
-  const uint16_t* abase = g.a + m0 * g.lda;
+  const uint16_t* abase = ROWS == kRowsM ? g.a + m0 * g.lda : g.a + m0;
+  const int64_t astep = ROWS == kRowsM ? 64 : 64 * g.lda;  // to the next stage
   const uint16_t* bbase = g.b + n0 * g.ldb;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
 
-  // This lane's global piece of each of the wave's loads (a load fills eight
-  // rows).  Rows past the end read the last row (their results are not used).
+  // This lane's global piece of each of the wave's loads (a load fills 1024 bytes,
+  // eight rows of 128).  Rows past the end read the last row (their results are
+  // not used); rows of m in [k][m] are padded to whole tiles.
   uint32_t offa[LA], offb[LB];
   {
     const int r = lane >> 3, p = lane & 7;
     const int64_t lasta = g.M - m0 - 1, lastb = g.N - n0 - 1;
 #pragma unroll
     for (int j = 0; j < LA; ++j) {
+      if constexpr (ROWS == kRowsK) {
+        constexpr int P = TM / 8;  // pieces of 16 bytes in a row
+        const int row = (wid * LA + j) * (kWave / P) + lane / P;
+        offa[j] = (uint32_t)(row * g.lda * 2) +
+                  (uint32_t)((lane & (P - 1)) ^ swizzle_k(row) << 1) * 16u;
+        continue;
+      }
       const int row = (wid * LA + j) * 8 + r;
       const int64_t rr = row < lasta ? row : lasta;
       offa[j] = (uint32_t)(rr * g.lda * 2) + (uint32_t)(p ^ swizzle(row & 15)) * 16u;
@@ -217,10 +243,10 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
     const uint16_t *base, *p;
     int pair, k;
   };
-  Walk wa = {abase, abase + g.pa[it0 / kt] + (int64_t)(it0 % kt) * 64, it0 / kt, it0 % kt};
+  Walk wa = {abase, abase + g.pa[it0 / kt] + (it0 % kt) * astep, it0 / kt, it0 % kt};
   Walk wb = {bbase, bbase + g.pb[it0 / kt] + (int64_t)(it0 % kt) * 64, it0 / kt, it0 % kt};
-  auto advance = [&](Walk& w, const int64_t* parts) __attribute__((always_inline)) {
-    w.p += 64;
+  auto advance = [&](Walk& w, const int64_t* parts, int64_t step) __attribute__((always_inline)) {
+    w.p += step;
     if (++w.k == kt && ++w.pair < g.npair) {
       w.k = 0;
       w.p = w.base + parts[w.pair];
@@ -256,6 +282,8 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
   // fragment addresses: row lane % 16 of a block of 16, piece 4 kk + lane / 16
   const int fr = lane & 15, fsw = swizzle(fr);
   const int fa = (wm * (TM / WM) + fr) * 128;
+  // A as [k][m]: row 8 (lane / 16) + (lane % 16) / 4 of a step, 8 bytes a lane
+  const int fk = (lane >> 4) * 8 + (fr >> 2);
   const int fb = NA * S::kStageA + (wn * (TN / WN) + fr) * 128;
   // Fragment reads of a chunk: all of B come first, since the first chunk of the
   // next step needs every one of them; A's are needed one a chunk.
@@ -266,8 +294,18 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
     const char* sb = lds + bufb * S::kStageB + fb + pc;
 #pragma unroll
     for (int r = R * j / MT; r < R * (j + 1) / MT; ++r) {
-      if (r < NT) bf[set][r] = *reinterpret_cast<const frag_t*>(sb + r * 2048);
-      else af[set][r - NT] = *reinterpret_cast<const frag_t*>(sa + (r - NT) * 2048);
+      if (r < NT) {
+        bf[set][r] = *reinterpret_cast<const frag_t*>(sb + r * 2048);
+      } else if constexpr (ROWS == kRowsM) {
+        af[set][r - NT] = *reinterpret_cast<const frag_t*>(sa + (r - NT) * 2048);
+      } else {
+        // four rows (of k) a read; the swizzle of a row and of the row 4 on are the same
+        const char* sk = lds + bufa * S::kStageA + (kk * 32 + fk) * (TM * 2) + (fr & 3) * 8 +
+                         ((wm * (TM / WM / 16) + r - NT) ^ swizzle_k(fk)) * 32;
+        const s16x4_t lo = read_columns(sk), hi = read_columns(sk + 4 * TM * 2);
+        const s16x8_t both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        af[set][r - NT] = __builtin_bit_cast(frag_t, both);
+      }
     }
   };
   auto multiply = [&](int set, int j) __attribute__((always_inline)) {
@@ -308,8 +346,8 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
       multiply(1, j);
     }
     if (fill) {
-      advance(wa, g.pa);
-      advance(wb, g.pb);
+      advance(wa, g.pa, astep);
+      advance(wb, g.pb, 64);
     }
     oa = ca;
     ca = na;
@@ -323,10 +361,10 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
     if (s < nk) {
 #pragma unroll
       for (int j = 0; j < LA; ++j) load_a(s, j);
-      advance(wa, g.pa);
+      advance(wa, g.pa, astep);
 #pragma unroll
       for (int j = 0; j < LB; ++j) load_b(s, j);
-      advance(wb, g.pb);
+      advance(wb, g.pb, 64);
     }
   }
   // stage 0 has landed: begun after it, NB - 1 stages
@@ -583,11 +621,12 @@ __global__ __launch_bounds__(1024) void k_ce_top(const float* __restrict__ top, 
   }
 }
 
-// [rows][D] -> [D][P][Rp] (row pitch ld), zero past `rows` and in rows that do
-// not count, whatever they hold.
+// [rows][D] -> [D][P][Rp] (row pitch ld), zero past `rows`.  With `ratio`, rows
+// whose share of the gradient is 0 are zero too, whatever they hold, and two-part
+// rows are multiplied by their share.
 template <typename IO, int P>
 __global__ __launch_bounds__(256) void k_ce_cols(const IO* __restrict__ src,
-                                                 const int64_t* __restrict__ target, int64_t V,
+                                                 const float* __restrict__ ratio,
                                                  const float* __restrict__ scale,
                                                  uint16_t* __restrict__ dst, int64_t rows,
                                                  int64_t D, int64_t Rp, int64_t ld) {
@@ -599,8 +638,12 @@ __global__ __launch_bounds__(256) void k_ce_cols(const IO* __restrict__ src,
   for (int i = 0; i < 16; ++i) {
     const int64_t r = r0 + ty + 4 * i, d = d0 + tx;
     bool ok = r < rows && d < D;
-    if (ok && target) ok = row_counts(target[r], V);
-    tile[ty + 4 * i][tx] = ok ? io_ld(src, r * D + d) * sc : 0.0f;
+    float share = 1.0f;
+    if (ok && ratio) {
+      share = ratio[r];
+      ok = share != 0.0f;
+    }
+    tile[ty + 4 * i][tx] = ok ? io_ld(src, r * D + d) * (P == 1 ? 1.0f : sc * share) : 0.0f;
   }
   __syncthreads();
 #pragma unroll
@@ -639,98 +682,95 @@ __global__ __launch_bounds__(256) void k_ce_join(const float2* __restrict__ part
   }
 }
 
-// max |grad_loss| over the rows that count, and each row's share of it.  One
+// top = the largest finite |grad_loss| of the rows that count (1 if that is 0), each
+// row's share grad_loss / top, and what its grad_x is multiplied by in the end: top
+// where G carries the share, else grad_loss; 0 in rows without a gradient.  One
 // workgroup.
 __global__ __launch_bounds__(1024) void k_ce_scale(const float* __restrict__ grad_loss,
                                                    const int64_t* __restrict__ target, int64_t N,
-                                                   int64_t V, float* __restrict__ ratio,
+                                                   int64_t V, int shared,
+                                                   float* __restrict__ ratio,
                                                    float* __restrict__ row_scale,
                                                    float* __restrict__ top_out) {
   __shared__ float red[16];
   float top = 0.0f;
-  for (int64_t n = threadIdx.x; n < N; n += 1024)
-    if (row_counts(target[n], V)) top = fmaxf(top, fabsf(grad_loss[n]));
+  for (int64_t n = threadIdx.x; n < N; n += 1024) {
+    const float v = row_counts(target[n], V) ? fabsf(grad_loss[n]) : 0.0f;
+    top = fmaxf(top, v < __builtin_inff() ? v : 0.0f);
+  }
   top = wave_top(top);
   if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = top;
   __syncthreads();
   top = red[0];
 #pragma unroll
   for (int w = 1; w < 16; ++w) top = fmaxf(top, red[w]);
+  if (top == 0.0f) top = 1.0f;
   for (int64_t n = threadIdx.x; n < N; n += 1024) {
     const float v = row_counts(target[n], V) ? grad_loss[n] : 0.0f;
-    row_scale[n] = v;
+    row_scale[n] = v == 0.0f ? 0.0f : shared ? top : v;
     ratio[n] = v == 0.0f ? 0.0f : v / top;
   }
   if (threadIdx.x == 0) *top_out = top;
 }
 
-// e -> G [rows][P][Vp] (row pitch ldg; bf16 over e's own fp16 values) and G^T
-// [classes][P][Np] (ldgt), 64 x 64 values a workgroup.  Columns of padding hold
-// 0: e is 0 past the last class, and rows past the last one are written as 0.
+// e -> G [rows][P][Vp] (row pitch ldg), per_row workgroups a row; rows up to the next
+// multiple of 64 are written as 0, as are rows whose `share` is 0, whatever their e
+// holds.  bf16 (P 1): over e's own fp16 values, G multiplied by the row's share.
+// fp32 (P 2): two parts of G itself, share only tells the rows without a gradient.
+// Classes of padding hold e = 0.
 template <typename E, int P>
 __global__ __launch_bounds__(256) void k_ce_g(const E* e, int64_t lde, const float2* __restrict__ part,
                                               int64_t tiles, int tile_m,
                                               const float* __restrict__ lse,
                                               const int64_t* __restrict__ target,
-                                              const float* __restrict__ ratio, uint16_t* g,
-                                              int64_t ldg, uint16_t* __restrict__ gt, int64_t ldgt,
-                                              int64_t rows, int64_t V, int64_t Vp, int64_t Np) {
-  __shared__ float tile[64][65];
-  const int64_t n0 = (int64_t)blockIdx.y * 64, v0 = (int64_t)blockIdx.x * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // four classes a thread, 16 rows a pass
+                                              const float* __restrict__ shares, uint16_t* g,
+                                              int64_t ldg, int64_t rows, int64_t Vp,
+                                              unsigned per_row) {
+  const int64_t n = blockIdx.x / per_row;
+  const int64_t t = n < rows ? target[n] : -1;
+  const float share = n < rows ? shares[n] : 0.0f;
+  const float own = share == 0.0f ? 0.0f : lse[n];
+  const float gs = P == 1 ? share : kGScale;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t n = n0 + ty + 16 * i, v = v0 + 4 * tx;
-    float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    float share = 0.0f;
-    if (n < rows) {
-      const int64_t t = target[n];
-      if (row_counts(t, V)) {
-        share = ratio[n];
-        // v0's tile of 64 lies inside one tile of the logits
-        const float f =
-            __builtin_amdgcn_exp2f((part[n * tiles + v0 / tile_m].x - lse[n]) * kLog2eF);
-        const int at = (int)(t - v);
-        float ev[4];
-        if constexpr (sizeof(E) == 2) {
-          const u32x2_t w = *reinterpret_cast<const u32x2_t*>(e + n * lde + v);
-          const uint32_t w0 = w.x, w1 = w.y;  // a bit cast of an element takes the vector's first
-          const f16x2_t a = __builtin_bit_cast(f16x2_t, w0), b = __builtin_bit_cast(f16x2_t, w1);
-          ev[0] = (float)a.x; ev[1] = (float)a.y; ev[2] = (float)b.x; ev[3] = (float)b.y;
-        } else {
-          const f32x4_t w = *reinterpret_cast<const f32x4_t*>(e + n * lde + v);
-          ev[0] = w.x; ev[1] = w.y; ev[2] = w.z; ev[3] = w.w;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t v = ((int64_t)(blockIdx.x % per_row) * 512 + i * 256 + threadIdx.x) * 8;
+    if (v >= Vp) return;
+    uint32_t q[P][4] = {};
+    if (share != 0.0f && v < tiles * tile_m) {
+      // eight classes lie inside one tile of the logits
+      const float f = __builtin_amdgcn_exp2f((part[n * tiles + v / tile_m].x - own) * kLog2eF);
+      float ev[8];
+      if constexpr (sizeof(E) == 2) {
+        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(e + n * lde + v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t wk = w[k];  // a bit cast of an element takes the vector's first
+          const f16x2_t h = __builtin_bit_cast(f16x2_t, wk);
+          ev[2 * k] = (float)h.x;
+          ev[2 * k + 1] = (float)h.y;
         }
+      } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = __builtin_fmaf(ev[j], f, j == at ? -1.0f : 0.0f);
+        for (int k = 0; k < 2; ++k) {
+          const f32x4_t w = *reinterpret_cast<const f32x4_t*>(e + n * lde + v + 4 * k);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) ev[4 * k + j] = w[j];
+        }
       }
-      const float gs = P == 1 ? 1.0f : kGScale;
-      uint16_t q[4][P];
+      const int64_t at = t - v;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) split_parts<P>(p[j] * gs, q[j]);
+      for (int k = 0; k < 4; ++k) {
+        uint16_t lo[P], hi[P];
+        split_parts<P>(__builtin_fmaf(ev[2 * k], f, at == 2 * k ? -1.0f : 0.0f) * gs, lo);
+        split_parts<P>(__builtin_fmaf(ev[2 * k + 1], f, at == 2 * k + 1 ? -1.0f : 0.0f) * gs, hi);
 #pragma unroll
-      for (int k = 0; k < P; ++k)
-        *reinterpret_cast<u32x2_t*>(g + n * ldg + k * Vp + v) =
-            u32x2_t{(uint32_t)q[0][k] | (uint32_t)q[1][k] << 16,
-                    (uint32_t)q[2][k] | (uint32_t)q[3][k] << 16};
+        for (int m = 0; m < P; ++m) q[m][k] = (uint32_t)lo[m] | (uint32_t)hi[m] << 16;
+      }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) tile[ty + 16 * i][4 * tx + j] = p[j] * share;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t v = v0 + ty + 16 * i, n = n0 + 4 * tx;
-    if (v >= V) continue;
-    const float gs = P == 1 ? 1.0f : kGScale;
-    uint16_t q[4][P];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) split_parts<P>(tile[4 * tx + j][ty + 16 * i] * gs, q[j]);
-#pragma unroll
-    for (int k = 0; k < P; ++k)
-      *reinterpret_cast<u32x2_t*>(gt + v * ldgt + k * Np + n) =
-          u32x2_t{(uint32_t)q[0][k] | (uint32_t)q[1][k] << 16,
-                  (uint32_t)q[2][k] | (uint32_t)q[3][k] << 16};
+    for (int m = 0; m < P; ++m)
+      *reinterpret_cast<u32x4_t*>(g + n * ldg + m * Vp + v) =
+          u32x4_t{q[m][0], q[m][1], q[m][2], q[m][3]};
   }
 }
 
@@ -807,27 +847,32 @@ void choose(int64_t M, int64_t N, int64_t K, int most_splits, int* shape, int64_
   }
 }
 
-template <class S, int EPI, int KEEP, bool F16>
+template <class S, int EPI, int KEEP, int ROWS, bool F16>
 hipError_t run_gemm(GemmArgs& g, hipStream_t stream) {
   g.tm = (int)(up(g.M, S::TM) / S::TM);
   g.tn = (int)(up(g.N, S::TN) / S::TN);
-  hipLaunchKernelGGL((k_gemm<S, EPI, KEEP, F16>), dim3((unsigned)((int64_t)g.tm * g.tn * g.splits)),
-                     dim3(S::kThreads), 0, stream, g);
+  hipLaunchKernelGGL((k_gemm<S, EPI, KEEP, F16, ROWS>),
+                     dim3((unsigned)((int64_t)g.tm * g.tn * g.splits)), dim3(S::kThreads), 0, stream,
+                     g);
   return hipGetLastError();
 }
 
-template <int EPI, int KEEP>
+// What e is kept as goes with the operands' type.
+template <class S, int EPI, int KEEP, int ROWS>
+hipError_t run_shape(GemmArgs& g, bool f16, hipStream_t stream) {
+  if constexpr (KEEP == kKeepF16) return run_gemm<S, EPI, KEEP, ROWS, false>(g, stream);
+  else if constexpr (KEEP == kKeepF32) return run_gemm<S, EPI, KEEP, ROWS, true>(g, stream);
+  else
+    return f16 ? run_gemm<S, EPI, KEEP, ROWS, true>(g, stream)
+               : run_gemm<S, EPI, KEEP, ROWS, false>(g, stream);
+}
+
+template <int EPI, int KEEP, int ROWS = kRowsM>
 hipError_t run(GemmArgs& g, int shape, bool f16, hipStream_t stream) {
   switch (shape) {
-    case 0:
-      return f16 ? run_gemm<Large, EPI, KEEP, true>(g, stream)
-                 : run_gemm<Large, EPI, KEEP, false>(g, stream);
-    case 1:
-      return f16 ? run_gemm<Medium, EPI, KEEP, true>(g, stream)
-                 : run_gemm<Medium, EPI, KEEP, false>(g, stream);
-    default:
-      return f16 ? run_gemm<Small, EPI, KEEP, true>(g, stream)
-                 : run_gemm<Small, EPI, KEEP, false>(g, stream);
+    case 0: return run_shape<Large, EPI, KEEP, ROWS>(g, f16, stream);
+    case 1: return run_shape<Medium, EPI, KEEP, ROWS>(g, f16, stream);
+    default: return run_shape<Small, EPI, KEEP, ROWS>(g, f16, stream);
   }
 }
 
@@ -849,7 +894,7 @@ CePlan plan_ce(int64_t N, int64_t V, int64_t D, int io) {
   // 128 bytes past a power of two: rows a power of two apart would meet in few
   // of the cache's channels
   p.ldg = p.parts * p.Vp + 64;
-  p.ldgt = p.parts * p.piece + 64;
+  p.ldx = p.parts * p.piece + 64;
   // the forward's only growing array is (maximum, sum) of each tile and row:
   // pieces of rows for it too (128 MiB; each still fills the GPU)
   const int64_t most_f = (kCePieceBytes / 4) / (p.Vp / 128 * 8) / 256 * 256;
@@ -938,7 +983,7 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
     return hipSuccess;
   }
   hipLaunchKernelGGL(k_ce_scale, dim3(1), dim3(1024), 0, stream, a.grad_loss, a.target, a.N, a.V,
-                     a.ratio, a.row_scale, a.top);
+                     bf ? 1 : 0, a.ratio, a.row_scale, a.top);
   LRS_CE(hipGetLastError());
   if (!bf) {
     hipLaunchKernelGGL(k_ce_top, dim3(1), dim3(1024), 0, stream, a.x_top, a.N, a.x_scale);
@@ -946,15 +991,15 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
     hipLaunchKernelGGL(k_ce_top, dim3(1), dim3(1024), 0, stream, a.w_top, a.V, a.w_scale);
     LRS_CE(hipGetLastError());
   }
-  auto cols = [&](const void* src, const int64_t* target, const float* scale, uint16_t* dst,
+  auto cols = [&](const void* src, const float* ratio, const float* scale, uint16_t* dst,
                   int64_t n, int64_t np, int64_t ld) -> hipError_t {
     const dim3 grid((unsigned)(up(np, 64) / 64), (unsigned)(up(a.D, 64) / 64));
     if (bf)
       hipLaunchKernelGGL((k_ce_cols<uint16_t, 1>), grid, dim3(256), 0, stream, (const uint16_t*)src,
-                         target, a.V, scale, dst, n, a.D, np, ld);
+                         ratio, scale, dst, n, a.D, np, ld);
     else
       hipLaunchKernelGGL((k_ce_cols<float, 2>), grid, dim3(256), 0, stream, (const float*)src,
-                         target, a.V, scale, dst, n, a.D, np, ld);
+                         ratio, scale, dst, n, a.D, np, ld);
     return hipGetLastError();
   };
   LRS_CE(cols(a.w, nullptr, a.w_scale, a.w_cols, a.V, p.Vp, p.ldg));
@@ -966,27 +1011,28 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
               : (run<kEpiLogits, kKeepF32>(l, p.shape_l, true, stream)));
     if (a.forward) LRS_CE(join(n0, n, p.tiles_l));
     const int tile_m = p.tm_l;
-    // the classes that the tiles cover
-    const dim3 gg((unsigned)(p.tiles_l * tile_m / 64), (unsigned)(p.piece / 64));
+    const unsigned per_row = (unsigned)(up(p.Vp, 4096) / 4096);
+    const dim3 gg(per_row * (unsigned)up(n, 64));
     if (bf)
       hipLaunchKernelGGL((k_ce_g<uint16_t, 1>), gg, dim3(256), 0, stream, (const uint16_t*)a.e,
                          a.lde, a.part, p.tiles_l, tile_m, a.lse + n0, a.target + n0, a.ratio + n0,
-                         a.g, p.ldg, a.gt, p.ldgt, n, a.V, p.Vp, p.piece);
+                         a.g, p.ldg, n, p.Vp, per_row);
     else
       hipLaunchKernelGGL((k_ce_g<float, 2>), gg, dim3(256), 0, stream, (const float*)a.e, a.lde,
-                         a.part, p.tiles_l, tile_m, a.lse + n0, a.target + n0, a.ratio + n0, a.g,
-                         p.ldg, a.gt, p.ldgt, n, a.V, p.Vp, p.piece);
+                         a.part, p.tiles_l, tile_m, a.lse + n0, a.target + n0, a.row_scale + n0,
+                         a.g, p.ldg, n, p.Vp, per_row);
     LRS_CE(hipGetLastError());
-    LRS_CE(cols((const char*)a.x + n0 * a.D * es, a.target + n0, a.x_scale, a.x_cols, n, p.piece,
-                p.ldgt));
+    LRS_CE(cols((const char*)a.x + n0 * a.D * es, a.ratio + n0, a.x_scale, a.x_cols, n, p.piece,
+                p.ldx));
     {
       GemmArgs g = base;
-      g.a = a.gt;
+      g.a = a.g;
       g.b = a.x_cols;
-      g.lda = g.ldb = p.ldgt;
+      g.lda = p.ldg;
+      g.ldb = p.ldx;
       g.M = a.V;
       g.N = a.D;
-      pairs(g, p.piece, p.piece, up(n, 64));
+      pairs(g, p.Vp, p.piece, up(n, 64));
       g.splits = (int)p.split_w;
       g.slots = p.slots_w ? a.slots_w : nullptr;
       g.add = n0 > 0;
@@ -995,7 +1041,7 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
       g.out_bf16 = bf;
       g.scale = a.top;
       g.unscale = bf ? nullptr : a.x_scale + 1;
-      LRS_CE((run<kEpiOut, kKeepNone>(g, p.shape_w, !bf, stream)));
+      LRS_CE((run<kEpiOut, kKeepNone, kRowsK>(g, p.shape_w, !bf, stream)));
     }
     {
       GemmArgs g = base;

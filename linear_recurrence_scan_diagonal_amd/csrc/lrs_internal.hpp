@@ -283,7 +283,7 @@ struct CePlan {
   int64_t Dp = 0, Vp = 0;           // features and classes, rounded up
   int64_t piece = 0, pieces = 0;    // rows of a piece of the gradient, and how many
   int64_t piece_f = 0;              // rows of a piece of the forward alone
-  int64_t ldg = 0, ldgt = 0;        // row pitch of G and w^T, of G^T and x^T
+  int64_t ldg = 0, ldx = 0;         // row pitch of G and w^T, of x^T
   int64_t tiles_f = 0, tiles_l = 0; // class tiles, forward alone and a piece's
   int tm_f = 0, tm_l = 0;           // classes of such a tile
   int shape_f = 0, shape_l = 0, shape_x = 0, shape_w = 0;  // tile shapes of the products
@@ -304,10 +304,10 @@ struct CeArgs {
   float2* part;               // [piece][class tiles]
   float* tlogit;              // [piece]
   // the gradient's
-  uint16_t *x_cols, *w_cols;  // [D][ldgt], [D][ldg]
+  uint16_t *x_cols, *w_cols;  // [D][ldx], [D][ldg]
   void* e;                    // [piece][lde]; bf16 inputs: G's own memory
   int64_t lde;
-  uint16_t *g, *gt;           // [piece][ldg], [V][ldgt]
+  uint16_t* g;                // [piece][ldg]
   float *ratio, *row_scale, *top;  // [N], [N], 1
   float *slots_x, *slots_w;   // [split_x][piece][D], [split_w][V][D]
 };
