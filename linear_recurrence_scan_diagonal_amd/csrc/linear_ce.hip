@@ -71,7 +71,7 @@ struct GemmArgs {
   int tm, tn, splits;                // tiles, and contiguous shares of the k loop
   // logits (m = class, n = row)
   const int64_t* target;
-  float2* part;     // [N][tm]: maximum and sum of each class tile
+  float2* part;     // [N][tm WM]: maximum and sum of each wave's classes
   float* tlogit;    // [N]: the target's logit
   const float *a_unscale, *b_unscale;  // [M to a whole tile], [N]: powers of two (fp32 operands)
   void* e;          // [N][lde]: exp(l - tile maximum), fp16 or fp32
@@ -118,14 +118,17 @@ __device__ __forceinline__ void tile_of(const GemmArgs& g, int& tm, int& tn, int
   const unsigned q = n / 8, r = n % 8, x = id % 8;
   id = x * q + (x < r ? x : r) + id / 8;
   const unsigned tiles = (unsigned)g.tm * (unsigned)g.tn;
-  split = (int)(id / tiles);
-  id %= tiles;
+  split = 0;
+  if (g.splits > 1) {
+    split = (int)(id / tiles);
+    id -= (unsigned)split * tiles;
+  }
   const unsigned per = 8u * (unsigned)g.tn;
-  const unsigned grp = id / per, in = id % per;
+  const unsigned grp = id / per, in = id - grp * per;
   const unsigned left = (unsigned)g.tm - grp * 8u;
   const unsigned gm = left < 8u ? left : 8u;
-  tm = (int)(grp * 8u + in % gm);
-  tn = (int)(in / gm);
+  tn = (int)(gm == 8u ? in / 8u : in / gm);
+  tm = (int)(grp * 8u + in - (unsigned)tn * gm);
 }
 
 // The piece of 16 bytes at which piece p of row r is kept in LDS is p ^ f(r):
@@ -153,8 +156,8 @@ __device__ __forceinline__ s16x4_t read_columns(const char* p) {
 // Written as an instruction that adds in place: through the builtin the register
 // allocator rotates hundreds of accumulators by copies in the loop.  Volatile,
 // so that products and the loads to LDS keep the order they are written in.
-// settle() has to come between the last product and the first use of a result
-// (the wait states that the compiler would count for the builtin).
+// The wait states between the last product and the first use of a result, which
+// the compiler would count for the builtin, are part of mma_last.
 template <bool F16>
 struct Frag;
 template <>
@@ -163,6 +166,11 @@ struct Frag<false> {
   static __device__ __forceinline__ void mma(V a, V b, f32x4_t& c) {
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
   }
+  static __device__ __forceinline__ void mma_last(V a, V b, f32x4_t& c) {
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0\n\ts_nop 15\n\ts_nop 15"
+                 : "+a"(c)
+                 : "v"(a), "v"(b));
+  }
 };
 template <>
 struct Frag<true> {
@@ -170,8 +178,12 @@ struct Frag<true> {
   static __device__ __forceinline__ void mma(V a, V b, f32x4_t& c) {
     asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
   }
+  static __device__ __forceinline__ void mma_last(V a, V b, f32x4_t& c) {
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0\n\ts_nop 15\n\ts_nop 15"
+                 : "+a"(c)
+                 : "v"(a), "v"(b));
+  }
 };
-__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 // Tile TM x TN by WM x WN waves, k in stages of 64 (rows of 128 bytes: whole
 // cache lines), NA buffers of A's part of a stage and NB of B's.
@@ -182,7 +194,7 @@ struct Shape {
   static constexpr int kStageA = TM * 128, kStageB = TN * 128;
   static constexpr int kLoadsA = TM / 8 / (WM * WN), kLoadsB = TN / 8 / (WM * WN);
   static constexpr int MT = TM / WM / 16, NT = TN / WN / 16;
-  static constexpr int kKeep = TN * (TM + 8) * 2 + WM * TN * 8;  // an fp16 tile, and the rows' sums
+  static constexpr int kKeep = WM * TN * (TM / WM + 8) * 2;  // an fp16 tile, by wave
   static constexpr int kBuffers = NA * kStageA + NB * kStageB;
   static constexpr int kLds = kBuffers > kKeep ? kBuffers : kKeep;
   static_assert(TM % (8 * WM * WN) == 0 && TN % (8 * WM * WN) == 0 && NB >= 2 && NA == NB + 1,
@@ -212,42 +224,46 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
   uint32_t offa[LA], offb[LB];
   {
     const int r = lane >> 3, p = lane & 7;
-    const int64_t lasta = g.M - m0 - 1, lastb = g.N - n0 - 1;
+    const int lasta = (int)(g.M - m0) - 1, lastb = (int)(g.N - n0) - 1;
+    const uint32_t pitcha = (uint32_t)g.lda * 2u, pitchb = (uint32_t)g.ldb * 2u;
 #pragma unroll
     for (int j = 0; j < LA; ++j) {
       if constexpr (ROWS == kRowsK) {
         constexpr int P = TM / 8;  // pieces of 16 bytes in a row
         const int row = (wid * LA + j) * (kWave / P) + lane / P;
-        offa[j] = (uint32_t)(row * g.lda * 2) +
+        offa[j] = (uint32_t)row * pitcha +
                   (uint32_t)((lane & (P - 1)) ^ swizzle_k(row) << 1) * 16u;
         continue;
       }
       const int row = (wid * LA + j) * 8 + r;
-      const int64_t rr = row < lasta ? row : lasta;
-      offa[j] = (uint32_t)(rr * g.lda * 2) + (uint32_t)(p ^ swizzle(row & 15)) * 16u;
+      offa[j] = (uint32_t)(row < lasta ? row : lasta) * pitcha + (uint32_t)(p ^ swizzle(row & 15)) * 16u;
     }
 #pragma unroll
     for (int j = 0; j < LB; ++j) {
       const int row = (wid * LB + j) * 8 + r;
-      const int64_t rr = row < lastb ? row : lastb;
-      offb[j] = (uint32_t)(rr * g.ldb * 2) + (uint32_t)(p ^ swizzle(row & 15)) * 16u;
+      offb[j] = (uint32_t)(row < lastb ? row : lastb) * pitchb + (uint32_t)(p ^ swizzle(row & 15)) * 16u;
     }
   }
-  const int kt = (int)(g.k / 64);
-  const int total = kt * g.npair;
-  const int it0 = (int)((int64_t)total * split / g.splits);
-  const int nk = (int)((int64_t)total * (split + 1) / g.splits) - it0;
+  // at most 3 * 2^15 stages, in at most 16 shares
+  const unsigned kt = (unsigned)g.k / 64u, total = kt * (unsigned)g.npair;
+  int it0 = 0, nk = (int)total, pair0 = 0, k0 = 0;
+  if (g.splits > 1) {
+    it0 = (int)(total * (unsigned)split / (unsigned)g.splits);
+    nk = (int)(total * (unsigned)(split + 1) / (unsigned)g.splits) - it0;
+    pair0 = (int)((unsigned)it0 / kt);
+    k0 = it0 - pair0 * (int)kt;
+  }
 
   // One operand's walk along k: the address of the next stage to load.
   struct Walk {
     const uint16_t *base, *p;
     int pair, k;
   };
-  Walk wa = {abase, abase + g.pa[it0 / kt] + (it0 % kt) * astep, it0 / kt, it0 % kt};
-  Walk wb = {bbase, bbase + g.pb[it0 / kt] + (int64_t)(it0 % kt) * 64, it0 / kt, it0 % kt};
+  Walk wa = {abase, abase + g.pa[pair0] + k0 * astep, pair0, k0};
+  Walk wb = {bbase, bbase + g.pb[pair0] + k0 * 64, pair0, k0};
   auto advance = [&](Walk& w, const int64_t* parts, int64_t step) __attribute__((always_inline)) {
     w.p += step;
-    if (++w.k == kt && ++w.pair < g.npair) {
+    if (++w.k == (int)kt && ++w.pair < g.npair) {
       w.k = 0;
       w.p = w.base + parts[w.pair];
     }
@@ -261,10 +277,6 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
   };
 
   f32x4_t acc[MT][NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
   // Pipeline.  A stage is two steps of 32 along k.  The fragments of a step are
   // read while the step before it is multiplied, also across the border of two
@@ -308,9 +320,12 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
       }
     }
   };
-  auto multiply = [&](int set, int j) __attribute__((always_inline)) {
+  auto multiply = [&](int set, int j, bool last) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < NT; ++q) Frag<F16>::mma(af[set][j], bf[set][q], acc[j][q]);
+    for (int q = 0; q < NT; ++q) {
+      if (last && q == NT - 1) Frag<F16>::mma_last(af[set][j], bf[set][q], acc[j][q]);
+      else Frag<F16>::mma(af[set][j], bf[set][q], acc[j][q]);
+    }
     __builtin_amdgcn_sched_barrier(0);
   };
   // B's loads go into the first chunks of their step
@@ -329,7 +344,7 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
 #pragma unroll
         for (int l = LA * j / MT; l < LA * (j + 1) / MT; ++l) load_a(oa, l);
       }
-      multiply(0, j);
+      multiply(0, j, false);
     }
     // the next stage has landed; begun after its last load: an A, and NB - 2 stages
     if (fill) wait_vm<LA + (NB - 2) * (LA + LB)>();
@@ -343,7 +358,7 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
 #pragma unroll
         for (int l = LB * j / CB; l < LB * (j + 1) / CB; ++l) load_b(cb, l);
       }
-      multiply(1, j);
+      multiply(1, j, !fill && j == MT - 1);  // a stage without loads may be the last
     }
     if (fill) {
       advance(wa, g.pa, astep);
@@ -367,6 +382,10 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
       advance(wb, g.pb, 64);
     }
   }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   // stage 0 has landed: begun after it, NB - 1 stages
   if (nk >= NB) wait_vm<(NB - 1) * (LA + LB)>();
   else wait_vm<0>();
@@ -379,7 +398,6 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
   int i = 0;
   for (; i + NB < nk; ++i) body(Yes());
   for (; i < nk; ++i) body(No());
-  settle();
   __syncthreads();  // the epilogues reuse the buffers
 
   // The lane's values: n = nb + 16 q, m = mb + 16 j + e.
@@ -389,109 +407,99 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
   const int mleft = (int)(g.M - mb < 16 * MT ? g.M - mb : 16 * MT);  // <= 0: none
 
   if constexpr (EPI == kEpiLogits) {
-    constexpr int PG = TM + 8;  // a padded row of e in LDS
-    float* red = reinterpret_cast<float*>(lds);         // [2][WM][TN]: maxima, sums
-    uint16_t* keep = reinterpret_cast<uint16_t*>(lds + WM * TN * 8);
+    // A wave's classes are a tile of the softmax of their own: no wave waits for
+    // another, and every logit is taken from its accumulator once.
+    constexpr int PG = TM / WM + 8;   // a padded row of e in LDS, the wave's own
+    constexpr int RP = TM / WM / 8;   // pieces of 16 bytes in such a row
+    uint16_t* keep = reinterpret_cast<uint16_t*>(lds) + wid * NT * 16 * PG;
     const bool whole = m0 + TM <= g.M;
+    const int64_t wave = (int64_t)tm * WM + wm, waves = (int64_t)g.tm * WM;
+    f32x4_t au[F16 ? MT : 1];
     if constexpr (F16) {
-      float bu[NT];
+      // past the last class: room of the workspace, masked below
 #pragma unroll
-      for (int q = 0; q < NT; ++q) bu[q] = nb + 16 * q < g.N ? g.b_unscale[nb + 16 * q] : 0.0f;
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-      {
-        // past the last class: room of the workspace, masked below
-        const f32x4_t au = *reinterpret_cast<const f32x4_t*>(g.a_unscale + mb + 16 * j);
-#pragma unroll
-        for (int q = 0; q < NT; ++q) acc[j][q] = acc[j][q] * bu[q] * au;
-      }
+      for (int j = 0; j < MT; ++j) au[j] = *reinterpret_cast<const f32x4_t*>(g.a_unscale + mb + 16 * j);
     }
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
       const int64_t n = nb + 16 * q;
+      f32x4_t v[MT];
+      const float bu = F16 && n < g.N ? g.b_unscale[n] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        asm volatile("" : "+a"(acc[j][q]));  // not read earlier: 128 values would not fit
+        v[j] = acc[j][q];
+        if constexpr (F16) v[j] = v[j] * bu * au[j];
+      }
       // the target's place among the lane's classes (it has those with bits 2 and 3 clear)
       const int64_t d = (n < g.N ? g.target[n] : -1) - mb;
       const int at = d >= 0 && d < mleft && (d & 12) == 0 ? (int)d : -1;
-      if (!whole) {
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (16 * j + e >= mleft) acc[j][q][e] = -__builtin_inff();
-      }
       if (__ballot(at >= 0)) {  // few tiles hold the target of one of 16 rows
         float tl = 0.0f;
 #pragma unroll
         for (int j = 0; j < MT; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (16 * j + e == at) tl = acc[j][q][e];
+            if (16 * j + e == at) tl = v[j][e];
         if (at >= 0) g.tlogit[n] = tl;
+      }
+      if (!whole) {
+        int left = mleft;
+        asm volatile("" : "+v"(left));  // 32 masks kept for all q would not fit
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * j + e >= left) v[j][e] = -__builtin_inff();
       }
       float mx = -__builtin_inff();
 #pragma unroll
       for (int j = 0; j < MT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, acc[j][q][e]);
+        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, v[j][e]);
       mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
-      if (lane < 16) red[wm * TN + ln + 16 * q] = mx;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      float top = red[ln + 16 * q];
-#pragma unroll
-      for (int w = 1; w < WM; ++w) top = fmaxf(top, red[w * TN + ln + 16 * q]);
-      const float top2 = top * kLog2eF;
+      // no class, or every logit -inf: all e are 0
+      const float top2 = mx == -__builtin_inff() ? 0.0f : mx * kLog2eF;
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < MT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[j][q][e], kLog2eF, -top2));
-          sum += v;
-          if constexpr (KEEP != kKeepNone) acc[j][q][e] = v;
+          v[j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[j][e], kLog2eF, -top2));
+          sum += v[j][e];
         }
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
-      if (lane < 16) red[WM * TN + wm * TN + ln + 16 * q] = sum;
+      if (lane < 16 && n < g.N) g.part[n * waves + wave] = make_float2(mx, sum);
       if constexpr (KEEP == kKeepF16) {
+        uint16_t* mine = keep + q * 16 * PG;
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-          const f16x2_t lo = {(_Float16)acc[j][q][0], (_Float16)acc[j][q][1]};
-          const f16x2_t hi = {(_Float16)acc[j][q][2], (_Float16)acc[j][q][3]};
-          *reinterpret_cast<u32x2_t*>(keep + (ln + 16 * q) * PG + lm + 16 * j) =
+          const f16x2_t lo = {(_Float16)v[j][0], (_Float16)v[j][1]};
+          const f16x2_t hi = {(_Float16)v[j][2], (_Float16)v[j][3]};
+          *reinterpret_cast<u32x2_t*>(mine + (lane & 15) * PG + 4 * (lane >> 4) + 16 * j) =
               u32x2_t{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        // whole rows of the wave's classes, so that full cache lines are written
+#pragma unroll
+        for (int c = lane; c < 16 * RP; c += kWave) {
+          const int r = c / RP, k = c % RP * 8;
+          const int64_t row = n0 + wn * (TN / WN) + 16 * q + r;
+          if (row < g.N)
+            *reinterpret_cast<u32x4_t*>((uint16_t*)g.e + row * g.lde + m0 + wm * (TM / WM) + k) =
+                *reinterpret_cast<const u32x4_t*>(mine + r * PG + k);
         }
       }
       if constexpr (KEEP == kKeepF32) {
-        if (nb + 16 * q < g.N) {
-          float* o = (float*)g.e + (nb + 16 * q) * g.lde + mb;
+        if (n < g.N) {
+          float* o = (float*)g.e + n * g.lde + mb;
 #pragma unroll
-          for (int j = 0; j < MT; ++j)
-            *reinterpret_cast<f32x4_t*>(o + 16 * j) = acc[j][q];
+          for (int j = 0; j < MT; ++j) *reinterpret_cast<f32x4_t*>(o + 16 * j) = v[j];
         }
       }
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < TN; c += S::kThreads) {
-      if (n0 + c >= g.N) continue;
-      float top = red[c], sum = red[WM * TN + c];
-#pragma unroll
-      for (int w = 1; w < WM; ++w) {
-        top = fmaxf(top, red[w * TN + c]);
-        sum += red[WM * TN + w * TN + c];
-      }
-      g.part[(n0 + c) * g.tm + tm] = make_float2(top, sum);
-    }
-    if constexpr (KEEP == kKeepF16) {
-      for (int c = threadIdx.x; c < TN * (TM / 8); c += S::kThreads) {
-        const int r = c / (TM / 8), k = c % (TM / 8) * 8;
-        if (n0 + r < g.N)
-          *reinterpret_cast<u32x4_t*>((uint16_t*)g.e + (n0 + r) * g.lde + m0 + k) =
-              *reinterpret_cast<const u32x4_t*>(keep + r * PG + k);
-      }
+      __builtin_amdgcn_sched_barrier(0);  // one q's values at a time
     }
   }
 
@@ -814,12 +822,12 @@ typedef Shape<256, 256, 2, 4, 3, 2, 2> Large;
 typedef Shape<128, 128, 2, 2, 3, 2, 2> Medium;
 typedef Shape<128, 64, 4, 1, 3, 2, 2> Small;
 struct ShapeInfo {
-  int tm, tn, wgs;
+  int tm, tn, wm, wgs;
   double tflops;
 };
-constexpr ShapeInfo kShapes[3] = {{Large::TM, Large::TN, 1, 1150.0},
-                                  {Medium::TM, Medium::TN, 2, 880.0},
-                                  {Small::TM, Small::TN, 2, 600.0}};
+constexpr ShapeInfo kShapes[3] = {{Large::TM, Large::TN, Large::WM, 1, 1150.0},
+                                  {Medium::TM, Medium::TN, Medium::WM, 2, 880.0},
+                                  {Small::TM, Small::TN, Small::WM, 2, 600.0}};
 
 int64_t tiles_of(int64_t M, int64_t N, const ShapeInfo& s) {
   return up(M, s.tm) / s.tm * (up(N, s.tn) / s.tn);
@@ -903,10 +911,11 @@ CePlan plan_ce(int64_t N, int64_t V, int64_t D, int io) {
   const int64_t K = p.Dp * (p.parts == 1 ? 1 : 3);
   choose(V, p.piece_f < N ? p.piece_f : N, K, 1, &p.shape_f, &one);
   choose(V, p.piece < N ? p.piece : N, K, 1, &p.shape_l, &one);
-  p.tm_f = kShapes[p.shape_f].tm;
-  p.tm_l = kShapes[p.shape_l].tm;
-  p.tiles_f = up(V, p.tm_f) / p.tm_f;
-  p.tiles_l = up(V, p.tm_l) / p.tm_l;
+  // a tile of the softmax is a wave's classes
+  const ShapeInfo &sf = kShapes[p.shape_f], &sl = kShapes[p.shape_l];
+  p.tm_l = sl.tm / sl.wm;
+  p.tiles_f = up(V, sf.tm) / sf.tm * sf.wm;
+  p.tiles_l = up(V, sl.tm) / p.tm_l;
   const int64_t n = p.piece < N ? p.piece : N, f = p.parts == 1 ? 1 : 3;
   choose(n, D, up(V, 64) * f, 16, &p.shape_x, &p.split_x);
   choose(V, D, up(n, 64) * f, 16, &p.shape_w, &p.split_w);

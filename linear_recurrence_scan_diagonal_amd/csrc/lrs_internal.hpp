@@ -285,7 +285,7 @@ struct CePlan {
   int64_t piece_f = 0;              // rows of a piece of the forward alone
   int64_t ldg = 0, ldx = 0;         // row pitch of G and w^T, of x^T
   int64_t tiles_f = 0, tiles_l = 0; // class tiles, forward alone and a piece's
-  int tm_f = 0, tm_l = 0;           // classes of such a tile
+  int tm_l = 0;                     // classes of a piece's tile
   int shape_f = 0, shape_l = 0, shape_x = 0, shape_w = 0;  // tile shapes of the products
   int64_t split_x = 1, split_w = 1;        // shares of the gradients' k loops
   bool slots_x = false, slots_w = false;   // fp32 partial results are kept
