@@ -569,15 +569,29 @@ __device__ __forceinline__ float wave_top(float v) {
   return v;
 }
 
-// bf16 [rows][D] -> [rows][Dp], zero past D; one wave a row.  With `target`,
-// rows that do not count become 0, whatever they hold.
+// bf16 [rows][D] -> [rows][Dp], zero past D; one wave a row, two values a lane and
+// four such pairs in flight (rows of an odd D are aligned to one value).
 __global__ __launch_bounds__(256) void k_ce_rows_bf16(const uint16_t* __restrict__ src,
                                                       uint16_t* __restrict__ dst, int64_t rows,
                                                       int64_t D, int64_t Dp) {
   const int lane = threadIdx.x & (kWave - 1);
   for (int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; row < rows;
-       row += (int64_t)gridDim.x * 4)
-    for (int64_t d = lane; d < Dp; d += kWave) dst[row * Dp + d] = d < D ? src[row * D + d] : 0;
+       row += (int64_t)gridDim.x * 4) {
+    const uint16_t* s = src + row * D;
+    for (int64_t d0 = 2 * lane; d0 < Dp; d0 += 8 * kWave) {
+      uint32_t v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t d = d0 + i * 2 * kWave;
+        v[i] = (d < D ? (uint32_t)s[d] : 0u) | (d + 1 < D ? (uint32_t)s[d + 1] << 16 : 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t d = d0 + i * 2 * kWave;
+        if (d < Dp) *reinterpret_cast<uint32_t*>(dst + row * Dp + d) = v[i];
+      }
+    }
+  }
 }
 
 // fp32 [rows][D] -> two fp16 parts [rows][2][Dp] scaled by the row's power of
@@ -666,7 +680,9 @@ __global__ __launch_bounds__(256) void k_ce_cols(const IO* __restrict__ src,
   }
 }
 
-// One wave a row: the tiles' maxima and sums become lse, and the loss.
+// One wave a row: the tiles' maxima and sums become lse, and the loss.  One pass,
+// four loads in flight a lane (two passes of single loads: 8.2 us against 3.9 for
+// 32 rows of 1000 tiles).
 __global__ __launch_bounds__(256) void k_ce_join(const float2* __restrict__ part,
                                                  const float* __restrict__ tlogit,
                                                  const int64_t* __restrict__ target,
@@ -676,11 +692,27 @@ __global__ __launch_bounds__(256) void k_ce_join(const float2* __restrict__ part
   const int64_t n = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
   if (n >= N) return;
   const float2* p = part + n * tiles;
-  float top = -__builtin_inff(), sum = 0.0f;
-  for (int64_t t = lane; t < tiles; t += kWave) top = fmaxf(top, p[t].x);
+  const float low = -__builtin_inff();
+  // (maximum, sum) of what was seen; a maximum of -inf means a sum of 0
+  auto base = [&](float t) { return t == low ? 0.0f : t; };
+  float top = low, sum = 0.0f;
+  for (int64_t t0 = lane; t0 < tiles; t0 += 4 * kWave) {
+    float2 v[4];
+    float next = top;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = t0 + i * kWave < tiles ? p[t0 + i * kWave] : make_float2(low, 0.0f);
+      next = fmaxf(next, v[i].x);
+    }
+    sum *= __builtin_amdgcn_exp2f((top - base(next)) * kLog2eF);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sum += v[i].y * __builtin_amdgcn_exp2f((v[i].x - base(next)) * kLog2eF);
+    top = next;
+  }
+  const float mine = top;
   top = wave_top(top);
-  for (int64_t t = lane; t < tiles; t += kWave)
-    sum += p[t].y * __builtin_amdgcn_exp2f((p[t].x - top) * kLog2eF);
+  sum *= __builtin_amdgcn_exp2f((mine - base(top)) * kLog2eF);
 #pragma unroll
   for (int o = kWave / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
   if (lane == 0) {
