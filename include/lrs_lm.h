@@ -132,9 +132,10 @@ LRS_API int lrs_linear_ce_fwd(const void *x, const void *w, const int64_t *targe
 
 /* Its gradient for given dL/dloss: with G = (exp(l - lse) - onehot) grad_loss
  * (rows of 0 where ignored), grad_x = G w and grad_w = G^T x, I/O type.  The
- * rows are taken in pieces: the exponentials of a piece's logits (made again
- * here) and its G are kept in the workspace, at most 2 GiB of it whatever the
- * vocabulary and the number of rows.  G is rounded to bf16 for bf16 inputs.
+ * rows are taken in pieces of at least 256 rows: the exponentials of a piece's
+ * logits (made again here) and its G are kept in the workspace, 1 GiB for bf16
+ * and 2 GiB for fp32 at most unless 256 rows take more.  G is rounded to bf16
+ * for bf16 inputs.
  * lse: as lrs_linear_ce_fwd wrote it.  grad_loss: [N] fp32. */
 LRS_API int lrs_linear_ce_bwd(const void *x, const void *w, const int64_t *target,
                               const float *lse, const float *grad_loss, void *grad_x,

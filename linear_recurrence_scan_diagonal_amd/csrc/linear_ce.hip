@@ -734,8 +734,10 @@ __global__ __launch_bounds__(1024) void k_ce_scale(const float* __restrict__ gra
                                                    float* __restrict__ top_out) {
   __shared__ float red[16];
   float top = 0.0f;
+#pragma unroll 8
   for (int64_t n = threadIdx.x; n < N; n += 1024) {
-    const float v = row_counts(target[n], V) ? fabsf(grad_loss[n]) : 0.0f;
+    const int64_t t = target[n];
+    const float g = grad_loss[n], v = row_counts(t, V) ? fabsf(g) : 0.0f;
     top = fmaxf(top, v < __builtin_inff() ? v : 0.0f);
   }
   top = wave_top(top);
@@ -745,8 +747,10 @@ __global__ __launch_bounds__(1024) void k_ce_scale(const float* __restrict__ gra
 #pragma unroll
   for (int w = 1; w < 16; ++w) top = fmaxf(top, red[w]);
   if (top == 0.0f) top = 1.0f;
+#pragma unroll 8
   for (int64_t n = threadIdx.x; n < N; n += 1024) {
-    const float v = row_counts(target[n], V) ? grad_loss[n] : 0.0f;
+    const int64_t t = target[n];
+    const float g = grad_loss[n], v = row_counts(t, V) ? g : 0.0f;
     row_scale[n] = v == 0.0f ? 0.0f : shared ? top : v;
     ratio[n] = v == 0.0f ? 0.0f : v / top;
   }
@@ -919,7 +923,7 @@ hipError_t run(GemmArgs& g, int shape, bool f16, hipStream_t stream) {
 }  // namespace
 
 // Pieces of the rows whose G takes at most this many bytes.
-constexpr int64_t kCePieceBytes = (int64_t)512 << 20;
+constexpr int64_t kCePieceBytes = (int64_t)1 << 30;
 
 CePlan plan_ce(int64_t N, int64_t V, int64_t D, int io) {
   CePlan p;
@@ -937,7 +941,7 @@ CePlan plan_ce(int64_t N, int64_t V, int64_t D, int io) {
   p.ldx = p.parts * p.piece + 64;
   // the forward's only growing array is (maximum, sum) of each tile and row:
   // pieces of rows for it too (128 MiB; each still fills the GPU)
-  const int64_t most_f = (kCePieceBytes / 4) / (p.Vp / 128 * 8) / 256 * 256;
+  const int64_t most_f = (kCePieceBytes / 8) / (p.Vp / 128 * 8) / 256 * 256;
   p.piece_f = most_f < 256 ? 256 : most_f > N ? N : most_f;
   int64_t one;
   const int64_t K = p.Dp * (p.parts == 1 ? 1 : 3);
