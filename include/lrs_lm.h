@@ -92,7 +92,8 @@ LRS_API int lrs_glr_step(const void *z_r, const void *z_i, const void *x, int64_
  *   buffer: the residual stream in place), and NULL without.
  * gamma, beta : [D] fp32; beta may be NULL (zero).
  * mean, rstd  : [R] fp32 outputs (both or neither), as lrs_layernorm_bwd takes
- *   them.  eps >= 0 and finite. */
+ *   them.  eps >= 0 and finite.
+ * Supported while R stays below 2^22, or below 2^26 - 4 where D <= 1024. */
 LRS_API int lrs_layernorm_fwd(const void *x, const void *residual, const float *gamma,
                               const float *beta, void *y, void *sum, float *mean, float *rstd,
                               int64_t R, int64_t D, float eps, int io_dtype, void *stream);

@@ -168,8 +168,8 @@ __global__ __launch_bounds__(1024) void k_param_sums(const float* __restrict__ p
   }
 }
 
-// One launch up to 1024 rows: 8 us against 2 x (4.8 + 4.8) us for three matrices
-// of 1024 x 1024.  Beyond, a column's rows in one workgroup take longer than two
+// One launch up to 1024 rows: 4 to 6 us against two launches of 4.8 us a pair of
+// matrices of up to 1024 x 1024.  Beyond, a column's rows in one workgroup take longer than two
 // stages.
 hipError_t launch_param_sums(const float* part, int nmat, int64_t R, int64_t D, double* acc,
                              float* const* outs, hipStream_t stream) {

@@ -18,18 +18,26 @@
 // two sequences), or one.
 //
 // The backward pass reads no h: the forward leaves the states that enter each
-// tile of kGlrRows steps (4 / 64 of a byte an element and byte of state), and
-// the tile runs its own forward maps again from there, which is exact in fp32
-// where a saved bf16 h would add its rounding to dL/dz_r.
+// tile of kGlrRows steps (one fp32 state in 64 elements), and the tile runs its
+// own forward maps again from there, which is exact in fp32 where a saved bf16 h
+// would add its rounding to dL/dz_r.
+//
+// What bounds it.  The forward moves 4 values an element and issues about 55
+// instructions (two sigmoids, an exponential, a root), the backward 7 and about 95.
+// At 2048 x 32 x 1024 bf16 the forward takes 127 to 137 us (4.1 TB/s) and the
+// backward 204 to 218 (4.5 TB/s): loads and issue overlap, and neither alone would
+// take that long.  A prompt of 16384 x 1 x 1024 takes 44 us (3.1 TB/s): 128
+// workgroups a time, joined by the look-back.
 #include "lrs_tbd.hpp"
 
 namespace lrs {
 
 namespace {
 
-// Time tiles of a look-back group.  The end states of the groups form a chain,
-// about 1.2 us a link: with 16 tiles a group instead of the other layers' 8 a
-// prompt of 16384 steps has 8 links of 128 x 16 steps (bf16).
+// Time tiles of a look-back group.  The end states of the groups form a chain: with
+// 16 tiles a group a prompt of 16384 steps (bf16: tiles of 128) has 8 links.  Groups
+// of 8, as in the other layers, take the same 40 to 45 us there; half the links
+// leave room for the longer prompts.
 constexpr int kGlrGroup = 16;
 
 // One row of a strided array: the lane's channels at byte offsets zo from a
@@ -86,7 +94,7 @@ __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.0f) + log
 
 // The exponent of a fully open gate, k = c softplus(decay), and -c times the
 // derivative of softplus: computed once a call (k_glr_prep) where a tile is one
-// of many, because with its 32 elements a thread the library functions and the
+// of many, because with its 16 elements a thread the library functions and the
 // division below would be a seventh of the backward's instructions.
 __device__ __forceinline__ void glr_rates(const GlrArgs& g, uint32_t d, float& k, float& dk) {
   const float v = g.decay[d];
@@ -315,7 +323,8 @@ __device__ __forceinline__ void glr_checkpoint(const GlrArgs& g, int64_t row0, i
 }
 
 // ---------------------------------------------------------------------------
-// forward, look-back tiles
+// forward, look-back tiles: where the channel blocks alone leave compute units idle
+// (1531 x 5 x 517 fp32: 23 us, 2.7 TB/s)
 // ---------------------------------------------------------------------------
 template <typename IO, int NW, int L, int CPT, bool FULL, bool NT, bool RST>
 __device__ __forceinline__ void glr_tile(const GlrArgs& g, int tb, int cb, bool multi,
@@ -366,7 +375,8 @@ __global__ __launch_bounds__(NW* kWave) void k_glr_fwd(GlrArgs g, int ncb, int n
 // persistent forward: one workgroup per channel block visits every time tile in
 // order, the state entering the tile carried in LDS, the next tile's rows loaded
 // into registers while the current one is processed; no look-back state and no
-// kernel that resets it.  Used when the channel blocks alone fill the GPU.
+// kernel that resets it.  Used when the channel blocks alone fill the GPU (2048 x 32
+// x 1024 bf16, 256 blocks: 4.1 TB/s).
 // ---------------------------------------------------------------------------
 template <typename IO, int NW, int L, int CPT, bool FULL, int PF, bool NT, bool RST>
 __device__ __forceinline__ void glr_persist_tile(const GlrArgs& g, const GlrChan<CPT>& ch,
@@ -707,7 +717,8 @@ __global__ __launch_bounds__(NW* kWave) void k_glr_bwd(GlrArgs g, int ncb, int n
 // while the current one is processed, the parameters' sums in registers until
 // the end.  As the forward, where the channel blocks alone fill the GPU: a tile's
 // rows and gates take 170 registers, so that a compute unit holds one workgroup
-// either way, and without the prefetch its loads and its arithmetic take turns.
+// either way, and without the prefetch its loads and its arithmetic take turns (308
+// us as look-back tiles against 204 to 218 at 2048 x 32 x 1024 bf16).
 // ---------------------------------------------------------------------------
 template <int NW, int CPT>
 struct GlrWalkShared {
@@ -829,7 +840,9 @@ __global__ __launch_bounds__(256) void k_glr_prep(GlrArgs g, float* __restrict__
 }
 
 // ---------------------------------------------------------------------------
-// single tokens: element-wise over [B, D], the state's row by its slot
+// single tokens: element-wise over [B, D], the state's row by its slot.  One thread
+// an element: at 64 x 1024 the 256 workgroups take 3.2 us, which is a launch and two
+// dependent loads; the caller's side of a call costs four times that.
 // ---------------------------------------------------------------------------
 template <typename IO>
 __global__ __launch_bounds__(256) void k_glr_step(GlrArgs g, const int32_t* __restrict__ slots,

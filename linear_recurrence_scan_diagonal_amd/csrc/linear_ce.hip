@@ -1,23 +1,26 @@
 // linear_ce.hip -- softmax cross entropy of the logits l = x w^T against one
-// class a row, and its gradient, without storing the logits.
+// class a row, and its gradient, without storing all logits.
 //
 //   lse_n = log sum_v exp l_nv,  loss_n = lse_n - l_{n,target},
 //   G = exp(l - lse) - onehot (0 in ignored rows),
 //   grad_x = diag(grad_loss) G w,  grad_w = G^T diag(grad_loss) x.
 //
 // Three products carry the work, all of the form C[m][n] = sum_k A[m][k] B[n][k]
-// with both operands contiguous along k (one matrix-core kernel, k_gemm, with
-// two epilogues):
-//   logits  m = class, n = row, k = feature, A = w, B = x.  A lane of the
-//           32x32 product holds one n and 16 values of m, so the softmax's
-//           maximum and sum over classes run inside a lane.  Each tile leaves
-//           its (maximum, sum) a row, joined afterwards;
-//   grad_w  m = class, n = feature, k = row, A = G^T, B = x^T;
+// (one matrix-core kernel, k_gemm, with two epilogues):
+//   logits  m = class, n = row, k = feature, A = w, B = x.  A lane holds one n and
+//           32 values of m, so most of the softmax's maximum and sum over classes
+//           runs inside a lane.  Each wave leaves the (maximum, sum) of its classes
+//           a row, joined afterwards;
+//   grad_w  m = class, n = feature, k = row, A = G read by columns, B = x^T;
 //   grad_x  m = row, n = feature, k = class, A = G, B = w^T.
 // For the gradient the rows are taken in pieces, whose e = exp(l - tile maximum)
-// is kept (fp16 for bf16 inputs, fp32 for fp32) until lse is known, turned into
-// G and G^T by one pass, and used up by the two gradient products; the piece is
-// chosen so that this stays within a fixed number of bytes.
+// is kept (fp16 for bf16 inputs, fp32 for fp32) until lse is known, turned into G
+// by one pass (for bf16 in place), and used up by the two gradient products; the
+// piece is chosen so that this stays within a fixed number of bytes.
+// What bounds it: the matrix cores' power.  At 16384 x 32768 x 1024 bf16 the
+// products run at 1460 (grad_x), 1400 (grad_w) and 1000 TFLOP/s (logits, with the
+// exponentials) where a large library product reaches 1360 to 1650; the rest, 0.45
+// of 3.1 ms, is k_ce_g and the transposed copies at 5.4 to 6 TB/s.
 // Operands that are not laid out like that (x^T, w^T, rows that are not a whole
 // number of k steps or not 16-byte aligned) are copied once into the workspace.
 //
@@ -31,12 +34,16 @@
 //
 // Rounding.  G is rounded to bf16 (two fp16 parts for fp32 inputs) before the
 // second and third product: an error of 2^-9 an element with random sign, which
-// adds to that of the rounded gradient.  It is rounded unscaled, where the
-// entries that dominate, p - 1 at the target, lie next to -1: scaled by a common
-// grad_loss, they would all be rounded the same way.  grad_x is scaled by row in
-// fp32 afterwards.  grad_w's sum runs over rows, so G^T carries grad_loss / max
-// |grad_loss| (exactly 1 for a mean) and the maximum is applied in fp32 at the
-// end.  Keeping e in fp16 (2^-12) adds 1% to the error of G in bf16.
+// adds to that of the rounded gradient.  The sum of grad_w runs over rows, so each
+// row's grad_loss has to be in one of its factors.  For bf16 G carries the row's
+// share grad_loss / max |grad_loss|, and the maximum is applied in fp32 at the end:
+// the share of a mean is exactly 1, and the entries that dominate, p - 1 at the
+// target, lie next to -1, where they are rounded finely; scaled by a common
+// grad_loss, they would all be rounded the same way.  x stays as it is: rounding it
+// a second time would cost more than it saves.  For fp32 the two parts of x^T carry
+// the share (2^-22 of an element is lost either way) and G none, so that a row with
+// a small grad_loss keeps all digits of its grad_x, which is scaled by grad_loss at
+// the end.  Keeping e in fp16 (2^-12) adds 1% to the error of G in bf16.
 #include "lrs_device.hpp"
 #include "lrs_internal.hpp"
 
@@ -131,18 +138,17 @@ __device__ __forceinline__ void tile_of(const GemmArgs& g, int& tm, int& tn, int
   tm = (int)(grp * 8u + in - (unsigned)tn * gm);
 }
 
-// The piece of 16 bytes at which piece p of row r is kept in LDS is p ^ f(r):
-// the 8 (or 16) rows that a fragment read touches at once then fall on
-// different banks (rows of 128 bytes).
-__device__ __forceinline__ int swizzle(int r) {
-  return (r & 7) ^ ((r >> 3) & 1);
-}
+// The piece of 16 bytes at which piece p of row r is kept in LDS is p ^ swizzle(r):
+// the rows that a fragment read touches at once then fall on different banks (rows
+// of 128 bytes).  Counted: no conflict; with bit 3 of the row in it as well, four
+// of a read's eight cycles (the products take the same time: power bounds them).
+__device__ __forceinline__ int swizzle(int r) { return r & 7; }
 
 // A stored as [k][m]: a stage is 64 rows of TM values, in LDS as rows of TM / 16
 // blocks of 32 bytes, block c of row r at c ^ swizzle_k(r).  The transposing read
 // gives each of 16 lanes one column of four rows that the lanes address together
 // (32 bytes of each); two such groups go through the banks at once, rows 0..3 and
-// 8..11 or the like, which the swizzle puts on eight different blocks.
+// 8..11 or the like, which the swizzle puts on eight different blocks (counted: no conflict).
 __device__ __forceinline__ int swizzle_k(int r) {
   return (r & 3) | ((r >> 3) & 1) << 2;
 }
@@ -757,6 +763,7 @@ __global__ __launch_bounds__(1024) void k_ce_scale(const float* __restrict__ gra
   if (threadIdx.x == 0) *top_out = top;
 }
 
+// Memory bound: 355 us for 1 GiB of e in bf16's case, 6.0 TB/s.
 // e -> G [rows][P][Vp] (row pitch ldg), per_row workgroups a row; rows up to the next
 // multiple of 64 are written as 0, as are rows whose `share` is 0, whatever their e
 // holds.  bf16 (P 1): over e's own fp16 values, G multiplied by the row's share.
@@ -850,8 +857,8 @@ unsigned blocks_for(int64_t n, int64_t per) {
   return (unsigned)(b < 1 ? 1 : b > 65536 ? 65536 : b);
 }
 
-// The tile shapes, with what a product of many tiles of it reaches (TFLOP/s,
-// measured at 8192 x 1024 x 32768) and the workgroups a compute unit holds: 256
+// The tile shapes, with what a product of many tiles of it reaches (TFLOP/s, by
+// which they are compared, measured at 8192 x 1024 x 32768) and the workgroups a compute unit holds: 256
 // x 256 by eight waves of 128 x 64 fills the LDS alone; the others are for
 // products with few tiles, where the largest would leave compute units idle.
 typedef Shape<256, 256, 2, 4, 3, 2, 2> Large;
@@ -922,7 +929,9 @@ hipError_t run(GemmArgs& g, int shape, bool f16, hipStream_t stream) {
 
 }  // namespace
 
-// Pieces of the rows whose G takes at most this many bytes.
+// Pieces of the rows whose G takes at most this many bytes.  Every piece adds its
+// part to an fp32 grad_w: 16384 x 32768 x 1024 bf16 takes 3264 us in two pieces of
+// 512 MiB and 3090 us in one of 1 GiB.
 constexpr int64_t kCePieceBytes = (int64_t)1 << 30;
 
 CePlan plan_ce(int64_t N, int64_t V, int64_t D, int io) {

@@ -297,6 +297,12 @@ int lrs_glr_step(const void* z_r, const void* z_i, const void* x, int64_t ld, co
 
 // -------------------------------------------------------------- layer norm
 
+// A row has 64 threads up to 1024 features (four rows a workgroup), at most 1024
+// beyond.
+static bool ln_grid_ok(int64_t R, int64_t D) {
+  return D <= 1024 ? grid_ok((R + 3) / 4, 256) : grid_ok(R, 1024);
+}
+
 int lrs_layernorm_fwd(const void* x, const void* residual, const float* gamma, const float* beta,
                       void* y, void* sum, float* mean, float* rstd, int64_t R, int64_t D,
                       float eps, int io_dtype, void* stream) {
@@ -318,7 +324,7 @@ int lrs_layernorm_fwd(const void* x, const void* residual, const float* gamma, c
   const Span others[] = {{gamma, db}, {beta, db}, {y, nb}, {mean, rb}, {rstd, rb},
                          {sx ? nullptr : x, nb}, {sr ? nullptr : residual, nb}};
   if (any_overlap(outs, 3, ins, 4) || any_overlap(sums, 1, others, 7)) return LRS_ERR_INVALID_ARG;
-  if (!grid_ok(R, 1024)) return LRS_ERR_UNSUPPORTED;
+  if (!ln_grid_ok(R, D)) return LRS_ERR_UNSUPPORTED;
   return hip_status(lrs::launch_layernorm_fwd(x, residual, gamma, beta, y, sum, mean, rstd, R, D,
                                               eps, io_dtype, (hipStream_t)stream));
 }
@@ -359,7 +365,7 @@ int lrs_layernorm_bwd(const void* s, const float* gamma, const float* mean, cons
   const Span outs[] = {{grad_x, nb}, {grad_gamma, db}, {grad_beta, db}};
   if (any_overlap(outs, 3, ins, 6)) return LRS_ERR_INVALID_ARG;
   const int64_t blocks = lrs::ln_bwd_blocks(R, D);
-  if (!grid_ok(R, 1024) || D > ((int64_t)1 << 31)) return LRS_ERR_UNSUPPORTED;
+  if (!ln_grid_ok(R, D) || D > ((int64_t)1 << 31)) return LRS_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < lrs_layernorm_bwd_workspace_bytes(R, D))
     return LRS_ERR_WORKSPACE;
   Carve cv(align_ptr(workspace));

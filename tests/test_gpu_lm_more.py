@@ -281,3 +281,15 @@ def test_classes_of_minus_infinity():
     want = torch.logsumexp(x.double() @ w.double().t(), 1)
     assert ((lse.double() - want).abs() <= 1e-5 * (1 + want.abs())).all()
     assert torch.isfinite(loss).all()
+
+
+def test_many_short_rows():
+    """Five million rows of 16 features: more than 2^32 / 1024."""
+    R, D = 5_000_000, 16
+    x, gamma, beta = rand(R, D, dtype=torch.bfloat16), 1 + 0.1 * rand(D, seed=1), rand(D, seed=2)
+    y, _, mean, rstd = lrs.layernorm_fwd(x, gamma, beta, save=True)
+    gx, _, _ = lrs.layernorm_bwd(x, gamma, mean, rstd, y)
+    part = slice(R - 1000, R)
+    ty, _, tm, tr = lrs.layernorm_fwd(x[part], gamma, beta, save=True)
+    tgx, _, _ = lrs.layernorm_bwd(x[part], gamma, tm, tr, ty)
+    assert torch.equal(y[part], ty) and torch.equal(gx[part], tgx)
