@@ -9,8 +9,9 @@
 // The recurrence is an affine map a step, so the tiles, the look-back and the
 // persistent walk are those of the other [T, B, D] layers (lrs_tbd.hpp); the
 // gates are evaluated once an element next to their loads.  With resets the
-// maps compose through affine<true>, which lets a factor of 0 replace the state
-// rather than multiply it: a NaN or an infinity of one document stays there.
+// maps compose through affine<true> and scale<true>, which let a factor of 0 replace
+// the state rather than multiply it, and stay 0 next to any other factor: a NaN or an
+// infinity of one document stays there, a gate that is NaN included.
 //
 // Inputs are rows of a wider projection (pitch ld): a lane's channels are at
 // b * ld + d of a row, computed once a thread.  A lane has two channels, read as
@@ -205,18 +206,8 @@ __device__ __forceinline__ void glr_cut(const uint8_t* reset, int64_t row, const
   }
 }
 
-// a * x, and one step a * x + b, where with SEL a factor of 0 gives 0 whatever x
-// is (the "legacy" product's rule: two instructions a step, where affine's
-// compare and select make three).
-template <bool SEL>
-__device__ __forceinline__ float scale(float a, float x) {
-  if constexpr (SEL) {
-    float r;
-    asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(x));
-    return r;
-  }
-  return a * x;
-}
+// One step a * x + b, where with SEL a factor of 0 gives b whatever x is (the legacy
+// product: two instructions a step, where affine's compare and select make three).
 template <bool SEL>
 __device__ __forceinline__ float step(float a, float x, float b) {
   return SEL ? scale<SEL>(a, x) + b : __builtin_fmaf(a, x, b);
@@ -291,7 +282,7 @@ __device__ __forceinline__ void glr_fold(const float (&av)[L][CPT], const float 
 #pragma unroll
     for (int i = 1; i < L; ++i) {
       B[k] = step<SEL>(av[i][k], B[k], bv[i][k]);
-      A[k] = A[k] * av[i][k];
+      A[k] = scale<SEL>(A[k], av[i][k]);
     }
   }
 }
@@ -514,7 +505,7 @@ __device__ __forceinline__ void glr_bwd_fold(const IoRow<IO, CPT> (&x)[L],
     for (int i = 0; i < L; ++i) {
       const float b = m[i][k] * gi[i][k] * x[i].get(k);  // 0 past the end (x reads as 0 there)
       FB[k] = i == 0 ? b : step<RST>(av[i][k], FB[k], b);
-      FA[k] = i == 0 ? av[i][k] : FA[k] * av[i][k];
+      FA[k] = i == 0 ? av[i][k] : scale<RST>(FA[k], av[i][k]);
     }
     // y passed on: lam_{L-1} = gh_{L-1} + y_in, lam_i = gh_i + a_{i+1} lam_{i+1},
     // y_out = a_0 lam_0 (gh and a are 0 and 1 past the end)
@@ -523,9 +514,9 @@ __device__ __forceinline__ void glr_bwd_fold(const IoRow<IO, CPT> (&x)[L],
 #pragma unroll
     for (int i = L - 2; i >= 0; --i) {
       B[k] = step<RST>(av[i + 1][k], B[k], gh[i].get(k));
-      A[k] = A[k] * av[i + 1][k];
+      A[k] = scale<RST>(A[k], av[i + 1][k]);
     }
-    A[k] = A[k] * av[0][k];
+    A[k] = scale<RST>(A[k], av[0][k]);
     B[k] = scale<RST>(av[0][k], B[k]);
   }
 }

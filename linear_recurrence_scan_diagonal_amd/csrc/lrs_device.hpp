@@ -214,6 +214,17 @@ __device__ __forceinline__ float affine(float a, float x, float b) {
   const float y = __builtin_fmaf(a, x, b);
   return SEL && a == 0.0f ? b : y;
 }
+// Its factor after another one's, a*b.  SEL: 0 if either is 0 (0 * NaN would be NaN,
+// and the restart in it lost), by the "legacy" product, whose rule that is.
+template <bool SEL>
+__device__ __forceinline__ float scale(float a, float b) {
+  if constexpr (SEL) {
+    float r;
+    asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+  }
+  return a * b;
+}
 
 // Lane-parallel form for the feature-contiguous kernels: each lane resolves
 // one channel of its own, groups of G blocks.  The lane loads every word it

@@ -181,7 +181,7 @@ constexpr int kColGroup = 8;
 // per-channel maps, run the look-back (multi-block) and share the carries; every
 // wave then composes the maps of the waves before it (wave order = scan order).
 // st points at this channel block's status row for time block 0; time blocks
-// are CW words apart.  SEL: maps with a factor of 0 replace the state (affine).
+// are CW words apart.  SEL: maps with a factor of 0 replace the state (affine, scale).
 // G: time blocks of a look-back group.
 template <int NW, int CPT, bool SEL = false, int G = kColGroup>
 __device__ __forceinline__ void col_enter_state(const float (&A)[CPT], const float (&B)[CPT],
@@ -211,7 +211,7 @@ __device__ __forceinline__ void col_enter_state(const float (&A)[CPT], const flo
       for (int w = 0; w < NW; ++w) {
         const float wa = s.A[w][j], wb = s.B[w][j];
         TB = affine<SEL>(wa, TB, wb);
-        TA = TA * wa;
+        TA = scale<SEL>(TA, wa);
       }
       float x_in = 0.0f;
       if (j < cvalid) {
@@ -238,7 +238,7 @@ __device__ __forceinline__ void col_enter_state(const float (&A)[CPT], const flo
     for (int k = 0; k < CPT; ++k) {
       const float wa = s.A[w][j0 + k], wb = s.B[w][j0 + k];
       PB[k] = affine<SEL>(wa, PB[k], wb);
-      PA[k] = PA[k] * wa;
+      PA[k] = scale<SEL>(PA[k], wa);
     }
   }
 #pragma unroll
@@ -274,7 +274,7 @@ struct PersistShared {
 
 // Publish this wave's per-channel maps (A, B) and return in x the state
 // entering this wave's first step: the maps of the earlier waves of the tile,
-// in order, applied to the carry.  par: the tile's parity.  SEL as in affine.
+// in order, applied to the carry.  par: the tile's parity.  SEL as above.
 template <int NW, int CPT, bool SEL = false>
 __device__ __forceinline__ void persist_enter(const float (&A)[CPT], const float (&B)[CPT],
                                               PersistShared<NW, CPT>& s, int wid, uint32_t off,
@@ -290,7 +290,7 @@ __device__ __forceinline__ void persist_enter(const float (&A)[CPT], const float
     float PA = 1.0f, PB = 0.0f;
     for (int w = 0; w < wid; ++w) {
       PB = affine<SEL>(s.A[par][w][off + k], PB, s.B[par][w][off + k]);
-      PA = PA * s.A[par][w][off + k];
+      PA = scale<SEL>(PA, s.A[par][w][off + k]);
     }
     x[k] = affine<SEL>(PA, s.carry[par][off + k], PB);
   }
