@@ -9,9 +9,10 @@
 // The recurrence is an affine map a step, so the tiles, the look-back and the
 // persistent walk are those of the other [T, B, D] layers (lrs_tbd.hpp); the
 // gates are evaluated once an element next to their loads.  With resets the
-// maps compose through affine<true> and scale<true>, which let a factor of 0 replace
-// the state rather than multiply it, and stay 0 next to any other factor: a NaN or an
-// infinity of one document stays there, a gate that is NaN included.
+// maps compose through affine<true> and factor<true>, which let a factor of 0 replace
+// the state rather than multiply it, next to any other factor, and keep the factors of a
+// document from rounding to 0: a NaN or an infinity of one document stays there, a gate
+// that is NaN included, and stays to its end.
 //
 // Inputs are rows of a wider projection (pitch ld): a lane's channels are at
 // b * ld + d of a row, computed once a thread.  A lane has two channels, read as
@@ -164,7 +165,7 @@ __device__ __forceinline__ void glr_decay(float t, float& a, float& m2) {
   }
   const float far = __builtin_amdgcn_exp2f(-kLog2e * t);
   const bool near = t < 0.125f;
-  a = near ? 1.0f - e : far;
+  a = near ? 1.0f - e : far + kLeastFactor;  // not 0, which is a restart
   m2 = near ? e * (2.0f - e) : __builtin_fmaf(-far, far, 1.0f);
 }
 
@@ -279,11 +280,14 @@ __device__ __forceinline__ void glr_fold(const float (&av)[L][CPT], const float 
   for (int k = 0; k < CPT; ++k) {
     A[k] = av[0][k];
     B[k] = bv[0][k];
+    float least = av[0][k];
 #pragma unroll
     for (int i = 1; i < L; ++i) {
       B[k] = step<SEL>(av[i][k], B[k], bv[i][k]);
-      A[k] = scale<SEL>(A[k], av[i][k]);
+      A[k] = A[k] * av[i][k];
+      least = fminf(least, av[i][k]);
     }
+    A[k] = factor<SEL>(A[k], least);
   }
 }
 
@@ -501,22 +505,21 @@ __device__ __forceinline__ void glr_bwd_fold(const IoRow<IO, CPT> (&x)[L],
                                              float (&FB)[CPT], float (&A)[CPT], float (&B)[CPT]) {
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
+    float least = av[0][k];
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       const float b = m[i][k] * gi[i][k] * x[i].get(k);  // 0 past the end (x reads as 0 there)
       FB[k] = i == 0 ? b : step<RST>(av[i][k], FB[k], b);
-      FA[k] = i == 0 ? av[i][k] : scale<RST>(FA[k], av[i][k]);
+      FA[k] = i == 0 ? av[i][k] : FA[k] * av[i][k];
+      least = fminf(least, av[i][k]);
     }
+    FA[k] = factor<RST>(FA[k], least);
     // y passed on: lam_{L-1} = gh_{L-1} + y_in, lam_i = gh_i + a_{i+1} lam_{i+1},
-    // y_out = a_0 lam_0 (gh and a are 0 and 1 past the end)
-    A[k] = 1.0f;
+    // y_out = a_0 lam_0 (gh and a are 0 and 1 past the end): the same factor
+    A[k] = FA[k];
     B[k] = gh[L - 1].get(k);
 #pragma unroll
-    for (int i = L - 2; i >= 0; --i) {
-      B[k] = step<RST>(av[i + 1][k], B[k], gh[i].get(k));
-      A[k] = scale<RST>(A[k], av[i + 1][k]);
-    }
-    A[k] = scale<RST>(A[k], av[0][k]);
+    for (int i = L - 2; i >= 0; --i) B[k] = step<RST>(av[i + 1][k], B[k], gh[i].get(k));
     B[k] = scale<RST>(av[0][k], B[k]);
   }
 }

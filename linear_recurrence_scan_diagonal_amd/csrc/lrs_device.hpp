@@ -214,8 +214,8 @@ __device__ __forceinline__ float affine(float a, float x, float b) {
   const float y = __builtin_fmaf(a, x, b);
   return SEL && a == 0.0f ? b : y;
 }
-// Its factor after another one's, a*b.  SEL: 0 if either is 0 (0 * NaN would be NaN,
-// and the restart in it lost), by the "legacy" product, whose rule that is.
+// a*b, with SEL 0 if either is 0 whatever the other is: the "legacy" product, whose
+// rule that is.
 template <bool SEL>
 __device__ __forceinline__ float scale(float a, float b) {
   if constexpr (SEL) {
@@ -224,6 +224,17 @@ __device__ __forceinline__ float scale(float a, float b) {
     return r;
   }
   return a * b;
+}
+// The factor of several maps in sequence, from the product of theirs and the least of
+// them.  SEL: 0 where one of them is 0 (next to a NaN the product would be NaN, and the
+// restart lost), and nowhere else: a product of small factors that rounds to 0 would cut
+// off a NaN in the middle of its document.  The smallest normal number added to every
+// other product keeps it from 0, and leaves NaN and whatever is above 2^-102 as it is.
+constexpr float kLeastFactor = 0x1p-126f;
+template <bool SEL>
+__device__ __forceinline__ float factor(float product, float least) {
+  if constexpr (SEL) return least == 0.0f ? 0.0f : product + kLeastFactor;
+  return product;
 }
 
 // Lane-parallel form for the feature-contiguous kernels: each lane resolves

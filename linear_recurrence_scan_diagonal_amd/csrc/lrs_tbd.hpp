@@ -181,7 +181,7 @@ constexpr int kColGroup = 8;
 // per-channel maps, run the look-back (multi-block) and share the carries; every
 // wave then composes the maps of the waves before it (wave order = scan order).
 // st points at this channel block's status row for time block 0; time blocks
-// are CW words apart.  SEL: maps with a factor of 0 replace the state (affine, scale).
+// are CW words apart.  SEL: maps with a factor of 0 replace the state (affine, factor).
 // G: time blocks of a look-back group.
 template <int NW, int CPT, bool SEL = false, int G = kColGroup>
 __device__ __forceinline__ void col_enter_state(const float (&A)[CPT], const float (&B)[CPT],
@@ -207,12 +207,14 @@ __device__ __forceinline__ void col_enter_state(const float (&A)[CPT], const flo
       // lane: the look-back's registers stay off the other waves' paths, and
       // each wave's status words are contiguous (whole cache lines)
       const int j = (wid - (NW - CPT)) * kWave + lane;
-      float TA = 1.0f, TB = 0.0f;
+      float TA = 1.0f, TB = 0.0f, least = 1.0f;
       for (int w = 0; w < NW; ++w) {
         const float wa = s.A[w][j], wb = s.B[w][j];
         TB = affine<SEL>(wa, TB, wb);
-        TA = scale<SEL>(TA, wa);
+        TA = TA * wa;
+        least = fminf(least, wa);
       }
+      TA = factor<SEL>(TA, least);
       float x_in = 0.0f;
       if (j < cvalid) {
         const bool gend = group_end(tb, G);
@@ -230,6 +232,15 @@ __device__ __forceinline__ void col_enter_state(const float (&A)[CPT], const flo
 #pragma unroll
     for (int k = 0; k < CPT; ++k) carry[k] = x0[k];
   }
+  if constexpr (SEL) {  // one map after the other: a factor of 0 is a restart
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) x[k] = carry[k];
+    for (int w = 0; w < wid; ++w) {
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) x[k] = affine<SEL>(s.A[w][j0 + k], x[k], s.B[w][j0 + k]);
+    }
+    return;
+  }
   float PA[CPT], PB[CPT];
 #pragma unroll
   for (int k = 0; k < CPT; ++k) { PA[k] = 1.0f; PB[k] = 0.0f; }
@@ -237,12 +248,12 @@ __device__ __forceinline__ void col_enter_state(const float (&A)[CPT], const flo
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
       const float wa = s.A[w][j0 + k], wb = s.B[w][j0 + k];
-      PB[k] = affine<SEL>(wa, PB[k], wb);
-      PA[k] = scale<SEL>(PA[k], wa);
+      PB[k] = __builtin_fmaf(wa, PB[k], wb);
+      PA[k] = PA[k] * wa;
     }
   }
 #pragma unroll
-  for (int k = 0; k < CPT; ++k) x[k] = affine<SEL>(PA[k], carry[k], PB[k]);
+  for (int k = 0; k < CPT; ++k) x[k] = __builtin_fmaf(PA[k], carry[k], PB[k]);
 }
 
 template <int NW, int CPT>
@@ -287,12 +298,18 @@ __device__ __forceinline__ void persist_enter(const float (&A)[CPT], const float
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
+    if constexpr (SEL) {  // one map after the other
+      x[k] = s.carry[par][off + k];
+      for (int w = 0; w < wid; ++w)
+        x[k] = affine<SEL>(s.A[par][w][off + k], x[k], s.B[par][w][off + k]);
+      continue;
+    }
     float PA = 1.0f, PB = 0.0f;
     for (int w = 0; w < wid; ++w) {
-      PB = affine<SEL>(s.A[par][w][off + k], PB, s.B[par][w][off + k]);
-      PA = scale<SEL>(PA, s.A[par][w][off + k]);
+      PB = __builtin_fmaf(s.A[par][w][off + k], PB, s.B[par][w][off + k]);
+      PA = PA * s.A[par][w][off + k];
     }
-    x[k] = affine<SEL>(PA, s.carry[par][off + k], PB);
+    x[k] = __builtin_fmaf(PA, s.carry[par][off + k], PB);
   }
 }
 

@@ -90,3 +90,22 @@ def test_whole_rows_of_nan(size, dtype):
         for z in parts:
             z[t, b] = float("nan")
     check(parts, p, s, reset)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("decay", [2.0, 30.0])
+def test_only_a_restart_cuts(size, dtype, decay):
+    """A short memory (a = exp(-17 r), and exp(-240 r) that fp32 rounds to 0) lets a
+    finite state fade, but a NaN stays to the end of its document, whether the call
+    has restarts or not; so does one of the gradient to the document's beginning."""
+    T, B, D = SIZES[size]
+    parts, p, s = make(T, B, D, dtype, seed=T + 2, decay=decay)
+    reset = torch.zeros((T, B), dtype=torch.uint8, device=DEV)
+    reset[T - 20] = 1
+    parts[2][5, 0, 3] = float("nan")
+    parts[0][7, B - 1, 8] = float("nan")
+    s["gh"][T - 40, B // 2, 11] = float("nan")
+    got, ref = check(parts, p, s, reset)
+    assert np.isnan(ref["h"][5:T - 20, 0, 3]).all() and np.isfinite(ref["h"][T - 20:]).all()
+    assert np.isnan(ref["grad_x"][:T - 39, B // 2, 11]).all()
