@@ -585,7 +585,7 @@ __device__ __forceinline__ void glr_bwd_walk(const GlrArgs& g, const GlrChan<CPT
       const float dgx = lam * mm;
       dx[k] = dgx * gi[i][k];
       di[k] = dgx * u * (1.0f - gi[i][k]);
-      const float rm = __builtin_amdgcn_rcpf(fmaxf(mm, 1e-30f));  // m = 0: with r = 0 below
+      const float rm = mm == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(mm);
       const float dla = scale<RST>(a, lam * __builtin_fmaf(-a * rm, u, hp[i][k]));
       const float dlr = dla * r[i][k];
       dr[k] = -dlr * ch.k[k] * (1.0f - r[i][k]);  // la = -k r
