@@ -55,6 +55,29 @@ DECAYS = {"long": lambda D: torch.linspace(-6.0, -4.4, D), "short": lambda D: to
           "mixed": lambda D: torch.linspace(-6.0, 3.0, D)[torch.randperm(D, generator=torch.Generator().manual_seed(1))]}
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("memory", DECAYS)
+@pytest.mark.parametrize("restart", [0.0, 0.03])
+def test_memories(size, dtype, memory, restart):
+    T, B, D = SIZES[size]
+    parts, p, rest = make(T, B, D, dtype, T + D, DECAYS[memory])
+    reset = None
+    if restart:
+        g = torch.Generator().manual_seed(T)
+        reset = (torch.rand(T, B, generator=g) < restart).to(torch.uint8).to(DEV)
+    check(parts, p, reset, *rest)
+
+
+def test_the_border_of_the_two_forms():
+    """k a hair below and above 1/8: no step between the forms."""
+    T, B, D = 200, 2, 128
+    border = float(np.log(np.expm1(1.0 / 64.0)))  # 8 softplus = 1/8
+    for seed, side in enumerate((-1e-4, 1e-4)):
+        parts, p, rest = make(T, B, D, torch.float32, seed, lambda D: torch.full((D,), border + side))
+        check(parts, p, None, *rest)
+
+
 @pytest.mark.parametrize("size", SIZES)
 def test_closed_gates_with_large_inputs(size):
     """A gate closed to the last bit has a = 1 and m = 0: nothing of x enters, however
