@@ -542,12 +542,24 @@ __device__ __forceinline__ void keep_packed(IoRow<uint16_t, 1> (&x)[L], IoRow<ui
 template <int L, int CPT>
 __device__ __forceinline__ void keep_packed(IoRow<float, CPT> (&)[L], IoRow<float, CPT> (&)[L]) {}
 
-template <int CPT>
+// Sums for bias_r, bias_i and k: S = float over a wave's rows of a tile, and S = double
+// over the tiles of a persistent walk, whose number has no bound (fp32 would lose 7e-5
+// of 40000 equal terms).
+template <int CPT, typename S = float>
 struct GlrSums {
-  float r[CPT], i[CPT], d[CPT];  // for bias_r, bias_i and k
+  S r[CPT], i[CPT], d[CPT];
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int k = 0; k < CPT; ++k) r[k] = i[k] = d[k] = 0.0f;
+    for (int k = 0; k < CPT; ++k) r[k] = i[k] = d[k] = 0;
+  }
+  template <typename T>
+  __device__ __forceinline__ void add(const GlrSums<CPT, T>& s) {
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) {
+      r[k] += (S)s.r[k];
+      i[k] += (S)s.i[k];
+      d[k] += (S)s.d[k];
+    }
   }
 };
 
@@ -607,18 +619,18 @@ __device__ __forceinline__ void glr_bwd_walk(const GlrArgs& g, const GlrChan<CPT
 
 // The waves' sums of a workgroup, added in wave order, to row `slot` of the
 // partial sums' `slots` rows.
-template <int NW, int CPT>
+template <int NW, int CPT, typename S>
 __device__ __forceinline__ void glr_bwd_sums(const GlrArgs& g, const GlrChan<CPT>& ch,
-                                             const GlrSums<CPT>& sum,
+                                             const GlrSums<CPT, S>& sum,
                                              float (&red)[3][NW][kWave * CPT], int wid, uint32_t off,
                                              int64_t cbase, int64_t slot, int64_t slots) {
   constexpr int CW = kWave * CPT;
   const int64_t C = g.B * g.D;
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
-    red[0][wid][off + k] = sum.r[k];
-    red[1][wid][off + k] = sum.i[k];
-    red[2][wid][off + k] = sum.d[k] * g.rates[g.D + ch.d[k]];  // with d k / d decay
+    red[0][wid][off + k] = (float)sum.r[k];
+    red[1][wid][off + k] = (float)sum.i[k];
+    red[2][wid][off + k] = (float)(sum.d[k] * g.rates[g.D + ch.d[k]]);  // with d k / d decay
   }
   __syncthreads();
   for (int j = threadIdx.x; j < 3 * CW; j += NW * kWave) {
@@ -682,7 +694,7 @@ __device__ __forceinline__ void glr_bwd_tile(const GlrArgs& g, int tb, int ntb, 
     for (int k = 0; k < CPT; ++k)
       if (k < nvc) g.grad_h0[c0 + k] = y[k];
   }
-  glr_bwd_sums<NW, CPT>(g, ch, sum, f.red, wid, off, cbase, ptb, ntb);
+  glr_bwd_sums<NW>(g, ch, sum, f.red, wid, off, cbase, ptb, ntb);
 }
 
 template <typename IO, int NW, int L, int CPT, bool NT, bool RST>
@@ -723,8 +735,8 @@ struct GlrWalkShared {
 template <typename IO, int NW, int L, int CPT, bool FULL, int PF, bool NT, bool RST>
 __device__ __forceinline__ void glr_bwd_persist_tile(
     const GlrArgs& g, const GlrChan<CPT>& ch, const uint32_t (&go)[CPT], int64_t row0, int64_t cbase,
-    uint32_t off, int nvc, GlrBwdRows<IO, L, CPT>& w, float (&ck)[CPT], GlrSums<CPT>& sum,
-    GlrWalkShared<NW, CPT>& s, int wid, int par) {
+    uint32_t off, int nvc, GlrBwdRows<IO, L, CPT>& w, float (&ck)[CPT],
+    GlrSums<CPT, double>& sum, GlrWalkShared<NW, CPT>& s, int wid, int par) {
   float r[L][CPT], gi[L][CPT], av[L][CPT], m[L][CPT];
   float FA[CPT], FB[CPT], A[CPT], B[CPT], y[CPT], hs[CPT];
   if (ch.near) glr_gates<true, IO, L, CPT, FULL>(g, ch, row0, nvc, w.in, r, gi, av, m);
@@ -756,7 +768,10 @@ __device__ __forceinline__ void glr_bwd_persist_tile(
     for (int k = 0; k < CPT; ++k)
       hs[k] = affine<RST>(s.fA[par][v][off + k], hs[k], s.fB[par][v][off + k]);
   }
-  glr_bwd_walk<IO, L, CPT, FULL, NT, RST>(g, ch, go, row0, nvc, x, gh, r, gi, av, m, hs, y, sum);
+  GlrSums<CPT> tile;
+  tile.clear();
+  glr_bwd_walk<IO, L, CPT, FULL, NT, RST>(g, ch, go, row0, nvc, x, gh, r, gi, av, m, hs, y, tile);
+  sum.add(tile);
   persist_advance<NW, CPT>(y, s.y, wid, off, par);
 }
 
@@ -783,7 +798,7 @@ __global__ __launch_bounds__(NW* kWave) void k_glr_bwd_persist(GlrArgs g) {
     go[k] = (ch.b[k] * (uint32_t)g.ld_grad + ch.d[k]) * (uint32_t)sizeof(IO);
   const int64_t ntb = (g.T + TW - 1) / TW;
   const int64_t w0 = (int64_t)(NW - 1 - wid) * L;
-  GlrSums<CPT> sum;
+  GlrSums<CPT, double> sum;
   sum.clear();
   GlrBwdRows<IO, L, CPT> w;
   float ck[CPT];
@@ -813,7 +828,7 @@ __global__ __launch_bounds__(NW* kWave) void k_glr_bwd_persist(GlrArgs g) {
     LRS_TILE(false, 0, tb);
   }
 #undef LRS_TILE
-  glr_bwd_sums<NW, CPT>(g, ch, sum, red, wid, off, cbase, 0, 1);
+  glr_bwd_sums<NW>(g, ch, sum, red, wid, off, cbase, 0, 1);
   if (g.grad_h0)  // past a barrier
     for (int j = threadIdx.x; j < CW; j += NW * kWave)
       if (cbase + j < C) g.grad_h0[cbase + j] = s.y.carry[ntb & 1][j];

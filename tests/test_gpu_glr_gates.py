@@ -78,6 +78,27 @@ def test_the_border_of_the_two_forms():
         check(parts, p, None, *rest)
 
 
+def test_parameter_gradients_of_a_long_walk():
+    """40000 steps of constant inputs, 32768 channels: every term of a parameter's
+    gradient has the same sign and nearly the same value, so a running fp32 sum would
+    lose up to 1e-4 of it.  All 512 sequences are alike."""
+    T, B, D = 40_000, 512, 64
+    g = torch.Generator().manual_seed(0)
+    rows = [(torch.randn(D, generator=g).abs() + 0.25).bfloat16() for _ in range(4)]  # z_r, z_i, x, grad_h
+    p = {"bias_r": 0.3 * torch.randn(D, generator=g), "bias_i": 0.3 * torch.randn(D, generator=g),
+         "decay": torch.linspace(-4.0, 0.0, D)}
+    one = [f64(v)[None, None].repeat(T, 0) for v in rows]
+    ref = R.glr(*one[:3], *(f64(v) for v in p.values()), 8.0, gh=one[3])
+    zr, zi, x, gh = (v.to(DEV).expand(T, B, D).contiguous() for v in rows)
+    p = {k: v.to(DEV) for k, v in p.items()}
+    ck = lrs.glr_checkpoints(zr)
+    lrs.glr_fwd(zr, zi, x, **p, checkpoints=ck)
+    grads = lrs.glr_bwd(zr, zi, x, **p, checkpoints=ck, grad_h=gh)
+    for name, t in list(zip(NAMES, grads))[3:6]:
+        off = np.abs(f64(t) / B - ref[name]) / ref["scale_" + name]
+        assert off.max() <= 1e-5, (name, off.max())
+
+
 @pytest.mark.parametrize("size", SIZES)
 def test_closed_gates_with_large_inputs(size):
     """A gate closed to the last bit has a = 1 and m = 0: nothing of x enters, however
