@@ -43,7 +43,7 @@
 // a second time would cost more than it saves.  For fp32 the two parts of x^T carry
 // the share (2^-22 of an element is lost either way) and G none, so that a row with
 // a small grad_loss keeps all digits of its grad_x, which is scaled by grad_loss at
-// the end.  Keeping e in fp16 (2^-12) adds 1% to the error of G in bf16.
+// the end.  Keeping e in fp16 (2^-12, see kLift) adds 1% to the error of G in bf16.
 #include "lrs_device.hpp"
 #include "lrs_internal.hpp"
 
@@ -64,6 +64,16 @@ constexpr float kGScale = 16384.0f;
 
 // What a logits tile leaves besides its maximum and sum.
 enum { kKeepNone = 0, kKeepF16 = 1, kKeepF32 = 2 };
+// e = 2^kLift exp(l - tile maximum).  fp16 (bf16 inputs) has all of its digits down to
+// 2^-14: lifted by 15, a class keeps them to 2^-29 of its tile's largest (20 nats) and
+// is 0 from 2^-40 on (27.7 nats).  The largest is a power of two, so that p - 1 of a
+// target that is nearly certain loses nothing to fp16.
+template <int KEEP>
+constexpr float kLift = KEEP == kKeepF16 ? 15.0f : 0.0f;
+// Maxima from here on are subtracted from the logits before the exponential's product
+// (one instruction a logit): in 2^(l log2 e - mx log2 e) the second product's rounding
+// would be an error of 2e-6 of e and grow with mx.
+constexpr float kLargeLogit = 32.0f;
 enum { kEpiLogits = 0, kEpiOut = 1 };
 // How A is stored: [m][k], or [k][m].
 enum { kRowsM = 0, kRowsK = 1 };
@@ -81,7 +91,7 @@ struct GemmArgs {
   float2* part;     // [N][tm WM]: maximum and sum of each wave's classes
   float* tlogit;    // [N]: the target's logit
   const float *a_unscale, *b_unscale;  // [M to a whole tile], [N]: powers of two (fp32 operands)
-  void* e;          // [N][lde]: exp(l - tile maximum), fp16 or fp32
+  void* e;          // [N][lde]: 2^kLift exp(l - tile maximum), fp16 or fp32
   int64_t lde;
   // products
   float* slots;        // [splits][M][N] fp32, or null
@@ -466,17 +476,27 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
       mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
       // no class, or every logit -inf: all e are 0
-      const float top2 = mx == -__builtin_inff() ? 0.0f : mx * kLog2eF;
+      float ref = mx == -__builtin_inff() ? 0.0f : mx;
+      if (__ballot(fabsf(ref) >= kLargeLogit)) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[j][e] -= ref;
+        ref = 0.0f;
+      }
+      const float lift = __builtin_fmaf(-ref, kLog2eF, kLift<KEEP>);
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < MT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          v[j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[j][e], kLog2eF, -top2));
+          v[j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[j][e], kLog2eF, lift));
           sum += v[j][e];
         }
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
+      // the sum to mx itself: without the lift as the exponents had it, rounding and all
+      sum *= __builtin_amdgcn_exp2f(-__builtin_fmaf(ref, kLog2eF, lift));
       if (lane < 16 && n < g.N) g.part[n * waves + wave] = make_float2(mx, sum);
       if constexpr (KEEP == kKeepF16) {
         uint16_t* mine = keep + q * 16 * PG;
@@ -789,7 +809,8 @@ __global__ __launch_bounds__(256) void k_ce_g(const E* e, int64_t lde, const flo
     uint32_t q[P][4] = {};
     if (share != 0.0f && v < tiles * tile_m) {
       // eight classes lie inside one tile of the logits
-      const float f = __builtin_amdgcn_exp2f((part[n * tiles + v / tile_m].x - own) * kLog2eF);
+      const float f = __builtin_amdgcn_exp2f(
+          __builtin_fmaf(part[n * tiles + v / tile_m].x - own, kLog2eF, -kLift<P == 1 ? kKeepF16 : kKeepF32>));
       float ev[8];
       if constexpr (sizeof(E) == 2) {
         const u32x4_t w = *reinterpret_cast<const u32x4_t*>(e + n * lde + v);
