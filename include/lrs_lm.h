@@ -8,7 +8,8 @@
  * The conventions of lrs.h hold: device pointers owned by the caller, a
  * caller's workspace sized by a query, an opaque stream, error codes and no
  * exceptions, arguments validated before any launch, element type LRS_F32 or
- * LRS_BF16 with fp32 state, statistics, parameters and arithmetic, and results
+ * LRS_BF16 with fp32 state, statistics, parameters and arithmetic (the products
+ * of the cross entropy take 16-bit factors, as described there), and results
  * that are bitwise the same from call to call.  Outputs must not overlap
  * inputs or other outputs unless a function says so.
  */
@@ -122,7 +123,11 @@ LRS_API int lrs_layernorm_bwd(const void *s, const float *gamma, const float *me
  * made tile by tile on the matrix cores and never stored.
  * x: [N,D], w: [V,D], I/O type.  target: [N] int64.  loss, lse: [N] fp32.
  * fp32 operands are split into two scaled fp16 parts and multiplied in three
- * products, which neglects 2^-22 of the result.
+ * products.  A sum of products is then off by up to 2^-21 of the sum of its
+ * absolute terms (not of the result, which may cancel), and a value below 2^-17
+ * of the largest it is scaled with is known to 2^-39 of that: the largest of its
+ * row for the logits, of the whole array for the gradients.  An infinity in an
+ * fp32 operand counts as NaN.
  * Supported while N, V and D stay below 2^21.
  * The workspace query takes whether the call makes the gradient. */
 LRS_API size_t lrs_linear_ce_workspace_bytes(int64_t N, int64_t V, int64_t D, int io_dtype,
@@ -139,6 +144,7 @@ LRS_API int lrs_linear_ce_fwd(const void *x, const void *w, const int64_t *targe
  * for bf16 inputs, from exponentials kept in fp16: a class more than 20 nats
  * below the likeliest of the 32 to 128 classes next to it begins to lose
  * digits in that row's gradient, and has none from 27 nats on.
+ * For fp32 inputs G is known to 2^-22 of itself or to 2^-50.
  * lse: as lrs_linear_ce_fwd wrote it.  grad_loss: [N] fp32. */
 LRS_API int lrs_linear_ce_bwd(const void *x, const void *w, const int64_t *target,
                               const float *lse, const float *grad_loss, void *grad_x,

@@ -27,10 +27,11 @@
 // fp32 operands are two fp16 parts, hi + lo = x to 2^-22, scaled by a power of
 // two that brings the row's (x and w as rows) or the array's (transposed) largest
 // value near fp16's largest, so that the parts' range is no limit: what is lost
-// is 2^-22 of an element or 2^-39 of the largest.  A product is the three part
-// products hi hi + hi lo + lo hi (a loop of the same kernel over pairs of parts),
-// about as exact as fp32 and, at the matrix cores' fp16 rate, five times as fast
-// as their fp32 rate.
+// is 2^-22 of an element or 2^-39 of the largest (for G 2^-50, see kLowLift).  A
+// product is the three part products hi hi + hi lo + lo hi (a loop of the same
+// kernel over pairs of parts), about as exact as fp32 and, at the matrix cores' fp16
+// rate, five times as fast as their fp32 rate.  An infinity has no such parts: it makes
+// NaN of its row's or class's logits.
 //
 // Rounding.  G is rounded to bf16 (two fp16 parts for fp32 inputs) before the
 // second and third product: an error of 2^-9 an element with random sign, which
@@ -59,8 +60,12 @@ typedef short s16x8_t __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2eF = 1.4426950408889634f;
 constexpr int kMaxPairs = 3;
-// fp32 inputs: G's parts are of G * 2^14.
-constexpr float kGScale = 16384.0f;
+// fp32 inputs: G's parts are of G * 2^14, the low one times 2^11 besides, where fp16 has
+// digits for it (it is at most 2^-11 of the high one); its partner in the products is the
+// other operand's high part over 2^11, a third part of x^T and w^T.  So G, whose elements
+// are as small as the classes are rare, is known to 2^-22 or 2^-50, whichever is more,
+// where unlifted parts end at 2^-39.
+constexpr float kGScale = 16384.0f, kLowLift = 2048.0f;
 
 // What a logits tile leaves besides its maximum and sum.
 enum { kKeepNone = 0, kKeepF16 = 1, kKeepF32 = 2 };
@@ -569,12 +574,12 @@ __device__ __forceinline__ uint16_t f16_bits(float v) {
   return __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 template <int P>
-__device__ __forceinline__ void split_parts(float v, uint16_t (&p)[P]) {
+__device__ __forceinline__ void split_parts(float v, uint16_t (&p)[P], float low_lift = 1.0f) {
   if constexpr (P == 1) {
     p[0] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
   } else {
     p[0] = f16_bits(v);
-    p[1] = f16_bits(v - (float)__builtin_bit_cast(_Float16, p[0]));
+    p[1] = f16_bits((v - (float)__builtin_bit_cast(_Float16, p[0])) * low_lift);
   }
 }
 
@@ -669,9 +674,9 @@ __global__ __launch_bounds__(1024) void k_ce_top(const float* __restrict__ top, 
   }
 }
 
-// [rows][D] -> [D][P][Rp] (row pitch ld), zero past `rows`.  With `ratio`, rows
-// whose share of the gradient is 0 are zero too, whatever they hold, and two-part
-// rows are multiplied by their share.
+// [rows][D] -> [D][P][Rp] (row pitch ld), zero past `rows`; two-part rows have the high
+// part over kLowLift as a third.  With `ratio`, rows whose share of the gradient is 0 are
+// zero too, whatever they hold, and two-part rows are multiplied by their share.
 template <typename IO, int P>
 __global__ __launch_bounds__(256) void k_ce_cols(const IO* __restrict__ src,
                                                  const float* __restrict__ ratio,
@@ -702,6 +707,9 @@ __global__ __launch_bounds__(256) void k_ce_cols(const IO* __restrict__ src,
       split_parts<P>(tile[tx][ty + 4 * i], p);
 #pragma unroll
       for (int k = 0; k < P; ++k) dst[d * ld + k * Rp + r] = p[k];
+      if constexpr (P == 2)
+        dst[d * ld + 2 * Rp + r] =
+            f16_bits((float)__builtin_bit_cast(_Float16, p[0]) * (1.0f / kLowLift));
     }
   }
 }
@@ -833,8 +841,9 @@ __global__ __launch_bounds__(256) void k_ce_g(const E* e, int64_t lde, const flo
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint16_t lo[P], hi[P];
-        split_parts<P>(__builtin_fmaf(ev[2 * k], f, at == 2 * k ? -1.0f : 0.0f) * gs, lo);
-        split_parts<P>(__builtin_fmaf(ev[2 * k + 1], f, at == 2 * k + 1 ? -1.0f : 0.0f) * gs, hi);
+        split_parts<P>(__builtin_fmaf(ev[2 * k], f, at == 2 * k ? -1.0f : 0.0f) * gs, lo, kLowLift);
+        split_parts<P>(__builtin_fmaf(ev[2 * k + 1], f, at == 2 * k + 1 ? -1.0f : 0.0f) * gs, hi,
+                       kLowLift);
 #pragma unroll
         for (int m = 0; m < P; ++m) q[m][k] = (uint32_t)lo[m] | (uint32_t)hi[m] << 16;
       }
@@ -967,8 +976,10 @@ CePlan plan_ce(int64_t N, int64_t V, int64_t D, int io) {
   p.pieces = (N + p.piece - 1) / p.piece;
   // 128 bytes past a power of two: rows a power of two apart would meet in few
   // of the cache's channels
+  const int64_t parts_b = p.parts == 1 ? 1 : 3;
   p.ldg = p.parts * p.Vp + 64;
-  p.ldx = p.parts * p.piece + 64;
+  p.ldw = parts_b * p.Vp + 64;
+  p.ldx = parts_b * p.piece + 64;
   // the forward's only growing array is (maximum, sum) of each tile and row:
   // pieces of rows for it too (128 MiB; each still fills the GPU)
   const int64_t most_f = (kCePieceBytes / 8) / (p.Vp / 128 * 8) / 256 * 256;
@@ -1001,10 +1012,12 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
   } while (0)
   GemmArgs base = {};
   base.npair = bf ? 1 : 3;
-  // smallest products first: lo hi, hi lo, hi hi
-  auto pairs = [&](GemmArgs& g, int64_t ka, int64_t kb, int64_t k) {
+  // smallest products first: lo hi, hi lo, hi hi; lifted: A's low part is lifted, and
+  // multiplied by B's third part
+  auto pairs = [&](GemmArgs& g, int64_t ka, int64_t kb, int64_t k, bool lifted) {
     if (!bf) {
       g.pa[0] = ka;
+      g.pb[0] = lifted ? 2 * kb : 0;
       g.pb[1] = kb;
     }
     g.k = k;
@@ -1040,7 +1053,7 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
     g.b_unscale = a.x_unscale + n0;
     g.e = a.e;
     g.lde = a.lde;
-    pairs(g, p.Dp, p.Dp, p.Dp);
+    pairs(g, p.Dp, p.Dp, p.Dp, false);
     return g;
   };
   auto join = [&](int64_t n0, int64_t n, int64_t tiles) {
@@ -1077,7 +1090,7 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
                          ratio, scale, dst, n, a.D, np, ld);
     return hipGetLastError();
   };
-  LRS_CE(cols(a.w, nullptr, a.w_scale, a.w_cols, a.V, p.Vp, p.ldg));
+  LRS_CE(cols(a.w, nullptr, a.w_scale, a.w_cols, a.V, p.Vp, p.ldw));
   for (int64_t n0 = 0; n0 < a.N; n0 += p.piece) {
     const int64_t n = a.N - n0 < p.piece ? a.N - n0 : p.piece;
     const bool last = n0 + n == a.N;
@@ -1107,7 +1120,7 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
       g.ldb = p.ldx;
       g.M = a.V;
       g.N = a.D;
-      pairs(g, p.Vp, p.piece, up(n, 64));
+      pairs(g, p.Vp, p.piece, up(n, 64), true);
       g.splits = (int)p.split_w;
       g.slots = p.slots_w ? a.slots_w : nullptr;
       g.add = n0 > 0;
@@ -1122,10 +1135,11 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
       GemmArgs g = base;
       g.a = a.g;
       g.b = a.w_cols;
-      g.lda = g.ldb = p.ldg;
+      g.lda = p.ldg;
+      g.ldb = p.ldw;
       g.M = n;
       g.N = a.D;
-      pairs(g, p.Vp, p.Vp, up(a.V, 64));
+      pairs(g, p.Vp, p.Vp, up(a.V, 64), true);
       g.splits = (int)p.split_x;
       g.slots = p.slots_x ? a.slots_x : nullptr;
       g.last = p.split_x == 1;

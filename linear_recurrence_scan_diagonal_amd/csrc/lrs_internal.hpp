@@ -283,7 +283,7 @@ struct CePlan {
   int64_t Dp = 0, Vp = 0;           // features and classes, rounded up
   int64_t piece = 0, pieces = 0;    // rows of a piece of the gradient, and how many
   int64_t piece_f = 0;              // rows of a piece of the forward alone
-  int64_t ldg = 0, ldx = 0;         // row pitch of G and w^T, of x^T
+  int64_t ldg = 0, ldw = 0, ldx = 0;  // row pitch of G, of w^T and of x^T
   int64_t tiles_f = 0, tiles_l = 0; // class tiles, forward alone and a piece's
   int tm_l = 0;                     // classes of a piece's tile
   int shape_f = 0, shape_l = 0, shape_x = 0, shape_w = 0;  // tile shapes of the products
@@ -304,7 +304,7 @@ struct CeArgs {
   float2* part;               // [piece][class tiles]
   float* tlogit;              // [piece]
   // the gradient's
-  uint16_t *x_cols, *w_cols;  // [D][ldx], [D][ldg]
+  uint16_t *x_cols, *w_cols;  // [D][ldx], [D][ldw]
   void* e;                    // [piece][lde]; bf16 inputs: G's own memory
   int64_t lde;
   uint16_t* g;                // [piece][ldg]

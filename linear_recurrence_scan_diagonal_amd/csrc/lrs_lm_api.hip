@@ -405,7 +405,7 @@ size_t ce_carve(const lrs::CePlan& p, int64_t N, int64_t V, int64_t D, bool back
   a->row_scale = cv.take<float>(N);
   a->top = cv.take<float>(1);
   a->x_cols = cv.take<uint16_t>(D * p.ldx);
-  a->w_cols = cv.take<uint16_t>(D * p.ldg);
+  a->w_cols = cv.take<uint16_t>(D * p.ldw);
   a->g = cv.take<uint16_t>(p.piece * p.ldg);
   a->e = f32 ? (void*)cv.take<float>(p.piece * (p.Vp + 32)) : (void*)a->g;
   a->lde = f32 ? p.Vp + 32 : p.ldg;
