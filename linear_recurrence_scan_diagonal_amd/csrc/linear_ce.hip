@@ -482,12 +482,13 @@ __global__ __launch_bounds__(S::kThreads, S::MINW) void k_gemm(GemmArgs g) {
       mx = fmaxf(mx, __shfl_xor(mx, 32));
       // no class, or every logit -inf: all e are 0
       float ref = mx == -__builtin_inff() ? 0.0f : mx;
-      if (__ballot(fabsf(ref) >= kLargeLogit)) {
+      if (__ballot(fabsf(ref) >= kLargeLogit)) {  // for those rows of the 16 alone
+        const float take = fabsf(ref) >= kLargeLogit ? ref : 0.0f;
 #pragma unroll
         for (int j = 0; j < MT; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[j][e] -= ref;
-        ref = 0.0f;
+          for (int e = 0; e < 4; ++e) v[j][e] -= take;
+        ref -= take;
       }
       const float lift = __builtin_fmaf(-ref, kLog2eF, kLift<KEEP>);
       float sum = 0.0f;

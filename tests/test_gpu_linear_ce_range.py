@@ -123,6 +123,21 @@ def test_large_logits(dtype):
 
 
 @BOTH
+@pytest.mark.parametrize("size", [3.0, 1e4])
+def test_rows_do_not_depend_on_their_neighbours(dtype, size):
+    """Loss, lse and gradient of a row have the same bits next to rows of any size."""
+    g = torch.Generator().manual_seed(10)
+    N, V, D = 80, 300, 64
+    x, w = torch.randn(N, D, generator=g).to(dtype).to(DEV), torch.randn(V, D, generator=g).to(dtype).to(DEV)
+    target, gl = torch.arange(N, device=DEV), torch.full((N,), 1.0 / N, device=DEV)
+    want = lrs.linear_ce_fwd_bwd(x, w, target, gl)
+    x2, own = x.clone(), torch.arange(N, device=DEV) % 5 != 0
+    x2[~own] *= size
+    got = lrs.linear_ce_fwd_bwd(x2, w, target, gl)
+    assert all(torch.equal(a[own], b[own]) for a, b in zip(got[:3], want))
+
+
+@BOTH
 def test_an_outlier_feature(dtype):
     """A class with a weight of 1e3 in a feature that x has little of: the other classes'
     parts of grad_x keep their digits."""
