@@ -627,10 +627,11 @@ __global__ __launch_bounds__(256) void k_ce_rows_bf16(const uint16_t* __restrict
 }
 
 // fp32 [rows][D] -> two fp16 parts [rows][2][Dp] scaled by the row's power of
-// two; unscale[row] undoes it and top[row] is the row's largest value (0 in rows
-// that do not count).  One wave a row.
+// two; unscale[row] undoes it and top[row] is the row's largest finite value, times its
+// `share` of the gradient if there are shares: what the transposed copy will hold of the
+// row (0 where the share is 0, whatever the row holds).  One wave a row.
 __global__ __launch_bounds__(256) void k_ce_rows_f32(const float* __restrict__ src,
-                                                     const int64_t* __restrict__ target, int64_t V,
+                                                     const float* __restrict__ shares,
                                                      uint16_t* __restrict__ dst,
                                                      float* __restrict__ unscale,
                                                      float* __restrict__ top_out, int64_t rows,
@@ -638,9 +639,14 @@ __global__ __launch_bounds__(256) void k_ce_rows_f32(const float* __restrict__ s
   const int lane = threadIdx.x & (kWave - 1);
   for (int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; row < rows;
        row += (int64_t)gridDim.x * 4) {
-    float top = 0.0f;
-    for (int64_t d = lane; d < D; d += kWave) top = fmaxf(top, fabsf(src[row * D + d]));
+    float top = 0.0f, finite = 0.0f;
+    for (int64_t d = lane; d < D; d += kWave) {
+      const float v = fabsf(src[row * D + d]);
+      top = fmaxf(top, v);
+      finite = fmaxf(finite, v < __builtin_inff() ? v : 0.0f);
+    }
     top = wave_top(top);
+    finite = wave_top(finite);
     float inv;
     const float sc = scale_for(top, inv);
     for (int64_t d = lane; d < Dp; d += kWave) {
@@ -651,7 +657,8 @@ __global__ __launch_bounds__(256) void k_ce_rows_f32(const float* __restrict__ s
     }
     if (lane == 0) {
       unscale[row] = inv;
-      top_out[row] = !target || row_counts(target[row], V) ? top : 0.0f;
+      const float share = shares ? fabsf(shares[row]) : 1.0f;
+      top_out[row] = share > 0.0f && share < __builtin_inff() ? finite * share : 0.0f;
     }
   }
 }
@@ -1026,7 +1033,7 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
   base.splits = 1;
   // rows of x and w as the logits' product takes them
   const uint16_t *xr = (const uint16_t*)a.x, *wr = (const uint16_t*)a.w;
-  auto rows = [&](const void* src, uint16_t* dst, int64_t n, const int64_t* target, float* unscale,
+  auto rows = [&](const void* src, uint16_t* dst, int64_t n, const float* shares, float* unscale,
                   float* top, const uint16_t** out) -> hipError_t {
     if (bf && p.Dp == a.D && ((uintptr_t)src & 15) == 0) return hipSuccess;
     *out = dst;
@@ -1035,10 +1042,15 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
                          (const uint16_t*)src, dst, n, a.D, p.Dp);
     else
       hipLaunchKernelGGL(k_ce_rows_f32, dim3(blocks_for(n, 4)), dim3(256), 0, stream,
-                         (const float*)src, target, a.V, dst, unscale, top, n, a.D, p.Dp);
+                         (const float*)src, shares, dst, unscale, top, n, a.D, p.Dp);
     return hipGetLastError();
   };
-  LRS_CE(rows(a.x, a.x_rows, a.N, a.target, a.x_unscale, a.x_top, &xr));
+  if (a.backward) {  // first: the shares enter the scale of x^T
+    hipLaunchKernelGGL(k_ce_scale, dim3(1), dim3(1024), 0, stream, a.grad_loss, a.target, a.N, a.V,
+                       bf ? 1 : 0, a.ratio, a.row_scale, a.top);
+    LRS_CE(hipGetLastError());
+  }
+  LRS_CE(rows(a.x, a.x_rows, a.N, a.backward ? a.ratio : nullptr, a.x_unscale, a.x_top, &xr));
   LRS_CE(rows(a.w, a.w_rows, a.V, nullptr, a.w_unscale, a.w_top, &wr));
   auto logits = [&](int64_t n0, int64_t n) {
     GemmArgs g = base;
@@ -1071,9 +1083,6 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
     }
     return hipSuccess;
   }
-  hipLaunchKernelGGL(k_ce_scale, dim3(1), dim3(1024), 0, stream, a.grad_loss, a.target, a.N, a.V,
-                     bf ? 1 : 0, a.ratio, a.row_scale, a.top);
-  LRS_CE(hipGetLastError());
   if (!bf) {
     hipLaunchKernelGGL(k_ce_top, dim3(1), dim3(1024), 0, stream, a.x_top, a.N, a.x_scale);
     LRS_CE(hipGetLastError());

@@ -138,6 +138,41 @@ def test_rows_do_not_depend_on_their_neighbours(dtype, size):
 
 
 @BOTH
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 1e12, -1e30])
+def test_rows_without_a_gradient_hold_anything(dtype, value):
+    """A row that counts, with a grad_loss of 0, changes no other row's gradient and
+    nothing of grad_w, whatever it holds."""
+    g = torch.Generator().manual_seed(6)
+    N, V, D = 90, 260, 64
+    x, w = torch.randn(N, D, generator=g).to(dtype).to(DEV), torch.randn(V, D, generator=g).to(dtype).to(DEV)
+    target = torch.arange(N, device=DEV)
+    gl = torch.full((N,), 0.5, device=DEV)
+    gl[11] = gl[60] = 0.0
+    want = lrs.linear_ce_fwd_bwd(x, w, target, gl)
+    x2 = x.clone()
+    x2[11, 3] = value
+    x2[60] = value
+    got = lrs.linear_ce_fwd_bwd(x2, w, target, gl)
+    assert torch.equal(got[2], want[2]) and torch.equal(got[3], want[3])
+    lse = lrs.linear_ce_fwd(x2, w, target)[1]
+    assert all(torch.equal(a, b) for a, b in zip(lrs.linear_ce_bwd(x2, w, target, lse, gl), want[2:]))
+    check(x, w, target, gl)
+
+
+@BOTH
+def test_large_rows_with_a_small_share(dtype):
+    """A row 1e9 times as large whose loss weighs 1e-12: its part of grad_w is small,
+    and the other rows' parts keep their digits."""
+    g = torch.Generator().manual_seed(7)
+    N, V, D = 120, 200, 40
+    x, w = torch.randn(N, D, generator=g), 0.2 * torch.randn(V, D, generator=g)
+    gl = torch.full((N,), 0.01)
+    x[17] *= 1e9
+    gl[17] = 1e-14
+    check(*(t.to(DEV) for t in (x.to(dtype), w.to(dtype), torch.arange(N), gl)))
+
+
+@BOTH
 def test_an_outlier_feature(dtype):
     """A class with a weight of 1e3 in a feature that x has little of: the other classes'
     parts of grad_x keep their digits."""
