@@ -881,11 +881,16 @@ __global__ __launch_bounds__(256) void k_ce_join_slots(const float* __restrict__
   }
 }
 
-__global__ __launch_bounds__(256) void k_ce_zero(uint32_t* __restrict__ p, int64_t bytes) {
+// Zero bytes, an even number of them from an even address: whole words, and what lies
+// before and behind them.
+__global__ __launch_bounds__(256) void k_ce_zero(uint16_t* __restrict__ p, int64_t bytes) {
+  const int64_t n = bytes / 2, head = ((uintptr_t)p & 2) ? 1 : 0, words = (n - head) / 2;
   const int64_t stride = (int64_t)gridDim.x * 256;
   const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  for (int64_t i = i0; i < bytes / 4; i += stride) p[i] = 0u;
-  if (i0 == 0 && (bytes & 2)) reinterpret_cast<uint16_t*>(p)[bytes / 2 - 1] = 0;
+  uint32_t* w = reinterpret_cast<uint32_t*>(p + head);
+  for (int64_t i = i0; i < words; i += stride) w[i] = 0u;
+  if (i0 == 0 && head) p[0] = 0;
+  if (i0 == 0 && head + 2 * words < n) p[n - 1] = 0;
 }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -1177,7 +1182,7 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
 
 hipError_t launch_zero(void* p, int64_t bytes, hipStream_t stream) {
   if (bytes <= 0) return hipSuccess;
-  hipLaunchKernelGGL(k_ce_zero, dim3(blocks_for(bytes, 4096)), dim3(256), 0, stream, (uint32_t*)p,
+  hipLaunchKernelGGL(k_ce_zero, dim3(blocks_for(bytes, 4096)), dim3(256), 0, stream, (uint16_t*)p,
                      bytes);
   return hipGetLastError();
 }

@@ -313,7 +313,7 @@ struct CeArgs {
 };
 CePlan plan_ce(int64_t N, int64_t V, int64_t D, int io);
 hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_t stream);
-// Fill with zero bytes (p aligned to 4, an even number of bytes).
+// Fill with zero bytes (p aligned to 2, an even number of bytes).
 hipError_t launch_zero(void* p, int64_t bytes, hipStream_t stream);
 
 }  // namespace lrs

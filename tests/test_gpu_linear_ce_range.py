@@ -183,3 +183,17 @@ def test_an_outlier_feature(dtype):
     w[33, 5] = 1e3
     check(*(t.to(DEV) for t in (x.to(dtype), w.to(dtype), torch.randint(0, V, (N,), generator=g),
                                 torch.full((N,), 1.0 / N))))
+
+
+@BOTH
+@pytest.mark.parametrize("V,D", [(30, 16), (7, 3), (1, 1), (1, 2), (3000, 501)])
+@pytest.mark.parametrize("shift", [0, 1, 2, 3])
+def test_no_rows_any_alignment(dtype, V, D, shift):
+    """Without rows grad_w is 0, to its first and last element and not past them,
+    wherever it begins."""
+    x, target, gl = (torch.empty(0, D, dtype=dtype, device=DEV), torch.empty(0, dtype=torch.int64, device=DEV),
+                     torch.empty(0, device=DEV))
+    wide = torch.full((V * D + 8,), 7.0, dtype=dtype, device=DEV)
+    gw = wide[shift:shift + V * D].view(V, D)
+    lrs.linear_ce_fwd_bwd(x, torch.ones(V, D, dtype=dtype, device=DEV), target, gl, out=(x.clone(), gw))
+    assert (gw == 0).all() and (wide[:shift] == 7).all() and (wide[shift + V * D:] == 7).all()
