@@ -110,7 +110,8 @@ struct GemmArgs {
 
 // One 16-byte piece a lane from global memory straight to LDS (lane l's piece
 // lands at dst + 16 l).  The instruction has no output register; the wait is
-// the caller's, by count.
+// the caller's, by count.  m0 is reserved: the compiler keeps nothing in it from one
+// statement to the next (and takes no clobber of it).
 __device__ __forceinline__ void dma16(uint32_t dst, uint32_t off, const uint16_t* base) {
   const uint64_t b = (uint64_t)base;
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b);
@@ -993,8 +994,9 @@ CePlan plan_ce(int64_t N, int64_t V, int64_t D, int io) {
   p.ldg = p.parts * p.Vp + 64;
   p.ldw = parts_b * p.Vp + 64;
   p.ldx = parts_b * p.piece + 64;
-  // the forward's only growing array is (maximum, sum) of each tile and row:
-  // pieces of rows for it too (128 MiB; each still fills the GPU)
+  // the forward's only growing array is (maximum, sum) of each tile and row: pieces
+  // of rows for it too (128 MiB at 128 classes a tile, and the shapes with smaller
+  // tiles are only chosen for so few rows that they stay below; each still fills the GPU)
   const int64_t most_f = (kCePieceBytes / 8) / (p.Vp / 128 * 8) / 256 * 256;
   p.piece_f = most_f < 256 ? 256 : most_f > N ? N : most_f;
   int64_t one;
