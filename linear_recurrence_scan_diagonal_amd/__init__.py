@@ -13,11 +13,12 @@ DEER_DEFAULT_KMAX = 5
 _BINDING_NAMES = ("scan_fwd", "scan_bwd", "scan_fwd_bwd", "sru_fwd", "sru_bwd", "deer_solve", "deer_stats",
                   "deer_bwd", "deer_solve_seq", "deer_eps_schedule", "lstm_fwd", "lstm_bwd",
                   "sru_deer_fwd", "rnn_seq", "scan_workspace_bytes", "plan_options",
-                  "LrsError", "load")
+                  "LrsError")
 
-# operators of recurrent language models (include/lrs_lm.h)
+# operators of recurrent language models (include/lrs_lm.h); load sets the prototypes
+# of both headers
 _LM_NAMES = ("glr_checkpoints", "glr_fwd", "glr_bwd", "glr_step", "layernorm_fwd", "layernorm_bwd",
-             "linear_ce_fwd", "linear_ce_bwd", "linear_ce_fwd_bwd")
+             "linear_ce_fwd", "linear_ce_bwd", "linear_ce_fwd_bwd", "load")
 
 __all__ = ["DEER_DEFAULT_EPS", "DEER_DEFAULT_KMAX", *_BINDING_NAMES, *_LM_NAMES]
 
