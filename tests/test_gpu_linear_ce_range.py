@@ -197,3 +197,21 @@ def test_no_rows_any_alignment(dtype, V, D, shift):
     gw = wide[shift:shift + V * D].view(V, D)
     lrs.linear_ce_fwd_bwd(x, torch.ones(V, D, dtype=dtype, device=DEV), target, gl, out=(x.clone(), gw))
     assert (gw == 0).all() and (wide[:shift] == 7).all() and (wide[shift + V * D:] == 7).all()
+
+
+@pytest.mark.parametrize("N,V,D,dtype", [(16384, 32768, 1024, torch.bfloat16), (4099, 50021, 777, torch.bfloat16),
+                                         (2048, 16384, 512, torch.float32), (40000, 40000, 72, torch.bfloat16)])
+def test_large_calls_repeat_themselves(N, V, D, dtype):
+    """Thousands of tiles, shares of the k loop and pieces of rows: the same bits from
+    call to call, from whatever the workspace held before."""
+    g = torch.Generator(device=DEV).manual_seed(N)
+    x = torch.randn(N, D, generator=g, device=DEV).to(dtype)
+    w = (torch.randn(V, D, generator=g, device=DEV) * 2 / D ** 0.5).to(dtype)
+    target = torch.randint(-V // 20, V, (N,), generator=g, device=DEV)
+    gl = torch.full((N,), 1.0 / N, device=DEV)
+    nbytes = lrs.load().lrs_linear_ce_workspace_bytes(N, V, D, int(dtype == torch.bfloat16), 1)
+    runs = []
+    for fill in (0, 255, 60, 127):
+        ws = torch.full((nbytes,), fill, dtype=torch.uint8, device=DEV)
+        runs.append(lrs.linear_ce_fwd_bwd(x, w, target, gl, workspace=ws))
+    assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(runs[0], r))
