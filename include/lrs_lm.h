@@ -53,7 +53,8 @@ LRS_API int lrs_glr_fwd(const void *z_r, const void *z_i, const void *x, int64_t
 /* Its backward pass.  With lam_t the whole gradient of h_t,
  *   lam_t = grad_h_t + a_{t+1} lam_{t+1}   (lam_T adds grad_h_last):
  *   dx = lam m i,  dz_i = lam m x i (1 - i),
- *   dla = lam (a h_{t-1} - (a^2 / m) i x)  (0 at a reset, where la = log a is fixed),
+ *   dla = lam (a h_{t-1} - (a^2 / m) i x)  (0 at a reset, and with it dz_r, whatever
+ *                                          z_r is there),
  *   dz_r = dla la (1 - r),  ddecay = sum dla (-c sigmoid(decay)) r,
  *   dbias_r, dbias_i = sums of dz_r, dz_i over steps and sequences,  dh0 = a_1 lam_1.
  * The term with 1/m is 0 where m is 0 (a gate closed to the last bit).

@@ -599,8 +599,9 @@ __device__ __forceinline__ void glr_bwd_walk(const GlrArgs& g, const GlrChan<CPT
       di[k] = dgx * u * (1.0f - gi[i][k]);
       const float rm = mm == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(mm);
       const float dla = scale<RST>(a, lam * __builtin_fmaf(-a * rm, u, hp[i][k]));
-      const float dlr = dla * r[i][k];
-      dr[k] = -dlr * ch.k[k] * (1.0f - r[i][k]);  // la = -k r
+      // at a restart 0 whatever the gate would have been
+      const float dlr = scale<RST>(dla, r[i][k]);
+      dr[k] = scale<RST>(-dlr * ch.k[k], 1.0f - r[i][k]);  // la = -k r
       sum.r[k] += dr[k];
       sum.i[k] += di[k];
       sum.d[k] += dlr;

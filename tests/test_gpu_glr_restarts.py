@@ -109,3 +109,22 @@ def test_only_a_restart_cuts(size, dtype, decay):
     got, ref = check(parts, p, s, reset)
     assert np.isnan(ref["h"][5:T - 20, 0, 3]).all() and np.isfinite(ref["h"][T - 20:]).all()
     assert np.isnan(ref["grad_x"][:T - 39, B // 2, 11]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", SIZES)
+def test_a_restart_does_not_look_at_its_own_gate(size, dtype):
+    """At a restart a = 0 and m = 1 whatever z_r is: the same results with a NaN there, and
+    a zero gradient."""
+    T, B, D = SIZES[size]
+    parts, p, s = make(T, B, D, dtype, seed=T + 3)
+    reset = torch.zeros((T, B), dtype=torch.uint8, device=DEV)
+    reset[0] = reset[33] = reset[64] = reset[T - 1] = 1
+    want, _ = check(parts, p, s, reset)
+    parts[0][reset != 0] = float("nan")
+    ck = lrs.glr_checkpoints(parts[0])
+    h, last = lrs.glr_fwd(*parts, **p, reset=reset, h0=s["h0"], want_h_last=True, checkpoints=ck)
+    grads = lrs.glr_bwd(*parts, **p, checkpoints=ck, grad_h=s["gh"], reset=reset, grad_h_last=s["gl"])
+    for name, t in {"h": h, "h_last": last, **dict(zip(NAMES, grads))}.items():
+        assert torch.equal(t, want[name]), name
+    assert (grads[0][reset != 0] == 0).all()
