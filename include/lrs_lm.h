@@ -3,7 +3,7 @@
  * linear recurrence with a learned decay (forward, backward, single tokens), a
  * layer norm with the residual added in (forward, backward), and the softmax
  * cross entropy of a linear head over a large vocabulary, with its gradient,
- * whose logits are never stored.
+ * without storing all of its logits.
  *
  * The conventions of lrs.h hold: device pointers owned by the caller, a
  * caller's workspace sized by a query, an opaque stream, error codes and no
@@ -121,7 +121,8 @@ LRS_API int lrs_layernorm_bwd(const void *s, const float *gamma, const float *me
  *   lse_n = log sum_v exp l_nv,   loss_n = lse_n - l_{n,target_n}.
  * A row whose target lies outside [0, V) is ignored: loss 0, no gradient, and
  * its x reaches no gradient of w (lse is written all the same).  The logits are
- * made tile by tile on the matrix cores and never stored.
+ * made tile by tile on the matrix cores: the forward stores none, the gradient
+ * the exponentials of a piece of the rows at a time (below).
  * x: [N,D], w: [V,D], I/O type.  target: [N] int64.  loss, lse: [N] fp32.
  * fp32 operands are split into two scaled fp16 parts and multiplied in three
  * products.  A sum of products is then off by up to 2^-21 of the sum of its

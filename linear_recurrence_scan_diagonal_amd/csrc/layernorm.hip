@@ -15,7 +15,10 @@
 //
 // Measured: 65536 x 1024 bf16 with a residual 91 us forward (5.9 TB/s) and 92 us
 // backward (5.8 TB/s; a copy of that size reaches 5.2); 5003 x 1711 fp32 16 and 25 us
-// (4.2 TB/s); 8192 x 8192 bf16 without a residual 45 us (6.0 TB/s); 64 rows, 4.6 us, are a launch and one pass of latency.
+// (4.2 TB/s); 8192 x 8192 bf16 without a residual 62 us (4.3 TB/s; 45 where part of the
+// input or output is still in the memory-side cache); 64 rows, 4.6 us, are a launch and
+// one pass of latency.  Wide rows are read once more for dx and once more for the sums
+// over rows: 8192 x 8192 fp32 backward 315 us, 2.6 TB/s of what it has to move.
 //
 // Groups are read at element alignment (the hardware allows it for global
 // memory), so that odd widths take the same path; only the last, incomplete

@@ -18,8 +18,8 @@
 // by one pass (for bf16 in place), and used up by the two gradient products; the
 // piece is chosen so that this stays within a fixed number of bytes.
 // What bounds it: the matrix cores' power.  At 16384 x 32768 x 1024 bf16 the
-// products run at 1460 (grad_x), 1400 (grad_w) and 1000 TFLOP/s (logits, with the
-// exponentials) where a large library product reaches 1360 to 1650; the rest, 0.45
+// products run at 1440 (grad_x), 1340 to 1400 (grad_w) and 1000 TFLOP/s (logits, with
+// the exponentials) where a large library product reaches 1360 to 1650; the rest, 0.45
 // of 3.1 ms, is k_ce_g and the transposed copies at 5.4 to 6 TB/s.
 // Operands that are not laid out like that (x^T, w^T, rows that are not a whole
 // number of k steps or not 16-byte aligned) are copied once into the workspace.
@@ -974,8 +974,12 @@ hipError_t run(GemmArgs& g, int shape, bool f16, hipStream_t stream) {
 }  // namespace
 
 // Pieces of the rows whose G takes at most this many bytes.  Every piece adds its
-// part to an fp32 grad_w: 16384 x 32768 x 1024 bf16 takes 3264 us in two pieces of
-// 512 MiB and 3090 us in one of 1 GiB.
+// part to an fp32 grad_w, so fewer are faster, and each takes its bytes of workspace.
+// Training in ms with 256 MiB, 512 MiB, 1, 2 and 4 GiB: 16384 x 32768 x 1024 bf16 3.66,
+// 3.29, 3.12 (one piece from here on); 32768 x 50021 x 512 bf16 8.65, 7.91, 6.57, 6.46,
+// 6.49; 16384 x 50021 x 512 fp32 11.3, 10.2, 8.74, 8.42, 8.50; 65536 x 131072 x 1024
+// bf16 88.7, 66.8, 56.2, 51.6, 50.5.  1 GiB is where most of it is gained; the last, of 16
+// pieces, is 8% from its best.
 constexpr int64_t kCePieceBytes = (int64_t)1 << 30;
 
 CePlan plan_ce(int64_t N, int64_t V, int64_t D, int io) {
