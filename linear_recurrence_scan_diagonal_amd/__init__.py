@@ -15,12 +15,16 @@ _BINDING_NAMES = ("scan_fwd", "scan_bwd", "scan_fwd_bwd", "sru_fwd", "sru_bwd", 
                   "sru_deer_fwd", "rnn_seq", "scan_workspace_bytes", "plan_options",
                   "LrsError")
 
-# operators of recurrent language models (include/lrs_lm.h); load sets the prototypes
-# of both headers
+# operators of recurrent language models (include/lrs_lm.h)
 _LM_NAMES = ("glr_checkpoints", "glr_fwd", "glr_bwd", "glr_step", "layernorm_fwd", "layernorm_bwd",
-             "linear_ce_fwd", "linear_ce_bwd", "linear_ce_fwd_bwd", "load")
+             "linear_ce_fwd", "linear_ce_bwd", "linear_ce_fwd_bwd")
 
-__all__ = ["DEER_DEFAULT_EPS", "DEER_DEFAULT_KMAX", *_BINDING_NAMES, *_LM_NAMES]
+# operators of delta-rule language models (include/lrs_block.h); load sets the prototypes
+# of all headers
+_BLOCK_NAMES = ("gdr_checkpoints", "gdr_fwd", "gdr_bwd", "gdr_step", "rmsnorm_fwd",
+                "rmsnorm_fwd_fp8", "rmsnorm_bwd", "logprobs_fwd", "logprobs_bwd", "load")
+
+__all__ = ["DEER_DEFAULT_EPS", "DEER_DEFAULT_KMAX", *_BINDING_NAMES, *_LM_NAMES, *_BLOCK_NAMES]
 
 
 def __getattr__(name):
@@ -30,6 +34,8 @@ def __getattr__(name):
         from . import binding as module
     elif name in _LM_NAMES:
         from . import lm as module
+    elif name in _BLOCK_NAMES:
+        from . import block as module
     else:
         raise AttributeError(name)
     globals()[name] = value = getattr(module, name)

@@ -16,7 +16,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "liblrs.so")
 
 SOURCES = ["common.hip", "scan_bdt.hip", "scan_tbd.hip", "scan_serial.hip", "gated_cell.hip", "sru_deer.hip",
-           "glr.hip", "layernorm.hip", "linear_ce.hip", "lrs_api.hip", "lrs_lm_api.hip"]
+           "glr.hip", "layernorm.hip", "linear_ce.hip", "gdr.hip", "rmsnorm.hip", "logprobs.hip",
+           "lrs_api.hip", "lrs_lm_api.hip", "lrs_block_api.hip"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: keep the compiler from forming packed fp32 VALU ops

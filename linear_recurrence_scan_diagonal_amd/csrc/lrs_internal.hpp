@@ -316,4 +316,73 @@ hipError_t launch_linear_ce(const CePlan& p, const CeArgs& a, int io, hipStream_
 // Fill with zero bytes (p aligned to 2, an even number of bytes).
 hipError_t launch_zero(void* p, int64_t bytes, hipStream_t stream);
 
+
+// Gated delta rule (gdr.hip).  Arrays as in lrs_block.h, then the workspace's own, by
+// chunk of kGdrRows steps, sequence and head (of v, or of q and k where marked *); the
+// backward also has the last group.
+constexpr int kGdrRows = 64;   // steps a chunk, and between two checkpoints
+constexpr int kGdrMostK = 128;
+constexpr int kGdrCoefs = 9;   // fp32 values a step that the preparation leaves
+struct GdrArgs {
+  const void *q, *k, *v;
+  int64_t ld_q, ld_k, ld_v;
+  const float *log_decay, *beta;
+  const uint8_t* reset;
+  const float* state0;
+  void* o;
+  float *state, *checkpoints;
+  int64_t T, B;
+  int H, Hk, K, V;
+  float scale;
+  uint64_t* cuts;                             // a bit a step that begins a document, by chunk and sequence
+  float *coef, *keeps;                        // [kGdrCoefs][64], 1
+  uint16_t *k_rows, *q_rows, *k_cols;         // * fragments
+  uint16_t *p_rows, *t2_rows;                 // fragments in two parts
+  const void* grad_o;
+  const float* grad_state;
+  void *grad_q, *grad_k, *grad_v;
+  int64_t ld_gq, ld_gk, ld_gv;
+  float *grad_log_decay, *grad_beta, *grad_state0;
+  uint16_t *q_cols, *tt_rows;                 // *, and of the other inverse
+  double* decay_sums;                         // [64]
+  float *delta, *w;                           // [64][Vp]
+  int64_t Vp;
+  float* grad_states;                         // [K][V]
+};
+hipError_t launch_gdr_fwd(const GdrArgs& a, int io, hipStream_t stream);
+hipError_t launch_gdr_bwd(const GdrArgs& a, int io, hipStream_t stream);
+hipError_t launch_gdr_step(const GdrArgs& a, int io, const int32_t* slots, float* state,
+                           int64_t nslots, hipStream_t stream);
+
+// RMS norm (rmsnorm.hip).  rms_bwd_blocks as ln_bwd_blocks, one sum a feature.
+hipError_t launch_rmsnorm_fwd(const void* x, const void* residual, const float* gamma, void* y,
+                              void* sum, float* rstd, int64_t R, int64_t D, float eps, int io,
+                              hipStream_t stream);
+// group: features that share a scale, 128 or D.
+hipError_t launch_rmsnorm_fp8(const void* x, const void* residual, const float* gamma, void* y,
+                              float* scales, void* sum, int64_t R, int64_t D, int64_t group,
+                              float eps, int io, hipStream_t stream);
+int64_t rms_bwd_blocks(int64_t R, int64_t D);
+hipError_t launch_rmsnorm_bwd(const void* s, const float* gamma, const float* rstd,
+                              const void* grad_y, const void* grad_sum, void* grad_x,
+                              float* grad_gamma, int64_t R, int64_t D, int io, float* part,
+                              double* acc, hipStream_t stream);
+
+// Log probabilities of given logits (logprobs.hip).
+struct LogprobArgs {
+  const void* logits;
+  int64_t ld;
+  const int64_t* target;
+  float *logprob, *entropy, *lse;
+  int64_t* top_ids;
+  float* top_logprobs;
+  int64_t N, V;
+  int top;
+  const float *grad_logprob, *grad_entropy;
+  void* grad_logits;
+  int64_t ld_grad;
+};
+hipError_t launch_logprobs_fwd(const LogprobArgs& a, int io, hipStream_t stream);
+hipError_t launch_logprobs_bwd(const LogprobArgs& a, int io, hipStream_t stream);
+
 }  // namespace lrs

@@ -14,40 +14,6 @@ hipError_t launch_copy_or_zero(float* dst, const float* src, int64_t n, hipStrea
 
 namespace {
 
-struct Span {
-  const void* p;
-  size_t n;
-};
-
-bool any_overlap(const Span* outs, int no, const Span* ins, int ni) {
-  for (int o = 0; o < no; ++o) {
-    for (int i = 0; i < ni; ++i)
-      if (overlap(outs[o].p, outs[o].n, ins[i].p, ins[i].n)) return true;
-    for (int o2 = o + 1; o2 < no; ++o2)
-      if (overlap(outs[o].p, outs[o].n, outs[o2].p, outs[o2].n)) return true;
-  }
-  return false;
-}
-
-// Bytes from the first to past the last element of `rows` rows of D elements,
-// ld apart.
-size_t strided_bytes(int64_t rows, int64_t ld, int64_t D, size_t es) {
-  return rows <= 0 ? 0 : ((size_t)(rows - 1) * (size_t)ld + (size_t)D) * es;
-}
-
-// Whether two sets of `rows` rows of D elements, each ld apart, share an
-// element: their extents may interleave (slices of one wider array).
-bool rows_overlap(const void* p, const void* q, int64_t rows, int64_t ld, int64_t D, size_t es) {
-  const size_t n = strided_bytes(rows, ld, D, es);
-  if (!overlap(p, n, q, n)) return false;
-  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-  const size_t off = (size_t)(a < b ? b - a : a - b) % ((size_t)ld * es);
-  return !(off >= (size_t)D * es && off <= (size_t)(ld - D) * es);
-}
-
-bool io_ok(int io) { return io == LRS_F32 || io == LRS_BF16; }
-size_t io_size(int io) { return io == LRS_BF16 ? 2 : 4; }
-
 // Sizes of a gated linear recurrence: no overflow, and 32-bit offsets inside
 // one time step.
 bool glr_shape(int64_t T, int64_t B, int64_t D, int64_t* C, int64_t* N) {
@@ -63,12 +29,6 @@ bool glr_step_fits(int64_t B, int64_t C, int64_t ld) {
 size_t glr_lookback_bytes(const lrs::ColPlan& p, int64_t D) {
   const int64_t nst = lrs::col_status_words(p);
   return nst > 0 ? lookback_bytes(nst, p.ncb) + align_up((size_t)(2 * D) * 4) : 0;
-}
-
-// Pitched extents inside int64 bytes.
-bool pitch_ok(int64_t T, int64_t B, int64_t ld) {
-  int64_t rows, n;
-  return mul_ok(T, B, &rows) && mul_ok(rows, ld, &n) && n <= ((int64_t)1 << 60);
 }
 
 }  // namespace
