@@ -41,14 +41,16 @@ extern "C" {
  * reset  : [T,B] bytes, or NULL for none.  state0: [B,H,K,V] fp32, or NULL (zero).
  * o      : [T,B,H,V] contiguous output.  state: [B,H,K,V] fp32 output, the state
  *          after the last step, or NULL; it may be state0's own buffer.
- * checkpoints : fp32 output [lrs_gdr_checkpoint_rows(T), B, H, K, V], the states
- *          that enter each chunk of 64 steps, which lrs_gdr_bwd reads; or NULL.
+ * checkpoints : fp32 output [lrs_gdr_checkpoint_rows(T), B, H, K + 64, V], for each
+ *          chunk of 64 steps the state that enters it and v - S^T k of its steps,
+ *          which lrs_gdr_bwd reads; or NULL.
  * Products take factors of two fp16 parts, scaled by a power of two (one part
  * where bf16 inputs need no more): a factor is known to 2^-22 of itself or to
  * 2^-39 of the largest of its row or column, whichever is more.  A value that is
  * not finite makes what its document computes from it NaN or infinite, up to
  * 63 steps before it (its chunk) and in the columns of V and heads it reaches.
- * Supported: K <= 128, and T*B*H/64 * 256 and B*H*V * 4 below 2^32. */
+ * Supported: K <= 128, B*H*V, B*ld_v and B*ld_gv below 2^23, (K+64)*V below 2^29, and
+ * the chunks ceil(T/64)*B*H below 2^24, times ceil(V/16) below 2^26. */
 LRS_API int64_t lrs_gdr_checkpoint_rows(int64_t T);
 LRS_API size_t lrs_gdr_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t K,
                                        int64_t V, int io_dtype);

@@ -110,10 +110,11 @@ def _gdr_inputs(q, k, v, log_decay, beta, dims):
 
 
 def gdr_checkpoints(k, v):
-    """The tensor that gdr_fwd fills for gdr_bwd: fp32, the state [B,H,K,V] that enters
-    each chunk of time steps.  k: [T,B,Hk,K], v: [T,B,H,V]."""
+    """The tensor that gdr_fwd fills for gdr_bwd: fp32, for each chunk of 64 time steps,
+    sequence and head the state [K,V] that enters it and [64,V] of its steps.
+    k: [T,B,Hk,K], v: [T,B,H,V]."""
     T, B, H, V = (int(n) for n in v.shape)
-    return torch.empty((load().lrs_gdr_checkpoint_rows(T), B, H, int(k.shape[-1]), V),
+    return torch.empty((load().lrs_gdr_checkpoint_rows(T), B, H, int(k.shape[-1]) + 64, V),
                        dtype=torch.float32, device=v.device)
 
 
@@ -132,8 +133,9 @@ def gdr_fwd(q, k, v, log_decay, beta, scale=None, reset=None, state0=None,
     reset = _reset(reset, T, B)
     shape = torch.Size((B, H, K, V))
     _check_dev("state0", state0, torch.float32, shape)
-    rows = lib.lrs_gdr_checkpoint_rows(T)
-    _check_dev("checkpoints", checkpoints, torch.float32, torch.Size((rows, *shape)))
+    if checkpoints is not None:
+        _check_dev("checkpoints", checkpoints, torch.float32,
+                   torch.Size((lib.lrs_gdr_checkpoint_rows(T), B, H, K + 64, V)))
     dev = v.device
     o = torch.empty((T, B, H, V), dtype=v.dtype, device=dev) if out is None else out
     _check_dev("out", o, v.dtype, v.shape)
@@ -162,7 +164,7 @@ def gdr_bwd(q, k, v, log_decay, beta, checkpoints, grad_o, scale=None, reset=Non
     if checkpoints is None:
         raise TypeError("checkpoints must be the tensor that gdr_fwd filled")
     _check_dev("checkpoints", checkpoints, torch.float32,
-               torch.Size((lib.lrs_gdr_checkpoint_rows(T), *shape)))
+               torch.Size((lib.lrs_gdr_checkpoint_rows(T), B, H, K + 64, V)))
     if grad_o is None:
         raise TypeError("grad_o must be a device tensor")
     _check_dev("grad_o", grad_o, v.dtype, v.shape)

@@ -14,8 +14,8 @@
 //   k_gdr_prep   every chunk at once: the [64,64] matrices D q k^T (P) and
 //                T2 = (I + L diag(beta))^-1, and q, k and these as operands of the
 //                matrix cores;
-//   k_gdr_chain  the chain over the chunks (and, for the backward, delta of every
-//                chunk from its checkpoint, all chunks at once);
+//   k_gdr_chain  the chain over the chunks, which leaves for the backward the state that
+//                enters each of them and its delta;
 //   k_gdr_back   the same chain in reverse, for dS: with do' = scale do
 //                du = P^T do' + exp(G_C - G) K dS,  w = T^T du (T = (I + diag(beta) L)^-1),
 //                dv = dR = beta w,  dS0 = exp(G_C) dS + (exp G q)^T do' - (exp G k)^T dR;
@@ -64,28 +64,31 @@ struct Split {
 };
 
 // A power of two that brings a largest absolute value to [2^14, 2^15), and its inverse.
-// An infinity or NaN counts as the largest finite binade: it stays what it is.
+// An infinity counts as the largest finite binade: it stays what it is.
 struct Scale {
   float up, down;
 };
-__device__ __forceinline__ Scale scale_of(uint32_t top) {  // bits of the absolute value
-  uint32_t e = top >> 23;
+__device__ __forceinline__ Scale scale_of(float top) {
+  uint32_t e = as_u32(top) >> 23;
   e = e < 15u ? 15u : e > 254u ? 254u : e;
   return {as_f32((268u - e) << 23), as_f32((e - 14u) << 23)};
 }
-__device__ __forceinline__ uint32_t abs_bits(float v) { return as_u32(v) & 0x7FFFFFFFu; }
-__device__ __forceinline__ uint32_t max_u(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// The largest over the four lanes that share a row or column (r = lane % 16).
-__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
-  m = max_u(m, (uint32_t)__shfl_xor((int)m, 16));
-  return max_u(m, (uint32_t)__shfl_xor((int)m, 32));
+// The largest absolute value over the four lanes that share a row or column (r = lane %
+// 16).  A NaN does not count; it stays NaN at any scale.
+__device__ __forceinline__ float quad_max(float m) {
+  const u32x2_t a = __builtin_bit_cast(
+      u32x2_t, __builtin_amdgcn_permlane16_swap(as_u32(m), as_u32(m), false, false));
+  m = fmaxf(as_f32(a.x), as_f32(a.y));
+  const u32x2_t b = __builtin_bit_cast(
+      u32x2_t, __builtin_amdgcn_permlane32_swap(as_u32(m), as_u32(m), false, false));
+  return fmaxf(as_f32(b.x), as_f32(b.y));
 }
 template <int N>
-__device__ __forceinline__ uint32_t top_of(const float (&v)[N]) {
-  uint32_t m = 0u;
+__device__ __forceinline__ float top_of(const float (&v)[N]) {
+  float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) m = max_u(m, abs_bits(v[i]));
+  for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i]));
   return m;
 }
 
@@ -169,11 +172,21 @@ __device__ __forceinline__ f16x8_t keep_steps(f16x8_t f, int ks, int s, int e) {
 // Workspace of a call, in arrays of chunk-heads: index (c B + b) Hk + hk, or with H, h.
 // ---------------------------------------------------------------------------
 // fp32 values a step that k_gdr_prep leaves, [chunk-head][kCoef][64]
-enum { kEnterK, kEnterQ, kLeaveK, kBeta, kRowT, kRowP, kRowT2, kRowKq, kRowKk, kCoef };
+enum { kEnterK, kEnterQ, kLeaveK, kBeta, kRowP, kRowT, kRowKq, kRowKk, kCoef };
+constexpr int kStagedCoefs = kRowT + 1;
 
-template <int KP>
+
 __device__ __forceinline__ f16x8_t frag(const uint16_t* base, int index) {
-  return *reinterpret_cast<const f16x8_t*>(base + (int64_t)index * kFrag + (threadIdx.x & 63) * 8);
+  return *reinterpret_cast<const f16x8_t*>(base + index * kFrag + (threadIdx.x & 63) * 8);
+}
+// Of a triangular [64,64] matrix six fragments are not all zeros: row tile rt has the
+// k steps 0..rt/2, and where the matrix is transposed rt/2..1.
+constexpr int kTri = 6;
+constexpr int kTriSet = 2 * kTri * kFrag;  // in two parts
+static_assert(kGdrMats == 2 * kTriSet + kCoef * kC * 2, "the workspace's");
+template <bool TRANSPOSED>
+__device__ __forceinline__ constexpr int tri(int rt, int ks) {
+  return TRANSPOSED ? (rt < 2 ? 2 * rt + ks : rt + 2) : (rt < 2 ? rt : 2 * rt - 2 + ks);
 }
 
 // ---------------------------------------------------------------------------
@@ -221,7 +234,7 @@ __device__ void invert(const Mat& am, Mat& tm) {
 }
 
 // Rows [s, e) of m (or of its transpose) as fragments in two parts, each row scaled by
-// its largest; 4 waves, 16 rows each.  dst: [part][row tile][k step][512].
+// its largest; 4 waves, 16 rows each.  dst: [part][kTri][512].
 template <bool TRANSPOSED>
 __device__ __forceinline__ void emit(const Mat& m, uint16_t* dst, float* row_scale, int s, int e) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, r = lane & 15;
@@ -238,10 +251,11 @@ __device__ __forceinline__ void emit(const Mat& m, uint16_t* dst, float* row_sca
   if (row < s || row >= e) return;
 #pragma unroll
   for (int ks = 0; ks < 2; ++ks) {
+    if (TRANSPOSED ? ks < w / 2 : ks > w / 2) continue;
     const Split p = split8(v + 8 * ks, sc.up);
-    uint16_t* to = dst + (w * 2 + ks) * kFrag + lane * 8;
+    uint16_t* to = dst + tri<TRANSPOSED>(w, ks) * kFrag + lane * 8;
     *reinterpret_cast<f16x8_t*>(to) = p.hi;
-    *reinterpret_cast<f16x8_t*>(to + 8 * kFrag) = p.lo;
+    *reinterpret_cast<f16x8_t*>(to + kTri * kFrag) = p.lo;
   }
   if (g == 0) row_scale[row] = sc.down;
 }
@@ -326,30 +340,14 @@ __global__ __launch_bounds__(256) void k_gdr_prep(GdrArgs a) {
   }
   __syncthreads();
 
-  // the heads that share k and q leave them once, and as columns over the steps too
+  // the heads that share k and q leave them once
   if (h % share == 0) {
     constexpr int kSet = NP * 4 * KS * kFrag;
+    uint16_t* to = a.kq_rows + kh * (2 * kSet);
     for (int i = threadIdx.x; i < kSet / 8; i += 256) {
-      *reinterpret_cast<f16x8_t*>(a.k_rows + kh * kSet + i * 8) =
-          *reinterpret_cast<const f16x8_t*>(&kf[0][0] + i * 8);
-      *reinterpret_cast<f16x8_t*>(a.q_rows + kh * kSet + i * 8) =
+      *reinterpret_cast<f16x8_t*>(to + i * 8) = *reinterpret_cast<const f16x8_t*>(&kf[0][0] + i * 8);
+      *reinterpret_cast<f16x8_t*>(to + kSet + i * 8) =
           *reinterpret_cast<const f16x8_t*>(&qf[0][0] + i * 8);
-    }
-    // fragment (part, row tile of K, k step of 32 steps)
-    for (int i = threadIdx.x; i < kSet / 8; i += 256) {
-      const int l = i & 63, f = i >> 6, ks = f & 1, kt = (f >> 1) % (KP / 16), p = f / (KP / 8);
-      const int col = 16 * kt + (l & 15);  // of K: its place in a row's fragments
-      const int in = (col >> 5) * kFrag + ((col >> 2) & 3) * 128 + ((col >> 4) & 1) * 4 + (col & 3);
-      f16x8_t kc, qc;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int step = 32 * ks + 16 * (e >> 2) + 4 * (l >> 4) + (e & 3);
-        const int at = (step >> 4) * KS * kFrag + in + (step & 15) * 8;
-        kc[e] = __builtin_bit_cast(_Float16, kf[p][at]);
-        if constexpr (BWD) qc[e] = __builtin_bit_cast(_Float16, qf[p][at]);
-      }
-      *reinterpret_cast<f16x8_t*>(a.k_cols + kh * kSet + i * 8) = kc;
-      if constexpr (BWD) *reinterpret_cast<f16x8_t*>(a.q_cols + kh * kSet + i * 8) = qc;
     }
   }
 
@@ -373,7 +371,7 @@ __global__ __launch_bounds__(256) void k_gdr_prep(GdrArgs a) {
   }
 
   const uint64_t cuts = cuts_s;
-  float* coef = a.coef + ch * (kCoef * kC);
+  float* coef = (float*)(a.mats + ch * kGdrMats + 2 * kTriSet);
   if (threadIdx.x < kC) {
     const int i = threadIdx.x;
     const float enter = expf((float)gs[i]), leave = expf((float)(gs[kC - 1] - gs[i]));
@@ -385,12 +383,11 @@ __global__ __launch_bounds__(256) void k_gdr_prep(GdrArgs a) {
     coef[kRowKq * kC + i] = rq[i];
     if (i == 0) a.keeps[ch] = expf((float)gs[kC - 1]);
   }
-  uint16_t* t2 = a.t2_rows + ch * (2 * 8 * kFrag);
-  uint16_t* pf = a.p_rows + ch * (2 * 8 * kFrag);
-  uint16_t* tt = BWD ? a.tt_rows + ch * (2 * 8 * kFrag) : nullptr;
+  uint16_t* tf = a.mats + ch * kGdrMats;
+  uint16_t* pf = tf + kTriSet;
   for (int s = 0; s < kC;) {
     const int e = seg_end(cuts, s);
-    // P, then L diag(beta) (and diag(beta) L for the backward)
+    // P, and L diag(beta), for the backward diag(beta) L
 #pragma unroll
     for (int ct = 0; ct < 4; ++ct)
 #pragma unroll
@@ -399,7 +396,7 @@ __global__ __launch_bounds__(256) void k_gdr_prep(GdrArgs a) {
         const bool in = cj <= ri && cj >= s && ri < e;
         const float d = in ? expf((float)(gs[ri] - gs[cj])) * rk[cj] : 0.0f;
         tm[ri][cj] = in ? qk[ct][i] * rq[ri] * d : 0.0f;
-        am[ri][cj] = in && cj < ri ? kk[ct][i] * rk[ri] * d * bt[cj] : 0.0f;
+        am[ri][cj] = in && cj < ri ? kk[ct][i] * rk[ri] * d * bt[BWD ? ri : cj] : 0.0f;
       }
     __syncthreads();
     emit<BWD>(tm, pf, coef + kRowP * kC, s, e);
@@ -411,23 +408,8 @@ __global__ __launch_bounds__(256) void k_gdr_prep(GdrArgs a) {
         if (ct != w) tm[16 * w + 4 * g + i][16 * ct + r] = 0.0f;  // each wave its rows
     __syncthreads();
     invert(am, tm);
-    emit<false>(tm, t2, coef + kRowT2 * kC, s, e);
+    emit<BWD>(tm, tf, coef + kRowT * kC, s, e);
     __syncthreads();
-    if constexpr (BWD) {
-#pragma unroll
-      for (int ct = 0; ct < 4; ++ct)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int ri = 16 * w + 4 * g + i, cj = 16 * ct + r;
-          const bool in = cj < ri && cj >= s && ri < e;
-          am[ri][cj] =
-              in ? kk[ct][i] * rk[ri] * rk[cj] * expf((float)(gs[ri] - gs[cj])) * bt[ri] : 0.0f;
-        }
-      __syncthreads();
-      invert(am, tm);
-      emit<true>(tm, tt, coef + kRowT * kC, s, e);
-      __syncthreads();
-    }
     s = e;
   }
 }
@@ -439,11 +421,11 @@ __global__ __launch_bounds__(256) void k_gdr_prep(GdrArgs a) {
 // A column's largest value over the four lanes that hold it, as its scale.
 template <int N>
 __device__ __forceinline__ Scale col_scale(const f32x4_t (&v)[N]) {
-  uint32_t m = 0u;
+  float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m = max_u(m, abs_bits(v[i][j]));
+    for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(v[i][j]));
   return scale_of(quad_max(m));
 }
 // Accumulators of 16-row tiles as right operands of k steps of 32.
@@ -469,408 +451,564 @@ __device__ __forceinline__ f32x4_t coef4(const float* coef, int which, int rt) {
   return *reinterpret_cast<const f32x4_t*>(coef + which * kC + 16 * rt + 4 * g);
 }
 
-// DELTA: one chunk a wave; leaves its delta, from its checkpoint.
-// Otherwise: the chain over all chunks.
-template <typename IO, int KP, bool DELTA>
-__global__ __launch_bounds__(256) void k_gdr_chain(GdrArgs a) {
-  constexpr int NP = kParts<IO>, KS = KP / 32, KT = KP / 16;
-  constexpr int kSet = NP * 4 * KS * kFrag;
-  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
-  const int vblocks = (a.V + 15) / 16;
-  const int64_t nc = (a.T + kC - 1) / kC, chains = a.B * a.H * vblocks;
-  int64_t id = (int64_t)blockIdx.x * (blockDim.x / 64) + (threadIdx.x >> 6);
-  if (id >= (DELTA ? nc : 1) * chains) return;  // whole waves
-  const int64_t c0 = DELTA ? id / chains : 0, c1 = DELTA ? c0 + 1 : nc;
-  if constexpr (DELTA) id -= c0 * chains;
-  const int vb = (int)(id % vblocks);
-  const int64_t bh = id / vblocks, b = bh / a.H;
-  const int h = (int)(bh % a.H), hk = h / (a.H / a.Hk);
-  const int col = 16 * vb + r;
-  const bool colin = col < a.V;
-  const int64_t sn = (int64_t)a.K * a.V;  // of one state
-
-  f32x4_t S[KT];
-  auto load_state = [&](const float* p) __attribute__((always_inline)) {
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = 16 * kt + 4 * g + i;
-        S[kt][i] = colin && k < a.K ? p[(int64_t)k * a.V + col] : 0.0f;
-      }
-  };
-  auto store_state = [&](float* p) __attribute__((always_inline)) {
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = 16 * kt + 4 * g + i;
-        if (colin && k < a.K) p[(int64_t)k * a.V + col] = S[kt][i];
-      }
-  };
-  if constexpr (DELTA) {
-    load_state(a.checkpoints + (c0 * a.B * a.H + bh) * sn);
-  } else if (a.state0) {
-    load_state(a.state0 + bh * sn);
-  } else {
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt) S[kt] = kZero4;
+// `bytes` (below 2^31) of memory from a base that is the same for all lanes, at 32-bit
+// offsets of the lanes' own: a load past the end gives 0 and a store there is dropped.
+// The second offset is the same for all lanes, and inside the array.
+struct Buffer {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ Buffer(const void* p, int64_t bytes)
+      : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, 0x00027000)) {}
+  __device__ __forceinline__ u32x4_t load16(uint32_t at, int uniform) const {
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, uniform, 0));
   }
+  __device__ __forceinline__ u32x2_t load8(uint32_t at) const {
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, (int)at, 0, 0));
+  }
+  __device__ __forceinline__ void load(uint32_t at, float& v) const {
+    v = as_f32((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)at, 0, 0));
+  }
+  __device__ __forceinline__ void load(uint32_t at, uint16_t& v) const {
+    v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)at, 0, 0);
+  }
+  __device__ __forceinline__ void store(uint32_t at, float v, const float*) const {
+    __builtin_amdgcn_raw_buffer_store_b32(as_u32(v), r, (int)at, 0, 0);
+  }
+  __device__ __forceinline__ void store(uint32_t at, float v, const uint16_t*) const {
+    __builtin_amdgcn_raw_buffer_store_b16((short)(pack_bf16x2(v, 0.0f) & 0xFFFFu), r, (int)at, 0, 0);
+  }
+};
 
-  for (int64_t c = c0; c < c1; ++c) {
-    const int64_t ch = (c * a.B + b) * a.H + h, kh = (c * a.B + b) * a.Hk + hk;
-    if (!DELTA && a.checkpoints) store_state(a.checkpoints + ch * sn);
-    const uint64_t cuts = a.cuts[c * a.B + b];
-    const float* coef = a.coef + ch * (kCoef * kC);
-    const uint16_t* kf = a.k_rows + kh * kSet;
-    const uint16_t* qf = a.q_rows + kh * kSet;
-    const uint16_t* kc = a.k_cols + kh * kSet;
-    const uint16_t* t2 = a.t2_rows + ch * (16 * kFrag);
-    const uint16_t* pf = a.p_rows + ch * (16 * kFrag);
-    float vv[4][4];
+// One chunk's operands: in registers on their way from memory, then in LDS for all waves
+// of the workgroup: k, q, T2 (or, transposed, T), P and the steps' coefficients.
+template <int NP, int KS, int NT>
+struct Stage {
+  static constexpr int kSet = NP * 4 * KS * kFrag;  // values of k or of q
+  static constexpr int kMats = 2 * kTriSet + kStagedCoefs * kC * 2;
+  static constexpr int kBytes = (2 * kSet + kMats) * 2;
+  static constexpr int NQ = 2 * kSet / 8 / NT, NM = (kMats / 8 + NT - 1) / NT;
+  static_assert(NQ * NT * 8 == 2 * kSet, "whole loads");
+  u32x4_t kq[NQ], m[NM];
+  u32x2_t cuts_v;  // the same for all lanes; read where they are used, so that the loads are
+  float keep_v;    // not waited for here
+  __device__ __forceinline__ void fetch(const GdrArgs& a, int64_t cb, int h, int hk) {
+    const int64_t ch = cb * a.H + h, kh = cb * a.Hk + hk;
+    const uint32_t at = threadIdx.x * 16u;
+    const Buffer fq(a.kq_rows + kh * (2 * kSet), 4 * kSet), fm(a.mats + ch * kGdrMats, 2 * kMats);
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt)
+    for (int i = 0; i < NQ; ++i) kq[i] = fq.load16(at, i * NT * 16);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t t = c * kC + 16 * rt + 4 * g + i;
-        vv[rt][i] = colin && t < a.T
-                        ? io_ld((const IO*)a.v, (t * a.B + b) * a.ld_v + (int64_t)h * a.V + col)
-                        : 0.0f;
-      }
-    for (int s = 0; s < kC;) {
-      const int e = seg_end(cuts, s);
-      const bool fresh = (cuts >> s) & 1, whole = s == 0 && e == kC;
-      f32x4_t R[4], O[4];
-      if (fresh) {
+    for (int i = 0; i < NM; ++i) m[i] = fm.load16(at + (uint32_t)(i * NT * 16), 0);
+    cuts_v = Buffer(a.cuts + cb, 8).load8(0);
+    Buffer(a.keeps + ch, 4).load(0, keep_v);
+  }
+  __device__ __forceinline__ uint64_t cuts() const {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(cuts_v.y) << 32 |
+           (uint32_t)__builtin_amdgcn_readfirstlane(cuts_v.x);
+  }
+  __device__ __forceinline__ void put(char* lds) const {
+    u32x4_t* to = reinterpret_cast<u32x4_t*>(lds) + threadIdx.x;
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) S[kt] = kZero4;
+    for (int i = 0; i < NQ; ++i) to[i * NT] = kq[i];
+    to += NQ * NT;
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          O[rt] = kZero4;
+    for (int i = 0; i < NM; ++i)
+      if ((i + 1) * NT <= kMats / 8 || (int)threadIdx.x + i * NT < kMats / 8) to[i * NT] = m[i];
+  }
+};
+// A fragment of k^T or q^T (row tile kt of K, steps 32 ks...) from their rows in LDS: the
+// transposing read gives each of 16 lanes one column of the four rows that they address
+// together, eight bytes a lane.
+template <int KS>
+__device__ __forceinline__ f16x8_t cols(const uint16_t* rows, int part, int kt, int ks) {
+  typedef short s16x4_t __attribute__((ext_vector_type(4)));
+  typedef short s16x8_t __attribute__((ext_vector_type(8)));
+  typedef __attribute__((address_space(3))) s16x4_t lds_t;
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const uint16_t* at = rows + ((part * 4 + 2 * ks) * KS + (kt >> 1)) * kFrag +
+                       ((r & 3) * 16 + 4 * g + (r >> 2)) * 8 + 4 * (kt & 1);
+  const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)at);
+  const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(at + KS * kFrag));
+  return __builtin_bit_cast(f16x8_t, (s16x8_t)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+struct Yes {
+  __device__ constexpr operator bool() const { return true; }
+};
+struct No {
+  __device__ constexpr operator bool() const { return false; }
+};
+
+// What a chain's wave has.  A workgroup has NCB blocks of 16 columns of a head, four waves
+// each; lane l has column r = l % 16.  Wave j of the four has the steps 16 j... of a chunk,
+// and the rows 32 j... of the state (where K <= 64: waves 0 and 1 alone).
+struct Wave {
+  int64_t bh, b;
+  int h, hk, col, j, block;
+  bool colin;
+  template <int NCB>
+  static __device__ __forceinline__ Wave make(const GdrArgs& a) {
+    constexpr int kCols = 16 * NCB;
+    const uint32_t vblocks = (uint32_t)(a.V + kCols - 1) / kCols;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Wave w;
+    const uint32_t bh = blockIdx.x / vblocks;
+    w.bh = bh;
+    w.b = bh / (uint32_t)a.H;
+    w.h = (int)(bh % (uint32_t)a.H);
+    w.hk = w.h / (a.H / a.Hk);
+    w.j = wave & 3;
+    w.block = wave >> 2;
+    w.col = (int)(blockIdx.x % vblocks) * kCols + w.block * 16 + (threadIdx.x & 15);
+    w.colin = w.col < a.V;
+    return w;
+  }
+};
+
+constexpr uint32_t kNowhere = 0x80000000u;  // past the end of any array here
+
+// 16 N rows of an array from row 16 t0 on, `pitch` elements apart: of rows 16 t + 4 g + 0..3
+// the lane's column.  Rows from `rows` on read as 0 and are not written, nor is a column
+// past V's end.
+template <typename IO>
+struct Rows {
+  Buffer buf;
+  uint32_t pitch, lane;
+  int t0;
+  __device__ __forceinline__ Rows(const IO* p, int64_t pitch_, int64_t rows, int width, const Wave& w,
+                                  int t0_)
+      : buf(p, rows <= 0 ? 0 : ((rows - 1) * pitch_ + width) * (int64_t)sizeof(IO)), t0(t0_) {
+    pitch = (uint32_t)pitch_ * (uint32_t)sizeof(IO);
+    const uint32_t g = (threadIdx.x & 63) >> 4;
+    lane = w.colin ? 4u * g * pitch + (uint32_t)w.col * (uint32_t)sizeof(IO) : kNowhere;
+  }
+  __device__ __forceinline__ uint32_t at(int t, int i) const {
+    return lane + (uint32_t)(16 * (t0 + t) + i) * pitch;
+  }
+  template <int N>
+  __device__ __forceinline__ void load(IO (&v)[N][4]) const {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) R[rt][i] = vv[rt][i];
-        }
-      } else {
-        const Scale sc = col_scale(S);
-        f16x8_t sb[KS][2];
-        to_operand<2>(S, sc.up, sb);
+    for (int t = 0; t < N; ++t)
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          f32x4_t x = kZero4, y = kZero4;
+      for (int i = 0; i < 4; ++i) buf.load(at(t, i), v[t][i]);
+  }
+  template <int N>
+  __device__ __forceinline__ void store(const f32x4_t (&v)[N]) const {
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            f16x8_t ka[NP], qa[NP];
+    for (int t = 0; t < N; ++t)
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-              ka[p] = frag<KP>(kf, (p * 4 + rt) * KS + ks);
-              if (!DELTA) qa[p] = frag<KP>(qf, (p * 4 + rt) * KS + ks);
-            }
-            x = mma_parts<NP, 2>(ka, sb[ks], x);
-            if (!DELTA) y = mma_parts<NP, 2>(qa, sb[ks], y);
-          }
-          const f32x4_t ek = coef4(coef, kEnterK, rt), eq = coef4(coef, kEnterQ, rt);
+      for (int i = 0; i < 4; ++i) buf.store(at(t, i), v[t][i], (const IO*)nullptr);
+  }
+  // of one tile the rows [s, e) only
+  __device__ __forceinline__ void store(const f32x4_t (&v)[1], int s, int e) const {
+    const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            R[rt][i] = __builtin_fmaf(-ek[i], x[i] * sc.down, vv[rt][i]);
-            O[rt][i] = DELTA ? 0.0f : eq[i] * (y[i] * sc.down);
-          }
-        }
-      }
-      if (!whole) {
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int step = 16 * rt + 4 * g + i;
-            R[rt][i] = step >= s && step < e ? R[rt][i] : 0.0f;
-          }
-      }
-      // delta = T2 R, u = beta delta
-      f32x4_t U[4];
-      {
-        const Scale sc = col_scale(R);
-        f16x8_t rb[2][2];
-        to_operand<2>(R, sc.up, rb);
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          f32x4_t x = kZero4;
-#pragma unroll
-          for (int ks = 0; ks <= rt / 2; ++ks) {
-            const f16x8_t ta[2] = {frag<KP>(t2, rt * 2 + ks), frag<KP>(t2, 8 + rt * 2 + ks)};
-            x = mma_parts<2, 2>(ta, rb[ks], x);
-          }
-          const f32x4_t rs = coef4(coef, kRowT2, rt), be = coef4(coef, kBeta, rt);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int step = 16 * rt + 4 * g + i;
-            const bool in = whole || (step >= s && step < e);
-            const float d = x[i] * sc.down * rs[i];
-            if constexpr (DELTA) {
-              if (in) a.delta[(ch * kC + step) * a.Vp + col] = colin ? d : 0.0f;
-            }
-            U[rt][i] = in ? d * be[i] : 0.0f;
-          }
-        }
-      }
-      if constexpr (!DELTA) {
-        const Scale sc = col_scale(U);
-        f16x8_t ub[2][2];
-        to_operand<2>(U, sc.up, ub);
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          f32x4_t x = kZero4;
-#pragma unroll
-          for (int ks = 0; ks <= rt / 2; ++ks) {
-            const f16x8_t pa[2] = {frag<KP>(pf, rt * 2 + ks), frag<KP>(pf, 8 + rt * 2 + ks)};
-            x = mma_parts<2, 2>(pa, ub[ks], x);
-          }
-          const f32x4_t rs = coef4(coef, kRowP, rt);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int step = 16 * rt + 4 * g + i;
-            const int64_t t = c * kC + step;
-            if (colin && t < a.T && step >= s && step < e)
-              io_st((IO*)a.o, ((t * a.B + b) * a.H + h) * a.V + col,
-                    __builtin_fmaf(x[i] * sc.down, rs[i] * a.scale, O[rt][i]));
-          }
-        }
-        if (e == kC) {  // the segment that leaves the chunk
-          f32x4_t L[4];
-#pragma unroll
-          for (int rt = 0; rt < 4; ++rt) {
-            const f32x4_t lv = coef4(coef, kLeaveK, rt);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int step = 16 * rt + 4 * g + i;
-              L[rt][i] = whole || step >= s ? U[rt][i] * lv[i] : 0.0f;
-            }
-          }
-          const Scale sl = col_scale(L);
-          f16x8_t lb[2][2];
-          to_operand<2>(L, sl.up, lb);
-          const float keep = a.keeps[ch];
-#pragma unroll
-          for (int kt = 0; kt < KT; ++kt) {
-            f32x4_t x = kZero4;
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-              f16x8_t ka[NP];
-#pragma unroll
-              for (int p = 0; p < NP; ++p) {
-                ka[p] = frag<KP>(kc, (p * KT + kt) * 2 + ks);
-                if (!whole) ka[p] = keep_steps(ka[p], ks, s, e);
-              }
-              x = mma_parts<NP, 2>(ka, lb[ks], x);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float add = x[i] * sl.down;
-              S[kt][i] = fresh ? add : __builtin_fmaf(keep, S[kt][i], add);
-            }
-          }
-        }
-      }
-      s = e;
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * t0 + 4 * g + i;
+      buf.store(row >= s && row < e ? at(0, i) : kNowhere, v[0][i], (const IO*)nullptr);
     }
   }
-  if constexpr (!DELTA) {
-    if (a.state) store_state(a.state + bh * sn);
+};
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(uint16_t v) { return as_f32((uint32_t)v << 16); }
+template <typename IO, int N>
+__device__ __forceinline__ void widen(const IO (&v)[N][4], f32x4_t (&out)[N]) {
+#pragma unroll
+  for (int t = 0; t < N; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[t][i] = widen(v[t][i]);
+}
+
+// What the four waves of a column block hand each other: the state as a right operand with
+// a scale for every 32 rows (its place is used again for the second of the chunk's vectors),
+// and the 64 steps of a vector in fp32, 16 bytes a lane and wave.
+template <int KS, bool BACK>
+struct Exchange {
+  static constexpr int kState = KS * 2 * kFrag * 2, kVec = 4 * 64 * 16;
+  static constexpr int kBytes = kState + kVec * (BACK ? 2 : 1) + KS * 16 * 4;
+  static_assert(kVec <= kState, "the second vector lies over the state");
+  char* base;
+  __device__ __forceinline__ uint16_t* state(int ks, int part) const {
+    return (uint16_t*)base + (ks * 2 + part) * kFrag + (threadIdx.x & 63) * 8;
   }
+  __device__ __forceinline__ f32x4_t* vec(int which, int j) const {
+    char* p = which == 1 ? base : base + kState + (which == 2 ? kVec : 0);
+    return (f32x4_t*)p + j * 64 + (threadIdx.x & 63);
+  }
+  __device__ __forceinline__ float* down(int ks) const {
+    return (float*)(base + kState + kVec * (BACK ? 2 : 1)) + ks * 16 + (threadIdx.x & 15);
+  }
+  // the wave's 32 rows of the state
+  __device__ __forceinline__ void put_state(const f32x4_t (&S)[2], int j) const {
+    const Scale sc = col_scale(S);
+    f16x8_t b[1][2];
+    to_operand<2>(S, sc.up, b);
+    *reinterpret_cast<f16x8_t*>(state(j, 0)) = b[0][0];
+    *reinterpret_cast<f16x8_t*>(state(j, 1)) = b[0][1];
+    if ((threadIdx.x & 63) < 16) *down(j) = sc.down;
+  }
+  __device__ __forceinline__ void get_vec(int which, f32x4_t (&v)[4]) const {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) v[t] = *vec(which, t);
+  }
+};
+
+// 16 rows of k S, and of q S: a product for every 32 rows of the state, which have scales
+// of their own.
+template <int NP, int KS, bool BOTH, typename X>
+__device__ __forceinline__ void times_state(const uint16_t* k_rows, const uint16_t* q_rows, int rt,
+                                            const X& x, f32x4_t& k_out, f32x4_t& q_out) {
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+    f16x8_t ka[NP], qa[NP], sb[2];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      ka[p] = frag(k_rows, (p * 4 + rt) * KS + ks);
+      if (BOTH) qa[p] = frag(q_rows, (p * 4 + rt) * KS + ks);
+    }
+    sb[0] = *reinterpret_cast<const f16x8_t*>(x.state(ks, 0));
+    sb[1] = *reinterpret_cast<const f16x8_t*>(x.state(ks, 1));
+    const float down = *x.down(ks);
+    const f32x4_t y = mma_parts<NP, 2>(ka, sb, kZero4);
+    f32x4_t z = kZero4;
+    if (BOTH) z = mma_parts<NP, 2>(qa, sb, kZero4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      k_out[i] = ks == 0 ? y[i] * down : __builtin_fmaf(y[i], down, k_out[i]);
+      if (BOTH) q_out[i] = ks == 0 ? z[i] * down : __builtin_fmaf(z[i], down, q_out[i]);
+    }
+  }
+}
+// 16 rows of a triangular matrix times a vector's right operand.
+template <bool TRANSPOSED, int PB>
+__device__ __forceinline__ f32x4_t times_tri(const uint16_t* m, int rt, const f16x8_t (&b)[2][PB]) {
+  f32x4_t x = kZero4;
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+    if (TRANSPOSED ? ks < rt / 2 : ks > rt / 2) continue;
+    const int f = tri<TRANSPOSED>(rt, ks);
+    const f16x8_t ma[2] = {frag(m, f), frag(m, kTri + f)};
+    x = mma_parts<2, PB>(ma, b[ks], x);
+  }
+  return x;
+}
+// 16 rows of k^T (or q^T) times a vector's right operand.
+template <int NP, int KS, bool FULL>
+__device__ __forceinline__ f32x4_t times_cols(const uint16_t* rows, int kt, const f16x8_t (&b)[2][2],
+                                              int s, int e) {
+  f32x4_t x = kZero4;
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+    f16x8_t ka[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      ka[p] = cols<KS>(rows, p, kt, ks);
+      if (!FULL) ka[p] = keep_steps(ka[p], ks, s, e);
+    }
+    x = mma_parts<NP, 2>(ka, b[ks], x);
+  }
+  return x;
+}
+
+// The chain over the chunks.  Between two barriers a wave makes 16 of a vector's 64 steps
+// from the whole of the one before: R from the state, delta and u from R, the state's next
+// value (32 rows) and o from u.
+template <typename IO, int KP, int NCB>
+__global__ __launch_bounds__(256 * NCB) void k_gdr_chain(GdrArgs a) {
+  constexpr int NP = kParts<IO>, KS = KP / 32;
+  typedef Stage<NP, KS, 256 * NCB> St;
+  typedef Exchange<KS, false> X;
+  __shared__ __align__(16) char lds[St::kBytes + NCB * X::kBytes];
+  const int g = (threadIdx.x & 63) >> 4;
+  const Wave w = Wave::make<NCB>(a);
+  const X x = {lds + St::kBytes + w.block * X::kBytes};
+  const int64_t nc = (a.T + kC - 1) / kC;
+  const int64_t sn = (int64_t)a.K * a.V, cn = (int64_t)(a.K + kC) * a.V;  // a state's, a checkpoint's
+  const int64_t vrow = (int64_t)a.H * a.V;
+  const bool owner = w.j < KS;
+  const uint16_t* kf = (const uint16_t*)lds;
+  const uint16_t* qf = kf + St::kSet;
+  const uint16_t* tf = qf + St::kSet;
+  const uint16_t* pf = tf + kTriSet;
+  const float* coef = (const float*)(pf + kTriSet);
+
+  f32x4_t S[2];
+  {
+    float s0[2][4];
+    Rows<float>(a.state0 + w.bh * sn, a.V, a.state0 && owner ? a.K : 0, a.V, w, 2 * w.j).load(s0);
+    widen(s0, S);
+  }
+  St st;
+  IO nv[1][4];  // the next chunk's v
+  // (the address of a chunk behind the last is not read: a length of 0)
+  auto fetch_v = [&](int64_t c) __attribute__((always_inline)) {
+    const int64_t left = a.T - c * kC;
+    Rows<IO>((const IO*)a.v + (c * kC * a.B + w.b) * a.ld_v + (int64_t)w.h * a.V, a.B * a.ld_v,
+             left < kC ? left : kC, a.V, w, w.j)
+        .load(nv);
+  };
+  fetch_v(0);
+  st.fetch(a, w.b, w.h, w.hk);
+  for (int64_t c = 0; c < nc; ++c) {
+    st.put(lds);
+    if (owner) x.put_state(S, w.j);
+    const uint64_t cuts = st.cuts();
+    const float keep = st.keep_v;
+    {
+      const int64_t next = c + 1 < nc ? c + 1 : c;
+      st.fetch(a, next * a.B + w.b, w.h, w.hk);
+    }
+    const int64_t ch = (c * a.B + w.b) * a.H + w.h, left = a.T - c * kC;
+    float* ck = a.checkpoints ? a.checkpoints + ch * cn : nullptr;
+    if (ck && owner) Rows<float>(ck, a.V, a.K, a.V, w, 2 * w.j).store(S);
+    const Rows<IO> out((const IO*)a.o + (c * kC * a.B + w.b) * vrow + (int64_t)w.h * a.V, a.B * vrow,
+                       left < kC ? left : kC, a.V, w, w.j);
+    __syncthreads();
+    f32x4_t R[1];
+
+    // steps [s, e) of the chunk, v in R; FULL: all of them, of a document that goes on
+    auto segment = [&](auto full, int s, int e, bool fresh) __attribute__((always_inline)) {
+      constexpr bool FULL = decltype(full)();
+      auto in = [&](int rt, int i) __attribute__((always_inline)) {
+        const int step = 16 * rt + 4 * g + i;
+        return FULL || (step >= s && step < e);
+      };
+      f32x4_t Q[1], D[1], V[4];
+      f32x4_t ks, qs;
+      if (FULL || !fresh) times_state<NP, KS, true>(kf, qf, w.j, x, ks, qs);
+      if (s == 0) {
+        widen(nv, R);
+        fetch_v(c + 1);
+      }
+      Q[0] = kZero4;
+      D[0] = R[0];
+      if (FULL || !fresh) {
+        const f32x4_t ek = coef4(coef, kEnterK, w.j), eq = coef4(coef, kEnterQ, w.j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          D[0][i] = __builtin_fmaf(-ek[i], ks[i], R[0][i]);
+          Q[0][i] = eq[i] * qs[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) D[0][i] = in(w.j, i) ? D[0][i] : 0.0f;
+      *x.vec(0, w.j) = D[0];
+      __syncthreads();
+      {  // delta = T2 R, u = beta delta
+        x.get_vec(0, V);
+        const Scale sc = col_scale(V);
+        f16x8_t b[2][2];
+        to_operand<2>(V, sc.up, b);
+        const f32x4_t y = times_tri<false>(tf, w.j, b);
+        const f32x4_t rs = coef4(coef, kRowT, w.j), be = coef4(coef, kBeta, w.j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) D[0][i] = y[i] * (sc.down * rs[i]);
+        if (ck) {
+          const Rows<float> delta(ck + sn, a.V, kC, a.V, w, w.j);
+          if (FULL) delta.store(D);
+          else delta.store(D, s, e);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) D[0][i] = in(w.j, i) ? D[0][i] * be[i] : 0.0f;
+      }
+      *x.vec(1, w.j) = D[0];
+      __syncthreads();
+      x.get_vec(1, V);
+      {
+        const Scale sc = col_scale(V);
+        f16x8_t b[2][2];
+        to_operand<2>(V, sc.up, b);
+        const f32x4_t y = times_tri<false>(pf, w.j, b);
+        const f32x4_t rs = coef4(coef, kRowP, w.j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          Q[0][i] = __builtin_fmaf(y[i], sc.down * (rs[i] * a.scale), Q[0][i]);
+        if (FULL) out.store(Q);
+        else out.store(Q, s, e);
+      }
+      if (e == kC && owner) {  // the segment that leaves the chunk
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          const f32x4_t lv = coef4(coef, kLeaveK, rt);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) V[rt][i] = in(rt, i) ? V[rt][i] * lv[i] : 0.0f;
+        }
+        const Scale sc = col_scale(V);
+        f16x8_t b[2][2];
+        to_operand<2>(V, sc.up, b);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const f32x4_t y = times_cols<NP, KS, FULL>(kf, 2 * w.j + t, b, s, e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            S[t][i] = __builtin_fmaf(y[i], sc.down, !FULL && fresh ? 0.0f : keep * S[t][i]);
+        }
+      }
+    };
+    if (cuts == 0) {
+      segment(Yes(), 0, kC, false);
+    } else {
+#pragma unroll 1
+      for (int s = 0; s < kC;) {
+        const int e = seg_end(cuts, s);
+        segment(No(), s, e, (cuts >> s) & 1);
+        s = e;
+      }
+    }
+    __syncthreads();  // before the next chunk's operands are put over these
+  }
+  if (a.state && owner) Rows<float>(a.state + w.bh * sn, a.V, a.K, a.V, w, 2 * w.j).store(S);
 }
 
 // The chain in reverse: dS, and w, dv and every chunk's dS on the way.
-template <typename IO, int KP>
-__global__ __launch_bounds__(256) void k_gdr_back(GdrArgs a) {
-  constexpr int NP = kParts<IO>, KS = KP / 32, KT = KP / 16;
-  constexpr int kSet = NP * 4 * KS * kFrag;
-  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
-  const int vblocks = (a.V + 15) / 16;
-  const int64_t id = (int64_t)blockIdx.x * (blockDim.x / 64) + (threadIdx.x >> 6);
-  if (id >= a.B * a.H * vblocks) return;  // whole waves
-  const int vb = (int)(id % vblocks);
-  const int64_t bh = id / vblocks, b = bh / a.H;
-  const int h = (int)(bh % a.H), hk = h / (a.H / a.Hk);
-  const int col = 16 * vb + r;
-  const bool colin = col < a.V;
+template <typename IO, int KP, int NCB>
+__global__ __launch_bounds__(256 * NCB) void k_gdr_back(GdrArgs a) {
+  constexpr int NP = kParts<IO>, KS = KP / 32;
+  typedef Stage<NP, KS, 256 * NCB> St;
+  typedef Exchange<KS, true> X;
+  __shared__ __align__(16) char lds[St::kBytes + NCB * X::kBytes];
+  const int g = (threadIdx.x & 63) >> 4;
+  const Wave w = Wave::make<NCB>(a);
+  const X x = {lds + St::kBytes + w.block * X::kBytes};
   const int64_t nc = (a.T + kC - 1) / kC;
-  const int64_t sn = (int64_t)a.K * a.V;
+  const int64_t sn = (int64_t)a.K * a.V, vrow = (int64_t)a.H * a.V;
+  const bool owner = w.j < KS;
+  const uint16_t* kf = (const uint16_t*)lds;
+  const uint16_t* qf = kf + St::kSet;
+  const uint16_t* tf = qf + St::kSet;
+  const uint16_t* pf = tf + kTriSet;
+  const float* coef = (const float*)(pf + kTriSet);
 
-  f32x4_t S[KT];  // dS
-#pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = 16 * kt + 4 * g + i;
-      S[kt][i] = a.grad_state && colin && k < a.K ? a.grad_state[bh * sn + (int64_t)k * a.V + col]
-                                                  : 0.0f;
-    }
-  auto store_state = [&](float* p) __attribute__((always_inline)) {
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = 16 * kt + 4 * g + i;
-        if (colin && k < a.K) p[(int64_t)k * a.V + col] = S[kt][i];
-      }
+  f32x4_t S[2];  // dS
+  {
+    float s0[2][4];
+    Rows<float>(a.grad_state + w.bh * sn, a.V, a.grad_state && owner ? a.K : 0, a.V, w, 2 * w.j).load(s0);
+    widen(s0, S);
+  }
+  St st;
+  IO ng[1][4];  // the next chunk's grad_o
+  auto fetch_o = [&](int64_t c) __attribute__((always_inline)) {
+    const int64_t left = a.T - c * kC;
+    Rows<IO>((const IO*)a.grad_o + (c * kC * a.B + w.b) * vrow + (int64_t)w.h * a.V, a.B * vrow,
+             left < kC ? left : kC, a.V, w, w.j)
+        .load(ng);
   };
-
+  fetch_o(nc - 1);
+  st.fetch(a, (nc - 1) * a.B + w.b, w.h, w.hk);
   for (int64_t c = nc - 1; c >= 0; --c) {
-    const int64_t ch = (c * a.B + b) * a.H + h, kh = (c * a.B + b) * a.Hk + hk;
-    store_state(a.grad_states + ch * sn);
-    const uint64_t cuts = a.cuts[c * a.B + b];
-    const float* coef = a.coef + ch * (kCoef * kC);
-    const uint16_t* kf = a.k_rows + kh * kSet;
-    const uint16_t* kc = a.k_cols + kh * kSet;
-    const uint16_t* qc = a.q_cols + kh * kSet;
-    const uint16_t* tt = a.tt_rows + ch * (16 * kFrag);
-    const uint16_t* pt = a.p_rows + ch * (16 * kFrag);
-    f32x4_t go[4];
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t t = c * kC + 16 * rt + 4 * g + i;
-        go[rt][i] = colin && t < a.T
-                        ? io_ld((const IO*)a.grad_o, ((t * a.B + b) * a.H + h) * a.V + col)
-                        : 0.0f;
-      }
-    for (int e = kC; e > 0;) {
-      const int s = seg_start(cuts, e - 1);
-      const bool fresh = (cuts >> s) & 1, whole = s == 0 && e == kC;
-      f32x4_t dO[4], U[4];
+    st.put(lds);
+    if (owner) x.put_state(S, w.j);
+    const uint64_t cuts = st.cuts();
+    const float keep = st.keep_v;
+    {
+      f32x4_t go[1];
+      widen(ng, go);
+      *x.vec(2, w.j) = go[0];
+      const int64_t next = c > 0 ? c - 1 : 0;
+      fetch_o(next);
+      st.fetch(a, next * a.B + w.b, w.h, w.hk);
+    }
+    const int64_t ch = (c * a.B + w.b) * a.H + w.h, left = a.T - c * kC;
+    if (owner) Rows<float>(a.grad_states + ch * sn, a.V, a.K, a.V, w, 2 * w.j).store(S);
+    const Rows<float> wout(a.w + ch * kC * a.V, a.V, kC, a.V, w, w.j);
+    const Rows<IO> vout((const IO*)a.grad_v + (c * kC * a.B + w.b) * a.ld_gv + (int64_t)w.h * a.V,
+                        a.B * a.ld_gv, left < kC ? left : kC, a.V, w, w.j);
+    __syncthreads();
+
+    auto segment = [&](auto full, int s, int e, bool fresh) __attribute__((always_inline)) {
+      constexpr bool FULL = decltype(full)();
+      auto in = [&](int rt, int i) __attribute__((always_inline)) {
+        const int step = 16 * rt + 4 * g + i;
+        return FULL || (step >= s && step < e);
+      };
+      f32x4_t D[1], dO[4], V[4];
+      x.get_vec(2, dO);
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int step = 16 * rt + 4 * g + i;
-          dO[rt][i] = whole || (step >= s && step < e) ? go[rt][i] : 0.0f;
-        }
-      // du = scale P^T do + exp(G_C - G) K dS
-      {
+        for (int i = 0; i < 4; ++i) dO[rt][i] = in(rt, i) ? dO[rt][i] : 0.0f;
+      {  // du = scale P^T do + exp(G_C - G) K dS
         const Scale sc = col_scale(dO);
-        f16x8_t ob[2][NP];
-        to_operand<NP>(dO, sc.up, ob);
+        f16x8_t b[2][NP];
+        to_operand<NP>(dO, sc.up, b);
+        const f32x4_t y = times_tri<true>(pf, w.j, b);
+        const f32x4_t rs = coef4(coef, kRowP, w.j);
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          f32x4_t x = kZero4;
-#pragma unroll
-          for (int ks = rt / 2; ks < 2; ++ks) {
-            const f16x8_t pa[2] = {frag<KP>(pt, rt * 2 + ks), frag<KP>(pt, 8 + rt * 2 + ks)};
-            x = mma_parts<2, NP>(pa, ob[ks], x);
-          }
-          const f32x4_t rs = coef4(coef, kRowP, rt);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) U[rt][i] = x[i] * sc.down * (rs[i] * a.scale);
-        }
+        for (int i = 0; i < 4; ++i) D[0][i] = y[i] * (sc.down * (rs[i] * a.scale));
       }
       if (e == kC) {
-        const Scale sc = col_scale(S);
-        f16x8_t sb[KS][2];
-        to_operand<2>(S, sc.up, sb);
+        f32x4_t ks, none;
+        times_state<NP, KS, false>(kf, nullptr, w.j, x, ks, none);
+        const f32x4_t lv = coef4(coef, kLeaveK, w.j);
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          f32x4_t x = kZero4;
+        for (int i = 0; i < 4; ++i) D[0][i] = __builtin_fmaf(ks[i], lv[i], D[0][i]);
+      }
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            f16x8_t ka[NP];
+      for (int i = 0; i < 4; ++i) D[0][i] = in(w.j, i) ? D[0][i] : 0.0f;
+      *x.vec(0, w.j) = D[0];
+      __syncthreads();
+      {  // w = T^T du, dv = beta w
+        x.get_vec(0, V);
+        const Scale sc = col_scale(V);
+        f16x8_t b[2][2];
+        to_operand<2>(V, sc.up, b);
+        const f32x4_t y = times_tri<true>(tf, w.j, b);
+        const f32x4_t rs = coef4(coef, kRowT, w.j), be = coef4(coef, kBeta, w.j);
 #pragma unroll
-            for (int p = 0; p < NP; ++p) ka[p] = frag<KP>(kf, (p * 4 + rt) * KS + ks);
-            x = mma_parts<NP, 2>(ka, sb[ks], x);
-          }
-          const f32x4_t lv = coef4(coef, kLeaveK, rt);
+        for (int i = 0; i < 4; ++i) D[0][i] = y[i] * (sc.down * rs[i]);
+        if (FULL) wout.store(D);
+        else wout.store(D, s, e);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) U[rt][i] = __builtin_fmaf(x[i] * sc.down, lv[i], U[rt][i]);
+        for (int i = 0; i < 4; ++i) D[0][i] = in(w.j, i) ? D[0][i] * be[i] : 0.0f;
+        if (FULL) vout.store(D);
+        else vout.store(D, s, e);
+      }
+      *x.vec(1, w.j) = D[0];
+      __syncthreads();
+      if (!owner) return;
+      if (!FULL && fresh) {
+        S[0] = S[1] = kZero4;
+        return;
+      }
+      // dS0 = exp(G_C) dS (of the last segment) + (exp G q)^T do' - (exp G k)^T dv
+      x.get_vec(1, V);
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) {
+        const f32x4_t eq = coef4(coef, kEnterQ, rt), ek = coef4(coef, kEnterK, rt);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dO[rt][i] = in(rt, i) ? dO[rt][i] * eq[i] : 0.0f;
+          V[rt][i] = in(rt, i) ? V[rt][i] * ek[i] : 0.0f;
         }
       }
-      if (!whole) {
+      const Scale sx = col_scale(dO), sy = col_scale(V);
+      f16x8_t xb[2][2], yb[2][2];
+      to_operand<2>(dO, sx.up, xb);
+      to_operand<2>(V, sy.up, yb);
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
+      for (int t = 0; t < 2; ++t) {
+        const f32x4_t p = times_cols<NP, KS, FULL>(qf, 2 * w.j + t, xb, s, e);
+        const f32x4_t y = times_cols<NP, KS, FULL>(kf, 2 * w.j + t, yb, s, e);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int step = 16 * rt + 4 * g + i;
-            U[rt][i] = step >= s && step < e ? U[rt][i] : 0.0f;
-          }
+        for (int i = 0; i < 4; ++i)
+          S[t][i] = __builtin_fmaf(p[i], sx.down,
+                                   __builtin_fmaf(-y[i], sy.down,
+                                                  FULL || e == kC ? keep * S[t][i] : 0.0f));
       }
-      // w = T^T du, dv = beta w
-      f32x4_t W[4];
-      {
-        const Scale sc = col_scale(U);
-        f16x8_t ub[2][2];
-        to_operand<2>(U, sc.up, ub);
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          f32x4_t x = kZero4;
-#pragma unroll
-          for (int ks = rt / 2; ks < 2; ++ks) {
-            const f16x8_t ta[2] = {frag<KP>(tt, rt * 2 + ks), frag<KP>(tt, 8 + rt * 2 + ks)};
-            x = mma_parts<2, 2>(ta, ub[ks], x);
-          }
-          const f32x4_t rs = coef4(coef, kRowT, rt), be = coef4(coef, kBeta, rt);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int step = 16 * rt + 4 * g + i;
-            const int64_t t = c * kC + step;
-            const bool in = step >= s && step < e;
-            const float d = in ? x[i] * sc.down * rs[i] : 0.0f;
-            const float dv = d * be[i];
-            if (in) a.w[(ch * kC + step) * a.Vp + col] = colin ? d : 0.0f;
-            if (in && colin && t < a.T)
-              io_st((IO*)a.grad_v, (t * a.B + b) * a.ld_gv + (int64_t)h * a.V + col, dv);
-            W[rt][i] = dv;
-          }
-        }
+    };
+    if (cuts == 0) {
+      segment(Yes(), 0, kC, false);
+    } else {
+#pragma unroll 1
+      for (int e = kC; e > 0;) {
+        const int s = seg_start(cuts, e - 1);
+        segment(No(), s, e, (cuts >> s) & 1);
+        e = s;
       }
-      if (fresh) {
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) S[kt] = kZero4;
-      } else {
-        // dS0 = exp(G_C) dS (of the last segment) + (exp G q)^T do' - (exp G k)^T dv
-        f32x4_t X[4], Y[4];
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          const f32x4_t eq = coef4(coef, kEnterQ, rt), ek = coef4(coef, kEnterK, rt);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int step = 16 * rt + 4 * g + i;
-            const bool in = whole || (step >= s && step < e);
-            X[rt][i] = in ? dO[rt][i] * eq[i] : 0.0f;
-            Y[rt][i] = in ? W[rt][i] * ek[i] : 0.0f;
-          }
-        }
-        const Scale sx = col_scale(X), sy = col_scale(Y);
-        f16x8_t xb[2][2], yb[2][2];
-        to_operand<2>(X, sx.up, xb);
-        to_operand<2>(Y, sy.up, yb);
-        const float keep = a.keeps[ch];
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-          f32x4_t x = kZero4, y = kZero4;
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            f16x8_t qa[NP], ka[NP];
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-              qa[p] = frag<KP>(qc, (p * KT + kt) * 2 + ks);
-              ka[p] = frag<KP>(kc, (p * KT + kt) * 2 + ks);
-              if (!whole) {
-                qa[p] = keep_steps(qa[p], ks, s, e);
-                ka[p] = keep_steps(ka[p], ks, s, e);
-              }
-            }
-            x = mma_parts<NP, 2>(qa, xb[ks], x);
-            y = mma_parts<NP, 2>(ka, yb[ks], y);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float add = x[i] * sx.down - y[i] * sy.down;
-            S[kt][i] = e == kC ? __builtin_fmaf(keep, S[kt][i], add) : add;
-          }
-        }
-      }
-      e = s;
     }
+    __syncthreads();  // before the next chunk's operands are put over these
   }
-  if (a.grad_state0) store_state(a.grad_state0 + bh * sn);
+  if (a.grad_state0 && owner)
+    Rows<float>(a.grad_state0 + w.bh * sn, a.V, a.K, a.V, w, 2 * w.j).store(S);
 }
 
 // ---------------------------------------------------------------------------
@@ -890,8 +1028,8 @@ template <typename IO, int KP>
 __global__ __launch_bounds__(256) void k_gdr_grads(GdrArgs a) {
   constexpr int NP = kParts<IO>, KS = KP / 32, KT = KP / 16;
   constexpr int kSet = NP * 4 * KS * kFrag;
-  constexpr int kStates = 2 * KT * 4 * kFrag * 2, kMats = 2 * (int)sizeof(Mat);
-  // fragments of S0 and dS, [row tile][32 columns][part]; then the matrices X and Z
+  constexpr int kStates = 2 * KT * 4 * kFrag * 2, kMats = 2 * (int)sizeof(Mat) + 2 * kSet * 2;
+  // fragments of S0 and dS, [row tile][32 columns][part]; then the matrices X and Z, k and q
   __shared__ __align__(16) char big[kStates > kMats ? kStates : kMats];
   __shared__ __align__(16) uint16_t df[16 * kFrag];  // of delta
   __shared__ float ro[kC], rw[kC], rd[kC], rs[KP], rg[KP], bt[kC], gam[kC], tail[kC], rkk[kC], rkq[kC];
@@ -901,18 +1039,17 @@ __global__ __launch_bounds__(256) void k_gdr_grads(GdrArgs a) {
   uint16_t* gf = sf + KT * 4 * kFrag;
   Mat& xm = *(Mat*)big;
   Mat& zm = *(Mat*)(big + sizeof(Mat));
+  uint16_t* kl = (uint16_t*)(big + 2 * sizeof(Mat));  // k and q, for their columns
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, r = lane & 15;
   const int64_t kh = blockIdx.x;
   const int hk = (int)(kh % a.Hk), share = a.H / a.Hk;
   const int64_t cb = kh / a.Hk, b = cb % a.B, c = cb / a.B;
-  const int64_t sn = (int64_t)a.K * a.V;
+  const int64_t sn = (int64_t)a.K * a.V, cn = (int64_t)(a.K + kC) * a.V;
   const uint64_t cuts = a.cuts[cb];
   const bool enters = !(cuts & 1), whole = cuts == 0;
   const int first_end = seg_end(cuts, 0), last_start = seg_start(cuts, kC - 1);
-  const uint16_t* kf = a.k_rows + kh * kSet;
-  const uint16_t* qf = a.q_rows + kh * kSet;
-  const uint16_t* kc = a.k_cols + kh * kSet;
-  const uint16_t* qc = a.q_cols + kh * kSet;
+  const uint16_t* kf = a.kq_rows + kh * (2 * kSet);
+  const uint16_t* qf = kf + kSet;
 
   f32x4_t tq[KT], tk[KT];
 #pragma unroll
@@ -923,7 +1060,7 @@ __global__ __launch_bounds__(256) void k_gdr_grads(GdrArgs a) {
     const int64_t ch = cb * a.H + h;
     if (threadIdx.x < kC) {
       const int i = threadIdx.x;
-      const float* coef = a.coef + ch * (kCoef * kC);
+      const float* coef = (const float*)(a.mats + ch * kGdrMats + 2 * kTriSet);
       gs[i] = a.decay_sums[ch * kC + i];
       bt[i] = coef[kBeta * kC + i];
       rkk[i] = coef[kRowKk * kC + i];
@@ -944,8 +1081,8 @@ __global__ __launch_bounds__(256) void k_gdr_grads(GdrArgs a) {
         const int row = 16 * w + r;
         const int64_t t = c * kC + row;
         float ov[16], wv[16], dv[16];
-        const float* wr = a.w + (ch * kC + row) * a.Vp;
-        const float* dr = a.delta + (ch * kC + row) * a.Vp;
+        const float* wr = a.w + (ch * kC + row) * a.V;
+        const float* dr = a.checkpoints + ch * cn + (int64_t)(a.K + row) * a.V;
         const IO* orow = (const IO*)a.grad_o + ((t * a.B + b) * a.H + h) * a.V;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -986,7 +1123,7 @@ __global__ __launch_bounds__(256) void k_gdr_grads(GdrArgs a) {
         for (int j = 0; j < 4; ++j) {
           const int col = v0 + 32 * (j >> 1) + 8 * g + 4 * (j & 1);
           const int n = k < a.K ? a.V : 0;
-          ld4(a.checkpoints + ch * sn + (int64_t)k * a.V, col, enters ? n : 0, s0 + 4 * j);
+          ld4(a.checkpoints + ch * cn + (int64_t)k * a.V, col, enters ? n : 0, s0 + 4 * j);
           ld4(a.grad_states + ch * sn + (int64_t)k * a.V, col, n, ds + 4 * j);
         }
 #pragma unroll
@@ -1016,7 +1153,7 @@ __global__ __launch_bounds__(256) void k_gdr_grads(GdrArgs a) {
         f32x4_t x = kZero4, y = kZero4;
 #pragma unroll
         for (int vs = 0; vs < 2; ++vs) {
-          const f16x8_t db[2] = {frag<KP>(df, (ct * 2 + vs) * 2), frag<KP>(df, (ct * 2 + vs) * 2 + 1)};
+          const f16x8_t db[2] = {frag(df, (ct * 2 + vs) * 2), frag(df, (ct * 2 + vs) * 2 + 1)};
           x = mma_parts<NP, 2>(oa[vs], db, x);
           y = mma_parts<2, 2>(wa[vs], db, y);
         }
@@ -1034,11 +1171,11 @@ __global__ __launch_bounds__(256) void k_gdr_grads(GdrArgs a) {
         for (int vs = 0; vs < 2; ++vs) {
           const int at = (kt * 2 + vs) * 2;
           if (enters) {
-            const f16x8_t sb[2] = {frag<KP>(sf, at), frag<KP>(sf, at + 1)};
+            const f16x8_t sb[2] = {frag(sf, at), frag(sf, at + 1)};
             x = mma_parts<NP, 2>(oa[vs], sb, x);
             y = mma_parts<2, 2>(wa[vs], sb, y);
           }
-          const f16x8_t gb[2] = {frag<KP>(gf, at), frag<KP>(gf, at + 1)};
+          const f16x8_t gb[2] = {frag(gf, at), frag(gf, at + 1)};
           z = mma_parts<2, 2>(da[vs], gb, z);
         }
         const float f = rs[16 * kt + r], fz = rg[16 * kt + r];
@@ -1051,6 +1188,9 @@ __global__ __launch_bounds__(256) void k_gdr_grads(GdrArgs a) {
       }
       __syncthreads();
     }
+
+    for (int i = threadIdx.x; i < 2 * kSet / 8; i += 256)
+      *reinterpret_cast<u32x4_t*>(kl + i * 8) = *reinterpret_cast<const u32x4_t*>(kf + i * 8);
 
     // the rows' factors; what their segment does not reach is 0, whatever it holds
     float dq_q[4], dk_k[4], dk_t[4];
@@ -1092,9 +1232,9 @@ __global__ __launch_bounds__(256) void k_gdr_grads(GdrArgs a) {
           f16x8_t ka[NP], qa[NP], kb[NP];
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            ka[p] = frag<KP>(kf, (p * 4 + w) * KS + ks);
-            qa[p] = frag<KP>(qf, (p * 4 + w) * KS + ks);
-            kb[p] = frag<KP>(kf, (p * 4 + ct) * KS + ks);
+            ka[p] = frag(kf, (p * 4 + w) * KS + ks);
+            qa[p] = frag(qf, (p * 4 + w) * KS + ks);
+            kb[p] = frag(kf, (p * 4 + ct) * KS + ks);
           }
           kk = mma_parts<NP, NP>(ka, kb, kk);
           qk = mma_parts<NP, NP>(qa, kb, qk);
@@ -1222,8 +1362,8 @@ __global__ __launch_bounds__(256) void k_gdr_grads(GdrArgs a) {
               f16x8_t kb[NP], qb[NP];
 #pragma unroll
               for (int p = 0; p < NP; ++p) {
-                kb[p] = frag<KP>(kc, (p * KT + kt) * 2 + ks);
-                qb[p] = frag<KP>(qc, (p * KT + kt) * 2 + ks);
+                kb[p] = cols<KS>(kl, p, kt, ks);
+                qb[p] = cols<KS>(kl + kSet, p, kt, ks);
                 if (!whole) {
                   kb[p] = keep_steps(kb[p], ks, s, e);
                   qb[p] = keep_steps(qb[p], ks, s, e);
@@ -1361,24 +1501,37 @@ __global__ __launch_bounds__(256) void k_gdr_step(GdrArgs a, const int32_t* __re
   }
 }
 
+// Column blocks of a chain's workgroup: as many as four, which read a chunk's operands
+// together, while every compute unit has a workgroup.
+template <typename F>
+void chain_blocks(const GdrArgs& a, F launch) {
+  const int64_t heads = a.B * a.H, cus = device_cus();
+  const int n = heads * ((a.V + 31) / 32) >= cus ? 2 : 1;
+  launch(n, dim3((unsigned)(heads * ((a.V + 16 * n - 1) / (16 * n)))), dim3(256 * n));
+}
+
 template <typename IO, int KP>
 hipError_t gdr_fwd(const GdrArgs& a, hipStream_t stream) {
-  const int64_t nc = (a.T + kC - 1) / kC, waves = a.B * a.H * ((a.V + 15) / 16);
+  const int64_t nc = (a.T + kC - 1) / kC;
   hipLaunchKernelGGL((k_gdr_prep<IO, KP, false>), dim3((unsigned)(nc * a.B * a.H)), dim3(256), 0,
                      stream, a);
-  hipLaunchKernelGGL((k_gdr_chain<IO, KP, false>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0,
-                     stream, a);
+  chain_blocks(a, [&](int n, dim3 grid, dim3 wg) {
+    if (n == 4) hipLaunchKernelGGL((k_gdr_chain<IO, KP, 4>), grid, wg, 0, stream, a);
+    else if (n == 2) hipLaunchKernelGGL((k_gdr_chain<IO, KP, 2>), grid, wg, 0, stream, a);
+    else hipLaunchKernelGGL((k_gdr_chain<IO, KP, 1>), grid, wg, 0, stream, a);
+  });
   return hipGetLastError();
 }
 template <typename IO, int KP>
 hipError_t gdr_bwd(const GdrArgs& a, hipStream_t stream) {
-  const int64_t nc = (a.T + kC - 1) / kC, waves = a.B * a.H * ((a.V + 15) / 16);
+  const int64_t nc = (a.T + kC - 1) / kC;
   hipLaunchKernelGGL((k_gdr_prep<IO, KP, true>), dim3((unsigned)(nc * a.B * a.H)), dim3(256), 0,
                      stream, a);
-  hipLaunchKernelGGL((k_gdr_chain<IO, KP, true>), dim3((unsigned)((nc * waves + 3) / 4)), dim3(256),
-                     0, stream, a);
-  hipLaunchKernelGGL((k_gdr_back<IO, KP>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, stream,
-                     a);
+  chain_blocks(a, [&](int n, dim3 grid, dim3 wg) {
+    if (n == 4) hipLaunchKernelGGL((k_gdr_back<IO, KP, 4>), grid, wg, 0, stream, a);
+    else if (n == 2) hipLaunchKernelGGL((k_gdr_back<IO, KP, 2>), grid, wg, 0, stream, a);
+    else hipLaunchKernelGGL((k_gdr_back<IO, KP, 1>), grid, wg, 0, stream, a);
+  });
   hipLaunchKernelGGL((k_gdr_grads<IO, KP>), dim3((unsigned)(nc * a.B * a.Hk)), dim3(256), 0, stream,
                      a);
   return hipGetLastError();

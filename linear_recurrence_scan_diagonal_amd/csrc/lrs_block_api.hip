@@ -16,7 +16,7 @@ namespace {
 // What the sizes of a gated delta rule give; no overflow anywhere.
 struct GdrSizes {
   int64_t chunks, rows, states, kw, vw;  // T B, B H K V, Hk K, H V
-  size_t es;
+  size_t es, saved;                    // bytes of an element, and of the checkpoints
 };
 bool gdr_sizes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t K, int64_t V, int io,
                GdrSizes* s) {
@@ -30,7 +30,9 @@ bool gdr_sizes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t K, int64_t V
     return false;
   s->chunks = T / lrs::kGdrRows + (T % lrs::kGdrRows != 0);
   if (!mul_ok(s->chunks, s->states, &n) || n > ((int64_t)1 << 58)) return false;
+  if (!mul_ok(n, lrs::kGdrRows + 1, &m) || m > ((int64_t)1 << 58)) return false;
   s->es = io_size(io);
+  s->saved = (size_t)(n + s->chunks * B * s->vw * lrs::kGdrRows) * 4;
   return true;
 }
 // The kernels' grids and 32-bit sizes.
@@ -42,28 +44,27 @@ bool gdr_fits(int64_t chunks, int64_t B, int64_t H, int64_t K, int64_t V) {
          mul_ok(n, columns, &n) && n < most;
 }
 
+// 31-bit byte offsets inside a chunk's rows of v and o (or their gradients) and a state.
+bool gdr_rows_fit(int64_t B, int64_t ld, int64_t K, int64_t V) {
+  int64_t n;
+  return mul_ok(B, ld, &n) && n < ((int64_t)1 << 23) && (K + lrs::kGdrRows) * V < ((int64_t)1 << 29);
+}
+
 // Carves the workspace of a call; with a null base it only counts.
 size_t gdr_carve(int64_t chunks, int64_t B, int64_t H, int64_t Hk, int64_t K, int64_t V, int io,
                  bool backward, void* ws, lrs::GdrArgs* a) {
   Carve cv(ws);
   constexpr int64_t C = lrs::kGdrRows;
   const int64_t nv = chunks * B * H, nk = chunks * B * Hk;
-  const int64_t set = (io == LRS_F32 ? 2 : 1) * C * (K <= 64 ? 64 : 128), pair = 2 * C * C;
+  // q and k as fragments of 64 steps, in one or two 16-bit parts
+  const int64_t set = (io == LRS_F32 ? 2 : 1) * C * (K <= 64 ? 64 : 128);
   a->cuts = cv.take<uint64_t>(chunks * B);
-  a->coef = cv.take<float>(nv * lrs::kGdrCoefs * C);
   a->keeps = cv.take<float>(nv);
-  a->k_rows = cv.take<uint16_t>(nk * set);
-  a->q_rows = cv.take<uint16_t>(nk * set);
-  a->k_cols = cv.take<uint16_t>(nk * set);
-  a->p_rows = cv.take<uint16_t>(nv * pair);
-  a->t2_rows = cv.take<uint16_t>(nv * pair);
+  a->mats = cv.take<uint16_t>(nv * lrs::kGdrMats);
+  a->kq_rows = cv.take<uint16_t>(nk * 2 * set);
   if (!backward) return cv.used;
-  a->Vp = (V + 15) / 16 * 16;
-  a->q_cols = cv.take<uint16_t>(nk * set);
-  a->tt_rows = cv.take<uint16_t>(nv * pair);
   a->decay_sums = cv.take<double>(nv * C);
-  a->delta = cv.take<float>(nv * C * a->Vp);
-  a->w = cv.take<float>(nv * C * a->Vp);
+  a->w = cv.take<float>(nv * C * V);
   a->grad_states = cv.take<float>(nv * K * V);
   return cv.used;
 }
@@ -183,9 +184,10 @@ int lrs_gdr_fwd(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const 
                       {log_decay, gb}, {beta, gb}, {reset, (size_t)z.rows},
                       {state == state0 ? nullptr : state0, sb}};
   const Span outs[] = {{o, (size_t)(z.rows * z.vw) * es}, {state, sb},
-                       {checkpoints, (size_t)z.chunks * sb}};
+                       {checkpoints, z.saved}};
   if (any_overlap(outs, 3, ins, 7)) return LRS_ERR_INVALID_ARG;
-  if (!gdr_fits(z.chunks, B, H, K, V)) return LRS_ERR_UNSUPPORTED;
+  if (!gdr_fits(z.chunks, B, H, K, V) || !gdr_rows_fit(B, ld_v, K, V) || !gdr_rows_fit(B, z.vw, K, V))
+    return LRS_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < gdr_workspace(T, B, H, Hk, K, V, io_dtype, false))
     return LRS_ERR_WORKSPACE;
   lrs::GdrArgs a = gdr_args(q, ld_q, k, ld_k, v, ld_v, log_decay, beta, T, B, H, Hk, K, V, scale);
@@ -240,7 +242,7 @@ int lrs_gdr_bwd(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const 
                       {k, strided_bytes(z.rows, ld_k, z.kw, es)},
                       {v, strided_bytes(z.rows, ld_v, z.vw, es)},
                       {log_decay, gb}, {beta, gb}, {reset, (size_t)z.rows},
-                      {checkpoints, (size_t)z.chunks * sb},
+                      {checkpoints, z.saved},
                       {grad_o, (size_t)(z.rows * z.vw) * es},
                       {grad_state == grad_state0 ? nullptr : grad_state, sb}};
   const Span outs[] = {{grad_log_decay, gb}, {grad_beta, gb}, {grad_state0, sb}};
@@ -256,7 +258,8 @@ int lrs_gdr_bwd(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const 
     if (slices_overlap(gz[i].p, gz[i].ld, gz[i].w, o.p, o.ld, o.w, z.rows, es))
       return LRS_ERR_INVALID_ARG;
   }
-  if (!gdr_fits(z.chunks, B, H, K, V)) return LRS_ERR_UNSUPPORTED;
+  if (!gdr_fits(z.chunks, B, H, K, V) || !gdr_rows_fit(B, ld_gv, K, V) || !gdr_rows_fit(B, z.vw, K, V))
+    return LRS_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < gdr_workspace(T, B, H, Hk, K, V, io_dtype, true))
     return LRS_ERR_WORKSPACE;
   lrs::GdrArgs a = gdr_args(q, ld_q, k, ld_k, v, ld_v, log_decay, beta, T, B, H, Hk, K, V, scale);

@@ -322,7 +322,7 @@ hipError_t launch_zero(void* p, int64_t bytes, hipStream_t stream);
 // backward also has the last group.
 constexpr int kGdrRows = 64;   // steps a chunk, and between two checkpoints
 constexpr int kGdrMostK = 128;
-constexpr int kGdrCoefs = 9;   // fp32 values a step that the preparation leaves
+constexpr int kGdrMats = 13312;  // 16-bit values of a chunk's matrices and coefficients
 struct GdrArgs {
   const void *q, *k, *v;
   int64_t ld_q, ld_k, ld_v;
@@ -335,18 +335,16 @@ struct GdrArgs {
   int H, Hk, K, V;
   float scale;
   uint64_t* cuts;                             // a bit a step that begins a document, by chunk and sequence
-  float *coef, *keeps;                        // [kGdrCoefs][64], 1
-  uint16_t *k_rows, *q_rows, *k_cols;         // * fragments
-  uint16_t *p_rows, *t2_rows;                 // fragments in two parts
+  float* keeps;                               // 1: the whole chunk's decay
+  uint16_t* mats;                             // [kGdrMats]
+  uint16_t* kq_rows;                          // * fragments of k, then of q
   const void* grad_o;
   const float* grad_state;
   void *grad_q, *grad_k, *grad_v;
   int64_t ld_gq, ld_gk, ld_gv;
   float *grad_log_decay, *grad_beta, *grad_state0;
-  uint16_t *q_cols, *tt_rows;                 // *, and of the other inverse
   double* decay_sums;                         // [64]
-  float *delta, *w;                           // [64][Vp]
-  int64_t Vp;
+  float* w;                                   // [64][V]
   float* grad_states;                         // [K][V]
 };
 hipError_t launch_gdr_fwd(const GdrArgs& a, int io, hipStream_t stream);

@@ -129,7 +129,7 @@ def test_rmsnorm_refusals(lib):
     assert fwd(x=None) == bad and fwd(y=None) == bad and fwd(eps=-1.0) == bad and fwd(eps=float("nan")) == bad
     assert fwd(res=q(5)) == bad and fwd(s=q(5)) == bad  # residual and sum go together
     assert fwd(y=q(1)) == bad and fwd(rstd=q(4)) == bad and fwd(io=5) == bad and fwd(R=-1) == bad
-    assert fwd(res=q(5), s=q(4)) == bad and fwd(R=0) == b.LRS_OK and fwd(R=1 << 23, D=2000) == b.LRS_ERR_UNSUPPORTED
+    assert fwd(res=q(5), s=q(4)) == bad and fwd(R=0) == b.LRS_OK and fwd(x=q(1 << 12), y=q(1 << 16), R=1 << 23, D=2000) == b.LRS_ERR_UNSUPPORTED
 
     def fp8(scales=q(5), group=128, y=q(4), R=2):
         return lib.lrs_rmsnorm_fwd_fp8(q(1), None, q(2), y, scales, None, R, 8, group, F(1e-5), 0, None)
