@@ -124,26 +124,89 @@ __device__ __forceinline__ f32x4_t mma_parts(const f16x8_t (&a)[PA], const f16x8
   return mma(a[0], b[0], c);
 }
 
+// Keeps the compiler from beginning the reads of what follows: it would begin them all and
+// run out of registers.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
 constexpr f32x4_t kZero4 = {0.0f, 0.0f, 0.0f, 0.0f};
 
-// Four elements from column c on of a row of n; 0 past the end.
-__device__ __forceinline__ void ld4(const float* row, int c, int n, float* v) {
-  if (c + 4 <= n) {
-    const f32x4_any q = *reinterpret_cast<const f32x4_any*>(row + c);
-    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-    return;
+// `bytes` (below 2^31) of memory from a base that is the same for all lanes, at 32-bit
+// offsets of the lanes' own: a load past the end gives 0 and a store there is dropped.
+// The second offset is the same for all lanes, and inside the array.
+struct Buffer {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ Buffer(const void* p, int64_t bytes)
+      : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, 0x00027000)) {}
+  __device__ __forceinline__ u32x4_t load16(uint32_t at, int uniform) const {
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, uniform, 0));
   }
+  __device__ __forceinline__ u32x2_t load8(uint32_t at) const {
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, (int)at, 0, 0));
+  }
+  __device__ __forceinline__ void load(uint32_t at, float& v) const {
+    v = as_f32((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)at, 0, 0));
+  }
+  __device__ __forceinline__ void load(uint32_t at, uint16_t& v) const {
+    v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)at, 0, 0);
+  }
+  __device__ __forceinline__ void store(uint32_t at, float v, const float*) const {
+    __builtin_amdgcn_raw_buffer_store_b32(as_u32(v), r, (int)at, 0, 0);
+  }
+  __device__ __forceinline__ void store(uint32_t at, float v, const uint16_t*) const {
+    __builtin_amdgcn_raw_buffer_store_b16((short)(pack_bf16x2(v, 0.0f) & 0xFFFFu), r, (int)at, 0, 0);
+  }
+};
+
+constexpr uint32_t kNowhere = 0x80000000u;  // past the end of any array here
+
+// Four neighbouring elements as they are in memory: a conversion would wait for them.
+template <typename IO>
+struct Quad;
+template <>
+struct Quad<float> {
+  u32x4_t q;
+  __device__ __forceinline__ void get(float* v) const {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = c + j < n ? row[c + j] : 0.0f;
-}
-__device__ __forceinline__ void ld4(const uint16_t* row, int c, int n, float* v) {
-  if (c + 4 <= n) {
-    const u32x2_any q = *reinterpret_cast<const u32x2_any*>(row + c);
+    for (int j = 0; j < 4; ++j) v[j] = as_f32(q[j]);
+  }
+};
+template <>
+struct Quad<uint16_t> {
+  u32x2_t q;
+  __device__ __forceinline__ void get(float* v) const {
     v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+  }
+};
+// Elements c..c+3 of a row of n that begins at byte `row` of the buffer; 0 from n on and
+// in rows that are not there.  vec: n is a multiple of four and the rows are aligned to it.
+__device__ __forceinline__ void ld_quad(const Buffer& b, uint32_t row, bool there, int c, int n,
+                                        bool vec, Quad<float>& q) {
+  if (vec) {
+    q.q = b.load16(there && c < n ? row + (uint32_t)c * 4u : kNowhere, 0);
     return;
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = c + j < n ? io_ld(row, c + j) : 0.0f;
+  for (int j = 0; j < 4; ++j) {
+    float v;
+    b.load(there && c + j < n ? row + (uint32_t)(c + j) * 4u : kNowhere, v);
+    q.q[j] = as_u32(v);
+  }
+}
+__device__ __forceinline__ void ld_quad(const Buffer& b, uint32_t row, bool there, int c, int n,
+                                        bool vec, Quad<uint16_t>& q) {
+  if (vec) {
+    q.q = b.load8(there && c < n ? row + (uint32_t)c * 2u : kNowhere);
+    return;
+  }
+  uint16_t v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b.load(there && c + j < n ? row + (uint32_t)(c + j) * 2u : kNowhere, v[j]);
+  q.q = u32x2_t{(uint32_t)v[0] | (uint32_t)v[1] << 16, (uint32_t)v[2] | (uint32_t)v[3] << 16};
+}
+// Whether rows of n elements, ld apart from p on, can be read in fours.
+template <typename IO>
+__device__ __forceinline__ bool quads(const void* p, int64_t ld, int n) {
+  return ((ld | n) & 3) == 0 && ((uintptr_t)p & (4 * sizeof(IO) - 1)) == 0;
 }
 
 // The segment that step i belongs to: its first step, given the chunk's restarts.
@@ -276,6 +339,21 @@ __global__ __launch_bounds__(256) void k_gdr_prep(GdrArgs a) {
   const int64_t b = cb % a.B, c = cb / a.B;
   const int64_t kh = cb * a.Hk + hk;
 
+  // 16 rows of k and q a wave
+  const int row = 16 * w + r;
+  const int64_t left = a.T - c * kC;
+  auto load = [&](const IO* base, int64_t ld, Quad<IO> (&v)[2 * KS]) __attribute__((always_inline)) {
+    const IO* p = base + ((c * kC * a.B + b) * ld + (int64_t)hk * a.K);
+    const int64_t pitch = a.B * ld, n = left < kC ? left : kC;
+    const Buffer buf(p, ((n - 1) * pitch + a.K) * (int64_t)sizeof(IO));
+    const bool vec = quads<IO>(base, ld, a.K);
+    const uint32_t at = (uint32_t)row * (uint32_t)pitch * (uint32_t)sizeof(IO);
+#pragma unroll
+    for (int j = 0; j < 2 * KS; ++j) ld_quad(buf, at, row < n, 16 * j + 4 * g, a.K, vec, v[j]);
+  };
+  Quad<IO> kraw[2 * KS], qraw[2 * KS];
+  load((const IO*)a.k, a.ld_k, kraw);
+  load((const IO*)a.q, a.ld_q, qraw);
   if (w == 0) {
     const int64_t t = c * kC + lane;
     const bool in = t < a.T;
@@ -304,21 +382,12 @@ __global__ __launch_bounds__(256) void k_gdr_prep(GdrArgs a) {
     }
     if constexpr (BWD) a.decay_sums[ch * kC + lane] = G;
   }
-
-  // 16 rows of k and q a wave
-  const int row = 16 * w + r;
-  const int64_t t = c * kC + row;
-  auto load = [&](const IO* base, int64_t ld, float (&v)[KP / 4]) __attribute__((always_inline)) {
-    const IO* p = base + ((t * a.B + b) * ld + (int64_t)hk * a.K);
-#pragma unroll
-    for (int j = 0; j < 2 * KS; ++j) {
-      if (t < a.T) ld4(p, 16 * j + 4 * g, a.K, v + 4 * j);
-      else v[4 * j] = v[4 * j + 1] = v[4 * j + 2] = v[4 * j + 3] = 0.0f;
-    }
-  };
   float kv[KP / 4], qv[KP / 4];
-  load((const IO*)a.k, a.ld_k, kv);
-  load((const IO*)a.q, a.ld_q, qv);
+#pragma unroll
+  for (int j = 0; j < 2 * KS; ++j) {
+    kraw[j].get(kv + 4 * j);
+    qraw[j].get(qv + 4 * j);
+  }
   const Scale sk = scale_of(quad_max(top_of(kv))), sq = scale_of(quad_max(top_of(qv)));
   f16x8_t qa[KS][NP];
 #pragma unroll
@@ -451,33 +520,6 @@ __device__ __forceinline__ f32x4_t coef4(const float* coef, int which, int rt) {
   return *reinterpret_cast<const f32x4_t*>(coef + which * kC + 16 * rt + 4 * g);
 }
 
-// `bytes` (below 2^31) of memory from a base that is the same for all lanes, at 32-bit
-// offsets of the lanes' own: a load past the end gives 0 and a store there is dropped.
-// The second offset is the same for all lanes, and inside the array.
-struct Buffer {
-  __amdgpu_buffer_rsrc_t r;
-  __device__ __forceinline__ Buffer(const void* p, int64_t bytes)
-      : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, 0x00027000)) {}
-  __device__ __forceinline__ u32x4_t load16(uint32_t at, int uniform) const {
-    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, uniform, 0));
-  }
-  __device__ __forceinline__ u32x2_t load8(uint32_t at) const {
-    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, (int)at, 0, 0));
-  }
-  __device__ __forceinline__ void load(uint32_t at, float& v) const {
-    v = as_f32((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)at, 0, 0));
-  }
-  __device__ __forceinline__ void load(uint32_t at, uint16_t& v) const {
-    v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)at, 0, 0);
-  }
-  __device__ __forceinline__ void store(uint32_t at, float v, const float*) const {
-    __builtin_amdgcn_raw_buffer_store_b32(as_u32(v), r, (int)at, 0, 0);
-  }
-  __device__ __forceinline__ void store(uint32_t at, float v, const uint16_t*) const {
-    __builtin_amdgcn_raw_buffer_store_b16((short)(pack_bf16x2(v, 0.0f) & 0xFFFFu), r, (int)at, 0, 0);
-  }
-};
-
 // One chunk's operands: in registers on their way from memory, then in LDS for all waves
 // of the workgroup: k, q, T2 (or, transposed, T), P and the steps' coefficients.
 template <int NP, int KS, int NT>
@@ -563,8 +605,6 @@ struct Wave {
     return w;
   }
 };
-
-constexpr uint32_t kNowhere = 0x80000000u;  // past the end of any array here
 
 // 16 N rows of an array from row 16 t0 on, `pitch` elements apart: of rows 16 t + 4 g + 0..3
 // the lane's column.  Rows from `rows` on read as 0 and are not written, nor is a column
@@ -1012,8 +1052,8 @@ __global__ __launch_bounds__(256 * NCB) void k_gdr_back(GdrArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// k_gdr_grads: one chunk of one head of q and k a workgroup, the heads that share them
-// one after the other, so that their sums need no atomics.  Wave w has the steps 16 w...
+// k_gdr_grads: one chunk of a head a workgroup.  Heads that share q and k leave their parts
+// of dq and dk in fp32, and k_gdr_shared adds them up, in the heads' order.
 // ---------------------------------------------------------------------------
 // Sum over the 16 lanes of a row of an accumulator.
 __device__ __forceinline__ float row16_sum(float v) {
@@ -1022,386 +1062,430 @@ __device__ __forceinline__ float row16_sum(float v) {
   return v;
 }
 
-constexpr int kVB = 64;  // columns of V at a time
+constexpr int kVB = 32;  // columns of V at a time
 
-template <typename IO, int KP>
-__global__ __launch_bounds__(256) void k_gdr_grads(GdrArgs a) {
-  constexpr int NP = kParts<IO>, KS = KP / 32, KT = KP / 16;
+template <bool B, typename X, typename Y>
+struct Choose {
+  typedef X type;
+};
+template <typename X, typename Y>
+struct Choose<false, X, Y> {
+  typedef Y type;
+};
+
+// Wave 4 x + j of the eight has the steps 16 j... and half x of the columns of its products.
+template <typename IO, int KP, bool SHARED>
+__global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
+  constexpr int NP = kParts<IO>, KS = KP / 32, KT = KP / 16, KH = KT / 2;
   constexpr int kSet = NP * 4 * KS * kFrag;
-  constexpr int kStates = 2 * KT * 4 * kFrag * 2, kMats = 2 * (int)sizeof(Mat) + 2 * kSet * 2;
-  // fragments of S0 and dS, [row tile][32 columns][part]; then the matrices X and Z, k and q
-  __shared__ __align__(16) char big[kStates > kMats ? kStates : kMats];
-  __shared__ __align__(16) uint16_t df[16 * kFrag];  // of delta
+  // fragments of 32 columns of do, w, delta, S0 and dS; then the matrices X and Z, k and q
+  constexpr int kBlock = (4 * NP + 16 + 4 * KT) * kFrag * 2, kMats = 2 * (int)sizeof(Mat) + 2 * kSet * 2;
+  __shared__ __align__(16) char big[kBlock > kMats ? kBlock : kMats];
   __shared__ float ro[kC], rw[kC], rd[kC], rs[KP], rg[KP], bt[kC], gam[kC], tail[kC], rkk[kC], rkq[kC];
-  __shared__ float row_e[kC], col_e[4][kC], rx[kC], rz[kC], rt_s[kC], dots[4], tails[4], bsum[kC];
+  __shared__ float row_e[2][kC], row_t[2][kC], col_e[4][kC], rx[kC], rz[kC], rt_s[kC], dots[8], bsum[kC];
   __shared__ double gs[kC];
-  uint16_t* sf = (uint16_t*)big;
-  uint16_t* gf = sf + KT * 4 * kFrag;
+  uint16_t* of = (uint16_t*)big;
+  uint16_t* wf = of + 4 * NP * kFrag;
+  uint16_t* df = wf + 8 * kFrag;
+  uint16_t* sf = df + 8 * kFrag;
+  uint16_t* gf = sf + 2 * KT * kFrag;
   Mat& xm = *(Mat*)big;
   Mat& zm = *(Mat*)(big + sizeof(Mat));
-  uint16_t* kl = (uint16_t*)(big + 2 * sizeof(Mat));  // k and q, for their columns
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, r = lane & 15;
-  const int64_t kh = blockIdx.x;
-  const int hk = (int)(kh % a.Hk), share = a.H / a.Hk;
-  const int64_t cb = kh / a.Hk, b = cb % a.B, c = cb / a.B;
+  uint16_t* kl = (uint16_t*)(big + 2 * sizeof(Mat));
+  uint16_t* ql = kl + kSet;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = wv & 3, half = wv >> 2;
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int64_t ch = blockIdx.x;
+  const int h = (int)((uint32_t)ch % (uint32_t)a.H), hk = h / (a.H / a.Hk);
+  const int64_t cb = (uint32_t)ch / (uint32_t)a.H, b = (uint32_t)cb % (uint32_t)a.B,
+                c = (uint32_t)cb / (uint32_t)a.B, kh = cb * a.Hk + hk;
   const int64_t sn = (int64_t)a.K * a.V, cn = (int64_t)(a.K + kC) * a.V;
+  const int64_t left = a.T - c * kC, n = left < kC ? left : kC;
   const uint64_t cuts = a.cuts[cb];
   const bool enters = !(cuts & 1), whole = cuts == 0;
   const int first_end = seg_end(cuts, 0), last_start = seg_start(cuts, kC - 1);
-  const uint16_t* kf = a.kq_rows + kh * (2 * kSet);
-  const uint16_t* qf = kf + kSet;
+  const uint16_t* kq = a.kq_rows + kh * (2 * kSet);
 
-  f32x4_t tq[KT], tk[KT];
+  if (threadIdx.x < kC) {
+    const int i = threadIdx.x;
+    const float* coef = (const float*)(a.mats + ch * kGdrMats + 2 * kTriSet);
+    const double G = a.decay_sums[ch * kC + i], last = a.decay_sums[ch * kC + kC - 1];
+    gs[i] = G;
+    bt[i] = coef[kBeta * kC + i];
+    rkk[i] = coef[kRowKk * kC + i];
+    rkq[i] = coef[kRowKq * kC + i];
+    gam[i] = expf((float)G);
+    tail[i] = expf((float)(last - G));
+  }
+  f32x4_t dP[2], dL[2], Q1[KH], K1[KH], K2[KH];
+  dP[0] = dP[1] = dL[0] = dL[1] = kZero4;
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt) tq[kt] = tk[kt] = kZero4;
+  for (int t = 0; t < KH; ++t) Q1[t] = K1[t] = K2[t] = kZero4;
+  float dbeta = 0.0f, dot = 0.0f;
 
-  for (int hh = 0; hh < share; ++hh) {
-    const int h = hk * share + hh;
-    const int64_t ch = cb * a.H + h;
-    if (threadIdx.x < kC) {
-      const int i = threadIdx.x;
-      const float* coef = (const float*)(a.mats + ch * kGdrMats + 2 * kTriSet);
-      gs[i] = a.decay_sums[ch * kC + i];
-      bt[i] = coef[kBeta * kC + i];
-      rkk[i] = coef[kRowKk * kC + i];
-      rkq[i] = coef[kRowKq * kC + i];
-      gam[i] = expf((float)gs[i]);
-      tail[i] = expf((float)(a.decay_sums[ch * kC + kC - 1] - gs[i]));
+  const Buffer bs(a.checkpoints + ch * cn, cn * 4), bg(a.grad_states + ch * sn, sn * 4);
+  const Buffer bw(a.w + ch * kC * a.V, (int64_t)kC * a.V * 4);
+  const int64_t po = a.B * a.H * a.V;
+  const Buffer bo((const IO*)a.grad_o + (c * kC * a.B + b) * a.H * a.V + (int64_t)h * a.V,
+                  ((n - 1) * po + a.V) * (int64_t)sizeof(IO));
+  const bool vec = quads<float>(a.checkpoints, 0, a.V), veco = quads<IO>(a.grad_o, 0, a.V);
+  // 16 rows x 32 columns as a fragment in two parts (column 8 g + e), scaled by row
+  auto put = [&](const float (&v)[8], uint16_t* to, int parts, float* down, int row)
+      __attribute__((always_inline)) {
+    const Scale sc = scale_of(quad_max(top_of(v)));
+    const Split p = split8(v, sc.up);
+    *reinterpret_cast<f16x8_t*>(to + lane * 8) = p.hi;
+    if (parts == 2) *reinterpret_cast<f16x8_t*>(to + kFrag + lane * 8) = p.lo;
+    if (g == 0) down[row] = sc.down;
+  };
+  for (int v0 = 0; v0 < a.V; v0 += kVB) {
+    const int col = v0 + 8 * g, row = 16 * w + r, k = 16 * wv + r;
+    Quad<float> s0[2], ds[2], wq[2], dq[2];
+    Quad<IO> oq[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (wv < KT) {
+        const uint32_t at = (uint32_t)k * (uint32_t)a.V * 4u;
+        ld_quad(bs, at, enters && k < a.K, col + 4 * j, a.V, vec, s0[j]);
+        ld_quad(bg, at, k < a.K, col + 4 * j, a.V, vec, ds[j]);
+      }
+      if (half == 0) {
+        ld_quad(bo, (uint32_t)row * (uint32_t)po * (uint32_t)sizeof(IO), row < n, col + 4 * j, a.V,
+                veco, oq[j]);
+      } else {
+        ld_quad(bw, (uint32_t)row * (uint32_t)a.V * 4u, true, col + 4 * j, a.V, vec, wq[j]);
+        ld_quad(bs, (uint32_t)(a.K + row) * (uint32_t)a.V * 4u, true, col + 4 * j, a.V, vec, dq[j]);
+      }
     }
-    f32x4_t dP[4], dL[4], Q1[KT], K1[KT], K2[KT];
+    if (half == 0) {
+      float v[8];
+      oq[0].get(v);
+      oq[1].get(v + 4);
+      put(v, of + w * NP * kFrag, NP, ro, row);
+    } else {
+      float v[8], u[8];
+      wq[0].get(v);
+      wq[1].get(v + 4);
+      dq[0].get(u);
+      dq[1].get(u + 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dP[i] = dL[i] = kZero4;
-#pragma unroll
-    for (int i = 0; i < KT; ++i) Q1[i] = K1[i] = K2[i] = kZero4;
-    float dbeta = 0.0f, dot = 0.0f;
-
-    for (int v0 = 0; v0 < a.V; v0 += kVB) {
-      f16x8_t oa[2][NP], wa[2][2], da[2][2];
-      {
-        const int row = 16 * w + r;
-        const int64_t t = c * kC + row;
-        float ov[16], wv[16], dv[16];
-        const float* wr = a.w + (ch * kC + row) * a.V;
-        const float* dr = a.checkpoints + ch * cn + (int64_t)(a.K + row) * a.V;
-        const IO* orow = (const IO*)a.grad_o + ((t * a.B + b) * a.H + h) * a.V;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int col = v0 + 32 * (j >> 1) + 8 * g + 4 * (j & 1);
-          ld4(wr, col, a.V, wv + 4 * j);
-          ld4(dr, col, a.V, dv + 4 * j);
-          if (t < a.T) ld4(orow, col, a.V, ov + 4 * j);
-          else ov[4 * j] = ov[4 * j + 1] = ov[4 * j + 2] = ov[4 * j + 3] = 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) dbeta = __builtin_fmaf(wv[j], dv[j], dbeta);
-        const Scale so = scale_of(quad_max(top_of(ov))), sw = scale_of(quad_max(top_of(wv))),
-                    sd = scale_of(quad_max(top_of(dv)));
-#pragma unroll
-        for (int vs = 0; vs < 2; ++vs) {
-          const Split o2 = split8<NP == 2>(ov + 8 * vs, so.up), w2 = split8(wv + 8 * vs, sw.up),
-                      d2 = split8(dv + 8 * vs, sd.up);
-          oa[vs][0] = o2.hi;
-          if constexpr (NP == 2) oa[vs][1] = o2.lo;
-          wa[vs][0] = w2.hi;
-          wa[vs][1] = w2.lo;
-          da[vs][0] = d2.hi;
-          da[vs][1] = d2.lo;
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-            *reinterpret_cast<f16x8_t*>(df + ((w * 2 + vs) * 2 + p) * kFrag + lane * 8) = da[vs][p];
-        }
-        if (g == 0) {
-          ro[row] = so.down;
-          rw[row] = sw.down;
-          rd[row] = sd.down;
-        }
-      }
-      for (int kt = w; kt < KT; kt += 4) {
-        const int k = 16 * kt + r;
-        float s0[16], ds[16];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int col = v0 + 32 * (j >> 1) + 8 * g + 4 * (j & 1);
-          const int n = k < a.K ? a.V : 0;
-          ld4(a.checkpoints + ch * cn + (int64_t)k * a.V, col, enters ? n : 0, s0 + 4 * j);
-          ld4(a.grad_states + ch * sn + (int64_t)k * a.V, col, n, ds + 4 * j);
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) dot = __builtin_fmaf(s0[j], ds[j], dot);
-        const Scale ss = scale_of(quad_max(top_of(s0))), sg = scale_of(quad_max(top_of(ds)));
-#pragma unroll
-        for (int vs = 0; vs < 2; ++vs) {
-          const Split s2 = split8(s0 + 8 * vs, ss.up), g2 = split8(ds + 8 * vs, sg.up);
-          const int at = (kt * 2 + vs) * 2 * kFrag + lane * 8;
-          *reinterpret_cast<f16x8_t*>(sf + at) = s2.hi;
-          *reinterpret_cast<f16x8_t*>(sf + at + kFrag) = s2.lo;
-          *reinterpret_cast<f16x8_t*>(gf + at) = g2.hi;
-          *reinterpret_cast<f16x8_t*>(gf + at + kFrag) = g2.lo;
-        }
-        if (g == 0) {
-          rs[k] = ss.down;
-          rg[k] = sg.down;
-        }
-      }
-      __syncthreads();
-      const f32x4_t fo = *reinterpret_cast<const f32x4_t*>(ro + 16 * w + 4 * g);
-      const f32x4_t fw = *reinterpret_cast<const f32x4_t*>(rw + 16 * w + 4 * g);
-      const f32x4_t fd = *reinterpret_cast<const f32x4_t*>(rd + 16 * w + 4 * g);
-#pragma unroll
-      for (int ct = 0; ct < 4; ++ct) {
-        if (ct > w) continue;
-        f32x4_t x = kZero4, y = kZero4;
-#pragma unroll
-        for (int vs = 0; vs < 2; ++vs) {
-          const f16x8_t db[2] = {frag(df, (ct * 2 + vs) * 2), frag(df, (ct * 2 + vs) * 2 + 1)};
-          x = mma_parts<NP, 2>(oa[vs], db, x);
-          y = mma_parts<2, 2>(wa[vs], db, y);
-        }
-        const float f = rd[16 * ct + r];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dP[ct][i] = __builtin_fmaf(x[i], fo[i] * f, dP[ct][i]);
-          dL[ct][i] = __builtin_fmaf(y[i], fw[i] * f, dL[ct][i]);
-        }
-      }
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        f32x4_t x = kZero4, y = kZero4, z = kZero4;
-#pragma unroll
-        for (int vs = 0; vs < 2; ++vs) {
-          const int at = (kt * 2 + vs) * 2;
-          if (enters) {
-            const f16x8_t sb[2] = {frag(sf, at), frag(sf, at + 1)};
-            x = mma_parts<NP, 2>(oa[vs], sb, x);
-            y = mma_parts<2, 2>(wa[vs], sb, y);
-          }
-          const f16x8_t gb[2] = {frag(gf, at), frag(gf, at + 1)};
-          z = mma_parts<2, 2>(da[vs], gb, z);
-        }
-        const float f = rs[16 * kt + r], fz = rg[16 * kt + r];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          Q1[kt][i] = __builtin_fmaf(x[i], fo[i] * f, Q1[kt][i]);
-          K1[kt][i] = __builtin_fmaf(y[i], fw[i] * f, K1[kt][i]);
-          K2[kt][i] = __builtin_fmaf(z[i], fd[i] * fz, K2[kt][i]);
-        }
-      }
-      __syncthreads();
+      for (int j = 0; j < 8; ++j) dbeta = __builtin_fmaf(v[j], u[j], dbeta);
+      put(v, wf + w * 2 * kFrag, 2, rw, row);
+      put(u, df + w * 2 * kFrag, 2, rd, row);
     }
-
-    for (int i = threadIdx.x; i < 2 * kSet / 8; i += 256)
-      *reinterpret_cast<u32x4_t*>(kl + i * 8) = *reinterpret_cast<const u32x4_t*>(kf + i * 8);
-
-    // the rows' factors; what their segment does not reach is 0, whatever it holds
-    float dq_q[4], dk_k[4], dk_t[4];
+    if (wv < KT) {
+      float v[8], u[8];
+      s0[0].get(v);
+      s0[1].get(v + 4);
+      ds[0].get(u);
+      ds[1].get(u + 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 16 * w + 4 * g + i;
-      const int64_t t = c * kC + row;
-      const bool first = enters && row < first_end, last = row >= last_start;
-      const float fq = gam[row] * a.scale, fk = -gam[row] * bt[row], ft = tail[row] * bt[row];
-      float s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-      const IO* qp = (const IO*)a.q + (t * a.B + b) * a.ld_q + (int64_t)hk * a.K;
-      const IO* kp = (const IO*)a.k + (t * a.B + b) * a.ld_k + (int64_t)hk * a.K;
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        Q1[kt][i] = first ? Q1[kt][i] * fq : 0.0f;
-        K1[kt][i] = first ? K1[kt][i] * fk : 0.0f;
-        K2[kt][i] = last ? K2[kt][i] * ft : 0.0f;
-        const int k = 16 * kt + r;
-        if (t < a.T && k < a.K) {
-          const float qv = io_ld(qp, k), kv = io_ld(kp, k);
-          s1 = __builtin_fmaf(qv, Q1[kt][i], s1);
-          s2 = __builtin_fmaf(kv, K1[kt][i], s2);
-          s3 = last ? __builtin_fmaf(kv, K2[kt][i], s3) : 0.0f;
-        }
-      }
-      dq_q[i] = row16_sum(s1);
-      dk_k[i] = row16_sum(s2);
-      dk_t[i] = row16_sum(s3);
+      for (int j = 0; j < 8; ++j) dot = __builtin_fmaf(v[j], u[j], dot);
+      put(v, sf + wv * 2 * kFrag, 2, rs, k);
+      put(u, gf + wv * 2 * kFrag, 2, rg, k);
     }
-
-    // X = dP D, Z = dL D and its transpose, and what the decay sums take from both
-    float re[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    __syncthreads();
+    f16x8_t oa[NP], wa[2], da[2];
 #pragma unroll
-    for (int ct = 0; ct < 4; ++ct) {
-      f32x4_t kk = kZero4, qk = kZero4;
-      if (ct <= w) {
+    for (int p = 0; p < NP; ++p) oa[p] = frag(of, w * NP + p);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          f16x8_t ka[NP], qa[NP], kb[NP];
+    for (int p = 0; p < 2; ++p) {
+      wa[p] = frag(wf, w * 2 + p);
+      da[p] = frag(df, w * 2 + p);
+    }
+    const f32x4_t fo = *reinterpret_cast<const f32x4_t*>(ro + 16 * w + 4 * g);
+    const f32x4_t fw = *reinterpret_cast<const f32x4_t*>(rw + 16 * w + 4 * g);
+    const f32x4_t fd = *reinterpret_cast<const f32x4_t*>(rd + 16 * w + 4 * g);
 #pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            ka[p] = frag(kf, (p * 4 + w) * KS + ks);
-            qa[p] = frag(qf, (p * 4 + w) * KS + ks);
-            kb[p] = frag(kf, (p * 4 + ct) * KS + ks);
-          }
-          kk = mma_parts<NP, NP>(ka, kb, kk);
-          qk = mma_parts<NP, NP>(qa, kb, qk);
-        }
-      }
-      const int cj = 16 * ct + r;
-      float ce = 0.0f;
+    for (int t = 0; t < 2; ++t) {
+      const int ct = 2 * half + t;
+      if (ct > w) continue;
+      const f16x8_t db[2] = {frag(df, ct * 2), frag(df, ct * 2 + 1)};
+      const f32x4_t x = mma_parts<NP, 2>(oa, db, kZero4), y = mma_parts<2, 2>(wa, db, kZero4);
+      const float f = rd[16 * ct + r];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int ri = 16 * w + 4 * g + i;
-        float x = 0.0f, z = 0.0f;
-        if (cj <= ri && cj >= seg_start(cuts, ri)) {
-          const float d = expf((float)(gs[ri] - gs[cj]));
-          x = dP[ct][i] * (a.scale * bt[cj]) * d;
-          float en = x * qk[i] * (rkq[ri] * rkk[cj]);
-          if (cj < ri) {
-            z = -dL[ct][i] * (bt[ri] * bt[cj]) * d;
-            en = __builtin_fmaf(z, kk[i] * (rkk[ri] * rkk[cj]), en);
-          }
-          re[i] += en;
-          ce += en;
-        }
-        xm[ri][cj] = x;
-        if (cj < ri) zm[ri][cj] = zm[cj][ri] = z;
-        if (cj == ri) zm[ri][ri] = 0.0f;
+        dP[t][i] = __builtin_fmaf(x[i], fo[i] * f, dP[t][i]);
+        dL[t][i] = __builtin_fmaf(y[i], fw[i] * f, dL[t][i]);
       }
-      ce += __shfl_xor(ce, 16);
-      ce += __shfl_xor(ce, 32);
-      if (g == 0) col_e[w][cj] = ce;
     }
-    float tsum = 0.0f;
+    fence();
+#pragma unroll
+    for (int t = 0; t < KH; ++t) {
+      const int kt = half * KH + t;
+      const f16x8_t sb[2] = {frag(sf, kt * 2), frag(sf, kt * 2 + 1)};
+      const f16x8_t gb[2] = {frag(gf, kt * 2), frag(gf, kt * 2 + 1)};
+      const f32x4_t x = mma_parts<NP, 2>(oa, sb, kZero4), y = mma_parts<2, 2>(wa, sb, kZero4),
+                    z = mma_parts<2, 2>(da, gb, kZero4);
+      const float f = rs[16 * kt + r], fz = rg[16 * kt + r];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        Q1[t][i] = __builtin_fmaf(x[i], fo[i] * f, Q1[t][i]);
+        K1[t][i] = __builtin_fmaf(y[i], fw[i] * f, K1[t][i]);
+        K2[t][i] = __builtin_fmaf(z[i], fd[i] * fz, K2[t][i]);
+      }
+      fence();
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < 2 * kSet / 8; i += 512)
+    *reinterpret_cast<u32x4_t*>(kl + i * 8) = *reinterpret_cast<const u32x4_t*>(kq + i * 8);
+  __syncthreads();
+
+  // the rows' factors; what their segment does not reach is 0, whatever it holds
+  float e_row[4], e_tail[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 16 * w + 4 * g + i;
+    const bool first = enters && row < first_end, last = row >= last_start;
+    const float fq = gam[row] * a.scale, fk = -gam[row] * bt[row], ft = tail[row] * bt[row];
+    float s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+    for (int t = 0; t < KH; ++t) {
+      Q1[t][i] = first ? Q1[t][i] * fq : 0.0f;
+      K1[t][i] = first ? K1[t][i] * fk : 0.0f;
+      K2[t][i] = last ? K2[t][i] * ft : 0.0f;
+      const int kt = half * KH + t;
+      float qv = 0.0f, kv = 0.0f;
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const int at = ((p * 4 + w) * KS + (kt >> 1)) * kFrag + ((r >> 2) * 16 + 4 * g + i) * 8 +
+                       4 * (kt & 1) + (r & 3);
+        qv += (float)__builtin_bit_cast(_Float16, ql[at]);
+        kv += (float)__builtin_bit_cast(_Float16, kl[at]);
+      }
+      s1 = __builtin_fmaf(qv, Q1[t][i], s1);
+      s2 = __builtin_fmaf(kv, K1[t][i], s2);
+      s3 = __builtin_fmaf(kv, K2[t][i], s3);
+    }
+    const float tk_i = last ? row16_sum(s3) * rkk[row] : 0.0f;
+    e_row[i] = row16_sum(s1) * rkq[row] + row16_sum(s2) * rkk[row] - tk_i;
+    e_tail[i] = tk_i;
+    fence();
+  }
+
+  // X = dP D, Z = dL D and its transpose, and what the decay sums take from both
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int ct = 2 * half + t;
+    f32x4_t kk = kZero4, qk = kZero4;
+    if (ct <= w) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        f16x8_t ka[NP], qa[NP], kb[NP];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          ka[p] = frag(kl, (p * 4 + w) * KS + ks);
+          qa[p] = frag(ql, (p * 4 + w) * KS + ks);
+          kb[p] = frag(kl, (p * 4 + ct) * KS + ks);
+        }
+        kk = mma_parts<NP, NP>(ka, kb, kk);
+        qk = mma_parts<NP, NP>(qa, kb, qk);
+        if (ks & 1) fence();
+      }
+    }
+    const int cj = 16 * ct + r;
+    float ce = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float e = row16_sum(re[i]);
-      if (r == 0) row_e[16 * w + 4 * g + i] = e + dq_q[i] + dk_k[i] - dk_t[i];
-      tsum += dk_t[i];
+      const int ri = 16 * w + 4 * g + i;
+      // selected, not branched over: the exponential may be anything outside the segment
+      const bool low = cj < ri && cj >= seg_start(cuts, ri);
+      const float d = expf((float)(gs[ri] - gs[cj]));
+      const float x = low || cj == ri ? dP[t][i] * (a.scale * bt[cj]) * (cj == ri ? 1.0f : d) : 0.0f;
+      const float z = low ? -dL[t][i] * (bt[ri] * bt[cj]) * d : 0.0f;
+      float en = low || cj == ri ? x * qk[i] * (rkq[ri] * rkk[cj]) : 0.0f;
+      en = low ? __builtin_fmaf(z, kk[i] * (rkk[ri] * rkk[cj]), en) : en;
+      e_row[i] += row16_sum(en);
+      ce += en;
+      xm[ri][cj] = x;
+      if (cj < ri) zm[ri][cj] = zm[cj][ri] = z;
+      if (cj == ri) zm[ri][ri] = 0.0f;
     }
-    tsum += __shfl_xor(tsum, 16);
-    tsum += __shfl_xor(tsum, 32);
+    ce += __shfl_xor(ce, 16);
+    ce += __shfl_xor(ce, 32);
+    if (g == 0) col_e[w][cj] = ce;
+    fence();
+  }
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) dot += __shfl_xor(dot, d);
+  for (int i = 0; i < 4; ++i) {
+    if (r == 0) {
+      row_e[half][16 * w + 4 * g + i] = e_row[i];
+      row_t[half][16 * w + 4 * g + i] = e_tail[i];
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) dot += __shfl_xor(dot, d);
+  if (half == 1) {
     dbeta += __shfl_xor(dbeta, 16);
     dbeta += __shfl_xor(dbeta, 32);
     if (g == 0) bsum[16 * w + r] = dbeta;
-    if (lane == 0) {
-      tails[w] = tsum;
-      dots[w] = dot;
-    }
-    __syncthreads();
+  }
+  if (lane == 0) dots[wv] = dot;
+  __syncthreads();
 
-    if (w == 0) {
-      // dlog_decay_t = sum of dG_i over the steps i >= t of its segment
-      double G = (double)row_e[lane] -
-                 ((((double)col_e[0][lane] + col_e[1][lane]) + col_e[2][lane]) + col_e[3][lane]);
-      const int end = seg_end(cuts, lane);
+  if (wv == 0) {
+    // dlog_decay_t = sum of dG_i over the steps i >= t of its segment
+    double G = ((double)row_e[0][lane] + row_e[1][lane]) -
+               ((((double)col_e[0][lane] + col_e[1][lane]) + col_e[2][lane]) + col_e[3][lane]);
+    double t = (double)row_t[0][lane] + row_t[1][lane];
+    const int end = seg_end(cuts, lane);
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const double after = __shfl_down(G, d);
-        if (lane + d < end) G += after;
-      }
-      if (end == kC) {
-        G += (((double)tails[0] + tails[1]) + tails[2]) + tails[3];
-        if (whole)
-          G += (double)gam[kC - 1] * ((((double)dots[0] + dots[1]) + dots[2]) + dots[3]);
-      }
-      const int64_t t = c * kC + lane;
-      if (t < a.T) {
-        const bool cut = (cuts >> lane) & 1;
-        a.grad_log_decay[(t * a.B + b) * a.H + h] = cut ? 0.0f : (float)G;
-        a.grad_beta[(t * a.B + b) * a.H + h] = bsum[lane];
+    for (int d = 1; d < 64; d <<= 1) {
+      const double after = __shfl_down(G, d);
+      if (lane + d < end) G += after;
+      t += __shfl_xor(t, d);
+    }
+    if (end == kC) {
+      G += t;
+      if (whole) {
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += dots[i];
+        G += (double)gam[kC - 1] * s;
       }
     }
+    if (lane < n) {
+      const bool cut = (cuts >> lane) & 1;
+      const int64_t at = ((c * kC + lane) * a.B + b) * a.H + h;
+      a.grad_log_decay[at] = cut ? 0.0f : (float)G;
+      a.grad_beta[at] = bsum[lane];
+    }
+  }
 
-    // dq += X k, dk += Z k + X^T q
-    {
-      const int row = 16 * w + r;
-      float xv[16], zv[16], tv[16];
+  // dq += X k, dk += Z k + X^T q
+  {
+    const int row = 16 * w + r;
+    float xv[16], zv[16], tv[16];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int col = 32 * ks + 16 * (j >> 2) + 4 * g + (j & 3);
+        xv[8 * ks + j] = xm[row][col] * rkk[col];
+        zv[8 * ks + j] = zm[row][col] * rkk[col];
+        tv[8 * ks + j] = xm[col][row] * rkq[col];
+      }
+    if (!whole) {  // a factor that is not finite belongs to its own segment
+      const int s = seg_start(cuts, row), e = seg_end(cuts, row);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int col = 32 * ks + 16 * (j >> 2) + 4 * g + (j & 3);
-          xv[8 * ks + j] = xm[row][col] * rkk[col];
-          zv[8 * ks + j] = zm[row][col] * rkk[col];
-          tv[8 * ks + j] = xm[col][row] * rkq[col];
+          if (col < s || col >= e) xv[8 * ks + j] = zv[8 * ks + j] = tv[8 * ks + j] = 0.0f;
         }
-      if (!whole) {  // a factor that is not finite belongs to its own segment
-        const int s = seg_start(cuts, row), e = seg_end(cuts, row);
+    }
+    const Scale sx = scale_of(quad_max(top_of(xv))), sz = scale_of(quad_max(top_of(zv))),
+                st = scale_of(quad_max(top_of(tv)));
+    if (g == 0 && half == 0) {
+      rx[row] = sx.down;
+      rz[row] = sz.down;
+      rt_s[row] = st.down;
+    }
+    f16x8_t xa[2][2], za[2][2], ta[2][2];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
+    for (int ks = 0; ks < 2; ++ks) {
+      const Split x2 = split8(xv + 8 * ks, sx.up), z2 = split8(zv + 8 * ks, sz.up),
+                  t2 = split8(tv + 8 * ks, st.up);
+      xa[ks][0] = x2.hi; xa[ks][1] = x2.lo;
+      za[ks][0] = z2.hi; za[ks][1] = z2.lo;
+      ta[ks][0] = t2.hi; ta[ks][1] = t2.lo;
+    }
+    __syncthreads();
+    const f32x4_t fx = *reinterpret_cast<const f32x4_t*>(rx + 16 * w + 4 * g);
+    const f32x4_t fz = *reinterpret_cast<const f32x4_t*>(rz + 16 * w + 4 * g);
+    const f32x4_t ft = *reinterpret_cast<const f32x4_t*>(rt_s + 16 * w + 4 * g);
+    // rows of segment [s, e); FULL: all
+    auto products = [&](auto full, int s, int e) __attribute__((always_inline)) {
+      constexpr bool FULL = decltype(full)();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int col = 32 * ks + 16 * (j >> 2) + 4 * g + (j & 3);
-            if (col < s || col >= e) xv[8 * ks + j] = zv[8 * ks + j] = tv[8 * ks + j] = 0.0f;
+      for (int t = 0; t < KH; ++t) {
+        const int kt = half * KH + t;
+        f32x4_t x = kZero4, y = kZero4, z = kZero4;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          f16x8_t kb[NP], qb[NP];
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            kb[p] = cols<KS>(kl, p, kt, ks);
+            qb[p] = cols<KS>(ql, p, kt, ks);
+            if (!FULL) {
+              kb[p] = keep_steps(kb[p], ks, s, e);
+              qb[p] = keep_steps(qb[p], ks, s, e);
+            }
           }
-      }
-      const Scale sx = scale_of(quad_max(top_of(xv))), sz = scale_of(quad_max(top_of(zv))),
-                  st = scale_of(quad_max(top_of(tv)));
-      if (g == 0) {
-        rx[row] = sx.down;
-        rz[row] = sz.down;
-        rt_s[row] = st.down;
-      }
-      f16x8_t xa[2][2], za[2][2], ta[2][2];
+          x = mma_parts<2, NP>(xa[ks], kb, x);
+          y = mma_parts<2, NP>(za[ks], kb, y);
+          z = mma_parts<2, NP>(ta[ks], qb, z);
+        }
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const Split x2 = split8(xv + 8 * ks, sx.up), z2 = split8(zv + 8 * ks, sz.up),
-                    t2 = split8(tv + 8 * ks, st.up);
-        xa[ks][0] = x2.hi; xa[ks][1] = x2.lo;
-        za[ks][0] = z2.hi; za[ks][1] = z2.lo;
-        ta[ks][0] = t2.hi; ta[ks][1] = t2.lo;
+        for (int i = 0; i < 4; ++i) {
+          const int ri = 16 * w + 4 * g + i;
+          if (FULL || (ri >= s && ri < e)) {
+            Q1[t][i] = __builtin_fmaf(x[i], fx[i], Q1[t][i]);
+            K1[t][i] = (K1[t][i] + K2[t][i]) + __builtin_fmaf(z[i], ft[i], y[i] * fz[i]);
+          }
+        }
+        fence();
       }
-      __syncthreads();
-      const f32x4_t fx = *reinterpret_cast<const f32x4_t*>(rx + 16 * w + 4 * g);
-      const f32x4_t fz = *reinterpret_cast<const f32x4_t*>(rz + 16 * w + 4 * g);
-      const f32x4_t ft = *reinterpret_cast<const f32x4_t*>(rt_s + 16 * w + 4 * g);
+    };
+    if (whole) {
+      products(Yes(), 0, kC);
+    } else {
+#pragma unroll 1
       for (int s = 0; s < kC;) {
         const int e = seg_end(cuts, s);
-        if (e > 16 * w && s < 16 * w + 16) {
-#pragma unroll
-          for (int kt = 0; kt < KT; ++kt) {
-            f32x4_t x = kZero4, y = kZero4, z = kZero4;
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-              f16x8_t kb[NP], qb[NP];
-#pragma unroll
-              for (int p = 0; p < NP; ++p) {
-                kb[p] = cols<KS>(kl, p, kt, ks);
-                qb[p] = cols<KS>(kl + kSet, p, kt, ks);
-                if (!whole) {
-                  kb[p] = keep_steps(kb[p], ks, s, e);
-                  qb[p] = keep_steps(qb[p], ks, s, e);
-                }
-              }
-              x = mma_parts<2, NP>(xa[ks], kb, x);
-              y = mma_parts<2, NP>(za[ks], kb, y);
-              z = mma_parts<2, NP>(ta[ks], qb, z);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int ri = 16 * w + 4 * g + i;
-              if (ri >= s && ri < e) {
-                tq[kt][i] += __builtin_fmaf(x[i], fx[i], Q1[kt][i]);
-                tk[kt][i] += (K1[kt][i] + K2[kt][i]) + __builtin_fmaf(z[i], ft[i], y[i] * fz[i]);
-              }
-            }
-          }
-        }
+        if (e > 16 * w && s < 16 * w + 16) products(No(), s, e);
         s = e;
       }
-      __syncthreads();
     }
   }
+
+  // dq and dk: rows 16 w + 4 g + i, columns 16 (half KH + t) + r
+  typedef typename Choose<SHARED, float, IO>::type Out;
+  const int64_t pq = SHARED ? a.K : a.B * a.ld_gq, pk = SHARED ? a.K : a.B * a.ld_gk;
+  const Out* to_q = SHARED ? (const Out*)(a.shared + ch * 2 * kC * a.K)
+                           : (const Out*)a.grad_q + (c * kC * a.B + b) * a.ld_gq + (int64_t)hk * a.K;
+  const Out* to_k = SHARED ? to_q + kC * a.K
+                           : (const Out*)a.grad_k + (c * kC * a.B + b) * a.ld_gk + (int64_t)hk * a.K;
+  const Buffer bq(to_q, ((n - 1) * pq + a.K) * (int64_t)sizeof(Out));
+  const Buffer bk(to_k, ((n - 1) * pk + a.K) * (int64_t)sizeof(Out));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = c * kC + 16 * w + 4 * g + i;
-    if (t >= a.T) continue;
-    IO* qo = (IO*)a.grad_q + (t * a.B + b) * a.ld_gq + (int64_t)hk * a.K;
-    IO* ko = (IO*)a.grad_k + (t * a.B + b) * a.ld_gk + (int64_t)hk * a.K;
+  for (int t = 0; t < KH; ++t) {
+    const int col = 16 * (half * KH + t) + r;
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-      const int k = 16 * kt + r;
-      if (k < a.K) {
-        io_st(qo, k, tq[kt][i]);
-        io_st(ko, k, tk[kt][i]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * w + 4 * g + i;
+      const bool in = row < n && col < a.K;
+      bq.store(in ? ((uint32_t)row * (uint32_t)pq + (uint32_t)col) * (uint32_t)sizeof(Out) : kNowhere,
+               Q1[t][i], (const Out*)nullptr);
+      bk.store(in ? ((uint32_t)row * (uint32_t)pk + (uint32_t)col) * (uint32_t)sizeof(Out) : kNowhere,
+               K1[t][i], (const Out*)nullptr);
     }
+  }
+}
+
+// blockIdx.x: chunk, sequence and head of q and k; the sums over the heads that share them.
+template <typename IO>
+__global__ __launch_bounds__(256) void k_gdr_shared(GdrArgs a) {
+  const uint32_t kh = blockIdx.x, hk = kh % (uint32_t)a.Hk, cb = kh / (uint32_t)a.Hk;
+  const int64_t b = cb % (uint32_t)a.B, c = cb / (uint32_t)a.B;
+  const int share = a.H / a.Hk;
+  const int64_t left = a.T - c * kC;
+  const int size = kC * a.K, rows = (int)(left < kC ? left : kC);
+  const float* from = a.shared + ((int64_t)cb * a.H + (int64_t)hk * share) * 2 * size;
+  for (int i = threadIdx.x; i < rows * a.K; i += 256) {
+    float q = from[i], k = from[size + i];
+    for (int s = 1; s < share; ++s) {
+      q += from[(int64_t)s * 2 * size + i];
+      k += from[(int64_t)s * 2 * size + size + i];
+    }
+    const int row = i / a.K, col = i - row * a.K;
+    const int64_t at = (c * kC + row) * a.B + b;
+    io_st((IO*)a.grad_q, at * a.ld_gq + (int64_t)hk * a.K + col, q);
+    io_st((IO*)a.grad_k, at * a.ld_gk + (int64_t)hk * a.K + col, k);
   }
 }
 
@@ -1532,8 +1616,13 @@ hipError_t gdr_bwd(const GdrArgs& a, hipStream_t stream) {
     else if (n == 2) hipLaunchKernelGGL((k_gdr_back<IO, KP, 2>), grid, wg, 0, stream, a);
     else hipLaunchKernelGGL((k_gdr_back<IO, KP, 1>), grid, wg, 0, stream, a);
   });
-  hipLaunchKernelGGL((k_gdr_grads<IO, KP>), dim3((unsigned)(nc * a.B * a.Hk)), dim3(256), 0, stream,
-                     a);
+  const dim3 groups((unsigned)(nc * a.B * a.H));
+  if (a.H == a.Hk) {
+    hipLaunchKernelGGL((k_gdr_grads<IO, KP, false>), groups, dim3(512), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((k_gdr_grads<IO, KP, true>), groups, dim3(512), 0, stream, a);
+    hipLaunchKernelGGL((k_gdr_shared<IO>), dim3((unsigned)(nc * a.B * a.Hk)), dim3(256), 0, stream, a);
+  }
   return hipGetLastError();
 }
 

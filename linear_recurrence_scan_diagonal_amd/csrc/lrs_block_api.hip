@@ -44,7 +44,7 @@ bool gdr_fits(int64_t chunks, int64_t B, int64_t H, int64_t K, int64_t V) {
          mul_ok(n, columns, &n) && n < most;
 }
 
-// 31-bit byte offsets inside a chunk's rows of v and o (or their gradients) and a state.
+// 31-bit byte offsets inside a chunk's rows of an array and inside a state.
 bool gdr_rows_fit(int64_t B, int64_t ld, int64_t K, int64_t V) {
   int64_t n;
   return mul_ok(B, ld, &n) && n < ((int64_t)1 << 23) && (K + lrs::kGdrRows) * V < ((int64_t)1 << 29);
@@ -66,6 +66,7 @@ size_t gdr_carve(int64_t chunks, int64_t B, int64_t H, int64_t Hk, int64_t K, in
   a->decay_sums = cv.take<double>(nv * C);
   a->w = cv.take<float>(nv * C * V);
   a->grad_states = cv.take<float>(nv * K * V);
+  a->shared = cv.take<float>(H > Hk ? nv * 2 * C * K : 0);
   return cv.used;
 }
 
@@ -186,7 +187,8 @@ int lrs_gdr_fwd(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const 
   const Span outs[] = {{o, (size_t)(z.rows * z.vw) * es}, {state, sb},
                        {checkpoints, z.saved}};
   if (any_overlap(outs, 3, ins, 7)) return LRS_ERR_INVALID_ARG;
-  if (!gdr_fits(z.chunks, B, H, K, V) || !gdr_rows_fit(B, ld_v, K, V) || !gdr_rows_fit(B, z.vw, K, V))
+  if (!gdr_fits(z.chunks, B, H, K, V) || !gdr_rows_fit(B, ld_q, K, V) ||
+      !gdr_rows_fit(B, ld_k, K, V) || !gdr_rows_fit(B, ld_v, K, V) || !gdr_rows_fit(B, z.vw, K, V))
     return LRS_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < gdr_workspace(T, B, H, Hk, K, V, io_dtype, false))
     return LRS_ERR_WORKSPACE;
@@ -258,8 +260,9 @@ int lrs_gdr_bwd(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const 
     if (slices_overlap(gz[i].p, gz[i].ld, gz[i].w, o.p, o.ld, o.w, z.rows, es))
       return LRS_ERR_INVALID_ARG;
   }
-  if (!gdr_fits(z.chunks, B, H, K, V) || !gdr_rows_fit(B, ld_gv, K, V) || !gdr_rows_fit(B, z.vw, K, V))
-    return LRS_ERR_UNSUPPORTED;
+  if (!gdr_fits(z.chunks, B, H, K, V) || !gdr_rows_fit(B, z.vw, K, V)) return LRS_ERR_UNSUPPORTED;
+  for (int64_t ld : lds)
+    if (!gdr_rows_fit(B, ld, K, V)) return LRS_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < gdr_workspace(T, B, H, Hk, K, V, io_dtype, true))
     return LRS_ERR_WORKSPACE;
   lrs::GdrArgs a = gdr_args(q, ld_q, k, ld_k, v, ld_v, log_decay, beta, T, B, H, Hk, K, V, scale);

@@ -346,6 +346,7 @@ struct GdrArgs {
   double* decay_sums;                         // [64]
   float* w;                                   // [64][V]
   float* grad_states;                         // [K][V]
+  float* shared;                              // [2][64][K]: dq and dk of heads that share q and k
 };
 hipError_t launch_gdr_fwd(const GdrArgs& a, int io, hipStream_t stream);
 hipError_t launch_gdr_bwd(const GdrArgs& a, int io, hipStream_t stream);
