@@ -41,9 +41,10 @@ extern "C" {
  * reset  : [T,B] bytes, or NULL for none.  state0: [B,H,K,V] fp32, or NULL (zero).
  * o      : [T,B,H,V] contiguous output.  state: [B,H,K,V] fp32 output, the state
  *          after the last step, or NULL; it may be state0's own buffer.
- * checkpoints : fp32 output [lrs_gdr_checkpoint_rows(T), B, H, K + 64, V], for each
- *          chunk of 64 steps the state that enters it and v - S^T k of its steps,
- *          which lrs_gdr_bwd reads; or NULL.
+ * checkpoints : fp32 output [lrs_gdr_checkpoint_rows(T), B, H, K + 64, V'], V' = V
+ *          rounded up to a multiple of 4, for each chunk of 64 steps the state that
+ *          enters it and v - S^T k of its steps, which lrs_gdr_bwd reads; or NULL.
+ *          Its padding needs no values.
  * Products take factors of two fp16 parts, scaled by a power of two (one part
  * where bf16 inputs need no more): a factor is known to 2^-22 of itself or to
  * 2^-39 of the largest of its row or column, whichever is more.  A value that is

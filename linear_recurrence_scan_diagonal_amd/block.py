@@ -111,11 +111,14 @@ def _gdr_inputs(q, k, v, log_decay, beta, dims):
 
 def gdr_checkpoints(k, v):
     """The tensor that gdr_fwd fills for gdr_bwd: fp32, for each chunk of 64 time steps,
-    sequence and head the state [K,V] that enters it and [64,V] of its steps.
-    k: [T,B,Hk,K], v: [T,B,H,V]."""
+    sequence and head the state [K,V] that enters it and [64,V] of its steps (V rounded
+    up to a multiple of 4).  k: [T,B,Hk,K], v: [T,B,H,V]."""
     T, B, H, V = (int(n) for n in v.shape)
-    return torch.empty((load().lrs_gdr_checkpoint_rows(T), B, H, int(k.shape[-1]) + 64, V),
-                       dtype=torch.float32, device=v.device)
+    return torch.empty(_saved(T, B, H, int(k.shape[-1]), V), dtype=torch.float32, device=v.device)
+
+
+def _saved(T, B, H, K, V):
+    return torch.Size((load().lrs_gdr_checkpoint_rows(T), B, H, K + 64, (V + 3) // 4 * 4))
 
 
 def gdr_fwd(q, k, v, log_decay, beta, scale=None, reset=None, state0=None,
@@ -134,8 +137,7 @@ def gdr_fwd(q, k, v, log_decay, beta, scale=None, reset=None, state0=None,
     shape = torch.Size((B, H, K, V))
     _check_dev("state0", state0, torch.float32, shape)
     if checkpoints is not None:
-        _check_dev("checkpoints", checkpoints, torch.float32,
-                   torch.Size((lib.lrs_gdr_checkpoint_rows(T), B, H, K + 64, V)))
+        _check_dev("checkpoints", checkpoints, torch.float32, _saved(T, B, H, K, V))
     dev = v.device
     o = torch.empty((T, B, H, V), dtype=v.dtype, device=dev) if out is None else out
     _check_dev("out", o, v.dtype, v.shape)
@@ -163,8 +165,7 @@ def gdr_bwd(q, k, v, log_decay, beta, checkpoints, grad_o, scale=None, reset=Non
     shape = torch.Size((B, H, K, V))
     if checkpoints is None:
         raise TypeError("checkpoints must be the tensor that gdr_fwd filled")
-    _check_dev("checkpoints", checkpoints, torch.float32,
-               torch.Size((lib.lrs_gdr_checkpoint_rows(T), B, H, K + 64, V)))
+    _check_dev("checkpoints", checkpoints, torch.float32, _saved(T, B, H, K, V))
     if grad_o is None:
         raise TypeError("grad_o must be a device tensor")
     _check_dev("grad_o", grad_o, v.dtype, v.shape)

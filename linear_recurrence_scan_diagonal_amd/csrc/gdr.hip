@@ -77,12 +77,13 @@ __device__ __forceinline__ Scale scale_of(float top) {
 // The largest absolute value over the four lanes that share a row or column (r = lane %
 // 16).  A NaN does not count; it stays NaN at any scale.
 __device__ __forceinline__ float quad_max(float m) {
-  const u32x2_t a = __builtin_bit_cast(
-      u32x2_t, __builtin_amdgcn_permlane16_swap(as_u32(m), as_u32(m), false, false));
-  m = fmaxf(as_f32(a.x), as_f32(a.y));
-  const u32x2_t b = __builtin_bit_cast(
-      u32x2_t, __builtin_amdgcn_permlane32_swap(as_u32(m), as_u32(m), false, false));
-  return fmaxf(as_f32(b.x), as_f32(b.y));
+  // not negative: whole numbers in the same order, without the instructions that make
+  // signalling NaNs quiet
+  const uint32_t u = as_u32(m);
+  const u32x2_t a = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane16_swap(u, u, false, false));
+  const uint32_t v = a.x > a.y ? a.x : a.y;
+  const u32x2_t b = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(v, v, false, false));
+  return as_f32(b.x > b.y ? b.x : b.y);
 }
 template <int N>
 __device__ __forceinline__ float top_of(const float (&v)[N]) {
@@ -178,34 +179,36 @@ struct Quad<uint16_t> {
   }
 };
 // Elements c..c+3 of a row of n that begins at byte `row` of the buffer; 0 from n on and
-// in rows that are not there.  vec: n is a multiple of four and the rows are aligned to it.
+// in rows that are not there.  VEC: n is a multiple of four and the rows are aligned to it.
+template <bool VEC>
 __device__ __forceinline__ void ld_quad(const Buffer& b, uint32_t row, bool there, int c, int n,
-                                        bool vec, Quad<float>& q) {
-  if (vec) {
+                                        Quad<float>& q) {
+  if constexpr (VEC) {
     q.q = b.load16(there && c < n ? row + (uint32_t)c * 4u : kNowhere, 0);
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float v;
-    b.load(there && c + j < n ? row + (uint32_t)(c + j) * 4u : kNowhere, v);
-    q.q[j] = as_u32(v);
+    for (int j = 0; j < 4; ++j) {
+      float v;
+      b.load(there && c + j < n ? row + (uint32_t)(c + j) * 4u : kNowhere, v);
+      q.q[j] = as_u32(v);
+    }
   }
 }
+template <bool VEC>
 __device__ __forceinline__ void ld_quad(const Buffer& b, uint32_t row, bool there, int c, int n,
-                                        bool vec, Quad<uint16_t>& q) {
-  if (vec) {
+                                        Quad<uint16_t>& q) {
+  if constexpr (VEC) {
     q.q = b.load8(there && c < n ? row + (uint32_t)c * 2u : kNowhere);
-    return;
-  }
-  uint16_t v[4];
+  } else {
+    uint16_t v[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) b.load(there && c + j < n ? row + (uint32_t)(c + j) * 2u : kNowhere, v[j]);
-  q.q = u32x2_t{(uint32_t)v[0] | (uint32_t)v[1] << 16, (uint32_t)v[2] | (uint32_t)v[3] << 16};
+    for (int j = 0; j < 4; ++j) b.load(there && c + j < n ? row + (uint32_t)(c + j) * 2u : kNowhere, v[j]);
+    q.q = u32x2_t{(uint32_t)v[0] | (uint32_t)v[1] << 16, (uint32_t)v[2] | (uint32_t)v[3] << 16};
+  }
 }
 // Whether rows of n elements, ld apart from p on, can be read in fours.
 template <typename IO>
-__device__ __forceinline__ bool quads(const void* p, int64_t ld, int n) {
+__host__ __device__ __forceinline__ bool quads(const void* p, int64_t ld, int n) {
   return ((ld | n) & 3) == 0 && ((uintptr_t)p & (4 * sizeof(IO) - 1)) == 0;
 }
 
@@ -230,6 +233,9 @@ __device__ __forceinline__ f16x8_t keep_steps(f16x8_t f, int ks, int s, int e) {
   }
   return f;
 }
+
+// Elements from row to row of the states and vectors that are kept in fp32: V in fours.
+__host__ __device__ __forceinline__ int64_t saved_pitch(int64_t V) { return gdr_saved_pitch(V); }
 
 // ---------------------------------------------------------------------------
 // Workspace of a call, in arrays of chunk-heads: index (c B + b) Hk + hk, or with H, h.
@@ -348,8 +354,13 @@ __global__ __launch_bounds__(256) void k_gdr_prep(GdrArgs a) {
     const Buffer buf(p, ((n - 1) * pitch + a.K) * (int64_t)sizeof(IO));
     const bool vec = quads<IO>(base, ld, a.K);
     const uint32_t at = (uint32_t)row * (uint32_t)pitch * (uint32_t)sizeof(IO);
+    if (vec) {
 #pragma unroll
-    for (int j = 0; j < 2 * KS; ++j) ld_quad(buf, at, row < n, 16 * j + 4 * g, a.K, vec, v[j]);
+      for (int j = 0; j < 2 * KS; ++j) ld_quad<true>(buf, at, row < n, 16 * j + 4 * g, a.K, v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2 * KS; ++j) ld_quad<false>(buf, at, row < n, 16 * j + 4 * g, a.K, v[j]);
+    }
   };
   Quad<IO> kraw[2 * KS], qraw[2 * KS];
   load((const IO*)a.k, a.ld_k, kraw);
@@ -580,16 +591,16 @@ struct No {
   __device__ constexpr operator bool() const { return false; }
 };
 
-// What a chain's wave has.  A workgroup has NCB blocks of 16 columns of a head, four waves
-// each; lane l has column r = l % 16.  Wave j of the four has the steps 16 j... of a chunk,
-// and the rows 32 j... of the state (where K <= 64: waves 0 and 1 alone).
+// What a chain's wave has.  A workgroup has NW * CB blocks of 16 columns of a head, and four
+// waves for every CB of them; lane l has column r = l % 16 of each.  Wave j of the four has the
+// steps 16 j... of a chunk, and the rows 32 j... of the state (where K <= 64: waves 0 and 1 alone).
 struct Wave {
   int64_t bh, b;
-  int h, hk, col, j, block;
-  bool colin;
-  template <int NCB>
+  int h, hk, j, block;  // block: the first one, in the workgroup
+  int col;              // the lane's column of it
+  template <int NW, int CB>
   static __device__ __forceinline__ Wave make(const GdrArgs& a) {
-    constexpr int kCols = 16 * NCB;
+    constexpr int kCols = 16 * NW * CB;
     const uint32_t vblocks = (uint32_t)(a.V + kCols - 1) / kCols;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Wave w;
@@ -599,27 +610,26 @@ struct Wave {
     w.h = (int)(bh % (uint32_t)a.H);
     w.hk = w.h / (a.H / a.Hk);
     w.j = wave & 3;
-    w.block = wave >> 2;
+    w.block = (wave >> 2) * CB;
     w.col = (int)(blockIdx.x % vblocks) * kCols + w.block * 16 + (threadIdx.x & 15);
-    w.colin = w.col < a.V;
     return w;
   }
 };
 
 // 16 N rows of an array from row 16 t0 on, `pitch` elements apart: of rows 16 t + 4 g + 0..3
-// the lane's column.  Rows from `rows` on read as 0 and are not written, nor is a column
-// past V's end.
+// the lane's column.  Rows from `rows` on read as 0 and are not written, nor are columns
+// from `width` on.
 template <typename IO>
 struct Rows {
   Buffer buf;
   uint32_t pitch, lane;
   int t0;
-  __device__ __forceinline__ Rows(const IO* p, int64_t pitch_, int64_t rows, int width, const Wave& w,
+  __device__ __forceinline__ Rows(const IO* p, int64_t pitch_, int64_t rows, int width, int col,
                                   int t0_)
       : buf(p, rows <= 0 ? 0 : ((rows - 1) * pitch_ + width) * (int64_t)sizeof(IO)), t0(t0_) {
     pitch = (uint32_t)pitch_ * (uint32_t)sizeof(IO);
     const uint32_t g = (threadIdx.x & 63) >> 4;
-    lane = w.colin ? 4u * g * pitch + (uint32_t)w.col * (uint32_t)sizeof(IO) : kNowhere;
+    lane = col < width ? 4u * g * pitch + (uint32_t)col * (uint32_t)sizeof(IO) : kNowhere;
   }
   __device__ __forceinline__ uint32_t at(int t, int i) const {
     return lane + (uint32_t)(16 * (t0 + t) + i) * pitch;
@@ -659,23 +669,21 @@ __device__ __forceinline__ void widen(const IO (&v)[N][4], f32x4_t (&out)[N]) {
 }
 
 // What the four waves of a column block hand each other: the state as a right operand with
-// a scale for every 32 rows (its place is used again for the second of the chunk's vectors),
-// and the 64 steps of a vector in fp32, 16 bytes a lane and wave.
+// a scale for every 32 rows, and the 64 steps of two or three vectors in fp32, 16 bytes a
+// lane and wave.
 template <int KS, bool BACK>
 struct Exchange {
   static constexpr int kState = KS * 2 * kFrag * 2, kVec = 4 * 64 * 16;
-  static constexpr int kBytes = kState + kVec * (BACK ? 2 : 1) + KS * 16 * 4;
-  static_assert(kVec <= kState, "the second vector lies over the state");
+  static constexpr int kBytes = kState + kVec * (BACK ? 3 : 2) + KS * 16 * 4;
   char* base;
   __device__ __forceinline__ uint16_t* state(int ks, int part) const {
     return (uint16_t*)base + (ks * 2 + part) * kFrag + (threadIdx.x & 63) * 8;
   }
   __device__ __forceinline__ f32x4_t* vec(int which, int j) const {
-    char* p = which == 1 ? base : base + kState + (which == 2 ? kVec : 0);
-    return (f32x4_t*)p + j * 64 + (threadIdx.x & 63);
+    return (f32x4_t*)(base + kState + which * kVec) + j * 64 + (threadIdx.x & 63);
   }
   __device__ __forceinline__ float* down(int ks) const {
-    return (float*)(base + kState + kVec * (BACK ? 2 : 1)) + ks * 16 + (threadIdx.x & 15);
+    return (float*)(base + kState + kVec * (BACK ? 3 : 2)) + ks * 16 + (threadIdx.x & 15);
   }
   // the wave's 32 rows of the state
   __device__ __forceinline__ void put_state(const f32x4_t (&S)[2], int j) const {
@@ -692,50 +700,58 @@ struct Exchange {
   }
 };
 
-// 16 rows of k S, and of q S: a product for every 32 rows of the state, which have scales
-// of their own.
-template <int NP, int KS, bool BOTH, typename X>
+// 16 rows of k S, and of q S, for CB column blocks: a product for every 32 rows of the state,
+// which have scales of their own.
+template <int NP, int KS, int CB, bool BOTH, typename X>
 __device__ __forceinline__ void times_state(const uint16_t* k_rows, const uint16_t* q_rows, int rt,
-                                            const X& x, f32x4_t& k_out, f32x4_t& q_out) {
+                                            const X (&x)[CB], f32x4_t (&k_out)[CB],
+                                            f32x4_t (&q_out)[CB]) {
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) {
-    f16x8_t ka[NP], qa[NP], sb[2];
+    f16x8_t ka[NP], qa[NP];
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       ka[p] = frag(k_rows, (p * 4 + rt) * KS + ks);
       if (BOTH) qa[p] = frag(q_rows, (p * 4 + rt) * KS + ks);
     }
-    sb[0] = *reinterpret_cast<const f16x8_t*>(x.state(ks, 0));
-    sb[1] = *reinterpret_cast<const f16x8_t*>(x.state(ks, 1));
-    const float down = *x.down(ks);
-    const f32x4_t y = mma_parts<NP, 2>(ka, sb, kZero4);
-    f32x4_t z = kZero4;
-    if (BOTH) z = mma_parts<NP, 2>(qa, sb, kZero4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      k_out[i] = ks == 0 ? y[i] * down : __builtin_fmaf(y[i], down, k_out[i]);
-      if (BOTH) q_out[i] = ks == 0 ? z[i] * down : __builtin_fmaf(z[i], down, q_out[i]);
+    for (int c = 0; c < CB; ++c) {
+      const f16x8_t sb[2] = {*reinterpret_cast<const f16x8_t*>(x[c].state(ks, 0)),
+                             *reinterpret_cast<const f16x8_t*>(x[c].state(ks, 1))};
+      const float down = *x[c].down(ks);
+      const f32x4_t y = mma_parts<NP, 2>(ka, sb, kZero4);
+      f32x4_t z = kZero4;
+      if (BOTH) z = mma_parts<NP, 2>(qa, sb, kZero4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        k_out[c][i] = ks == 0 ? y[i] * down : __builtin_fmaf(y[i], down, k_out[c][i]);
+        if (BOTH) q_out[c][i] = ks == 0 ? z[i] * down : __builtin_fmaf(z[i], down, q_out[c][i]);
+      }
     }
+    if (CB > 1) fence();
   }
 }
-// 16 rows of a triangular matrix times a vector's right operand.
-template <bool TRANSPOSED, int PB>
-__device__ __forceinline__ f32x4_t times_tri(const uint16_t* m, int rt, const f16x8_t (&b)[2][PB]) {
-  f32x4_t x = kZero4;
+// 16 rows of a triangular matrix times vectors' right operands.
+template <bool TRANSPOSED, int CB, int PB>
+__device__ __forceinline__ void times_tri(const uint16_t* m, int rt, const f16x8_t (&b)[CB][2][PB],
+                                          f32x4_t (&x)[CB]) {
+#pragma unroll
+  for (int c = 0; c < CB; ++c) x[c] = kZero4;
 #pragma unroll
   for (int ks = 0; ks < 2; ++ks) {
     if (TRANSPOSED ? ks < rt / 2 : ks > rt / 2) continue;
     const int f = tri<TRANSPOSED>(rt, ks);
     const f16x8_t ma[2] = {frag(m, f), frag(m, kTri + f)};
-    x = mma_parts<2, PB>(ma, b[ks], x);
+#pragma unroll
+    for (int c = 0; c < CB; ++c) x[c] = mma_parts<2, PB>(ma, b[c][ks], x[c]);
   }
-  return x;
 }
-// 16 rows of k^T (or q^T) times a vector's right operand.
-template <int NP, int KS, bool FULL>
-__device__ __forceinline__ f32x4_t times_cols(const uint16_t* rows, int kt, const f16x8_t (&b)[2][2],
-                                              int s, int e) {
-  f32x4_t x = kZero4;
+// 16 rows of k^T (or q^T) times vectors' right operands.
+template <int NP, int KS, int CB, bool FULL>
+__device__ __forceinline__ void times_cols(const uint16_t* rows, int kt, const f16x8_t (&b)[CB][2][2],
+                                           int s, int e, f32x4_t (&x)[CB]) {
+#pragma unroll
+  for (int c = 0; c < CB; ++c) x[c] = kZero4;
 #pragma unroll
   for (int ks = 0; ks < 2; ++ks) {
     f16x8_t ka[NP];
@@ -744,26 +760,35 @@ __device__ __forceinline__ f32x4_t times_cols(const uint16_t* rows, int kt, cons
       ka[p] = cols<KS>(rows, p, kt, ks);
       if (!FULL) ka[p] = keep_steps(ka[p], ks, s, e);
     }
-    x = mma_parts<NP, 2>(ka, b[ks], x);
+#pragma unroll
+    for (int c = 0; c < CB; ++c) x[c] = mma_parts<NP, 2>(ka, b[c][ks], x[c]);
   }
-  return x;
+}
+template <int PARTS>
+__device__ __forceinline__ float vec_operand(const f32x4_t (&v)[4], f16x8_t (&b)[2][PARTS]) {
+  const Scale sc = col_scale(v);
+  to_operand<PARTS>(v, sc.up, b);
+  return sc.down;
 }
 
 // The chain over the chunks.  Between two barriers a wave makes 16 of a vector's 64 steps
 // from the whole of the one before: R from the state, delta and u from R, the state's next
 // value (32 rows) and o from u.
-template <typename IO, int KP, int NCB>
-__global__ __launch_bounds__(256 * NCB) void k_gdr_chain(GdrArgs a) {
+template <typename IO, int KP, int NW, int CB>
+__global__ __launch_bounds__(256 * NW) void k_gdr_chain(GdrArgs a) {
   constexpr int NP = kParts<IO>, KS = KP / 32;
-  typedef Stage<NP, KS, 256 * NCB> St;
+  typedef Stage<NP, KS, 256 * NW> St;
   typedef Exchange<KS, false> X;
-  __shared__ __align__(16) char lds[St::kBytes + NCB * X::kBytes];
+  __shared__ __align__(16) char lds[St::kBytes + NW * CB * X::kBytes];
   const int g = (threadIdx.x & 63) >> 4;
-  const Wave w = Wave::make<NCB>(a);
-  const X x = {lds + St::kBytes + w.block * X::kBytes};
+  const Wave w = Wave::make<NW, CB>(a);
+  X x[CB];
+#pragma unroll
+  for (int c = 0; c < CB; ++c) x[c].base = lds + St::kBytes + (w.block + c) * X::kBytes;
   const int64_t nc = (a.T + kC - 1) / kC;
-  const int64_t sn = (int64_t)a.K * a.V, cn = (int64_t)(a.K + kC) * a.V;  // a state's, a checkpoint's
-  const int64_t vrow = (int64_t)a.H * a.V;
+  const int64_t sn = (int64_t)a.K * a.V, vrow = (int64_t)a.H * a.V;
+  const int vp = (int)saved_pitch(a.V);
+  const int64_t cn = (int64_t)(a.K + kC) * vp;  // of a checkpoint
   const bool owner = w.j < KS;
   const uint16_t* kf = (const uint16_t*)lds;
   const uint16_t* qf = kf + St::kSet;
@@ -771,39 +796,44 @@ __global__ __launch_bounds__(256 * NCB) void k_gdr_chain(GdrArgs a) {
   const uint16_t* pf = tf + kTriSet;
   const float* coef = (const float*)(pf + kTriSet);
 
-  f32x4_t S[2];
-  {
+  f32x4_t S[CB][2];
+#pragma unroll
+  for (int c = 0; c < CB; ++c) {
     float s0[2][4];
-    Rows<float>(a.state0 + w.bh * sn, a.V, a.state0 && owner ? a.K : 0, a.V, w, 2 * w.j).load(s0);
-    widen(s0, S);
+    Rows<float>(a.state0 + w.bh * sn, a.V, a.state0 && owner ? a.K : 0, a.V, w.col + 16 * c, 2 * w.j)
+        .load(s0);
+    widen(s0, S[c]);
+    if (owner) x[c].put_state(S[c], w.j);
   }
   St st;
-  IO nv[1][4];  // the next chunk's v
+  IO nv[CB][1][4];  // the next chunk's v
   // (the address of a chunk behind the last is not read: a length of 0)
-  auto fetch_v = [&](int64_t c) __attribute__((always_inline)) {
-    const int64_t left = a.T - c * kC;
-    Rows<IO>((const IO*)a.v + (c * kC * a.B + w.b) * a.ld_v + (int64_t)w.h * a.V, a.B * a.ld_v,
-             left < kC ? left : kC, a.V, w, w.j)
-        .load(nv);
+  auto fetch_v = [&](int64_t t) __attribute__((always_inline)) {
+    const int64_t left = a.T - t * kC;
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+      Rows<IO>((const IO*)a.v + (t * kC * a.B + w.b) * a.ld_v + (int64_t)w.h * a.V, a.B * a.ld_v,
+               left < kC ? left : kC, a.V, w.col + 16 * c, w.j)
+          .load(nv[c]);
   };
   fetch_v(0);
   st.fetch(a, w.b, w.h, w.hk);
-  for (int64_t c = 0; c < nc; ++c) {
+  for (int64_t t = 0; t < nc; ++t) {
     st.put(lds);
-    if (owner) x.put_state(S, w.j);
     const uint64_t cuts = st.cuts();
     const float keep = st.keep_v;
     {
-      const int64_t next = c + 1 < nc ? c + 1 : c;
+      const int64_t next = t + 1 < nc ? t + 1 : t;
       st.fetch(a, next * a.B + w.b, w.h, w.hk);
     }
-    const int64_t ch = (c * a.B + w.b) * a.H + w.h, left = a.T - c * kC;
+    const int64_t ch = (t * a.B + w.b) * a.H + w.h, left = a.T - t * kC;
     float* ck = a.checkpoints ? a.checkpoints + ch * cn : nullptr;
-    if (ck && owner) Rows<float>(ck, a.V, a.K, a.V, w, 2 * w.j).store(S);
-    const Rows<IO> out((const IO*)a.o + (c * kC * a.B + w.b) * vrow + (int64_t)w.h * a.V, a.B * vrow,
-                       left < kC ? left : kC, a.V, w, w.j);
+    if (ck && owner) {
+#pragma unroll
+      for (int c = 0; c < CB; ++c) Rows<float>(ck, vp, a.K, vp, w.col + 16 * c, 2 * w.j).store(S[c]);
+    }
     __syncthreads();
-    f32x4_t R[1];
+    f32x4_t R[CB][1];
 
     // steps [s, e) of the chunk, v in R; FULL: all of them, of a document that goes on
     auto segment = [&](auto full, int s, int e, bool fresh) __attribute__((always_inline)) {
@@ -812,76 +842,112 @@ __global__ __launch_bounds__(256 * NCB) void k_gdr_chain(GdrArgs a) {
         const int step = 16 * rt + 4 * g + i;
         return FULL || (step >= s && step < e);
       };
-      f32x4_t Q[1], D[1], V[4];
-      f32x4_t ks, qs;
-      if (FULL || !fresh) times_state<NP, KS, true>(kf, qf, w.j, x, ks, qs);
+      f32x4_t Q[CB][1], D[CB][1], V[4], y[CB], z[CB];
+      if (FULL || !fresh) times_state<NP, KS, CB, true>(kf, qf, w.j, x, y, z);
       if (s == 0) {
-        widen(nv, R);
-        fetch_v(c + 1);
+#pragma unroll
+        for (int c = 0; c < CB; ++c) widen(nv[c], R[c]);
+        fetch_v(t + 1);
       }
-      Q[0] = kZero4;
-      D[0] = R[0];
-      if (FULL || !fresh) {
+      {
         const f32x4_t ek = coef4(coef, kEnterK, w.j), eq = coef4(coef, kEnterQ, w.j);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          D[0][i] = __builtin_fmaf(-ek[i], ks[i], R[0][i]);
-          Q[0][i] = eq[i] * qs[i];
+        for (int c = 0; c < CB; ++c) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float d = R[c][0][i], q = 0.0f;
+            if (FULL || !fresh) {
+              d = __builtin_fmaf(-ek[i], y[c][i], d);
+              q = eq[i] * z[c][i];
+            }
+            D[c][0][i] = in(w.j, i) ? d : 0.0f;
+            Q[c][0][i] = q;
+          }
+          *x[c].vec(0, w.j) = D[c][0];
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) D[0][i] = in(w.j, i) ? D[0][i] : 0.0f;
-      *x.vec(0, w.j) = D[0];
       __syncthreads();
       {  // delta = T2 R, u = beta delta
-        x.get_vec(0, V);
-        const Scale sc = col_scale(V);
-        f16x8_t b[2][2];
-        to_operand<2>(V, sc.up, b);
-        const f32x4_t y = times_tri<false>(tf, w.j, b);
+        f16x8_t b[CB][2][2];
+        float down[CB];
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+          x[c].get_vec(0, V);
+          down[c] = vec_operand<2>(V, b[c]);
+          if (CB > 1) fence();
+        }
+        times_tri<false, CB, 2>(tf, w.j, b, y);
         const f32x4_t rs = coef4(coef, kRowT, w.j), be = coef4(coef, kBeta, w.j);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) D[0][i] = y[i] * (sc.down * rs[i]);
-        if (ck) {
-          const Rows<float> delta(ck + sn, a.V, kC, a.V, w, w.j);
-          if (FULL) delta.store(D);
-          else delta.store(D, s, e);
+        for (int c = 0; c < CB; ++c) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) D[c][0][i] = y[c][i] * (down[c] * rs[i]);
+          if (ck) {
+            const Rows<float> delta(ck + (int64_t)a.K * vp, vp, kC, vp, w.col + 16 * c, w.j);
+            if (FULL) delta.store(D[c]);
+            else delta.store(D[c], s, e);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) D[c][0][i] = in(w.j, i) ? D[c][0][i] * be[i] : 0.0f;
+          *x[c].vec(1, w.j) = D[c][0];
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) D[0][i] = in(w.j, i) ? D[0][i] * be[i] : 0.0f;
       }
-      *x.vec(1, w.j) = D[0];
       __syncthreads();
-      x.get_vec(1, V);
-      {
-        const Scale sc = col_scale(V);
-        f16x8_t b[2][2];
-        to_operand<2>(V, sc.up, b);
-        const f32x4_t y = times_tri<false>(pf, w.j, b);
-        const f32x4_t rs = coef4(coef, kRowP, w.j);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          Q[0][i] = __builtin_fmaf(y[i], sc.down * (rs[i] * a.scale), Q[0][i]);
-        if (FULL) out.store(Q);
-        else out.store(Q, s, e);
+      // u for o, and for the state; two blocks read it twice, one at a time, to have the registers
+      f16x8_t b[CB][2][2];
+      float down[CB];
+      if (CB == 1) {
+        x[0].get_vec(1, V);
+        down[0] = vec_operand<2>(V, b[0]);
       }
       if (e == kC && owner) {  // the segment that leaves the chunk
+        f16x8_t bl[CB][2][2];
+        float downl[CB];
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          const f32x4_t lv = coef4(coef, kLeaveK, rt);
+        for (int c = 0; c < CB; ++c) {
+          if (CB > 1) x[c].get_vec(1, V);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) V[rt][i] = in(rt, i) ? V[rt][i] * lv[i] : 0.0f;
+          for (int rt = 0; rt < 4; ++rt) {
+            const f32x4_t lv = coef4(coef, kLeaveK, rt);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) V[rt][i] = in(rt, i) ? V[rt][i] * lv[i] : 0.0f;
+          }
+          downl[c] = vec_operand<2>(V, bl[c]);
+          if (CB > 1) fence();
         }
-        const Scale sc = col_scale(V);
-        f16x8_t b[2][2];
-        to_operand<2>(V, sc.up, b);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const f32x4_t y = times_cols<NP, KS, FULL>(kf, 2 * w.j + t, b, s, e);
+        for (int k = 0; k < 2; ++k) {
+          times_cols<NP, KS, CB, FULL>(kf, 2 * w.j + k, bl, s, e, y);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            S[t][i] = __builtin_fmaf(y[i], sc.down, !FULL && fresh ? 0.0f : keep * S[t][i]);
+          for (int c = 0; c < CB; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              S[c][k][i] = __builtin_fmaf(y[c][i], downl[c], !FULL && fresh ? 0.0f : keep * S[c][k][i]);
+          if (CB > 1) fence();
         }
+#pragma unroll
+        for (int c = 0; c < CB; ++c) x[c].put_state(S[c], w.j);
+        if (CB > 1) fence();
+      }
+      if (CB > 1) {
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+          x[c].get_vec(1, V);
+          down[c] = vec_operand<2>(V, b[c]);
+          fence();
+        }
+      }
+      times_tri<false, CB, 2>(pf, w.j, b, y);
+      const f32x4_t rs = coef4(coef, kRowP, w.j);
+#pragma unroll
+      for (int c = 0; c < CB; ++c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          Q[c][0][i] = __builtin_fmaf(y[c][i], down[c] * (rs[i] * a.scale), Q[c][0][i]);
+        const Rows<IO> out((const IO*)a.o + (t * kC * a.B + w.b) * vrow + (int64_t)w.h * a.V, a.B * vrow,
+                           left < kC ? left : kC, a.V, w.col + 16 * c, w.j);
+        if (FULL) out.store(Q[c]);
+        else out.store(Q[c], s, e);
       }
     };
     if (cuts == 0) {
@@ -896,21 +962,28 @@ __global__ __launch_bounds__(256 * NCB) void k_gdr_chain(GdrArgs a) {
     }
     __syncthreads();  // before the next chunk's operands are put over these
   }
-  if (a.state && owner) Rows<float>(a.state + w.bh * sn, a.V, a.K, a.V, w, 2 * w.j).store(S);
+  if (a.state && owner) {
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+      Rows<float>(a.state + w.bh * sn, a.V, a.K, a.V, w.col + 16 * c, 2 * w.j).store(S[c]);
+  }
 }
 
 // The chain in reverse: dS, and w, dv and every chunk's dS on the way.
-template <typename IO, int KP, int NCB>
-__global__ __launch_bounds__(256 * NCB) void k_gdr_back(GdrArgs a) {
+template <typename IO, int KP, int NW, int CB>
+__global__ __launch_bounds__(256 * NW) void k_gdr_back(GdrArgs a) {
   constexpr int NP = kParts<IO>, KS = KP / 32;
-  typedef Stage<NP, KS, 256 * NCB> St;
+  typedef Stage<NP, KS, 256 * NW> St;
   typedef Exchange<KS, true> X;
-  __shared__ __align__(16) char lds[St::kBytes + NCB * X::kBytes];
+  __shared__ __align__(16) char lds[St::kBytes + NW * CB * X::kBytes];
   const int g = (threadIdx.x & 63) >> 4;
-  const Wave w = Wave::make<NCB>(a);
-  const X x = {lds + St::kBytes + w.block * X::kBytes};
+  const Wave w = Wave::make<NW, CB>(a);
+  X x[CB];
+#pragma unroll
+  for (int c = 0; c < CB; ++c) x[c].base = lds + St::kBytes + (w.block + c) * X::kBytes;
   const int64_t nc = (a.T + kC - 1) / kC;
   const int64_t sn = (int64_t)a.K * a.V, vrow = (int64_t)a.H * a.V;
+  const int vp = (int)saved_pitch(a.V);
   const bool owner = w.j < KS;
   const uint16_t* kf = (const uint16_t*)lds;
   const uint16_t* qf = kf + St::kSet;
@@ -918,40 +991,52 @@ __global__ __launch_bounds__(256 * NCB) void k_gdr_back(GdrArgs a) {
   const uint16_t* pf = tf + kTriSet;
   const float* coef = (const float*)(pf + kTriSet);
 
-  f32x4_t S[2];  // dS
-  {
-    float s0[2][4];
-    Rows<float>(a.grad_state + w.bh * sn, a.V, a.grad_state && owner ? a.K : 0, a.V, w, 2 * w.j).load(s0);
-    widen(s0, S);
-  }
-  St st;
-  IO ng[1][4];  // the next chunk's grad_o
-  auto fetch_o = [&](int64_t c) __attribute__((always_inline)) {
-    const int64_t left = a.T - c * kC;
-    Rows<IO>((const IO*)a.grad_o + (c * kC * a.B + w.b) * vrow + (int64_t)w.h * a.V, a.B * vrow,
-             left < kC ? left : kC, a.V, w, w.j)
-        .load(ng);
+  f32x4_t S[CB][2];  // dS
+  IO ng[CB][1][4];   // the next chunk's grad_o
+  auto fetch_o = [&](int64_t t) __attribute__((always_inline)) {
+    const int64_t left = a.T - t * kC;
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+      Rows<IO>((const IO*)a.grad_o + (t * kC * a.B + w.b) * vrow + (int64_t)w.h * a.V, a.B * vrow,
+               left < kC ? left : kC, a.V, w.col + 16 * c, w.j)
+          .load(ng[c]);
   };
+  auto put_o = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < CB; ++c) {
+      f32x4_t go[1];
+      widen(ng[c], go);
+      *x[c].vec(2, w.j) = go[0];
+    }
+  };
+  St st;
   fetch_o(nc - 1);
   st.fetch(a, (nc - 1) * a.B + w.b, w.h, w.hk);
-  for (int64_t c = nc - 1; c >= 0; --c) {
+#pragma unroll
+  for (int c = 0; c < CB; ++c) {
+    float s0[2][4];
+    Rows<float>(a.grad_state + w.bh * sn, a.V, a.grad_state && owner ? a.K : 0, a.V, w.col + 16 * c,
+                2 * w.j)
+        .load(s0);
+    widen(s0, S[c]);
+    if (owner) x[c].put_state(S[c], w.j);
+  }
+  put_o();
+  for (int64_t t = nc - 1; t >= 0; --t) {
     st.put(lds);
-    if (owner) x.put_state(S, w.j);
     const uint64_t cuts = st.cuts();
     const float keep = st.keep_v;
     {
-      f32x4_t go[1];
-      widen(ng, go);
-      *x.vec(2, w.j) = go[0];
-      const int64_t next = c > 0 ? c - 1 : 0;
+      const int64_t next = t > 0 ? t - 1 : 0;
       fetch_o(next);
       st.fetch(a, next * a.B + w.b, w.h, w.hk);
     }
-    const int64_t ch = (c * a.B + w.b) * a.H + w.h, left = a.T - c * kC;
-    if (owner) Rows<float>(a.grad_states + ch * sn, a.V, a.K, a.V, w, 2 * w.j).store(S);
-    const Rows<float> wout(a.w + ch * kC * a.V, a.V, kC, a.V, w, w.j);
-    const Rows<IO> vout((const IO*)a.grad_v + (c * kC * a.B + w.b) * a.ld_gv + (int64_t)w.h * a.V,
-                        a.B * a.ld_gv, left < kC ? left : kC, a.V, w, w.j);
+    const int64_t ch = (t * a.B + w.b) * a.H + w.h, left = a.T - t * kC;
+    if (owner) {
+#pragma unroll
+      for (int c = 0; c < CB; ++c)
+        Rows<float>(a.grad_states + ch * a.K * vp, vp, a.K, vp, w.col + 16 * c, 2 * w.j).store(S[c]);
+    }
     __syncthreads();
 
     auto segment = [&](auto full, int s, int e, bool fresh) __attribute__((always_inline)) {
@@ -960,79 +1045,107 @@ __global__ __launch_bounds__(256 * NCB) void k_gdr_back(GdrArgs a) {
         const int step = 16 * rt + 4 * g + i;
         return FULL || (step >= s && step < e);
       };
-      f32x4_t D[1], dO[4], V[4];
-      x.get_vec(2, dO);
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dO[rt][i] = in(rt, i) ? dO[rt][i] : 0.0f;
+      f32x4_t D[CB][1], dO[CB][4], V[4], y[CB], z[CB];
       {  // du = scale P^T do + exp(G_C - G) K dS
-        const Scale sc = col_scale(dO);
-        f16x8_t b[2][NP];
-        to_operand<NP>(dO, sc.up, b);
-        const f32x4_t y = times_tri<true>(pf, w.j, b);
+        f16x8_t b[CB][2][NP];
+        float down[CB];
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+          x[c].get_vec(2, dO[c]);
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dO[c][rt][i] = in(rt, i) ? dO[c][rt][i] : 0.0f;
+          down[c] = vec_operand<NP>(dO[c], b[c]);
+          if (CB > 1) fence();
+        }
+        times_tri<true, CB, NP>(pf, w.j, b, y);
         const f32x4_t rs = coef4(coef, kRowP, w.j);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) D[0][i] = y[i] * (sc.down * (rs[i] * a.scale));
+        for (int c = 0; c < CB; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) D[c][0][i] = y[c][i] * (down[c] * (rs[i] * a.scale));
       }
       if (e == kC) {
-        f32x4_t ks, none;
-        times_state<NP, KS, false>(kf, nullptr, w.j, x, ks, none);
+        times_state<NP, KS, CB, false>(kf, nullptr, w.j, x, y, z);
         const f32x4_t lv = coef4(coef, kLeaveK, w.j);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) D[0][i] = __builtin_fmaf(ks[i], lv[i], D[0][i]);
+        for (int c = 0; c < CB; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) D[c][0][i] = __builtin_fmaf(y[c][i], lv[i], D[c][0][i]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) D[0][i] = in(w.j, i) ? D[0][i] : 0.0f;
-      *x.vec(0, w.j) = D[0];
+      for (int c = 0; c < CB; ++c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) D[c][0][i] = in(w.j, i) ? D[c][0][i] : 0.0f;
+        *x[c].vec(0, w.j) = D[c][0];
+      }
       __syncthreads();
       {  // w = T^T du, dv = beta w
-        x.get_vec(0, V);
-        const Scale sc = col_scale(V);
-        f16x8_t b[2][2];
-        to_operand<2>(V, sc.up, b);
-        const f32x4_t y = times_tri<true>(tf, w.j, b);
+        f16x8_t b[CB][2][2];
+        float down[CB];
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+          x[c].get_vec(0, V);
+          down[c] = vec_operand<2>(V, b[c]);
+          if (CB > 1) fence();
+        }
+        times_tri<true, CB, 2>(tf, w.j, b, y);
         const f32x4_t rs = coef4(coef, kRowT, w.j), be = coef4(coef, kBeta, w.j);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) D[0][i] = y[i] * (sc.down * rs[i]);
-        if (FULL) wout.store(D);
-        else wout.store(D, s, e);
+        for (int c = 0; c < CB; ++c) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) D[0][i] = in(w.j, i) ? D[0][i] * be[i] : 0.0f;
-        if (FULL) vout.store(D);
-        else vout.store(D, s, e);
+          for (int i = 0; i < 4; ++i) D[c][0][i] = y[c][i] * (down[c] * rs[i]);
+          const Rows<float> wout(a.w + ch * kC * vp, vp, kC, vp, w.col + 16 * c, w.j);
+          if (FULL) wout.store(D[c]);
+          else wout.store(D[c], s, e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) D[c][0][i] = in(w.j, i) ? D[c][0][i] * be[i] : 0.0f;
+          *x[c].vec(1, w.j) = D[c][0];
+          const Rows<IO> vout((const IO*)a.grad_v + (t * kC * a.B + w.b) * a.ld_gv + (int64_t)w.h * a.V,
+                              a.B * a.ld_gv, left < kC ? left : kC, a.V, w.col + 16 * c, w.j);
+          if (FULL) vout.store(D[c]);
+          else vout.store(D[c], s, e);
+        }
       }
-      *x.vec(1, w.j) = D[0];
       __syncthreads();
       if (!owner) return;
       if (!FULL && fresh) {
-        S[0] = S[1] = kZero4;
+#pragma unroll
+        for (int c = 0; c < CB; ++c) S[c][0] = S[c][1] = kZero4;
         return;
       }
       // dS0 = exp(G_C) dS (of the last segment) + (exp G q)^T do' - (exp G k)^T dv
-      x.get_vec(1, V);
+      f16x8_t xb[CB][2][2], yb[CB][2][2];
+      float dx[CB], dy[CB];
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt) {
-        const f32x4_t eq = coef4(coef, kEnterQ, rt), ek = coef4(coef, kEnterK, rt);
+      for (int c = 0; c < CB; ++c) {
+        x[c].get_vec(1, V);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dO[rt][i] = in(rt, i) ? dO[rt][i] * eq[i] : 0.0f;
-          V[rt][i] = in(rt, i) ? V[rt][i] * ek[i] : 0.0f;
+        for (int rt = 0; rt < 4; ++rt) {
+          const f32x4_t eq = coef4(coef, kEnterQ, rt), ek = coef4(coef, kEnterK, rt);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dO[c][rt][i] = in(rt, i) ? dO[c][rt][i] * eq[i] : 0.0f;
+            V[rt][i] = in(rt, i) ? V[rt][i] * ek[i] : 0.0f;
+          }
         }
+        dx[c] = vec_operand<2>(dO[c], xb[c]);
+        dy[c] = vec_operand<2>(V, yb[c]);
+        if (CB > 1) fence();
       }
-      const Scale sx = col_scale(dO), sy = col_scale(V);
-      f16x8_t xb[2][2], yb[2][2];
-      to_operand<2>(dO, sx.up, xb);
-      to_operand<2>(V, sy.up, yb);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const f32x4_t p = times_cols<NP, KS, FULL>(qf, 2 * w.j + t, xb, s, e);
-        const f32x4_t y = times_cols<NP, KS, FULL>(kf, 2 * w.j + t, yb, s, e);
+      for (int k = 0; k < 2; ++k) {
+        times_cols<NP, KS, CB, FULL>(qf, 2 * w.j + k, xb, s, e, y);
+        times_cols<NP, KS, CB, FULL>(kf, 2 * w.j + k, yb, s, e, z);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          S[t][i] = __builtin_fmaf(p[i], sx.down,
-                                   __builtin_fmaf(-y[i], sy.down,
-                                                  FULL || e == kC ? keep * S[t][i] : 0.0f));
+        for (int c = 0; c < CB; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            S[c][k][i] = __builtin_fmaf(y[c][i], dx[c],
+                                        __builtin_fmaf(-z[c][i], dy[c],
+                                                       FULL || e == kC ? keep * S[c][k][i] : 0.0f));
+        if (CB > 1) fence();
       }
     };
     if (cuts == 0) {
@@ -1045,10 +1158,19 @@ __global__ __launch_bounds__(256 * NCB) void k_gdr_back(GdrArgs a) {
         e = s;
       }
     }
+    // the state was read before the chunk's first barrier, grad_o before its last segment's
+    if (owner) {
+#pragma unroll
+      for (int c = 0; c < CB; ++c) x[c].put_state(S[c], w.j);
+    }
+    put_o();
     __syncthreads();  // before the next chunk's operands are put over these
   }
-  if (a.grad_state0 && owner)
-    Rows<float>(a.grad_state0 + w.bh * sn, a.V, a.K, a.V, w, 2 * w.j).store(S);
+  if (a.grad_state0 && owner) {
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+      Rows<float>(a.grad_state0 + w.bh * sn, a.V, a.K, a.V, w.col + 16 * c, 2 * w.j).store(S[c]);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1057,24 +1179,21 @@ __global__ __launch_bounds__(256 * NCB) void k_gdr_back(GdrArgs a) {
 // ---------------------------------------------------------------------------
 // Sum over the 16 lanes of a row of an accumulator.
 __device__ __forceinline__ float row16_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) v += __shfl_xor(v, d);
+#define LRS_ROR(N) \
+  v += as_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)as_u32(v), 0x120 + N, 0xf, 0xf, false))
+  LRS_ROR(8);
+  LRS_ROR(4);
+  LRS_ROR(2);
+  LRS_ROR(1);
+#undef LRS_ROR
   return v;
 }
 
 constexpr int kVB = 32;  // columns of V at a time
 
-template <bool B, typename X, typename Y>
-struct Choose {
-  typedef X type;
-};
-template <typename X, typename Y>
-struct Choose<false, X, Y> {
-  typedef Y type;
-};
-
 // Wave 4 x + j of the eight has the steps 16 j... and half x of the columns of its products.
-template <typename IO, int KP, bool SHARED>
+// VEC: the rows of grad_o can be read in fours.
+template <typename IO, int KP, bool VEC>
 __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
   constexpr int NP = kParts<IO>, KS = KP / 32, KT = KP / 16, KH = KT / 2;
   constexpr int kSet = NP * 4 * KS * kFrag;
@@ -1100,7 +1219,8 @@ __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
   const int h = (int)((uint32_t)ch % (uint32_t)a.H), hk = h / (a.H / a.Hk);
   const int64_t cb = (uint32_t)ch / (uint32_t)a.H, b = (uint32_t)cb % (uint32_t)a.B,
                 c = (uint32_t)cb / (uint32_t)a.B, kh = cb * a.Hk + hk;
-  const int64_t sn = (int64_t)a.K * a.V, cn = (int64_t)(a.K + kC) * a.V;
+  const int vp = (int)saved_pitch(a.V);
+  const int64_t sn = (int64_t)a.K * vp, cn = (int64_t)(a.K + kC) * vp;
   const int64_t left = a.T - c * kC, n = left < kC ? left : kC;
   const uint64_t cuts = a.cuts[cb];
   const bool enters = !(cuts & 1), whole = cuts == 0;
@@ -1125,11 +1245,10 @@ __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
   float dbeta = 0.0f, dot = 0.0f;
 
   const Buffer bs(a.checkpoints + ch * cn, cn * 4), bg(a.grad_states + ch * sn, sn * 4);
-  const Buffer bw(a.w + ch * kC * a.V, (int64_t)kC * a.V * 4);
+  const Buffer bw(a.w + ch * kC * vp, (int64_t)kC * vp * 4);
   const int64_t po = a.B * a.H * a.V;
   const Buffer bo((const IO*)a.grad_o + (c * kC * a.B + b) * a.H * a.V + (int64_t)h * a.V,
                   ((n - 1) * po + a.V) * (int64_t)sizeof(IO));
-  const bool vec = quads<float>(a.checkpoints, 0, a.V), veco = quads<IO>(a.grad_o, 0, a.V);
   // 16 rows x 32 columns as a fragment in two parts (column 8 g + e), scaled by row
   auto put = [&](const float (&v)[8], uint16_t* to, int parts, float* down, int row)
       __attribute__((always_inline)) {
@@ -1139,25 +1258,30 @@ __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
     if (parts == 2) *reinterpret_cast<f16x8_t*>(to + kFrag + lane * 8) = p.lo;
     if (g == 0) down[row] = sc.down;
   };
-  for (int v0 = 0; v0 < a.V; v0 += kVB) {
-    const int col = v0 + 8 * g, row = 16 * w + r, k = 16 * wv + r;
-    Quad<float> s0[2], ds[2], wq[2], dq[2];
-    Quad<IO> oq[2];
+  // the next 32 columns are in flight, as they are in memory
+  Quad<float> s0[2], ds[2], wq[2], dq[2];
+  Quad<IO> oq[2];
+  const int row = 16 * w + r, k = 16 * wv + r;
+  auto fetch = [&](int v0) __attribute__((always_inline)) {
+    const int col = v0 + 8 * g;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (wv < KT) {
-        const uint32_t at = (uint32_t)k * (uint32_t)a.V * 4u;
-        ld_quad(bs, at, enters && k < a.K, col + 4 * j, a.V, vec, s0[j]);
-        ld_quad(bg, at, k < a.K, col + 4 * j, a.V, vec, ds[j]);
+        const uint32_t at = (uint32_t)k * (uint32_t)vp * 4u;
+        ld_quad<true>(bs, at, enters && k < a.K, col + 4 * j, vp, s0[j]);
+        ld_quad<true>(bg, at, k < a.K, col + 4 * j, vp, ds[j]);
       }
       if (half == 0) {
-        ld_quad(bo, (uint32_t)row * (uint32_t)po * (uint32_t)sizeof(IO), row < n, col + 4 * j, a.V,
-                veco, oq[j]);
+        ld_quad<VEC>(bo, (uint32_t)row * (uint32_t)po * (uint32_t)sizeof(IO), row < n, col + 4 * j,
+                     a.V, oq[j]);
       } else {
-        ld_quad(bw, (uint32_t)row * (uint32_t)a.V * 4u, true, col + 4 * j, a.V, vec, wq[j]);
-        ld_quad(bs, (uint32_t)(a.K + row) * (uint32_t)a.V * 4u, true, col + 4 * j, a.V, vec, dq[j]);
+        ld_quad<true>(bw, (uint32_t)row * (uint32_t)vp * 4u, true, col + 4 * j, vp, wq[j]);
+        ld_quad<true>(bs, (uint32_t)(a.K + row) * (uint32_t)vp * 4u, true, col + 4 * j, vp, dq[j]);
       }
     }
+  };
+  fetch(0);
+  for (int v0 = 0; v0 < a.V; v0 += kVB) {
     if (half == 0) {
       float v[8];
       oq[0].get(v);
@@ -1185,6 +1309,7 @@ __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
       put(v, sf + wv * 2 * kFrag, 2, rs, k);
       put(u, gf + wv * 2 * kFrag, 2, rg, k);
     }
+    if (v0 + kVB < a.V) fetch(v0 + kVB);
     __syncthreads();
     f16x8_t oa[NP], wa[2], da[2];
 #pragma unroll
@@ -1259,8 +1384,9 @@ __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
       s2 = __builtin_fmaf(kv, K1[t][i], s2);
       s3 = __builtin_fmaf(kv, K2[t][i], s3);
     }
-    const float tk_i = last ? row16_sum(s3) * rkk[row] : 0.0f;
-    e_row[i] = row16_sum(s1) * rkq[row] + row16_sum(s2) * rkk[row] - tk_i;
+    // of this lane's columns; summed over the lanes below
+    const float tk_i = last ? s3 * rkk[row] : 0.0f;
+    e_row[i] = s1 * rkq[row] + s2 * rkk[row] - tk_i;
     e_tail[i] = tk_i;
     fence();
   }
@@ -1297,7 +1423,7 @@ __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
       const float z = low ? -dL[t][i] * (bt[ri] * bt[cj]) * d : 0.0f;
       float en = low || cj == ri ? x * qk[i] * (rkq[ri] * rkk[cj]) : 0.0f;
       en = low ? __builtin_fmaf(z, kk[i] * (rkk[ri] * rkk[cj]), en) : en;
-      e_row[i] += row16_sum(en);
+      e_row[i] += en;
       ce += en;
       xm[ri][cj] = x;
       if (cj < ri) zm[ri][cj] = zm[cj][ri] = z;
@@ -1310,6 +1436,8 @@ __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    e_row[i] = row16_sum(e_row[i]);
+    e_tail[i] = row16_sum(e_tail[i]);
     if (r == 0) {
       row_e[half][16 * w + 4 * g + i] = e_row[i];
       row_t[half][16 * w + 4 * g + i] = e_tail[i];
@@ -1444,26 +1572,28 @@ __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
   }
 
   // dq and dk: rows 16 w + 4 g + i, columns 16 (half KH + t) + r
-  typedef typename Choose<SHARED, float, IO>::type Out;
-  const int64_t pq = SHARED ? a.K : a.B * a.ld_gq, pk = SHARED ? a.K : a.B * a.ld_gk;
-  const Out* to_q = SHARED ? (const Out*)(a.shared + ch * 2 * kC * a.K)
-                           : (const Out*)a.grad_q + (c * kC * a.B + b) * a.ld_gq + (int64_t)hk * a.K;
-  const Out* to_k = SHARED ? to_q + kC * a.K
-                           : (const Out*)a.grad_k + (c * kC * a.B + b) * a.ld_gk + (int64_t)hk * a.K;
-  const Buffer bq(to_q, ((n - 1) * pq + a.K) * (int64_t)sizeof(Out));
-  const Buffer bk(to_k, ((n - 1) * pk + a.K) * (int64_t)sizeof(Out));
+  auto write = [&](const auto* to, int64_t pitch, const f32x4_t (&v)[KH]) __attribute__((always_inline)) {
+    typedef decltype(to) P;
+    constexpr uint32_t es = sizeof(*to);
+    const Buffer buf(to, ((n - 1) * pitch + a.K) * (int64_t)es);
 #pragma unroll
-  for (int t = 0; t < KH; ++t) {
-    const int col = 16 * (half * KH + t) + r;
+    for (int t = 0; t < KH; ++t) {
+      const int col = 16 * (half * KH + t) + r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 16 * w + 4 * g + i;
-      const bool in = row < n && col < a.K;
-      bq.store(in ? ((uint32_t)row * (uint32_t)pq + (uint32_t)col) * (uint32_t)sizeof(Out) : kNowhere,
-               Q1[t][i], (const Out*)nullptr);
-      bk.store(in ? ((uint32_t)row * (uint32_t)pk + (uint32_t)col) * (uint32_t)sizeof(Out) : kNowhere,
-               K1[t][i], (const Out*)nullptr);
+      for (int i = 0; i < 4; ++i) {
+        const int at = 16 * w + 4 * g + i;
+        buf.store(at < n && col < a.K ? ((uint32_t)at * (uint32_t)pitch + (uint32_t)col) * es : kNowhere,
+                  v[t][i], (P)nullptr);
+      }
     }
+  };
+  if (a.shared) {
+    const float* to = a.shared + ch * 2 * kC * a.K;
+    write(to, a.K, Q1);
+    write(to + kC * a.K, a.K, K1);
+  } else {
+    write((const IO*)a.grad_q + (c * kC * a.B + b) * a.ld_gq + (int64_t)hk * a.K, a.B * a.ld_gq, Q1);
+    write((const IO*)a.grad_k + (c * kC * a.B + b) * a.ld_gk + (int64_t)hk * a.K, a.B * a.ld_gk, K1);
   }
 }
 
@@ -1585,13 +1715,14 @@ __global__ __launch_bounds__(256) void k_gdr_step(GdrArgs a, const int32_t* __re
   }
 }
 
-// Column blocks of a chain's workgroup: as many as four, which read a chunk's operands
-// together, while every compute unit has a workgroup.
+// Column blocks of a chain's workgroup, two a wave: four, which read a chunk's operands
+// together and hide each other's waits, while every compute unit has a workgroup; else one,
+// for the shortest chunk.
 template <typename F>
-void chain_blocks(const GdrArgs& a, F launch) {
+void chain_shape(const GdrArgs& a, bool most_four, F launch) {
   const int64_t heads = a.B * a.H, cus = device_cus();
-  const int n = heads * ((a.V + 31) / 32) >= cus ? 2 : 1;
-  launch(n, dim3((unsigned)(heads * ((a.V + 16 * n - 1) / (16 * n)))), dim3(256 * n));
+  const int n = heads * ((a.V + 63) / 64) >= cus && most_four ? 4 : heads * ((a.V + 31) / 32) >= cus ? 2 : 1;
+  launch(n, dim3((unsigned)(heads * ((a.V + 16 * n - 1) / (16 * n)))));
 }
 
 template <typename IO, int KP>
@@ -1599,30 +1730,35 @@ hipError_t gdr_fwd(const GdrArgs& a, hipStream_t stream) {
   const int64_t nc = (a.T + kC - 1) / kC;
   hipLaunchKernelGGL((k_gdr_prep<IO, KP, false>), dim3((unsigned)(nc * a.B * a.H)), dim3(256), 0,
                      stream, a);
-  chain_blocks(a, [&](int n, dim3 grid, dim3 wg) {
-    if (n == 4) hipLaunchKernelGGL((k_gdr_chain<IO, KP, 4>), grid, wg, 0, stream, a);
-    else if (n == 2) hipLaunchKernelGGL((k_gdr_chain<IO, KP, 2>), grid, wg, 0, stream, a);
-    else hipLaunchKernelGGL((k_gdr_chain<IO, KP, 1>), grid, wg, 0, stream, a);
+  chain_shape(a, true, [&](int n, dim3 grid) {
+    if (n == 4) hipLaunchKernelGGL((k_gdr_chain<IO, KP, 2, 2>), grid, dim3(512), 0, stream, a);
+    else if (n == 2) hipLaunchKernelGGL((k_gdr_chain<IO, KP, 1, 2>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((k_gdr_chain<IO, KP, 1, 1>), grid, dim3(256), 0, stream, a);
   });
   return hipGetLastError();
 }
 template <typename IO, int KP>
 hipError_t gdr_bwd(const GdrArgs& a, hipStream_t stream) {
   const int64_t nc = (a.T + kC - 1) / kC;
+  // four blocks of fp32 with K > 64 do not fit into LDS
+  constexpr bool kFour = sizeof(IO) == 2 || KP == 64;
   hipLaunchKernelGGL((k_gdr_prep<IO, KP, true>), dim3((unsigned)(nc * a.B * a.H)), dim3(256), 0,
                      stream, a);
-  chain_blocks(a, [&](int n, dim3 grid, dim3 wg) {
-    if (n == 4) hipLaunchKernelGGL((k_gdr_back<IO, KP, 4>), grid, wg, 0, stream, a);
-    else if (n == 2) hipLaunchKernelGGL((k_gdr_back<IO, KP, 2>), grid, wg, 0, stream, a);
-    else hipLaunchKernelGGL((k_gdr_back<IO, KP, 1>), grid, wg, 0, stream, a);
+  chain_shape(a, kFour, [&](int n, dim3 grid) {
+    if (kFour && n == 4)
+      hipLaunchKernelGGL((k_gdr_back<IO, KP, kFour ? 2 : 1, 2>), grid, dim3(512), 0, stream, a);
+    else if (n == 2)
+      hipLaunchKernelGGL((k_gdr_back<IO, KP, 1, 2>), grid, dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL((k_gdr_back<IO, KP, 1, 1>), grid, dim3(256), 0, stream, a);
   });
   const dim3 groups((unsigned)(nc * a.B * a.H));
-  if (a.H == a.Hk) {
-    hipLaunchKernelGGL((k_gdr_grads<IO, KP, false>), groups, dim3(512), 0, stream, a);
-  } else {
+  if (quads<IO>(a.grad_o, 0, a.V))
     hipLaunchKernelGGL((k_gdr_grads<IO, KP, true>), groups, dim3(512), 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_gdr_grads<IO, KP, false>), groups, dim3(512), 0, stream, a);
+  if (a.shared)
     hipLaunchKernelGGL((k_gdr_shared<IO>), dim3((unsigned)(nc * a.B * a.Hk)), dim3(256), 0, stream, a);
-  }
   return hipGetLastError();
 }
 

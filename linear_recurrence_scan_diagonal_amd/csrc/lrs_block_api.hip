@@ -30,9 +30,9 @@ bool gdr_sizes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t K, int64_t V
     return false;
   s->chunks = T / lrs::kGdrRows + (T % lrs::kGdrRows != 0);
   if (!mul_ok(s->chunks, s->states, &n) || n > ((int64_t)1 << 58)) return false;
-  if (!mul_ok(n, lrs::kGdrRows + 1, &m) || m > ((int64_t)1 << 58)) return false;
+  if (!mul_ok(n, 4 * (lrs::kGdrRows + 1), &m) || m > ((int64_t)1 << 60)) return false;
   s->es = io_size(io);
-  s->saved = (size_t)(n + s->chunks * B * s->vw * lrs::kGdrRows) * 4;
+  s->saved = (size_t)(s->chunks * B * H * (K + lrs::kGdrRows) * lrs::gdr_saved_pitch(V)) * 4;
   return true;
 }
 // The kernels' grids and 32-bit sizes.
@@ -64,8 +64,8 @@ size_t gdr_carve(int64_t chunks, int64_t B, int64_t H, int64_t Hk, int64_t K, in
   a->kq_rows = cv.take<uint16_t>(nk * 2 * set);
   if (!backward) return cv.used;
   a->decay_sums = cv.take<double>(nv * C);
-  a->w = cv.take<float>(nv * C * V);
-  a->grad_states = cv.take<float>(nv * K * V);
+  a->w = cv.take<float>(nv * C * lrs::gdr_saved_pitch(V));
+  a->grad_states = cv.take<float>(nv * K * lrs::gdr_saved_pitch(V));
   a->shared = cv.take<float>(H > Hk ? nv * 2 * C * K : 0);
   return cv.used;
 }

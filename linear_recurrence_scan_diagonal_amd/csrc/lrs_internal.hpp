@@ -322,6 +322,8 @@ hipError_t launch_zero(void* p, int64_t bytes, hipStream_t stream);
 // backward also has the last group.
 constexpr int kGdrRows = 64;   // steps a chunk, and between two checkpoints
 constexpr int kGdrMostK = 128;
+// Elements from row to row of the states and vectors kept in fp32: V in fours.
+__host__ __device__ __forceinline__ int64_t gdr_saved_pitch(int64_t V) { return (V + 3) & ~(int64_t)3; }
 constexpr int kGdrMats = 13312;  // 16-bit values of a chunk's matrices and coefficients
 struct GdrArgs {
   const void *q, *k, *v;
@@ -344,8 +346,8 @@ struct GdrArgs {
   int64_t ld_gq, ld_gk, ld_gv;
   float *grad_log_decay, *grad_beta, *grad_state0;
   double* decay_sums;                         // [64]
-  float* w;                                   // [64][V]
-  float* grad_states;                         // [K][V]
+  float* w;                                   // [64][V], rows gdr_saved_pitch apart
+  float* grad_states;                         // [K][V], the same
   float* shared;                              // [2][64][K]: dq and dk of heads that share q and k
 };
 hipError_t launch_gdr_fwd(const GdrArgs& a, int io, hipStream_t stream);
