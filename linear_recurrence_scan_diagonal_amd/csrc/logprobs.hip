@@ -5,22 +5,20 @@
 //   lse = m + log s,  logprob = (l_target - m) - log s,  entropy = log s - t / s;
 //   grad_l = grad_logprob (onehot - p) - grad_entropy p (log p + entropy).
 //
-// Memory bound: the logits are read once.  Without alternatives a row streams through its
-// threads, each with a maximum of its own so far and sums relative to it (a larger value
-// rescales them, which is rare after the first few).  With alternatives a row is held in
-// the registers of 256 to 1024 threads (up to 16 groups of 16 bytes a thread), where it is
-// looked at three times; rows too wide for that are read again (and found in the caches).
+// Memory bound: the logits are read once.  A row streams through the 256 (or, where rows
+// are few, 1024) threads of a workgroup, each with a maximum of its own so far and sums
+// relative to it; a larger value rescales them, which is rare after the first few.
 //
-// The `top` largest.  Every thread has the first of its largest values from the pass over
-// the maximum; the largest of 64 (or 128) groups of threads are ranked, and the top-th of
-// them is a bound: there are `top` values at or above it, and hardly more (25 for the 20
-// largest of random logits).  Those are collected in LDS, which few threads have to take
-// part in, and ranked by counting.  A value and its index make one whole number, so that
-// nothing is equal and the order does not depend on who came first.  Where the bound is
-// -infinity (few tokens are allowed), those that are not are candidates, and the first 128
-// places, among which are enough of the others.  Rows with more candidates than the LDS
-// holds (large values side by side, or a NaN) are read `top` times again, each time for
-// the largest below the one before.
+// The `top` largest.  Every thread also keeps the place of the first of its largest values;
+// the largest of 64 (or 128) groups of threads are ranked, and the top-th of them is a
+// bound: there are `top` values at or above it, and hardly more (25 for the 20 largest of
+// random logits).  Only threads whose own largest reaches it read their part again, leave
+// the values in LDS, and those are ranked by counting.  A value and its index make one
+// whole number, so that nothing is equal and the order does not depend on who came first.
+// Where the bound is -infinity (few tokens are allowed), the values above it are
+// candidates, and the first 128 places, among which are enough of the others.  Rows with
+// more candidates than the LDS holds (many equal values over 1024 threads, or a NaN) are
+// read `top` times again, each time for the largest below the one before.
 #include "lrs_device.hpp"
 #include "lrs_internal.hpp"
 #include "lrs_rows.hpp"
@@ -31,7 +29,7 @@ namespace {
 
 constexpr float kLog2eF = 1.4426950408889634f;
 constexpr float kFarBelow = -200.0f;  // exp of it is 0: a logit of -infinity adds 0, not 0 * infinity
-constexpr int kCandidates = 2048;  // a row of equal values has 64 to 2048
+constexpr int kCandidates = 2048;  // a row of equal values has 32 a rank (256 threads)
 constexpr uint64_t kNoKey = 0;
 constexpr uint32_t kFirst = 0x80000000u;  // the low half of index 0; an index is below 2^24
 
@@ -72,7 +70,10 @@ __device__ __forceinline__ float row_lse(const RowOut& o, bool has_nan) {
 }
 
 constexpr float kInf = __builtin_inff();
-constexpr float kLowest = -3.4e38f;  // behind a row's end, where sums are made: adds 0
+constexpr float kLowest = -3.402823466e38f;  // the lowest finite value, a mask to some
+// The backward takes |lse| up to here as it was rounded, to 2^-17; beyond, where rounding
+// would show in p, it sums the row again.
+constexpr float kExactLse = 256.0f;
 
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
@@ -80,84 +81,68 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-// exp(l - m) and its product with l - m, added up over a group.  CLAMP: -infinity among
-// the values adds 0 instead of NaN to the second sum.
-template <bool CLAMP, int G>
+// exp(l - m) and its product with l - m, added up over a group.  While there is nothing but
+// -infinity, m is that, and the lowest finite value stands for it.
+template <int G>
 __device__ __forceinline__ void add_group(const float (&v)[G], float m, float& s, float& t) {
+  m = fmaxf(m, kLowest);
 #pragma unroll
   for (int j = 0; j < G; ++j) {
     const float c = v[j] - m;
     const float x = __builtin_amdgcn_exp2f(c * kLog2eF);
     s += x;
-    t = __builtin_fmaf(x, CLAMP ? fmaxf(c, kFarBelow) : c, t);
+    t = __builtin_fmaf(x, fmaxf(c, kFarBelow), t);
   }
 }
+// A larger maximum: the sums become relative to it.
+__device__ __forceinline__ void raise(float x, float& m, float& s, float& t) {
+  const float d = m - x, f = __builtin_amdgcn_exp2f(d * kLog2eF);
+  t = __builtin_fmaf(s * f, d, t * f);
+  s *= f;
+  m = x;
+  if (!(s > 0.0f)) t = s = s == s ? 0.0f : s;  // nothing yet: d was not finite
+}
+// A thread's sums, relative to the row's maximum.
+__device__ __forceinline__ void lower(float top, float m, float& s, float& t) {
+  const float d = fmaxf(m - top, kFarBelow), f = __builtin_amdgcn_exp2f(d * kLog2eF);
+  t = __builtin_fmaf(s * f, d, t * f);
+  s *= f;
+}
 
-// The groups of 16 bytes of a row, held in registers (NV > 0) or read again (NV = 0).  An
-// index is below 2^24.
-template <typename IO, int BT, int NV>
+// A row's groups of 16 bytes, every BT-th a thread's.  An index is below 2^24.
+template <typename IO, int BT>
 struct Row {
   static constexpr int G = kGroup<IO>;
-  u32x4_t q[NV > 0 ? NV : 1];
   const IO* row;
   int V;
-  // whether every thread's group i is inside the row; the same for all threads
-  __device__ __forceinline__ bool full(int i) const { return (i + 1) * (BT * G) <= V; }
   __device__ __forceinline__ int at(int i) const { return (i * BT + (int)threadIdx.x) * G; }
-  __device__ __forceinline__ u32x4_t load(int i) const {
-    if (full(i)) return *reinterpret_cast<const u32x4_any*>(row + at(i));
-    return ld_raw<false>(row, at(i), V);
-  }
-  __device__ __forceinline__ void open(const IO* p, int64_t n) {
-    row = p;
-    V = (int)n;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) q[i] = load(i);
-  }
-  // the values of a group that begins at e, `fill` behind the row's end
-  __device__ __forceinline__ void get(u32x4_t raw, int e, float fill, float (&v)[G]) const {
-    unpack(raw, v);
+  // the values of the group that begins at e, `fill` behind the row's end
+  __device__ __forceinline__ void group(int e, float fill, float (&v)[G]) const {
+    unpack(ld_raw<false>(row, e, V), v);
 #pragma unroll
     for (int j = 0; j < G; ++j) v[j] = e + j < V ? v[j] : fill;
   }
-  // f(values, first index), every group of this thread in rising order
+  // f(values, first index), every group of this thread in rising order, four in flight
   template <typename F>
-  __device__ __forceinline__ void each(float fill, F f) {
-    if constexpr (NV > 0) {
+  __device__ __forceinline__ void each(float fill, F f) const {
+    constexpr int kStep = BT * G;
+    int i = 0;
+    for (; (i + 4) * kStep <= V; i += 4) {
+      u32x4_t q[4];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
+      for (int k = 0; k < 4; ++k) q[k] = *reinterpret_cast<const u32x4_any*>(row + at(i + k));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
         float v[G];
-        // opaque, or a pass's unpacked values would be kept for the next one
-        asm volatile("" : "+v"(q[i]));
-        if (full(i)) unpack(q[i], v);
-        else get(q[i], at(i), fill, v);
-        f(v, at(i));
-        __builtin_amdgcn_sched_barrier(0);  // one group after the other: registers
-      }
-    } else {
-      int i = 0;
-#pragma unroll 4
-      for (; full(i); ++i) {
-        float v[G];
-        unpack(*reinterpret_cast<const u32x4_any*>(row + at(i)), v);
-        f(v, at(i));
-      }
-      if (at(i) < V) {
-        float v[G];
-        get(ld_raw<false>(row, at(i), V), at(i), fill, v);
-        f(v, at(i));
+        unpack(q[k], v);
+        f(v, at(i + k));
       }
     }
-  }
-  __device__ __forceinline__ void group(int e, float fill, float (&v)[G]) const {
-    u32x4_t raw = {0u, 0u, 0u, 0u};
-    if constexpr (NV > 0) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) raw = at(i) == e ? q[i] : raw;
-    } else {
-      raw = ld_raw<false>(row, e, V);
+    for (; at(i) < V; ++i) {
+      float v[G];
+      group(at(i), fill, v);
+      f(v, at(i));
     }
-    get(raw, e, fill, v);
   }
 };
 template <int G>
@@ -170,7 +155,7 @@ __device__ __forceinline__ float group_max(const float (&v)[G]) {
 
 // Whether the row has a NaN, for all threads of the workgroup.
 template <typename R>
-__device__ __forceinline__ bool row_has_nan(R& row, int* bad) {
+__device__ __forceinline__ bool row_has_nan(const R& row, int* bad) {
   if (threadIdx.x == 0) *bad = 0;
   __syncthreads();
   bool nan = false;
@@ -190,45 +175,58 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t n, const
   a.lse[n] = row_lse(o, nan);
 }
 
-// No alternatives: the row streams past.
-template <typename IO, int BT>
+template <typename IO, int BT, bool TOP>
 __global__ __launch_bounds__(BT) void k_logprobs(LogprobArgs a) {
   constexpr int G = kGroup<IO>, NW = BT / kWave;
   __shared__ float red[NW][3];
-  __shared__ int bad;
+  __shared__ uint64_t cand[TOP ? kCandidates : 1], best_of[TOP ? NW : 1];
+  __shared__ int count, bad;
   const int64_t n = blockIdx.x;
-  Row<IO, BT, 0> row;
-  row.open((const IO*)a.logits + n * a.ld, a.V);
+  const Row<IO, BT> row = {(const IO*)a.logits + n * a.ld, (int)a.V};
   const int64_t target = a.target[n];
   const bool counted = target >= 0 && target < a.V;
   float tl = 0.0f;
-  if (threadIdx.x == 0 && counted) tl = io_ld(row.row, target);
-
-  float m = kLowest, s = 0.0f, t = 0.0f;
-  row.each(kLowest, [&](const float (&v)[G], int e) __attribute__((always_inline)) {
-    const float x = group_max(v);
-    if (x > m) {  // exp(m - x), and t is relative to the new maximum
-      const float d = m - x, f = __builtin_amdgcn_exp2f(d * kLog2eF);
-      t = __builtin_fmaf(s * f, d, t * f);
-      s *= f;
-      m = x;
-      if (!(s > 0.0f)) t = s = s == s ? 0.0f : s;  // nothing yet: d was not finite
-    }
-    add_group<true>(v, m, s, t);
-  });
-  // the threads' sums, brought to the row's maximum
-  const float wm = wave_max(m);
-  const int w = threadIdx.x / kWave;
-  if ((threadIdx.x & (kWave - 1)) == 0) red[w][0] = wm;
-  __syncthreads();
-  float top = red[0][0];
-#pragma unroll
-  for (int i = 1; i < NW; ++i) top = fmaxf(top, red[i][0]);
-  {
-    const float d = fmaxf(m - top, kFarBelow), f = __builtin_amdgcn_exp2f(d * kLog2eF);
-    t = __builtin_fmaf(s * f, d, t * f);
-    s *= f;
+  if (threadIdx.x == 0) {
+    if (TOP) count = 0;
+    if (counted) tl = io_ld(row.row, target);
   }
+
+  float m = -kInf, s = 0.0f, t = 0.0f;
+  int where = row.at(0);  // the first group that holds the thread's largest
+  row.each(-kInf, [&](const float (&v)[G], int e) __attribute__((always_inline)) {
+    const float x = group_max(v);
+    if (x > m) {
+      where = e;
+      raise(x, m, s, t);
+    }
+    add_group(v, m, s, t);
+  });
+  const int w = threadIdx.x / kWave;
+  {
+    const float wm = wave_max(m);
+    if ((threadIdx.x & (kWave - 1)) == 0) red[w][0] = wm;
+  }
+  uint64_t mine = kNoKey;
+  const int groups = a.top > 32 ? 128 : 64;
+  if constexpr (TOP) {
+    if (row.at(0) < row.V) {
+      float v[G];
+      row.group(where, -kInf, v);
+#pragma unroll
+      for (int j = G - 1; j >= 0; --j)
+        if (v[j] == m && where + j < row.V) mine = key_of(m, where + j);
+    }
+    const int per = BT / groups;
+    uint64_t key = mine;
+    for (int o = per / 2; o > 0; o >>= 1) key = max_key(key, shfl_xor_key(key, o));
+    if (threadIdx.x % per == 0) cand[threadIdx.x / per] = key;
+  }
+  __syncthreads();
+  // the threads' sums, brought to the row's maximum
+  float top_value = red[0][0];
+#pragma unroll
+  for (int i = 1; i < NW; ++i) top_value = fmaxf(top_value, red[i][0]);
+  lower(top_value, m, s, t);
 #pragma unroll
   for (int o = kWave / 2; o > 0; o >>= 1) {
     s += __shfl_xor(s, o);
@@ -237,6 +235,18 @@ __global__ __launch_bounds__(BT) void k_logprobs(LogprobArgs a) {
   if ((threadIdx.x & (kWave - 1)) == 0) {
     red[w][1] = s;
     red[w][2] = t;
+  }
+  if constexpr (TOP) {
+    if ((int)threadIdx.x < groups) {
+      const uint64_t k = cand[threadIdx.x];
+      int rank = 0;
+#pragma unroll 16
+      for (int i = 0; i < groups; ++i) {
+        const uint64_t o = cand[i];
+        rank += o > k || (o == k && i < (int)threadIdx.x);
+      }
+      if (rank == a.top - 1) best_of[0] = k;
+    }
   }
   __syncthreads();
   s = t = 0.0f;
@@ -246,201 +256,106 @@ __global__ __launch_bounds__(BT) void k_logprobs(LogprobArgs a) {
     t += red[i][2];
   }
   // the same for all threads: nothing but -infinity, an infinity or a NaN
-  const bool odd = !(s > 0.0f) || !(fabsf(top) < -kLowest);
+  const bool odd = !(s > 0.0f) || !(fabsf(top_value) < kInf);
   bool nan = false;
   if (odd) {
     nan = row_has_nan(row, &bad);
-    if (!(top > kLowest)) top = -kInf;
-    if (!(fabsf(top) < kInf) || nan) s = __builtin_nanf("");
+    s = __builtin_nanf("");
   }
-  if (threadIdx.x == 0) write_row(a, n, row_out(top, s, t), tl, counted, nan);
+  const RowOut out = row_out(top_value, s, t);
+  if (threadIdx.x == 0) write_row(a, n, out, tl, counted, nan);
+  if constexpr (TOP) {
+    const int top = a.top;
+    int64_t* ids = a.top_ids + n * top;
+    float* lps = a.top_logprobs + n * top;
+    auto emit = [&](int rank, uint64_t key) __attribute__((always_inline)) {
+      ids[rank] = key_index(key);
+      lps[rank] = (key_value(key) - out.m) - out.log_s;
+    };
+    const uint64_t bound = best_of[0];
+    bool many = odd;
+    if (!odd) {
+      __syncthreads();  // cand is written again
+      const float least = bound == kNoKey ? -kInf : key_value(bound);  // no key: groups without values
+      if (mine >= bound || least == -kInf) {
+        row.each(-kInf, [&](const float (&v)[G], int e) __attribute__((always_inline)) {
+          const float x = group_max(v);
+          if (!(least == -kInf ? x > least || e < 128 : x >= least)) return;
+#pragma unroll
+          for (int j = 0; j < G; ++j) {
+            const uint64_t k = key_of(v[j], e + j);
+            if (e + j < row.V && (least == -kInf ? v[j] > least || e + j < 128 : k >= bound)) {
+              const int i = atomicAdd(&count, 1);
+              if (i < kCandidates) cand[i] = k;
+            }
+          }
+        });
+      }
+      __syncthreads();
+      const int found = count;
+      many = found > kCandidates;
+      if (!many) {
+        for (int i = threadIdx.x; i < found; i += BT) {
+          const uint64_t k = cand[i];
+          int rank = 0;
+#pragma unroll 8
+          for (int j = 0; j < found; ++j) rank += cand[j] > k;
+          if (rank < top) emit(rank, k);
+        }
+      }
+    }
+    if (many) {
+      uint64_t last = ~0ull;  // above every key
+      for (int r = 0; r < top; ++r) {
+        uint64_t key = kNoKey;
+        row.each(-kInf, [&](const float (&v)[G], int e) __attribute__((always_inline)) {
+#pragma unroll
+          for (int j = 0; j < G; ++j) {
+            const uint64_t k = key_of(v[j], e + j);
+            if (k < last && e + j < row.V) key = max_key(key, k);
+          }
+        });
+#pragma unroll
+        for (int o = kWave / 2; o > 0; o >>= 1) key = max_key(key, shfl_xor_key(key, o));
+        __syncthreads();
+        if ((threadIdx.x & (kWave - 1)) == 0) best_of[threadIdx.x / kWave] = key;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NW; ++i) key = max_key(key, best_of[i]);
+        if (threadIdx.x == 0) emit(r, key);
+        last = key;
+      }
+    }
+  }
 }
 
-// With alternatives.
-template <typename IO, int BT, int NV>
-__global__ __launch_bounds__(BT) void k_logprobs_top(LogprobArgs a) {
-  constexpr int G = kGroup<IO>, NW = BT / kWave;
-  __shared__ float red[NW][3];
-  __shared__ uint64_t cand[kCandidates], best_of[NW];
-  __shared__ int count, bad;
-  const int64_t n = blockIdx.x;
-  Row<IO, BT, NV> row;
-  row.open((const IO*)a.logits + n * a.ld, a.V);
-  const int64_t target = a.target[n];
-  const bool counted = target >= 0 && target < a.V;
-  float tl = 0.0f;
-  if (threadIdx.x == 0) {
-    count = 0;
-    if (counted) tl = io_ld(row.row, target);
-  }
-
-  // the maximum, and the thread's first group that holds its own
-  float m = -kInf;
-  int where = row.at(0);
-  row.each(-kInf, [&](const float (&v)[G], int e) __attribute__((always_inline)) {
-    const float x = group_max(v);
-    where = x > m ? e : where;
-    m = fmaxf(m, x);
-  });
-  const float own = m;
-  const int w = threadIdx.x / kWave;
-  m = wave_max(m);
-  if ((threadIdx.x & (kWave - 1)) == 0) red[w][0] = m;
-  // the thread's largest value and its first place, and the largest of each group of threads:
-  // 64 groups, 128 for more than 32 alternatives
-  uint64_t mine = kNoKey;
-  if (row.at(0) < a.V) {
-    float v[G];
-    row.group(where, -kInf, v);
-    int j0 = G;
-#pragma unroll
-    for (int j = G - 1; j >= 0; --j) j0 = v[j] == own && where + j < a.V ? j : j0;
-    if (j0 < G) mine = key_of(own, where + j0);
-  }
-  const int groups = a.top > 32 ? 128 : 64, per = BT / groups;
-  {
-    uint64_t key = mine;
-    for (int o = per / 2; o > 0; o >>= 1) key = max_key(key, shfl_xor_key(key, o));
-    if (threadIdx.x % per == 0) cand[threadIdx.x / per] = key;
-  }
-  __syncthreads();
-  m = red[0][0];
-#pragma unroll
-  for (int i = 1; i < NW; ++i) m = fmaxf(m, red[i][0]);
-  // the top-th largest of the groups, found by the first wave (or two) while the others go on
-  if ((int)threadIdx.x < groups) {
-    const uint64_t k = cand[threadIdx.x];
-    int rank = 0;
-#pragma unroll 16
-    for (int i = 0; i < groups; ++i) {
-      const uint64_t o = cand[i];
-      rank += o > k || (o == k && i < (int)threadIdx.x);
-    }
-    if (rank == a.top - 1) best_of[0] = k;
-  }
+// A row's maximum and the logarithm of its sum.
+template <typename IO>
+__device__ __forceinline__ float2 row_sum_of(const IO* row, int V) {
+  constexpr int G = kGroup<IO>;
+  __shared__ float red[2][256 / kWave];
+  const Row<IO, 256> all = {row, V};
   float s = 0.0f, t = 0.0f;
-  row.each(kLowest, [&](const float (&v)[G], int e) __attribute__((always_inline)) {
-    add_group<false>(v, m, s, t);
+  float m = -kInf;
+  all.each(-kInf, [&](const float (&v)[G], int) __attribute__((always_inline)) {
+    const float x = group_max(v);
+    if (x > m) raise(x, m, s, t);
+    add_group(v, m, s, t);
   });
-  if (t != t && s == s) {  // -infinity among the values
-    s = t = 0.0f;
-    Row<IO, BT, 0> again;
-    again.open(row.row, row.V);
-    again.each(kLowest, [&](const float (&v)[G], int e) __attribute__((always_inline)) {
-      add_group<true>(v, m, s, t);
-    });
-  }
-#pragma unroll
-  for (int o = kWave / 2; o > 0; o >>= 1) {
-    s += __shfl_xor(s, o);
-    t += __shfl_xor(t, o);
-  }
-  if ((threadIdx.x & (kWave - 1)) == 0) {
-    red[w][1] = s;
-    red[w][2] = t;
-  }
+  const float wm = wave_max(m);
+  if ((threadIdx.x & (kWave - 1)) == 0) red[0][threadIdx.x / kWave] = wm;
   __syncthreads();
-  const uint64_t found_bound = best_of[0];
-  s = t = 0.0f;
+  float top = red[0][0];
 #pragma unroll
-  for (int i = 0; i < NW; ++i) {
-    s += red[i][1];
-    t += red[i][2];
-  }
-  const bool odd = !(fabsf(m) < kInf) || s != s;  // the same for all threads
-  bool nan = false;
-  if (odd) {
-    Row<IO, BT, 0> again;
-    again.open(row.row, row.V);
-    nan = row_has_nan(again, &bad);
-  }
-  const RowOut out = row_out(m, odd ? __builtin_nanf("") : s, t);
-  if (threadIdx.x == 0) write_row(a, n, out, tl, counted, nan);
-
-  const int top = a.top;
-  int64_t* ids = a.top_ids + n * top;
-  float* lps = a.top_logprobs + n * top;
-  auto emit = [&](int rank, uint64_t key) __attribute__((always_inline)) {
-    ids[rank] = key_index(key);
-    lps[rank] = (key_value(key) - m) - out.log_s;
-  };
-  bool many = odd;
-  if (!odd) {
-    const uint64_t bound = found_bound;
-    const float least = bound == kNoKey ? -kInf : key_value(bound);  // no key: groups without values
-    if (mine >= bound || least == -kInf) {
-      // the groups that hold candidates, by number, and then those one at a time, read again
-      auto take = [&](int e) __attribute__((always_inline)) {
-        float v[G];
-        row.get(ld_raw<false>(row.row, e, row.V), e, -kInf, v);
+  for (int i = 1; i < 256 / kWave; ++i) top = fmaxf(top, red[0][i]);
+  lower(top, m, s, t);
+  s = wave_sum(s);
+  if ((threadIdx.x & (kWave - 1)) == 0) red[1][threadIdx.x / kWave] = s;
+  __syncthreads();
+  s = red[1][0];
 #pragma unroll
-        for (int j = 0; j < G; ++j) {
-          const uint64_t k = key_of(v[j], e + j);
-          if (e + j < row.V && (least == -kInf ? v[j] > least || e + j < 128 : k >= bound)) {
-            const int i = atomicAdd(&count, 1);
-            if (i < kCandidates) cand[i] = k;
-          }
-        }
-      };
-      auto holds = [&](const float (&v)[G], int e) __attribute__((always_inline)) {
-        const float x = group_max(v);
-        return least == -kInf ? x > least || e < 128 : x >= least;
-      };
-      if constexpr (NV > 0) {
-        uint32_t some = 0u;
-        int i = 0;
-        row.each(-kInf, [&](const float (&v)[G], int e) __attribute__((always_inline)) {
-          some |= holds(v, e) ? 1u << i : 0u;
-          ++i;
-        });
-        while (some) {
-          const int n = __builtin_ctz(some);
-          some &= some - 1u;
-          take(row.at(n));
-        }
-      } else {
-        row.each(-kInf, [&](const float (&v)[G], int e) __attribute__((always_inline)) {
-          if (holds(v, e)) take(e);
-        });
-      }
-    }
-    __syncthreads();
-    const int found = count;
-    many = found > kCandidates;
-    if (!many) {
-      for (int i = threadIdx.x; i < found; i += BT) {
-        const uint64_t k = cand[i];
-        int rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < found; ++j) rank += cand[j] > k;
-        if (rank < top) emit(rank, k);
-      }
-    }
-  }
-  if (many) {
-    Row<IO, BT, 0> again;
-    again.open(row.row, row.V);
-    uint64_t last = ~0ull;  // above every key
-    for (int r = 0; r < top; ++r) {
-      uint64_t key = kNoKey;
-      again.each(-kInf, [&](const float (&v)[G], int e) __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < G; ++j) {
-          const uint64_t k = key_of(v[j], e + j);
-          if (k < last && e + j < row.V) key = max_key(key, k);
-        }
-      });
-#pragma unroll
-      for (int o = kWave / 2; o > 0; o >>= 1) key = max_key(key, shfl_xor_key(key, o));
-      __syncthreads();
-      if ((threadIdx.x & (kWave - 1)) == 0) best_of[threadIdx.x / kWave] = key;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < NW; ++i) key = max_key(key, best_of[i]);
-      if (threadIdx.x == 0) emit(r, key);
-      last = key;
-    }
-  }
+  for (int i = 1; i < 256 / kWave; ++i) s += red[1][i];
+  return make_float2(top, logf(s));
 }
 
 // One group of 16 bytes a thread and step; blockIdx.x = row, blockIdx.y = piece of it.
@@ -457,6 +372,13 @@ __global__ __launch_bounds__(256) void k_logprobs_bwd(LogprobArgs a, int64_t pie
   const float base = __builtin_fmaf(ge, h, gl);  // grad = -p (gl + ge (c + h))
   // a row that asks for nothing gets 0, whatever its logits are (padding)
   const bool none = !(target >= 0 && target < a.V) && ge == 0.0f;
+  // log p = (l - m) - log_s
+  float m = lse, log_s = 0.0f;
+  if (fabsf(lse) > kExactLse && fabsf(lse) < kInf) {  // the same for all threads
+    const float2 all = row_sum_of<IO>(row, (int)a.V);
+    m = all.x;
+    log_s = all.y;
+  }
   const int64_t e1 = (int64_t)(blockIdx.y + 1) * piece;
   const int64_t end = e1 < a.V ? e1 : a.V;
 #pragma unroll 4
@@ -465,7 +387,7 @@ __global__ __launch_bounds__(256) void k_logprobs_bwd(LogprobArgs a, int64_t pie
     ld_group<NT>(row, e, a.V, v);
 #pragma unroll
     for (int j = 0; j < G; ++j) {
-      const float c = v[j] - lse;
+      const float c = (v[j] - m) - log_s;
       const float p = __builtin_amdgcn_exp2f(c * kLog2eF);
       const float g = p * -__builtin_fmaf(ge, fmaxf(c, kFarBelow), base);
       v[j] = none ? 0.0f : e + j == target ? g + gl : g;
@@ -478,21 +400,16 @@ template <typename IO>
 void logprobs(const LogprobArgs& a, hipStream_t stream) {
   const int64_t groups = (a.V + kGroup<IO> - 1) / kGroup<IO>;
   const dim3 grid((unsigned)a.N);
-  if (a.top == 0) {
-    // several rows a compute unit while there are rows enough, else the most threads a row
-    if (a.N >= 2 * device_cus() || groups <= 512)
-      hipLaunchKernelGGL((k_logprobs<IO, 256>), grid, dim3(256), 0, stream, a);
-    else
-      hipLaunchKernelGGL((k_logprobs<IO, 1024>), grid, dim3(1024), 0, stream, a);
-    return;
+  // several rows a compute unit while there are rows enough, else the most threads a row
+  const bool few = a.N < 2 * device_cus() && groups > 512;
+#define LRS_LP(BT, TOP) hipLaunchKernelGGL((k_logprobs<IO, BT, TOP>), grid, dim3(BT), 0, stream, a)
+  if (a.top > 0) {
+    if (few) LRS_LP(1024, true);
+    else LRS_LP(256, true);
+  } else {
+    if (few) LRS_LP(1024, false);
+    else LRS_LP(256, false);
   }
-#define LRS_LP(BT, NV) hipLaunchKernelGGL((k_logprobs_top<IO, BT, NV>), grid, dim3(BT), 0, stream, a)
-  if (groups <= 256 * 4) LRS_LP(256, 4);
-  else if (groups <= 512 * 4) LRS_LP(512, 4);
-  else if (groups <= 512 * 8) LRS_LP(512, 8);
-  else if (groups <= 1024 * 8) LRS_LP(1024, 8);
-  else if (groups <= 1024 * 16) LRS_LP(1024, 16);
-  else LRS_LP(1024, 0);
 #undef LRS_LP
 }
 
@@ -507,8 +424,9 @@ hipError_t launch_logprobs_fwd(const LogprobArgs& a, int io, hipStream_t stream)
 hipError_t launch_logprobs_bwd(const LogprobArgs& a, int io, hipStream_t stream) {
   const int group = io == kIoBf16 ? 8 : 4;
   const bool nt = 2 * a.N * a.V * (io == kIoBf16 ? 2 : 4) >= kStreamFootprint;
-  // pieces of four to eight groups a thread
-  const int64_t piece = 256 * 8 * group, pieces = (a.V + piece - 1) / piece;
+  // pieces of eight groups a thread; in place one, as a workgroup may read the whole row
+  const int64_t step = 256 * 8 * group, steps = (a.V + step - 1) / step;
+  const int64_t pieces = a.grad_logits == a.logits ? 1 : steps, piece = step * (steps / pieces);
   const dim3 grid((unsigned)a.N, (unsigned)pieces);
 #define LRS_LPB(IO, NT) \
   hipLaunchKernelGGL((k_logprobs_bwd<IO, NT>), grid, dim3(256), 0, stream, a, piece)
