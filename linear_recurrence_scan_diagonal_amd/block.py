@@ -226,7 +226,8 @@ def _rms_inputs(x, gamma, residual, out_sum):
     s = None
     if residual is not None:
         s = torch.empty_like(x) if out_sum is None else out_sum
-        _check_dev("out_sum", s, x.dtype, x.shape)
+        if out_sum is not None:
+            _check_dev("out_sum", s, x.dtype, x.shape)
     return x.numel() // D if D else 0, D, s
 
 
@@ -239,7 +240,8 @@ def rmsnorm_fwd(x, gamma, residual=None, eps: float = 1e-6, save: bool = False, 
     lib = load()
     R, D, s = _rms_inputs(x, gamma, residual, out_sum)
     y = torch.empty_like(x) if out is None else out
-    _check_dev("out", y, x.dtype, x.shape)
+    if out is not None:
+        _check_dev("out", y, x.dtype, x.shape)
     rstd = torch.empty(R, dtype=torch.float32, device=x.device) if save else None
     _call(lib.lrs_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(y), _ptr(s), _ptr(rstd),
                               R, D, float(eps), DTYPES[x.dtype], _stream(x.device)),
@@ -256,9 +258,12 @@ def rmsnorm_fwd_fp8(x, gamma, residual=None, eps: float = 1e-6, group: int = 128
     R, D, s = _rms_inputs(x, gamma, residual, out_sum)
     if group not in (0, 128):
         raise ValueError("group must be 128, or 0 for the whole row")
-    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device) if out is None else out
-    _check_dev("out", q, torch.float8_e4m3fn, x.shape)
-    scales = torch.empty((R, -(-D // group) if group else 1), dtype=torch.float32, device=x.device)
+    if out is None:
+        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    else:
+        q = out
+        _check_dev("out", q, torch.float8_e4m3fn, x.shape)
+    scales = gamma.new_empty((R, -(-D // group) if group else 1))
     _call(lib.lrs_rmsnorm_fwd_fp8(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(q), _ptr(scales),
                                   _ptr(s), R, D, group, float(eps), DTYPES[x.dtype],
                                   _stream(x.device)), "lrs_rmsnorm_fwd_fp8")
