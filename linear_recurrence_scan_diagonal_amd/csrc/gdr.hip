@@ -541,31 +541,36 @@ struct Stage {
   static constexpr int NQ = 2 * kSet / 8 / NT, NM = (kMats / 8 + NT - 1) / NT;
   static_assert(NQ * NT * 8 == 2 * kSet, "whole loads");
   u32x4_t kq[NQ], m[NM];
-  u32x2_t cuts_v;  // the same for all lanes; read where they are used, so that the loads are
-  float keep_v;    // not waited for here
   __device__ __forceinline__ void fetch(const GdrArgs& a, int64_t cb, int h, int hk) {
     const int64_t ch = cb * a.H + h, kh = cb * a.Hk + hk;
-    const uint32_t at = threadIdx.x * 16u;
+    const uint32_t at = (threadIdx.x % NT) * 16u;
     const Buffer fq(a.kq_rows + kh * (2 * kSet), 4 * kSet), fm(a.mats + ch * kGdrMats, 2 * kMats);
 #pragma unroll
     for (int i = 0; i < NQ; ++i) kq[i] = fq.load16(at, i * NT * 16);
 #pragma unroll
     for (int i = 0; i < NM; ++i) m[i] = fm.load16(at + (uint32_t)(i * NT * 16), 0);
-    cuts_v = Buffer(a.cuts + cb, 8).load8(0);
-    Buffer(a.keeps + ch, 4).load(0, keep_v);
-  }
-  __device__ __forceinline__ uint64_t cuts() const {
-    return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(cuts_v.y) << 32 |
-           (uint32_t)__builtin_amdgcn_readfirstlane(cuts_v.x);
   }
   __device__ __forceinline__ void put(char* lds) const {
-    u32x4_t* to = reinterpret_cast<u32x4_t*>(lds) + threadIdx.x;
+    u32x4_t* to = reinterpret_cast<u32x4_t*>(lds) + threadIdx.x % NT;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) to[i * NT] = kq[i];
     to += NQ * NT;
 #pragma unroll
     for (int i = 0; i < NM; ++i)
-      if ((i + 1) * NT <= kMats / 8 || (int)threadIdx.x + i * NT < kMats / 8) to[i * NT] = m[i];
+      if ((i + 1) * NT <= kMats / 8 || (int)(threadIdx.x % NT) + i * NT < kMats / 8) to[i * NT] = m[i];
+  }
+};
+// What a chunk's steps have in common.
+struct Marks {
+  u32x2_t cuts_v;  // the same for all lanes; read where they are used, so that the loads are
+  float keep_v;    // not waited for here
+  __device__ __forceinline__ void fetch(const GdrArgs& a, int64_t cb, int h) {
+    cuts_v = Buffer(a.cuts + cb, 8).load8(0);
+    Buffer(a.keeps + cb * a.H + h, 4).load(0, keep_v);
+  }
+  __device__ __forceinline__ uint64_t cuts() const {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(cuts_v.y) << 32 |
+           (uint32_t)__builtin_amdgcn_readfirstlane(cuts_v.x);
   }
 };
 // A fragment of k^T or q^T (row tile kt of K, steps 32 ks...) from their rows in LDS: the
@@ -594,24 +599,38 @@ struct No {
 // What a chain's wave has.  A workgroup has NW * CB blocks of 16 columns of a head, and four
 // waves for every CB of them; lane l has column r = l % 16 of each.  Wave j of the four has the
 // steps 16 j... of a chunk, and the rows 32 j... of the state (where K <= 64: waves 0 and 1 alone).
+// With two times four waves and one block a wave, the workgroup has one block in all: the
+// first four walk the chain, and the others compute what the chain does not wait for.
+template <int NW, int CB>
+constexpr bool kHelped = NW == 2 && CB == 1;
+// Then the helpers alone bring in the operands, into the other of two buffers, where LDS has
+// room for two.
+template <typename IO, int KP, int NW, int CB>
+constexpr bool kTwo = kHelped<NW, CB> && (sizeof(IO) == 2 || KP == 64);
 struct Wave {
   int64_t bh, b;
   int h, hk, j, block;  // block: the first one, in the workgroup
   int col;              // the lane's column of it
+  bool walks;           // not a helper
   template <int NW, int CB>
   static __device__ __forceinline__ Wave make(const GdrArgs& a) {
-    constexpr int kCols = 16 * NW * CB;
+    constexpr bool HELPED = kHelped<NW, CB>;
+    constexpr int kCols = 16 * (HELPED ? 1 : NW) * CB;
     const uint32_t vblocks = (uint32_t)(a.V + kCols - 1) / kCols;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Wave w;
-    const uint32_t bh = blockIdx.x / vblocks;
+    // workgroups go to the eight XCDs in turn: those of one head to the same, for its L2 cache
+    const uint32_t x = blockIdx.x % 8, some = gridDim.x / 8, more = gridDim.x % 8;
+    const uint32_t n = x * some + (x < more ? x : more) + blockIdx.x / 8;
+    const uint32_t bh = n / vblocks;
     w.bh = bh;
     w.b = bh / (uint32_t)a.H;
     w.h = (int)(bh % (uint32_t)a.H);
     w.hk = w.h / (a.H / a.Hk);
     w.j = wave & 3;
-    w.block = (wave >> 2) * CB;
-    w.col = (int)(blockIdx.x % vblocks) * kCols + w.block * 16 + (threadIdx.x & 15);
+    w.block = HELPED ? 0 : (wave >> 2) * CB;
+    w.walks = !HELPED || wave < 4;
+    w.col = (int)(n % vblocks) * kCols + w.block * 16 + (threadIdx.x & 15);
     return w;
   }
 };
@@ -669,12 +688,12 @@ __device__ __forceinline__ void widen(const IO (&v)[N][4], f32x4_t (&out)[N]) {
 }
 
 // What the four waves of a column block hand each other: the state as a right operand with
-// a scale for every 32 rows, and the 64 steps of two or three vectors in fp32, 16 bytes a
-// lane and wave.
-template <int KS, bool BACK>
+// a scale for every 32 rows, and the 64 steps of VECS vectors in fp32, 16 bytes a lane and
+// wave.
+template <int KS, int VECS>
 struct Exchange {
   static constexpr int kState = KS * 2 * kFrag * 2, kVec = 4 * 64 * 16;
-  static constexpr int kBytes = kState + kVec * (BACK ? 3 : 2) + KS * 16 * 4;
+  static constexpr int kBytes = kState + kVec * VECS + KS * 16 * 4;
   char* base;
   __device__ __forceinline__ uint16_t* state(int ks, int part) const {
     return (uint16_t*)base + (ks * 2 + part) * kFrag + (threadIdx.x & 63) * 8;
@@ -683,7 +702,7 @@ struct Exchange {
     return (f32x4_t*)(base + kState + which * kVec) + j * 64 + (threadIdx.x & 63);
   }
   __device__ __forceinline__ float* down(int ks) const {
-    return (float*)(base + kState + kVec * (BACK ? 3 : 2)) + ks * 16 + (threadIdx.x & 15);
+    return (float*)(base + kState + kVec * VECS) + ks * 16 + (threadIdx.x & 15);
   }
   // the wave's 32 rows of the state
   __device__ __forceinline__ void put_state(const f32x4_t (&S)[2], int j) const {
@@ -777,400 +796,488 @@ __device__ __forceinline__ float vec_operand(const f32x4_t (&v)[4], f16x8_t (&b)
 template <typename IO, int KP, int NW, int CB>
 __global__ __launch_bounds__(256 * NW) void k_gdr_chain(GdrArgs a) {
   constexpr int NP = kParts<IO>, KS = KP / 32;
-  typedef Stage<NP, KS, 256 * NW> St;
-  typedef Exchange<KS, false> X;
-  __shared__ __align__(16) char lds[St::kBytes + NW * CB * X::kBytes];
+  constexpr bool HELPED = kHelped<NW, CB>, TWO = kTwo<IO, KP, NW, CB>;
+  typedef Stage<NP, KS, TWO ? 256 : 256 * NW> St;
+  typedef Exchange<KS, 2> X;
+  constexpr int kOperands = St::kBytes * (TWO ? 2 : 1);
+  __shared__ __align__(16) char lds[kOperands + (HELPED ? 1 : NW) * CB * X::kBytes];
   const int g = (threadIdx.x & 63) >> 4;
   const Wave w = Wave::make<NW, CB>(a);
   X x[CB];
 #pragma unroll
-  for (int c = 0; c < CB; ++c) x[c].base = lds + St::kBytes + (w.block + c) * X::kBytes;
+  for (int c = 0; c < CB; ++c) x[c].base = lds + kOperands + (w.block + c) * X::kBytes;
   const int64_t nc = (a.T + kC - 1) / kC;
   const int64_t sn = (int64_t)a.K * a.V, vrow = (int64_t)a.H * a.V;
   const int vp = (int)saved_pitch(a.V);
   const int64_t cn = (int64_t)(a.K + kC) * vp;  // of a checkpoint
-  const bool owner = w.j < KS;
-  const uint16_t* kf = (const uint16_t*)lds;
-  const uint16_t* qf = kf + St::kSet;
-  const uint16_t* tf = qf + St::kSet;
-  const uint16_t* pf = tf + kTriSet;
-  const float* coef = (const float*)(pf + kTriSet);
 
-  f32x4_t S[CB][2];
+  auto run = [&](auto walks, auto helps) __attribute__((always_inline)) {
+    constexpr bool WALKS = decltype(walks)(), HELPS = decltype(helps)();
+    const bool owner = WALKS && w.j < KS;
+    f32x4_t S[CB][2];
 #pragma unroll
-  for (int c = 0; c < CB; ++c) {
-    float s0[2][4];
-    Rows<float>(a.state0 + w.bh * sn, a.V, a.state0 && owner ? a.K : 0, a.V, w.col + 16 * c, 2 * w.j)
-        .load(s0);
-    widen(s0, S[c]);
-    if (owner) x[c].put_state(S[c], w.j);
-  }
-  St st;
-  IO nv[CB][1][4];  // the next chunk's v
-  // (the address of a chunk behind the last is not read: a length of 0)
-  auto fetch_v = [&](int64_t t) __attribute__((always_inline)) {
-    const int64_t left = a.T - t * kC;
-#pragma unroll
-    for (int c = 0; c < CB; ++c)
-      Rows<IO>((const IO*)a.v + (t * kC * a.B + w.b) * a.ld_v + (int64_t)w.h * a.V, a.B * a.ld_v,
-               left < kC ? left : kC, a.V, w.col + 16 * c, w.j)
-          .load(nv[c]);
-  };
-  fetch_v(0);
-  st.fetch(a, w.b, w.h, w.hk);
-  for (int64_t t = 0; t < nc; ++t) {
-    st.put(lds);
-    const uint64_t cuts = st.cuts();
-    const float keep = st.keep_v;
-    {
-      const int64_t next = t + 1 < nc ? t + 1 : t;
-      st.fetch(a, next * a.B + w.b, w.h, w.hk);
+    for (int c = 0; c < CB; ++c) {
+      float s0[2][4];
+      Rows<float>(a.state0 + w.bh * sn, a.V, a.state0 && owner ? a.K : 0, a.V, w.col + 16 * c, 2 * w.j)
+          .load(s0);
+      widen(s0, S[c]);
+      if (owner) x[c].put_state(S[c], w.j);
     }
-    const int64_t ch = (t * a.B + w.b) * a.H + w.h, left = a.T - t * kC;
-    float* ck = a.checkpoints ? a.checkpoints + ch * cn : nullptr;
-    if (ck && owner) {
+    St st;
+    IO nv[CB][1][4];  // the next chunk's v
+    // (the address of a chunk behind the last is not read: a length of 0)
+    auto fetch_v = [&](int64_t t) __attribute__((always_inline)) {
+      const int64_t left = a.T - t * kC;
 #pragma unroll
-      for (int c = 0; c < CB; ++c) Rows<float>(ck, vp, a.K, vp, w.col + 16 * c, 2 * w.j).store(S[c]);
-    }
-    __syncthreads();
-    f32x4_t R[CB][1];
-
-    // steps [s, e) of the chunk, v in R; FULL: all of them, of a document that goes on
-    auto segment = [&](auto full, int s, int e, bool fresh) __attribute__((always_inline)) {
-      constexpr bool FULL = decltype(full)();
-      auto in = [&](int rt, int i) __attribute__((always_inline)) {
-        const int step = 16 * rt + 4 * g + i;
-        return FULL || (step >= s && step < e);
-      };
-      f32x4_t Q[CB][1], D[CB][1], V[4], y[CB], z[CB];
-      if (FULL || !fresh) times_state<NP, KS, CB, true>(kf, qf, w.j, x, y, z);
-      if (s == 0) {
-#pragma unroll
-        for (int c = 0; c < CB; ++c) widen(nv[c], R[c]);
-        fetch_v(t + 1);
-      }
-      {
-        const f32x4_t ek = coef4(coef, kEnterK, w.j), eq = coef4(coef, kEnterQ, w.j);
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float d = R[c][0][i], q = 0.0f;
-            if (FULL || !fresh) {
-              d = __builtin_fmaf(-ek[i], y[c][i], d);
-              q = eq[i] * z[c][i];
-            }
-            D[c][0][i] = in(w.j, i) ? d : 0.0f;
-            Q[c][0][i] = q;
-          }
-          *x[c].vec(0, w.j) = D[c][0];
-        }
+      for (int c = 0; c < CB; ++c)
+        Rows<IO>((const IO*)a.v + (t * kC * a.B + w.b) * a.ld_v + (int64_t)w.h * a.V, a.B * a.ld_v,
+                 left < kC ? left : kC, a.V, w.col + 16 * c, w.j)
+            .load(nv[c]);
+    };
+    if (WALKS) fetch_v(0);
+    Marks marks;
+    auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+      st.fetch(a, (t < nc ? t : nc - 1) * a.B + w.b, w.h, w.hk);
+    };
+    marks.fetch(a, w.b, w.h);
+    if (!TWO || !WALKS) fetch(0);
+    if constexpr (TWO) {
+      if (!WALKS) {
+        st.put(lds);
+        fetch(1);
       }
       __syncthreads();
-      {  // delta = T2 R, u = beta delta
+    }
+    for (int64_t t = 0; t < nc; ++t) {
+      const int here = TWO && (t & 1) ? St::kBytes : 0;
+      const uint16_t* kf = (const uint16_t*)(lds + here);
+      const uint16_t* qf = kf + St::kSet;
+      const uint16_t* tf = qf + St::kSet;
+      const uint16_t* pf = tf + kTriSet;
+      const float* coef = (const float*)(pf + kTriSet);
+      if constexpr (!TWO) {
+        st.put(lds);
+        fetch(t + 1);
+      }
+      const uint64_t cuts = marks.cuts();
+      const float keep = marks.keep_v;
+      marks.fetch(a, (t + 1 < nc ? t + 1 : t) * a.B + w.b, w.h);
+      const int64_t ch = (t * a.B + w.b) * a.H + w.h, left = a.T - t * kC;
+      float* ck = a.checkpoints ? a.checkpoints + ch * cn : nullptr;
+      if (ck && owner) {
+#pragma unroll
+        for (int c = 0; c < CB; ++c) Rows<float>(ck, vp, a.K, vp, w.col + 16 * c, 2 * w.j).store(S[c]);
+      }
+      if constexpr (!TWO) __syncthreads();
+      f32x4_t R[CB][1];
+
+      // steps [s, e) of the chunk, v in R; FULL: all of them, of a document that goes on
+      auto segment = [&](auto full, int s, int e, bool fresh) __attribute__((always_inline)) {
+        constexpr bool FULL = decltype(full)();
+        auto in = [&](int rt, int i) __attribute__((always_inline)) {
+          const int step = 16 * rt + 4 * g + i;
+          return FULL || (step >= s && step < e);
+        };
+        f32x4_t Q[CB][1], D[CB][1], V[4], y[CB], z[CB];
+        // helpers have q S in y
+        if (FULL || !fresh) times_state<NP, KS, CB, !HELPED>(WALKS ? kf : qf, qf, w.j, x, y, z);
+        if (WALKS && s == 0) {
+#pragma unroll
+          for (int c = 0; c < CB; ++c) widen(nv[c], R[c]);
+          fetch_v(t + 1);
+        }
+        {
+          const f32x4_t ek = coef4(coef, kEnterK, w.j), eq = coef4(coef, kEnterQ, w.j);
+#pragma unroll
+          for (int c = 0; c < CB; ++c) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float d = R[c][0][i], q = 0.0f;
+              if (FULL || !fresh) {
+                d = __builtin_fmaf(-ek[i], y[c][i], d);
+                q = eq[i] * (HELPED ? y : z)[c][i];
+              }
+              D[c][0][i] = in(w.j, i) ? d : 0.0f;
+              Q[c][0][i] = q;
+            }
+            if (WALKS) *x[c].vec(0, w.j) = D[c][0];
+          }
+        }
+        __syncthreads();
+        if constexpr (TWO) {
+          if (!WALKS && s == 0) {  // the chunk before has left the other buffer
+            st.put(lds + (St::kBytes - here));
+            fetch(t + 2);
+          }
+        }
+        if (WALKS) {  // delta = T2 R, u = beta delta
+          f16x8_t b[CB][2][2];
+          float down[CB];
+#pragma unroll
+          for (int c = 0; c < CB; ++c) {
+            x[c].get_vec(0, V);
+            down[c] = vec_operand<2>(V, b[c]);
+            if (CB > 1) fence();
+          }
+          times_tri<false, CB, 2>(tf, w.j, b, y);
+          const f32x4_t rs = coef4(coef, kRowT, w.j), be = coef4(coef, kBeta, w.j);
+#pragma unroll
+          for (int c = 0; c < CB; ++c) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) D[c][0][i] = y[c][i] * (down[c] * rs[i]);
+            if (ck) {
+              const Rows<float> delta(ck + (int64_t)a.K * vp, vp, kC, vp, w.col + 16 * c, w.j);
+              if (FULL) delta.store(D[c]);
+              else delta.store(D[c], s, e);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) D[c][0][i] = in(w.j, i) ? D[c][0][i] * be[i] : 0.0f;
+            *x[c].vec(1, w.j) = D[c][0];
+          }
+        }
+        __syncthreads();
+        // u for o, and for the state; two blocks read it twice, one at a time, to have the registers
         f16x8_t b[CB][2][2];
         float down[CB];
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {
-          x[c].get_vec(0, V);
-          down[c] = vec_operand<2>(V, b[c]);
-          if (CB > 1) fence();
+        if (CB == 1) {
+          x[0].get_vec(1, V);
+          if (HELPS) down[0] = vec_operand<2>(V, b[0]);
         }
-        times_tri<false, CB, 2>(tf, w.j, b, y);
-        const f32x4_t rs = coef4(coef, kRowT, w.j), be = coef4(coef, kBeta, w.j);
+        if (e == kC && owner) {  // the segment that leaves the chunk
+          f16x8_t bl[CB][2][2];
+          float downl[CB];
 #pragma unroll
-        for (int c = 0; c < CB; ++c) {
+          for (int c = 0; c < CB; ++c) {
+            if (CB > 1) x[c].get_vec(1, V);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) D[c][0][i] = y[c][i] * (down[c] * rs[i]);
-          if (ck) {
-            const Rows<float> delta(ck + (int64_t)a.K * vp, vp, kC, vp, w.col + 16 * c, w.j);
-            if (FULL) delta.store(D[c]);
-            else delta.store(D[c], s, e);
+            for (int rt = 0; rt < 4; ++rt) {
+              const f32x4_t lv = coef4(coef, kLeaveK, rt);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) V[rt][i] = in(rt, i) ? V[rt][i] * lv[i] : 0.0f;
+            }
+            downl[c] = vec_operand<2>(V, bl[c]);
+            if (CB > 1) fence();
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) D[c][0][i] = in(w.j, i) ? D[c][0][i] * be[i] : 0.0f;
-          *x[c].vec(1, w.j) = D[c][0];
-        }
-      }
-      __syncthreads();
-      // u for o, and for the state; two blocks read it twice, one at a time, to have the registers
-      f16x8_t b[CB][2][2];
-      float down[CB];
-      if (CB == 1) {
-        x[0].get_vec(1, V);
-        down[0] = vec_operand<2>(V, b[0]);
-      }
-      if (e == kC && owner) {  // the segment that leaves the chunk
-        f16x8_t bl[CB][2][2];
-        float downl[CB];
+          for (int k = 0; k < 2; ++k) {
+            times_cols<NP, KS, CB, FULL>(kf, 2 * w.j + k, bl, s, e, y);
 #pragma unroll
-        for (int c = 0; c < CB; ++c) {
-          if (CB > 1) x[c].get_vec(1, V);
+            for (int c = 0; c < CB; ++c)
 #pragma unroll
-          for (int rt = 0; rt < 4; ++rt) {
-            const f32x4_t lv = coef4(coef, kLeaveK, rt);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) V[rt][i] = in(rt, i) ? V[rt][i] * lv[i] : 0.0f;
+              for (int i = 0; i < 4; ++i)
+                S[c][k][i] = __builtin_fmaf(y[c][i], downl[c], !FULL && fresh ? 0.0f : keep * S[c][k][i]);
+            if (CB > 1) fence();
           }
-          downl[c] = vec_operand<2>(V, bl[c]);
+#pragma unroll
+          for (int c = 0; c < CB; ++c) x[c].put_state(S[c], w.j);
           if (CB > 1) fence();
         }
+        if (CB > 1) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          times_cols<NP, KS, CB, FULL>(kf, 2 * w.j + k, bl, s, e, y);
-#pragma unroll
-          for (int c = 0; c < CB; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              S[c][k][i] = __builtin_fmaf(y[c][i], downl[c], !FULL && fresh ? 0.0f : keep * S[c][k][i]);
-          if (CB > 1) fence();
+          for (int c = 0; c < CB; ++c) {
+            x[c].get_vec(1, V);
+            down[c] = vec_operand<2>(V, b[c]);
+            fence();
+          }
         }
-#pragma unroll
-        for (int c = 0; c < CB; ++c) x[c].put_state(S[c], w.j);
-        if (CB > 1) fence();
-      }
-      if (CB > 1) {
+        if (!HELPS) return;
+        times_tri<false, CB, 2>(pf, w.j, b, y);
+        const f32x4_t rs = coef4(coef, kRowP, w.j);
 #pragma unroll
         for (int c = 0; c < CB; ++c) {
-          x[c].get_vec(1, V);
-          down[c] = vec_operand<2>(V, b[c]);
-          fence();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            Q[c][0][i] = __builtin_fmaf(y[c][i], down[c] * (rs[i] * a.scale), Q[c][0][i]);
+          const Rows<IO> out((const IO*)a.o + (t * kC * a.B + w.b) * vrow + (int64_t)w.h * a.V, a.B * vrow,
+                             left < kC ? left : kC, a.V, w.col + 16 * c, w.j);
+          if (FULL) out.store(Q[c]);
+          else out.store(Q[c], s, e);
         }
-      }
-      times_tri<false, CB, 2>(pf, w.j, b, y);
-      const f32x4_t rs = coef4(coef, kRowP, w.j);
-#pragma unroll
-      for (int c = 0; c < CB; ++c) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          Q[c][0][i] = __builtin_fmaf(y[c][i], down[c] * (rs[i] * a.scale), Q[c][0][i]);
-        const Rows<IO> out((const IO*)a.o + (t * kC * a.B + w.b) * vrow + (int64_t)w.h * a.V, a.B * vrow,
-                           left < kC ? left : kC, a.V, w.col + 16 * c, w.j);
-        if (FULL) out.store(Q[c]);
-        else out.store(Q[c], s, e);
-      }
-    };
-    if (cuts == 0) {
-      segment(Yes(), 0, kC, false);
-    } else {
+      };
+      if (cuts == 0) {
+        segment(Yes(), 0, kC, false);
+      } else {
 #pragma unroll 1
-      for (int s = 0; s < kC;) {
-        const int e = seg_end(cuts, s);
-        segment(No(), s, e, (cuts >> s) & 1);
-        s = e;
+        for (int s = 0; s < kC;) {
+          const int e = seg_end(cuts, s);
+          segment(No(), s, e, (cuts >> s) & 1);
+          s = e;
+        }
       }
+      __syncthreads();  // the next state and operands are there, and these may be written over
     }
-    __syncthreads();  // before the next chunk's operands are put over these
-  }
-  if (a.state && owner) {
+    if (a.state && owner) {
 #pragma unroll
-    for (int c = 0; c < CB; ++c)
-      Rows<float>(a.state + w.bh * sn, a.V, a.K, a.V, w.col + 16 * c, 2 * w.j).store(S[c]);
-  }
+      for (int c = 0; c < CB; ++c)
+        Rows<float>(a.state + w.bh * sn, a.V, a.K, a.V, w.col + 16 * c, 2 * w.j).store(S[c]);
+    }
+  };
+  // code of their own, with as many barriers
+  if constexpr (!HELPED) run(Yes(), Yes());
+  else if (w.walks) run(Yes(), No());
+  else run(No(), Yes());
 }
 
 // The chain in reverse: dS, and w, dv and every chunk's dS on the way.
 template <typename IO, int KP, int NW, int CB>
 __global__ __launch_bounds__(256 * NW) void k_gdr_back(GdrArgs a) {
   constexpr int NP = kParts<IO>, KS = KP / 32;
-  typedef Stage<NP, KS, 256 * NW> St;
-  typedef Exchange<KS, true> X;
-  __shared__ __align__(16) char lds[St::kBytes + NW * CB * X::kBytes];
+  constexpr bool HELPED = kHelped<NW, CB>, TWO = kTwo<IO, KP, NW, CB>;
+  typedef Stage<NP, KS, TWO ? 256 : 256 * NW> St;
+  // with helpers also their part of du, and of dS: two vectors' room
+  typedef Exchange<KS, HELPED ? 6 : 3> X;
+  constexpr int kOperands = St::kBytes * (TWO ? 2 : 1);
+  __shared__ __align__(16) char lds[kOperands + (HELPED ? 1 : NW) * CB * X::kBytes];
   const int g = (threadIdx.x & 63) >> 4;
   const Wave w = Wave::make<NW, CB>(a);
   X x[CB];
 #pragma unroll
-  for (int c = 0; c < CB; ++c) x[c].base = lds + St::kBytes + (w.block + c) * X::kBytes;
+  for (int c = 0; c < CB; ++c) x[c].base = lds + kOperands + (w.block + c) * X::kBytes;
   const int64_t nc = (a.T + kC - 1) / kC;
   const int64_t sn = (int64_t)a.K * a.V, vrow = (int64_t)a.H * a.V;
   const int vp = (int)saved_pitch(a.V);
-  const bool owner = w.j < KS;
-  const uint16_t* kf = (const uint16_t*)lds;
-  const uint16_t* qf = kf + St::kSet;
-  const uint16_t* tf = qf + St::kSet;
-  const uint16_t* pf = tf + kTriSet;
-  const float* coef = (const float*)(pf + kTriSet);
 
-  f32x4_t S[CB][2];  // dS
-  IO ng[CB][1][4];   // the next chunk's grad_o
-  auto fetch_o = [&](int64_t t) __attribute__((always_inline)) {
-    const int64_t left = a.T - t * kC;
-#pragma unroll
-    for (int c = 0; c < CB; ++c)
-      Rows<IO>((const IO*)a.grad_o + (t * kC * a.B + w.b) * vrow + (int64_t)w.h * a.V, a.B * vrow,
-               left < kC ? left : kC, a.V, w.col + 16 * c, w.j)
-          .load(ng[c]);
-  };
-  auto put_o = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int c = 0; c < CB; ++c) {
-      f32x4_t go[1];
-      widen(ng[c], go);
-      *x[c].vec(2, w.j) = go[0];
-    }
-  };
-  St st;
-  fetch_o(nc - 1);
-  st.fetch(a, (nc - 1) * a.B + w.b, w.h, w.hk);
-#pragma unroll
-  for (int c = 0; c < CB; ++c) {
-    float s0[2][4];
-    Rows<float>(a.grad_state + w.bh * sn, a.V, a.grad_state && owner ? a.K : 0, a.V, w.col + 16 * c,
-                2 * w.j)
-        .load(s0);
-    widen(s0, S[c]);
-    if (owner) x[c].put_state(S[c], w.j);
-  }
-  put_o();
-  for (int64_t t = nc - 1; t >= 0; --t) {
-    st.put(lds);
-    const uint64_t cuts = st.cuts();
-    const float keep = st.keep_v;
-    {
-      const int64_t next = t > 0 ? t - 1 : 0;
-      fetch_o(next);
-      st.fetch(a, next * a.B + w.b, w.h, w.hk);
-    }
-    const int64_t ch = (t * a.B + w.b) * a.H + w.h, left = a.T - t * kC;
-    if (owner) {
+  auto run = [&](auto walks, auto helps) __attribute__((always_inline)) {
+    constexpr bool WALKS = decltype(walks)(), HELPS = decltype(helps)();
+    const bool owner = WALKS && w.j < KS;
+    f32x4_t S[CB][2];  // dS
+    IO ng[CB][1][4];   // the next chunk's grad_o
+    auto fetch_o = [&](int64_t t) __attribute__((always_inline)) {
+      const int64_t left = a.T - t * kC;
 #pragma unroll
       for (int c = 0; c < CB; ++c)
-        Rows<float>(a.grad_states + ch * a.K * vp, vp, a.K, vp, w.col + 16 * c, 2 * w.j).store(S[c]);
-    }
-    __syncthreads();
-
-    auto segment = [&](auto full, int s, int e, bool fresh) __attribute__((always_inline)) {
-      constexpr bool FULL = decltype(full)();
-      auto in = [&](int rt, int i) __attribute__((always_inline)) {
-        const int step = 16 * rt + 4 * g + i;
-        return FULL || (step >= s && step < e);
-      };
-      f32x4_t D[CB][1], dO[CB][4], V[4], y[CB], z[CB];
-      {  // du = scale P^T do + exp(G_C - G) K dS
-        f16x8_t b[CB][2][NP];
-        float down[CB];
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {
-          x[c].get_vec(2, dO[c]);
-#pragma unroll
-          for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dO[c][rt][i] = in(rt, i) ? dO[c][rt][i] : 0.0f;
-          down[c] = vec_operand<NP>(dO[c], b[c]);
-          if (CB > 1) fence();
-        }
-        times_tri<true, CB, NP>(pf, w.j, b, y);
-        const f32x4_t rs = coef4(coef, kRowP, w.j);
-#pragma unroll
-        for (int c = 0; c < CB; ++c)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) D[c][0][i] = y[c][i] * (down[c] * (rs[i] * a.scale));
-      }
-      if (e == kC) {
-        times_state<NP, KS, CB, false>(kf, nullptr, w.j, x, y, z);
-        const f32x4_t lv = coef4(coef, kLeaveK, w.j);
-#pragma unroll
-        for (int c = 0; c < CB; ++c)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) D[c][0][i] = __builtin_fmaf(y[c][i], lv[i], D[c][0][i]);
-      }
+        Rows<IO>((const IO*)a.grad_o + (t * kC * a.B + w.b) * vrow + (int64_t)w.h * a.V, a.B * vrow,
+                 left < kC ? left : kC, a.V, w.col + 16 * c, w.j)
+            .load(ng[c]);
+    };
+    auto put_o = [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int c = 0; c < CB; ++c) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) D[c][0][i] = in(w.j, i) ? D[c][0][i] : 0.0f;
-        *x[c].vec(0, w.j) = D[c][0];
-      }
-      __syncthreads();
-      {  // w = T^T du, dv = beta w
-        f16x8_t b[CB][2][2];
-        float down[CB];
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {
-          x[c].get_vec(0, V);
-          down[c] = vec_operand<2>(V, b[c]);
-          if (CB > 1) fence();
-        }
-        times_tri<true, CB, 2>(tf, w.j, b, y);
-        const f32x4_t rs = coef4(coef, kRowT, w.j), be = coef4(coef, kBeta, w.j);
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) D[c][0][i] = y[c][i] * (down[c] * rs[i]);
-          const Rows<float> wout(a.w + ch * kC * vp, vp, kC, vp, w.col + 16 * c, w.j);
-          if (FULL) wout.store(D[c]);
-          else wout.store(D[c], s, e);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) D[c][0][i] = in(w.j, i) ? D[c][0][i] * be[i] : 0.0f;
-          *x[c].vec(1, w.j) = D[c][0];
-          const Rows<IO> vout((const IO*)a.grad_v + (t * kC * a.B + w.b) * a.ld_gv + (int64_t)w.h * a.V,
-                              a.B * a.ld_gv, left < kC ? left : kC, a.V, w.col + 16 * c, w.j);
-          if (FULL) vout.store(D[c]);
-          else vout.store(D[c], s, e);
-        }
-      }
-      __syncthreads();
-      if (!owner) return;
-      if (!FULL && fresh) {
-#pragma unroll
-        for (int c = 0; c < CB; ++c) S[c][0] = S[c][1] = kZero4;
-        return;
-      }
-      // dS0 = exp(G_C) dS (of the last segment) + (exp G q)^T do' - (exp G k)^T dv
-      f16x8_t xb[CB][2][2], yb[CB][2][2];
-      float dx[CB], dy[CB];
-#pragma unroll
-      for (int c = 0; c < CB; ++c) {
-        x[c].get_vec(1, V);
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          const f32x4_t eq = coef4(coef, kEnterQ, rt), ek = coef4(coef, kEnterK, rt);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            dO[c][rt][i] = in(rt, i) ? dO[c][rt][i] * eq[i] : 0.0f;
-            V[rt][i] = in(rt, i) ? V[rt][i] * ek[i] : 0.0f;
-          }
-        }
-        dx[c] = vec_operand<2>(dO[c], xb[c]);
-        dy[c] = vec_operand<2>(V, yb[c]);
-        if (CB > 1) fence();
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        times_cols<NP, KS, CB, FULL>(qf, 2 * w.j + k, xb, s, e, y);
-        times_cols<NP, KS, CB, FULL>(kf, 2 * w.j + k, yb, s, e, z);
-#pragma unroll
-        for (int c = 0; c < CB; ++c)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            S[c][k][i] = __builtin_fmaf(y[c][i], dx[c],
-                                        __builtin_fmaf(-z[c][i], dy[c],
-                                                       FULL || e == kC ? keep * S[c][k][i] : 0.0f));
-        if (CB > 1) fence();
+        f32x4_t go[1];
+        widen(ng[c], go);
+        *x[c].vec(2, w.j) = go[0];
       }
     };
-    if (cuts == 0) {
-      segment(Yes(), 0, kC, false);
-    } else {
-#pragma unroll 1
-      for (int e = kC; e > 0;) {
-        const int s = seg_start(cuts, e - 1);
-        segment(No(), s, e, (cuts >> s) & 1);
-        e = s;
+    St st;
+    if (WALKS) fetch_o(nc - 1);
+    Marks marks;
+    auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+      st.fetch(a, (t > 0 ? t : 0) * a.B + w.b, w.h, w.hk);
+    };
+    marks.fetch(a, (nc - 1) * a.B + w.b, w.h);
+    if (!TWO || !WALKS) fetch(nc - 1);
+#pragma unroll
+    for (int c = 0; c < CB; ++c) {
+      float s0[2][4];
+      Rows<float>(a.grad_state + w.bh * sn, a.V, a.grad_state && owner ? a.K : 0, a.V, w.col + 16 * c,
+                  2 * w.j)
+          .load(s0);
+      widen(s0, S[c]);
+      if (owner) x[c].put_state(S[c], w.j);
+    }
+    if (WALKS) put_o();
+    if constexpr (TWO) {
+      if (!WALKS) {
+        st.put(lds + ((nc - 1) & 1) * St::kBytes);
+        fetch(nc - 2);
       }
+      __syncthreads();
     }
-    // the state was read before the chunk's first barrier, grad_o before its last segment's
-    if (owner) {
+    for (int64_t t = nc - 1; t >= 0; --t) {
+      const int here = TWO && (t & 1) ? St::kBytes : 0;
+      const uint16_t* kf = (const uint16_t*)(lds + here);
+      const uint16_t* qf = kf + St::kSet;
+      const uint16_t* tf = qf + St::kSet;
+      const uint16_t* pf = tf + kTriSet;
+      const float* coef = (const float*)(pf + kTriSet);
+      if constexpr (!TWO) st.put(lds);
+      const uint64_t cuts = marks.cuts();
+      const float keep = marks.keep_v;
+      const int64_t next = t > 0 ? t - 1 : 0;
+      if (WALKS) fetch_o(next);
+      if constexpr (!TWO) fetch(next);
+      marks.fetch(a, next * a.B + w.b, w.h);
+      const int64_t ch = (t * a.B + w.b) * a.H + w.h, left = a.T - t * kC;
+      if (owner) {
 #pragma unroll
-      for (int c = 0; c < CB; ++c) x[c].put_state(S[c], w.j);
+        for (int c = 0; c < CB; ++c)
+          Rows<float>(a.grad_states + ch * a.K * vp, vp, a.K, vp, w.col + 16 * c, 2 * w.j).store(S[c]);
+      }
+      if constexpr (!TWO) __syncthreads();
+
+      auto segment = [&](auto full, int s, int e, bool fresh) __attribute__((always_inline)) {
+        constexpr bool FULL = decltype(full)();
+        auto in = [&](int rt, int i) __attribute__((always_inline)) {
+          const int step = 16 * rt + 4 * g + i;
+          return FULL || (step >= s && step < e);
+        };
+        f32x4_t D[CB][1], dO[CB][4], V[4], y[CB], z[CB];
+        if (HELPS) {  // du = scale P^T do + exp(G_C - G) K dS
+          f16x8_t b[CB][2][NP];
+          float down[CB];
+#pragma unroll
+          for (int c = 0; c < CB; ++c) {
+            x[c].get_vec(2, dO[c]);
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) dO[c][rt][i] = in(rt, i) ? dO[c][rt][i] : 0.0f;
+            down[c] = vec_operand<NP>(dO[c], b[c]);
+            if (CB > 1) fence();
+          }
+          times_tri<true, CB, NP>(pf, w.j, b, y);
+          const f32x4_t rs = coef4(coef, kRowP, w.j);
+#pragma unroll
+          for (int c = 0; c < CB; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) D[c][0][i] = y[c][i] * (down[c] * (rs[i] * a.scale));
+          if constexpr (HELPED) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) D[0][0][i] = in(w.j, i) ? D[0][0][i] : 0.0f;
+            *x[0].vec(3, w.j) = D[0][0];
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < CB; ++c) D[c][0] = kZero4;
+        }
+        if (WALKS && e == kC) {
+          times_state<NP, KS, CB, false>(kf, nullptr, w.j, x, y, z);
+          const f32x4_t lv = coef4(coef, kLeaveK, w.j);
+#pragma unroll
+          for (int c = 0; c < CB; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) D[c][0][i] = __builtin_fmaf(y[c][i], lv[i], D[c][0][i]);
+        }
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) D[c][0][i] = in(w.j, i) ? D[c][0][i] : 0.0f;
+          if (WALKS) *x[c].vec(0, w.j) = D[c][0];
+        }
+        __syncthreads();
+        if constexpr (HELPED) {
+          if (!WALKS && w.j < KS && !(!FULL && fresh)) {  // (exp G q)^T do', 32 rows
+            f16x8_t b[1][2][2];
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+              const f32x4_t eq = coef4(coef, kEnterQ, rt);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) dO[0][rt][i] = in(rt, i) ? dO[0][rt][i] * eq[i] : 0.0f;
+            }
+            const float down = vec_operand<2>(dO[0], b[0]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              times_cols<NP, KS, 1, FULL>(qf, 2 * w.j + k, b, s, e, y);
+              *x[0].vec(4 + k, w.j) = y[0] * down;
+            }
+          }
+        }
+        if (WALKS) {  // w = T^T du, dv = beta w
+          f16x8_t b[CB][2][2];
+          float down[CB];
+#pragma unroll
+          for (int c = 0; c < CB; ++c) {
+            x[c].get_vec(0, V);
+            if constexpr (HELPED) {
+#pragma unroll
+              for (int rt = 0; rt < 4; ++rt) V[rt] += *x[c].vec(3, rt);
+            }
+            down[c] = vec_operand<2>(V, b[c]);
+            if (CB > 1) fence();
+          }
+          times_tri<true, CB, 2>(tf, w.j, b, y);
+          const f32x4_t rs = coef4(coef, kRowT, w.j), be = coef4(coef, kBeta, w.j);
+#pragma unroll
+          for (int c = 0; c < CB; ++c) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) D[c][0][i] = y[c][i] * (down[c] * rs[i]);
+            const Rows<float> wout(a.w + ch * kC * vp, vp, kC, vp, w.col + 16 * c, w.j);
+            if (FULL) wout.store(D[c]);
+            else wout.store(D[c], s, e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) D[c][0][i] = in(w.j, i) ? D[c][0][i] * be[i] : 0.0f;
+            *x[c].vec(1, w.j) = D[c][0];
+            const Rows<IO> vout((const IO*)a.grad_v + (t * kC * a.B + w.b) * a.ld_gv + (int64_t)w.h * a.V,
+                                a.B * a.ld_gv, left < kC ? left : kC, a.V, w.col + 16 * c, w.j);
+            if (FULL) vout.store(D[c]);
+            else vout.store(D[c], s, e);
+          }
+        }
+        __syncthreads();
+        if constexpr (TWO) {
+          if (!WALKS && e == kC) {  // the chunk behind has left the other buffer
+            st.put(lds + (St::kBytes - here));
+            fetch(t - 2);
+          }
+        }
+        if (!owner) return;
+        if (!FULL && fresh) {
+#pragma unroll
+          for (int c = 0; c < CB; ++c) S[c][0] = S[c][1] = kZero4;
+          return;
+        }
+        // dS0 = exp(G_C) dS (of the last segment) + (exp G q)^T do' - (exp G k)^T dv
+        f16x8_t xb[CB][2][2], yb[CB][2][2];
+        float dx[CB], dy[CB];
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+          x[c].get_vec(1, V);
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) {
+            const f32x4_t eq = coef4(coef, kEnterQ, rt), ek = coef4(coef, kEnterK, rt);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (!HELPED) dO[c][rt][i] = in(rt, i) ? dO[c][rt][i] * eq[i] : 0.0f;
+              V[rt][i] = in(rt, i) ? V[rt][i] * ek[i] : 0.0f;
+            }
+          }
+          dx[c] = HELPED ? 1.0f : vec_operand<2>(dO[c], xb[c]);
+          dy[c] = vec_operand<2>(V, yb[c]);
+          if (CB > 1) fence();
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if constexpr (HELPED) y[0] = *x[0].vec(4 + k, w.j);
+          else times_cols<NP, KS, CB, FULL>(qf, 2 * w.j + k, xb, s, e, y);
+          times_cols<NP, KS, CB, FULL>(kf, 2 * w.j + k, yb, s, e, z);
+#pragma unroll
+          for (int c = 0; c < CB; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              S[c][k][i] = __builtin_fmaf(y[c][i], dx[c],
+                                          __builtin_fmaf(-z[c][i], dy[c],
+                                                         FULL || e == kC ? keep * S[c][k][i] : 0.0f));
+          if (CB > 1) fence();
+        }
+      };
+      if (cuts == 0) {
+        segment(Yes(), 0, kC, false);
+      } else {
+#pragma unroll 1
+        for (int e = kC; e > 0;) {
+          const int s = seg_start(cuts, e - 1);
+          segment(No(), s, e, (cuts >> s) & 1);
+          e = s;
+        }
+      }
+      // the state was read before the chunk's first barrier, grad_o before its last segment's
+      if (owner) {
+#pragma unroll
+        for (int c = 0; c < CB; ++c) x[c].put_state(S[c], w.j);
+      }
+      if (WALKS) put_o();
+      __syncthreads();  // the next state and operands are there, and these may be written over
     }
-    put_o();
-    __syncthreads();  // before the next chunk's operands are put over these
-  }
-  if (a.grad_state0 && owner) {
+    if (a.grad_state0 && owner) {
 #pragma unroll
-    for (int c = 0; c < CB; ++c)
-      Rows<float>(a.grad_state0 + w.bh * sn, a.V, a.K, a.V, w.col + 16 * c, 2 * w.j).store(S[c]);
-  }
+      for (int c = 0; c < CB; ++c)
+        Rows<float>(a.grad_state0 + w.bh * sn, a.V, a.K, a.V, w.col + 16 * c, 2 * w.j).store(S[c]);
+    }
+  };
+  // code of their own, with as many barriers
+  if constexpr (!HELPED) run(Yes(), Yes());
+  else if (w.walks) run(Yes(), No());
+  else run(No(), Yes());
 }
 
 // ---------------------------------------------------------------------------
@@ -1716,8 +1823,8 @@ __global__ __launch_bounds__(256) void k_gdr_step(GdrArgs a, const int32_t* __re
 }
 
 // Column blocks of a chain's workgroup, two a wave: four, which read a chunk's operands
-// together and hide each other's waits, while every compute unit has a workgroup; else one,
-// for the shortest chunk.
+// together and hide each other's waits, while every compute unit has a workgroup; else one
+// and four more waves that help it, for the shortest chunk.
 template <typename F>
 void chain_shape(const GdrArgs& a, bool most_four, F launch) {
   const int64_t heads = a.B * a.H, cus = device_cus();
@@ -1733,7 +1840,7 @@ hipError_t gdr_fwd(const GdrArgs& a, hipStream_t stream) {
   chain_shape(a, true, [&](int n, dim3 grid) {
     if (n == 4) hipLaunchKernelGGL((k_gdr_chain<IO, KP, 2, 2>), grid, dim3(512), 0, stream, a);
     else if (n == 2) hipLaunchKernelGGL((k_gdr_chain<IO, KP, 1, 2>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((k_gdr_chain<IO, KP, 1, 1>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((k_gdr_chain<IO, KP, 2, 1>), grid, dim3(512), 0, stream, a);
   });
   return hipGetLastError();
 }
@@ -1750,7 +1857,7 @@ hipError_t gdr_bwd(const GdrArgs& a, hipStream_t stream) {
     else if (n == 2)
       hipLaunchKernelGGL((k_gdr_back<IO, KP, 1, 2>), grid, dim3(256), 0, stream, a);
     else
-      hipLaunchKernelGGL((k_gdr_back<IO, KP, 1, 1>), grid, dim3(256), 0, stream, a);
+      hipLaunchKernelGGL((k_gdr_back<IO, KP, 2, 1>), grid, dim3(512), 0, stream, a);
   });
   const dim3 groups((unsigned)(nc * a.B * a.H));
   if (quads<IO>(a.grad_o, 0, a.V))
