@@ -568,6 +568,9 @@ struct Marks {
     cuts_v = Buffer(a.cuts + cb, 8).load8(0);
     Buffer(a.keeps + cb * a.H + h, 4).load(0, keep_v);
   }
+  __device__ __forceinline__ float keep() const {
+    return as_f32((uint32_t)__builtin_amdgcn_readfirstlane((int)as_u32(keep_v)));
+  }
   __device__ __forceinline__ uint64_t cuts() const {
     return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(cuts_v.y) << 32 |
            (uint32_t)__builtin_amdgcn_readfirstlane(cuts_v.x);
@@ -860,7 +863,7 @@ __global__ __launch_bounds__(256 * NW) void k_gdr_chain(GdrArgs a) {
         fetch(t + 1);
       }
       const uint64_t cuts = marks.cuts();
-      const float keep = marks.keep_v;
+      const float keep = marks.keep();
       marks.fetch(a, (t + 1 < nc ? t + 1 : t) * a.B + w.b, w.h);
       const int64_t ch = (t * a.B + w.b) * a.H + w.h, left = a.T - t * kC;
       float* ck = a.checkpoints ? a.checkpoints + ch * cn : nullptr;
@@ -870,6 +873,22 @@ __global__ __launch_bounds__(256 * NW) void k_gdr_chain(GdrArgs a) {
       }
       if constexpr (!TWO) __syncthreads();
       f32x4_t R[CB][1];
+      // The next chunk's v.  Two blocks have no registers for it before the first product.
+      auto take_v = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int c = 0; c < CB; ++c) widen(nv[c], R[c]);
+        fetch_v(t + 1);
+      };
+      if (WALKS && CB == 1) take_v();
+
+      // The next chunk's operands, into the buffer that the chunk before has left; where o is
+      // not yet written, as the loads are waited for in order with the stores.
+      auto bring = [&]() __attribute__((always_inline)) {
+        if constexpr (TWO && !WALKS) {
+          st.put(lds + (St::kBytes - here));
+          fetch(t + 2);
+        }
+      };
 
       // steps [s, e) of the chunk, v in R; FULL: all of them, of a document that goes on
       auto segment = [&](auto full, int s, int e, bool fresh) __attribute__((always_inline)) {
@@ -881,11 +900,7 @@ __global__ __launch_bounds__(256 * NW) void k_gdr_chain(GdrArgs a) {
         f32x4_t Q[CB][1], D[CB][1], V[4], y[CB], z[CB];
         // helpers have q S in y
         if (FULL || !fresh) times_state<NP, KS, CB, !HELPED>(WALKS ? kf : qf, qf, w.j, x, y, z);
-        if (WALKS && s == 0) {
-#pragma unroll
-          for (int c = 0; c < CB; ++c) widen(nv[c], R[c]);
-          fetch_v(t + 1);
-        }
+        if (WALKS && CB > 1 && s == 0) take_v();
         {
           const f32x4_t ek = coef4(coef, kEnterK, w.j), eq = coef4(coef, kEnterQ, w.j);
 #pragma unroll
@@ -904,12 +919,7 @@ __global__ __launch_bounds__(256 * NW) void k_gdr_chain(GdrArgs a) {
           }
         }
         __syncthreads();
-        if constexpr (TWO) {
-          if (!WALKS && s == 0) {  // the chunk before has left the other buffer
-            st.put(lds + (St::kBytes - here));
-            fetch(t + 2);
-          }
-        }
+        if constexpr (FULL) bring();
         if (WALKS) {  // delta = T2 R, u = beta delta
           f16x8_t b[CB][2][2];
           float down[CB];
@@ -1003,6 +1013,7 @@ __global__ __launch_bounds__(256 * NW) void k_gdr_chain(GdrArgs a) {
           segment(No(), s, e, (cuts >> s) & 1);
           s = e;
         }
+        bring();
       }
       __syncthreads();  // the next state and operands are there, and these may be written over
     }
@@ -1092,7 +1103,7 @@ __global__ __launch_bounds__(256 * NW) void k_gdr_back(GdrArgs a) {
       const float* coef = (const float*)(pf + kTriSet);
       if constexpr (!TWO) st.put(lds);
       const uint64_t cuts = marks.cuts();
-      const float keep = marks.keep_v;
+      const float keep = marks.keep();
       const int64_t next = t > 0 ? t - 1 : 0;
       if (WALKS) fetch_o(next);
       if constexpr (!TWO) fetch(next);
@@ -1204,12 +1215,6 @@ __global__ __launch_bounds__(256 * NW) void k_gdr_back(GdrArgs a) {
           }
         }
         __syncthreads();
-        if constexpr (TWO) {
-          if (!WALKS && e == kC) {  // the chunk behind has left the other buffer
-            st.put(lds + (St::kBytes - here));
-            fetch(t - 2);
-          }
-        }
         if (!owner) return;
         if (!FULL && fresh) {
 #pragma unroll
@@ -1266,6 +1271,10 @@ __global__ __launch_bounds__(256 * NW) void k_gdr_back(GdrArgs a) {
         for (int c = 0; c < CB; ++c) x[c].put_state(S[c], w.j);
       }
       if (WALKS) put_o();
+      if constexpr (TWO && !WALKS) {  // the chunk behind has left the other buffer
+        st.put(lds + (St::kBytes - here));
+        fetch(t - 2);
+      }
       __syncthreads();  // the next state and operands are there, and these may be written over
     }
     if (a.grad_state0 && owner) {
