@@ -19,6 +19,13 @@
 // candidates, and the first 128 places, among which are enough of the others.  Rows with
 // more candidates than the LDS holds (many equal values over 1024 threads, or a NaN) are
 // read `top` times again, each time for the largest below the one before.
+//
+// Measured: 8192 x 32768 bf16 with 20 alternatives 150 to 157 us (3.6 TB/s: eight exponentials
+// for 16 bytes, beside the loads); 4099 x 50021 fp32 forward 146 us (5.6 TB/s), backward
+// 306 us (5.4 TB/s);
+// 64 x 32000 bf16 with 8 alternatives 13.9 us: a row's 16 waves' loads, sums, ranks and a
+// second reading one behind the other (12.2 with the row kept in registers, which took up
+// to 193 us at 8192 rows).
 #include "lrs_device.hpp"
 #include "lrs_internal.hpp"
 #include "lrs_rows.hpp"
@@ -400,7 +407,8 @@ template <typename IO>
 void logprobs(const LogprobArgs& a, hipStream_t stream) {
   const int64_t groups = (a.V + kGroup<IO> - 1) / kGroup<IO>;
   const dim3 grid((unsigned)a.N);
-  // several rows a compute unit while there are rows enough, else the most threads a row
+  // Several rows a compute unit while there are rows enough, else the most threads a row:
+  // 64 x 32000 takes 13.9 us with 1024 threads, 14.7 with 512.
   const bool few = a.N < 2 * device_cus() && groups > 512;
 #define LRS_LP(BT, TOP) hipLaunchKernelGGL((k_logprobs<IO, BT, TOP>), grid, dim3(BT), 0, stream, a)
   if (a.top > 0) {
