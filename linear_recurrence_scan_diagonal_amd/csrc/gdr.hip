@@ -1839,13 +1839,19 @@ __global__ __launch_bounds__(256) void k_gdr_step(GdrArgs a, const int32_t* __re
   }
 }
 
-// Column blocks of a chain's workgroup, two a wave: four, which read a chunk's operands
-// together and hide each other's waits, while every compute unit has a workgroup; else one
-// and four more waves that help it, for the shortest chunk.
+// Column blocks of a chain's workgroup: one with helpers, for the shortest chunk, while every
+// workgroup has a compute unit of its own, then two, then four (two a wave), which read a
+// chunk's operands together and hide each other's waits.  Forward / backward of 1024 steps with K
+// = V = 128, bf16, in us a call:
+//   heads      one        two        four
+//   32       64 / 126   95 / 165  108 / 189
+//   64      110 / 238  107 / 250  119 / 268
+//   96      160 / 356  191 / 412  133 / 353
+//   128     212 / 483  206 / 493  150 / 433
 template <typename F>
 void chain_shape(const GdrArgs& a, bool most_four, F launch) {
   const int64_t heads = a.B * a.H, cus = device_cus();
-  const int n = heads * ((a.V + 63) / 64) >= cus && most_four ? 4 : heads * ((a.V + 31) / 32) >= cus ? 2 : 1;
+  const int n = heads * ((a.V + 15) / 16) <= cus ? 1 : heads * ((a.V + 31) / 32) <= cus || !most_four ? 2 : 4;
   launch(n, dim3((unsigned)(heads * ((a.V + 16 * n - 1) / (16 * n)))));
 }
 
