@@ -1310,6 +1310,21 @@ __device__ __forceinline__ float row16_sum(float v) {
 #undef LRS_ROR
   return v;
 }
+__device__ __forceinline__ double row16_sum(double v) {
+#define LRS_ROR(N)                                                                              \
+  {                                                                                             \
+    const u32x2_t u = __builtin_bit_cast(u32x2_t, v);                                           \
+    const u32x2_t x = {(uint32_t)__builtin_amdgcn_update_dpp(0, (int)u.x, 0x120 + N, 0xf, 0xf, false), \
+                       (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u.y, 0x120 + N, 0xf, 0xf, false)}; \
+    v += __builtin_bit_cast(double, x);                                                         \
+  }
+  LRS_ROR(8)
+  LRS_ROR(4)
+  LRS_ROR(2)
+  LRS_ROR(1)
+#undef LRS_ROR
+  return v;
+}
 
 constexpr int kVB = 32;  // columns of V at a time
 
@@ -1323,8 +1338,8 @@ __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
   constexpr int kBlock = (4 * NP + 16 + 4 * KT) * kFrag * 2, kMats = 2 * (int)sizeof(Mat) + 2 * kSet * 2;
   __shared__ __align__(16) char big[kBlock > kMats ? kBlock : kMats];
   __shared__ float ro[kC], rw[kC], rd[kC], rs[KP], rg[KP], bt[kC], gam[kC], tail[kC], rkk[kC], rkq[kC];
-  __shared__ float row_e[2][kC], row_t[2][kC], col_e[4][kC], rx[kC], rz[kC], rt_s[kC], dots[8], bsum[kC];
-  __shared__ double gs[kC];
+  __shared__ float row_t[2][kC], rx[kC], rz[kC], rt_s[kC], dots[8], bsum[kC];
+  __shared__ double gs[kC], row_e[2][kC], col_e[4][kC];
   uint16_t* of = (uint16_t*)big;
   uint16_t* wf = of + 4 * NP * kFrag;
   uint16_t* df = wf + 8 * kFrag;
@@ -1481,7 +1496,8 @@ __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
   __syncthreads();
 
   // the rows' factors; what their segment does not reach is 0, whatever it holds
-  float e_row[4], e_tail[4];
+  double e_row[4];
+  float e_tail[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = 16 * w + 4 * g + i;
@@ -1507,13 +1523,15 @@ __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
       s3 = __builtin_fmaf(kv, K2[t][i], s3);
     }
     // of this lane's columns; summed over the lanes below
-    const float tk_i = last ? s3 * rkk[row] : 0.0f;
-    e_row[i] = s1 * rkq[row] + s2 * rkk[row] - tk_i;
-    e_tail[i] = tk_i;
+    e_row[i] = s1 * rkq[row] + s2 * rkk[row];
+    e_tail[i] = last ? s3 * rkk[row] : 0.0f;
     fence();
   }
 
-  // X = dP D, Z = dL D and its transpose, and what the decay sums take from both
+  // X = dP D, Z = dL D and its transpose, and what the decay sums take from both: E_ij with the
+  // factor exp(G_i - G_j).  Step t's gradient has the E_ij of j < t <= i, as the sum of the
+  // rows minus the columns from t on; the others cancel, and may be larger by any power of e.
+  // So both sums are in fp64, and the diagonal, which has no such factor, is in neither.
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int ct = 2 * half + t;
@@ -1534,7 +1552,7 @@ __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
       }
     }
     const int cj = 16 * ct + r;
-    float ce = 0.0f;
+    double ce = 0.0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int ri = 16 * w + 4 * g + i;
@@ -1543,10 +1561,10 @@ __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
       const float d = expf((float)(gs[ri] - gs[cj]));
       const float x = low || cj == ri ? dP[t][i] * (a.scale * bt[cj]) * (cj == ri ? 1.0f : d) : 0.0f;
       const float z = low ? -dL[t][i] * (bt[ri] * bt[cj]) * d : 0.0f;
-      float en = low || cj == ri ? x * qk[i] * (rkq[ri] * rkk[cj]) : 0.0f;
-      en = low ? __builtin_fmaf(z, kk[i] * (rkk[ri] * rkk[cj]), en) : en;
-      e_row[i] += en;
-      ce += en;
+      const float en = low ? __builtin_fmaf(z, kk[i] * (rkk[ri] * rkk[cj]),
+                                            x * qk[i] * (rkq[ri] * rkk[cj])) : 0.0f;
+      e_row[i] += (double)en;
+      ce += (double)en;
       xm[ri][cj] = x;
       if (cj < ri) zm[ri][cj] = zm[cj][ri] = z;
       if (cj == ri) zm[ri][ri] = 0.0f;
@@ -1576,19 +1594,21 @@ __global__ __launch_bounds__(512) void k_gdr_grads(GdrArgs a) {
   __syncthreads();
 
   if (wv == 0) {
-    // dlog_decay_t = sum of dG_i over the steps i >= t of its segment
-    double G = ((double)row_e[0][lane] + row_e[1][lane]) -
-               ((((double)col_e[0][lane] + col_e[1][lane]) + col_e[2][lane]) + col_e[3][lane]);
+    // dlog_decay_t = sum of dG_i over the steps i >= t of its segment, and of what its steps
+    // before t leave for the chunks behind
+    double G = (row_e[0][lane] + row_e[1][lane]) -
+               (((col_e[0][lane] + col_e[1][lane]) + col_e[2][lane]) + col_e[3][lane]);
     double t = (double)row_t[0][lane] + row_t[1][lane];
     const int end = seg_end(cuts, lane);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const double after = __shfl_down(G, d);
+      const double after = __shfl_down(G, d), before = __shfl_up(t, d);
       if (lane + d < end) G += after;
-      t += __shfl_xor(t, d);
+      if (lane >= d) t += before;
     }
+    const double left_behind = __shfl_up(t, 1);
     if (end == kC) {
-      G += t;
+      if (lane > 0) G += left_behind;
       if (whole) {
         double s = 0.0;
 #pragma unroll
