@@ -139,6 +139,7 @@ int rms_call(const void* x, const void* residual, const float* gamma, void* y, f
                                                     s));
 }
 
+// An index below 2^24 in the kernels, and 256 threads a row (more only for few rows).
 constexpr int64_t kLpMost = (int64_t)1 << 24;
 
 }  // namespace
@@ -394,7 +395,6 @@ int lrs_logprobs_fwd(const void* logits, int64_t ld, const int64_t* target, floa
   const Span outs[] = {{logprob, nb}, {entropy, nb}, {lse, nb}, {top_ids, tn * 8},
                        {top_logprobs, tn * 4}};
   if (any_overlap(outs, 5, ins, 2)) return LRS_ERR_INVALID_ARG;
-  if (!grid_ok(N, 1024)) return LRS_ERR_UNSUPPORTED;
   lrs::LogprobArgs a = {};
   a.logits = logits;
   a.ld = ld;
