@@ -365,9 +365,10 @@ __device__ __forceinline__ float2 row_sum_of(const IO* row, int V) {
   return make_float2(top, logf(s));
 }
 
-// One group of 16 bytes a thread and step; blockIdx.x = row, blockIdx.y = piece of it.
+// One group of 16 bytes a thread and step; blockIdx.x = row, blockIdx.y = piece of it, and of
+// a row that is summed again, by each workgroup that has a part of it, a larger piece.
 template <typename IO, bool NT>
-__global__ __launch_bounds__(256) void k_logprobs_bwd(LogprobArgs a, int64_t piece) {
+__global__ __launch_bounds__(256) void k_logprobs_bwd(LogprobArgs a, int64_t piece, int64_t far_piece) {
   constexpr int G = kGroup<IO>;
   const int64_t n = blockIdx.x;
   const IO* row = (const IO*)a.logits + n * a.ld;
@@ -382,6 +383,8 @@ __global__ __launch_bounds__(256) void k_logprobs_bwd(LogprobArgs a, int64_t pie
   // log p = (l - m) - log_s
   float m = lse, log_s = 0.0f;
   if (fabsf(lse) > kExactLse && fabsf(lse) < kInf) {  // the same for all threads
+    piece = far_piece;
+    if (blockIdx.y * piece >= a.V) return;
     const float2 all = row_sum_of<IO>(row, (int)a.V);
     m = all.x;
     log_s = all.y;
@@ -435,9 +438,15 @@ hipError_t launch_logprobs_bwd(const LogprobArgs& a, int io, hipStream_t stream)
   // pieces of eight groups a thread; in place one, as a workgroup may read the whole row
   const int64_t step = 256 * 8 * group, steps = (a.V + step - 1) / step;
   const int64_t pieces = a.grad_logits == a.logits ? 1 : steps, piece = step * (steps / pieces);
+  // Summing a row again reads all of it, so a piece each would read it V / 8192 times (fp32):
+  // then as many as fill the compute units with four workgroups each.  Logits 1000 away from 0,
+  // fp32, in us, by every piece and so: 1000 x 150000 2428 and 334 (239 near 0), 256 x 150000 411
+  // and 103 (112 by one workgroup a row), 16 x 150000 31 both (77 by one).
+  const int64_t most = 4 * (int64_t)device_cus() / a.N, far = most < 1 ? 1 : most < pieces ? most : pieces;
+  const int64_t far_piece = piece * ((pieces + far - 1) / far);
   const dim3 grid((unsigned)a.N, (unsigned)pieces);
 #define LRS_LPB(IO, NT) \
-  hipLaunchKernelGGL((k_logprobs_bwd<IO, NT>), grid, dim3(256), 0, stream, a, piece)
+  hipLaunchKernelGGL((k_logprobs_bwd<IO, NT>), grid, dim3(256), 0, stream, a, piece, far_piece)
   if (io == kIoBf16) {
     if (nt) LRS_LPB(uint16_t, true);
     else LRS_LPB(uint16_t, false);

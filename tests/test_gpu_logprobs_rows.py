@@ -24,3 +24,47 @@ def test_many_rows(N, V):
     assert torch.equal(out[3][:, 0].cpu(), logits.argmax(1))
     grad = lrs.logprobs_bwd(logits.to(DEV), target.to(DEV), out[2], None, gl.to(DEV))
     assert ((grad.cpu().double() - ref["grad_logits"]).abs() <= 1.6e-5).all()
+
+
+def test_far_from_0_costs_one_more_reading():
+    """The gradient sums a row again whose lse is far from 0: that is one more reading of the row,
+    half as much again as the call's own reads and writes, whatever the row's width.  Bound: four times
+    the call near 0."""
+    N, V = 1000, 150000
+    x = torch.randn(N, V, device=DEV)
+    target = torch.zeros(N, dtype=torch.int64, device=DEV)
+    gl, out = torch.ones(N, device=DEV), torch.empty_like(x)
+    took = []
+    for _ in range(2):
+        lse = lrs.logprobs_fwd(x, target)[2]
+        runs = []
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            lrs.logprobs_bwd(x, target, lse, None, gl, out=out)
+            b.record()
+            torch.cuda.synchronize()
+            runs.append(a.elapsed_time(b))
+        took.append(min(runs))
+        x += 1000.0
+    assert took[1] <= 4 * took[0], took
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N,V", [(1, 40001), (30, 40001), (300, 50021), (1100, 20011)])
+def test_far_from_0_in_pieces(N, V, dtype):
+    """Rows far from 0, near it and wholly masked together, in every number of pieces: out of
+    place as in place, bit for bit."""
+    g = torch.Generator(device=DEV).manual_seed(N)
+    x = 3 * torch.randn(N, V, generator=g, device=DEV)
+    x[::2] += 1000.0
+    x[7::9] = -torch.inf
+    x = x.to(dtype)
+    target = torch.randint(0, V, (N,), generator=g, device=DEV)
+    gl, ge = (torch.randn(N, generator=g, device=DEV) for _ in range(2))
+    _, entropy, lse, _, _ = lrs.logprobs_fwd(x, target)
+    apart = lrs.logprobs_bwd(x, target, lse, entropy, gl, ge)
+    lrs.logprobs_bwd(x, target, lse, entropy, gl, ge, out=x)
+    kind = torch.int32 if dtype == torch.float32 else torch.int16
+    nan = torch.isnan(x)
+    assert torch.equal(torch.isnan(apart), nan) and torch.equal(apart.view(kind)[~nan], x.view(kind)[~nan])
