@@ -35,12 +35,12 @@ bool gdr_sizes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t K, int64_t V
   s->saved = (size_t)(s->chunks * B * H * (K + lrs::kGdrRows) * lrs::gdr_saved_pitch(V)) * 4;
   return true;
 }
-// The kernels' grids and 32-bit sizes.
-bool gdr_fits(int64_t chunks, int64_t B, int64_t H, int64_t K, int64_t V) {
+// The kernels' grids and 32-bit sizes: 256 threads a chunk and head, 512 in the backward.
+bool gdr_fits(int64_t chunks, int64_t B, int64_t H, int64_t K, int64_t V, bool backward) {
   const int64_t most = (int64_t)1 << 26, columns = (V + 15) / 16;
   int64_t n;
   return K <= lrs::kGdrMostK && V < ((int64_t)1 << 24) && H < ((int64_t)1 << 24) &&
-         mul_ok(B, H, &n) && mul_ok(n, chunks > 0 ? chunks : 1, &n) && n < most / 4 &&
+         mul_ok(B, H, &n) && mul_ok(n, chunks > 0 ? chunks : 1, &n) && n < most / (backward ? 8 : 4) &&
          mul_ok(n, columns, &n) && n < most;
 }
 
@@ -73,7 +73,7 @@ size_t gdr_carve(int64_t chunks, int64_t B, int64_t H, int64_t Hk, int64_t K, in
 size_t gdr_workspace(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t K, int64_t V, int io,
                      bool backward) {
   GdrSizes z;
-  if (!gdr_sizes(T, B, H, Hk, K, V, io, &z) || z.rows == 0 || !gdr_fits(z.chunks, B, H, K, V))
+  if (!gdr_sizes(T, B, H, Hk, K, V, io, &z) || z.rows == 0 || !gdr_fits(z.chunks, B, H, K, V, backward))
     return 0;
   lrs::GdrArgs a = {};
   return kAlign + gdr_carve(z.chunks, B, H, Hk, K, V, io, backward, nullptr, &a);
@@ -188,7 +188,7 @@ int lrs_gdr_fwd(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const 
   const Span outs[] = {{o, (size_t)(z.rows * z.vw) * es}, {state, sb},
                        {checkpoints, z.saved}};
   if (any_overlap(outs, 3, ins, 7)) return LRS_ERR_INVALID_ARG;
-  if (!gdr_fits(z.chunks, B, H, K, V) || !gdr_rows_fit(B, ld_q, K, V) ||
+  if (!gdr_fits(z.chunks, B, H, K, V, false) || !gdr_rows_fit(B, ld_q, K, V) ||
       !gdr_rows_fit(B, ld_k, K, V) || !gdr_rows_fit(B, ld_v, K, V) || !gdr_rows_fit(B, z.vw, K, V))
     return LRS_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < gdr_workspace(T, B, H, Hk, K, V, io_dtype, false))
@@ -261,7 +261,8 @@ int lrs_gdr_bwd(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const 
     if (slices_overlap(gz[i].p, gz[i].ld, gz[i].w, o.p, o.ld, o.w, z.rows, es))
       return LRS_ERR_INVALID_ARG;
   }
-  if (!gdr_fits(z.chunks, B, H, K, V) || !gdr_rows_fit(B, z.vw, K, V)) return LRS_ERR_UNSUPPORTED;
+  if (!gdr_fits(z.chunks, B, H, K, V, true) || !gdr_rows_fit(B, z.vw, K, V))
+    return LRS_ERR_UNSUPPORTED;
   for (int64_t ld : lds)
     if (!gdr_rows_fit(B, ld, K, V)) return LRS_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < gdr_workspace(T, B, H, Hk, K, V, io_dtype, true))
