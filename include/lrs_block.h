@@ -50,7 +50,7 @@ extern "C" {
  * 2^-39 of the largest of its row or column, whichever is more.  A value that is
  * not finite makes what its document computes from it NaN or infinite, up to
  * 63 steps before it (its chunk) and in the columns of V and heads it reaches.
- * Supported: K <= 128, B*H*V and B*ld below 2^23 for every row pitch ld, (K+64)*V below 2^29, and
+ * Supported: K <= 128, B*H*V and B*ld below 2^23 for every row pitch ld, (K+64)*V' below 2^29, and
  * the chunks ceil(T/64)*B*H below 2^24 (2^23 for lrs_gdr_bwd), times ceil(V/16) below 2^26. */
 LRS_API int64_t lrs_gdr_checkpoint_rows(int64_t T);
 LRS_API size_t lrs_gdr_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t Hk, int64_t K,

@@ -44,10 +44,11 @@ bool gdr_fits(int64_t chunks, int64_t B, int64_t H, int64_t K, int64_t V, bool b
          mul_ok(n, columns, &n) && n < most;
 }
 
-// 31-bit byte offsets inside a chunk's rows of an array and inside a state.
+// 31-bit byte offsets inside a chunk's rows of an array and inside what is kept of a chunk.
 bool gdr_rows_fit(int64_t B, int64_t ld, int64_t K, int64_t V) {
   int64_t n;
-  return mul_ok(B, ld, &n) && n < ((int64_t)1 << 23) && (K + lrs::kGdrRows) * V < ((int64_t)1 << 29);
+  return mul_ok(B, ld, &n) && n < ((int64_t)1 << 23) &&
+         (K + lrs::kGdrRows) * lrs::gdr_saved_pitch(V) < ((int64_t)1 << 29);
 }
 
 // Carves the workspace of a call; with a null base it only counts.

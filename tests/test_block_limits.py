@@ -50,3 +50,15 @@ def test_chunks_of_the_delta_rule(lib):
             assert query(T, B, H, Hk, 1, 1, 0) == 0
             assert gdr(lib, backward, T - 64, B, H, Hk, 1, 1) == b.LRS_ERR_WORKSPACE
             assert query(T - 64, B, H, Hk, 1, 1, 0) > 0
+
+
+def test_padded_rows_of_a_state(lib):
+    """Kept states have rows of V rounded up to 4, and their chunk's bytes stay below 2^31."""
+    from linear_recurrence_scan_diagonal_amd import binding as b
+    for backward in (False, True):
+        for K, V in ((128, (1 << 29) // 192 // 4 * 4), (64, (1 << 22) - 4), (1, (1 << 23) - 8)):
+            if (K + 64) * V < 1 << 29:
+                assert gdr(lib, backward, 1, 1, 1, 1, K, V) == b.LRS_ERR_WORKSPACE, (K, V)
+            for more in (1, 2, 3, 4):  # the next four
+                if (K + 64) * (V + more) < 1 << 29 <= (K + 64) * (V + 4):
+                    assert gdr(lib, backward, 1, 1, 1, 1, K, V + more) == b.LRS_ERR_UNSUPPORTED, (K, V + more)
