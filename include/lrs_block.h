@@ -113,7 +113,7 @@ LRS_API int lrs_rmsnorm_fwd(const void *x, const void *residual, const float *ga
  * the last one shorter where D is no multiple; 0: the whole row)
  *   scale = max |y| / 448, at least 2^-120 (1 where every y is 0),
  *   q = y / scale rounded to e4m3 (nearest, ties to even),
- * taken from y in fp32.  q: [R,D] bytes, e4m3 without infinities (OCP); scales:
+ * taken from y in fp32, each quotient rounded to fp32 first.  q: [R,D] bytes, e4m3 without infinities (OCP); scales:
  * [R, ceil(D / group)] fp32.  A group with a NaN or an infinity has a scale that
  * is not finite and q NaN.  Supported as lrs_rmsnorm_fwd. */
 LRS_API int lrs_rmsnorm_fwd_fp8(const void *x, const void *residual, const float *gamma,
