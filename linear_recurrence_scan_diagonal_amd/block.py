@@ -1,6 +1,6 @@
 """ctypes binding of the operators of delta-rule language models (include/lrs_block.h).
 
-Argument marshalling only, in the manner of ``binding`` and ``lm``: shapes and dtypes
+Argument marshalling only, in the manner of ``binding`` and ``lm``: shapes, dtypes and devices
 are checked, outputs and workspaces are torch device tensors, and raw pointers plus the
 current HIP stream go to the C ABI.
 """
@@ -12,7 +12,8 @@ import torch
 
 from . import lm
 from .binding import DTYPES, _i64, _int, _sz, _vp
-from .lm import _call, _check_dev, _ptr, _reset, _stream, _workspace
+from .binding import _check_dev as _refuse
+from .lm import _call, _ptr, _stream
 
 EXPORTS = ("lrs_gdr_checkpoint_rows", "lrs_gdr_workspace_bytes", "lrs_gdr_fwd",
            "lrs_gdr_bwd_workspace_bytes", "lrs_gdr_bwd", "lrs_gdr_step", "lrs_rmsnorm_fwd",
@@ -24,7 +25,7 @@ _lib = None
 
 def load():
     """liblrs.so with the prototypes of lrs.h, lrs_lm.h and lrs_block.h set."""
-    global _lib
+    global _lib, _several
     lib = lm.load()
     if _lib is lib:
         return lib
@@ -48,8 +49,52 @@ def load():
     for name in EXPORTS:
         if name.endswith(("_fwd", "_bwd", "_step", "_fp8")):
             getattr(lib, name).restype = _int
+    _several = torch.cuda.device_count() > 1
     _lib = lib
     return lib
+
+
+_current = torch._C._cuda_getDevice
+_several = True  # whether the process sees more devices than one (asked by load: a call's
+                 # check takes 0.4 us)
+
+
+def _elsewhere(t):
+    """Whether t is on a device that is not the current one, which launches on the default
+    stream go to: such a call is made again with t's device as the current one."""
+    return isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != _current()
+
+
+def _same_device(name, t, dev):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev} like the other tensors, got {t.device}")
+
+
+def _check_dev(name, t, dtype, shape, dev):
+    """A contiguous tensor of this type and shape on device number dev, or None."""
+    if t is None:
+        return
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _refuse(name, t, dtype, shape)
+    _same_device(name, t, dev)
+
+
+def _workspace(nbytes, dev, workspace):
+    ws = lm._workspace(nbytes, dev, workspace)
+    if workspace is not None and ws is not None:
+        _same_device("workspace", ws, dev.index)
+    return ws
+
+
+def _reset(reset, T, B, dev):
+    reset = lm._reset(reset, T, B)
+    if reset is not None:
+        _same_device("reset", reset, dev)
+    return reset
 
 
 def _heads(name, t, lead, like=None):
@@ -60,8 +105,10 @@ def _heads(name, t, lead, like=None):
         raise TypeError(f"{name} must be a device tensor")
     if t.dtype not in DTYPES:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    if like is not None and t.dtype is not like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if like is not None and (t.dtype is not like.dtype or t.get_device() != like.get_device()):
+        if t.dtype is not like.dtype:
+            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+        _same_device(name, t, like.get_device())
     shape, stride = t.shape, t.stride()
     n = len(lead)
     if len(shape) != n + 2 or shape[:n] != lead:
@@ -100,11 +147,11 @@ def _gdr_inputs(q, k, v, log_decay, beta, dims):
         raise ValueError(f"q must have the shape of k, {tuple(k.shape)}, got {tuple(q.shape)}")
     if not Hk or not H or H % Hk:
         raise ValueError(f"v's heads ({H}) must be a multiple of k's ({Hk})")
-    gates = torch.Size((*lead, H))
+    gates, index = torch.Size((*lead, H)), v.get_device()
     for name, t in (("log_decay", log_decay), ("beta", beta)):
         if t is None:
             raise TypeError(f"{name} must be a device tensor")
-        _check_dev(name, t, torch.float32, gates)
+        _check_dev(name, t, torch.float32, gates, index)
     return lead, H, Hk, K, V, (q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v,
                                log_decay.data_ptr(), beta.data_ptr())
 
@@ -132,15 +179,20 @@ def gdr_fwd(q, k, v, log_decay, beta, scale=None, reset=None, state0=None,
     bool, nonzero where a document starts.  state0: [B,H,K,V] fp32.  checkpoints: a
     tensor of gdr_checkpoints, filled for gdr_bwd.  Returns o [T,B,H,V], or (o, state)."""
     lib = load()
+    if _several and _elsewhere(v):
+        with torch.cuda.device(v.device):
+            return gdr_fwd(q, k, v, log_decay, beta, scale, reset, state0, want_state,
+                           checkpoints, out, workspace)
     (T, B), H, Hk, K, V, args = _gdr_inputs(q, k, v, log_decay, beta, 2)
-    reset = _reset(reset, T, B)
-    shape = torch.Size((B, H, K, V))
-    _check_dev("state0", state0, torch.float32, shape)
-    if checkpoints is not None:
-        _check_dev("checkpoints", checkpoints, torch.float32, _saved(T, B, H, K, V))
     dev = v.device
+    index = dev.index
+    reset = _reset(reset, T, B, index)
+    shape = torch.Size((B, H, K, V))
+    _check_dev("state0", state0, torch.float32, shape, index)
+    if checkpoints is not None:
+        _check_dev("checkpoints", checkpoints, torch.float32, _saved(T, B, H, K, V), index)
     o = torch.empty((T, B, H, V), dtype=v.dtype, device=dev) if out is None else out
-    _check_dev("out", o, v.dtype, v.shape)
+    _check_dev("out", o, v.dtype, v.shape, index)
     state = torch.empty(shape, dtype=torch.float32, device=dev) if want_state else None
     io = DTYPES[v.dtype]
     nbytes = lib.lrs_gdr_workspace_bytes(T, B, H, Hk, K, V, io)
@@ -160,17 +212,22 @@ def gdr_bwd(q, k, v, log_decay, beta, checkpoints, grad_o, scale=None, reset=Non
     gradient.  Returns (grad_q, grad_k, grad_v, grad_log_decay, grad_beta,
     grad_state0)."""
     lib = load()
+    if _several and _elsewhere(v):
+        with torch.cuda.device(v.device):
+            return gdr_bwd(q, k, v, log_decay, beta, checkpoints, grad_o, scale, reset,
+                           grad_state, grad_qkv, workspace)
     (T, B), H, Hk, K, V, args = _gdr_inputs(q, k, v, log_decay, beta, 2)
-    reset = _reset(reset, T, B)
+    dev = v.device
+    index = dev.index
+    reset = _reset(reset, T, B, index)
     shape = torch.Size((B, H, K, V))
     if checkpoints is None:
         raise TypeError("checkpoints must be the tensor that gdr_fwd filled")
-    _check_dev("checkpoints", checkpoints, torch.float32, _saved(T, B, H, K, V))
+    _check_dev("checkpoints", checkpoints, torch.float32, _saved(T, B, H, K, V), index)
     if grad_o is None:
         raise TypeError("grad_o must be a device tensor")
-    _check_dev("grad_o", grad_o, v.dtype, v.shape)
-    _check_dev("grad_state", grad_state, torch.float32, shape)
-    dev = v.device
+    _check_dev("grad_o", grad_o, v.dtype, v.shape, index)
+    _check_dev("grad_state", grad_state, torch.float32, shape, index)
     if grad_qkv is None:
         grad_qkv = tuple(torch.empty(t.shape, dtype=v.dtype, device=dev) for t in (q, k, v))
     grads = []
@@ -197,15 +254,19 @@ def gdr_step(q, k, v, log_decay, beta, state, slots=None, scale=None, out=None):
     int32, each sequence's row of state (outside [0, S): idle, o = 0), or None for
     row b.  Returns o [B,H,V]."""
     lib = load()
+    if _several and _elsewhere(v):
+        with torch.cuda.device(v.device):
+            return gdr_step(q, k, v, log_decay, beta, state, slots, scale, out)
     (B,), H, Hk, K, V, args = _gdr_inputs(q, k, v, log_decay, beta, 1)
     if not isinstance(state, torch.Tensor) or state.dim() != 4 or state.shape[1:] != (H, K, V):
         raise ValueError(f"state must be [S,{H},{K},{V}]")
-    _check_dev("state", state, torch.float32, state.shape)
-    _check_dev("slots", slots, torch.int32, (B,))
+    index = v.get_device()
+    _check_dev("state", state, torch.float32, state.shape, index)
+    _check_dev("slots", slots, torch.int32, (B,), index)
     if slots is None and state.shape[0] < B:
         raise ValueError("state needs a row for every sequence")
     o = torch.empty((B, H, V), dtype=v.dtype, device=v.device) if out is None else out
-    _check_dev("out", o, v.dtype, v.shape)
+    _check_dev("out", o, v.dtype, v.shape, index)
     _call(lib.lrs_gdr_step(*args, _ptr(slots), state.data_ptr(), o.data_ptr(), B, H, Hk, K, V,
                            state.shape[0], K ** -0.5 if scale is None else float(scale),
                            DTYPES[v.dtype], _stream(v.device)), "lrs_gdr_step")
@@ -215,19 +276,22 @@ def gdr_step(q, k, v, log_decay, beta, state, slots=None, scale=None, out=None):
 def _rms_inputs(x, gamma, residual, out_sum):
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise TypeError("x must be a device tensor")
-    _check_dev("x", x, x.dtype, x.shape)
+    index = x.get_device()
+    if index < 0:
+        raise TypeError("x must be a device tensor")
+    _check_dev("x", x, x.dtype, x.shape, index)
     if x.dtype not in DTYPES:
         raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
     D = int(x.shape[-1])
     if gamma is None:
         raise TypeError("gamma must be a device tensor")
-    _check_dev("gamma", gamma, torch.float32, (D,))
-    _check_dev("residual", residual, x.dtype, x.shape)
+    _check_dev("gamma", gamma, torch.float32, (D,), index)
+    _check_dev("residual", residual, x.dtype, x.shape, index)
     s = None
     if residual is not None:
         s = torch.empty_like(x) if out_sum is None else out_sum
         if out_sum is not None:
-            _check_dev("out_sum", s, x.dtype, x.shape)
+            _check_dev("out_sum", s, x.dtype, x.shape, index)
     return x.numel() // D if D else 0, D, s
 
 
@@ -238,10 +302,13 @@ def rmsnorm_fwd(x, gamma, residual=None, eps: float = 1e-6, save: bool = False, 
     None, rstd); rstd ([rows] fp32) is None unless save, and is what rmsnorm_bwd
     takes.  out_sum may be x or residual (the residual stream in place)."""
     lib = load()
+    if _several and _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return rmsnorm_fwd(x, gamma, residual, eps, save, out, out_sum)
     R, D, s = _rms_inputs(x, gamma, residual, out_sum)
     y = torch.empty_like(x) if out is None else out
     if out is not None:
-        _check_dev("out", y, x.dtype, x.shape)
+        _check_dev("out", y, x.dtype, x.shape, x.get_device())
     rstd = torch.empty(R, dtype=torch.float32, device=x.device) if save else None
     _call(lib.lrs_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(y), _ptr(s), _ptr(rstd),
                               R, D, float(eps), DTYPES[x.dtype], _stream(x.device)),
@@ -255,6 +322,9 @@ def rmsnorm_fwd_fp8(x, gamma, residual=None, eps: float = 1e-6, group: int = 128
     scales [rows, groups] fp32, one for every `group` = 128 features of a row, or for
     the whole row with group = 0; q * scale is y.  Returns (q, scales, s or None)."""
     lib = load()
+    if _several and _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return rmsnorm_fwd_fp8(x, gamma, residual, eps, group, out, out_sum)
     R, D, s = _rms_inputs(x, gamma, residual, out_sum)
     if group not in (0, 128):
         raise ValueError("group must be 128, or 0 for the whole row")
@@ -262,7 +332,7 @@ def rmsnorm_fwd_fp8(x, gamma, residual=None, eps: float = 1e-6, group: int = 128
         q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     else:
         q = out
-        _check_dev("out", q, torch.float8_e4m3fn, x.shape)
+        _check_dev("out", q, torch.float8_e4m3fn, x.shape, x.get_device())
     scales = gamma.new_empty((R, -(-D // group) if group else 1))
     _call(lib.lrs_rmsnorm_fwd_fp8(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(q), _ptr(scales),
                                   _ptr(s), R, D, group, float(eps), DTYPES[x.dtype],
@@ -275,15 +345,19 @@ def rmsnorm_bwd(s, gamma, rstd, grad_y, grad_sum=None, out=None, workspace=None)
     gradient that reaches s from elsewhere, or None.  out may be grad_y or grad_sum.
     Returns (grad_x, grad_gamma); grad_x is also the residual's gradient."""
     lib = load()
+    if _several and _elsewhere(s):
+        with torch.cuda.device(s.device):
+            return rmsnorm_bwd(s, gamma, rstd, grad_y, grad_sum, out, workspace)
     R, D, _ = _rms_inputs(s, gamma, None, None)
+    index = s.get_device()
     for name, t, dtype, shape in (("rstd", rstd, torch.float32, (R,)),
                                   ("grad_y", grad_y, s.dtype, s.shape)):
         if t is None:
             raise TypeError(f"{name} must be a device tensor")
-        _check_dev(name, t, dtype, shape)
-    _check_dev("grad_sum", grad_sum, s.dtype, s.shape)
+        _check_dev(name, t, dtype, shape, index)
+    _check_dev("grad_sum", grad_sum, s.dtype, s.shape, index)
     gx = torch.empty_like(s) if out is None else out
-    _check_dev("out", gx, s.dtype, s.shape)
+    _check_dev("out", gx, s.dtype, s.shape, index)
     gg = torch.empty(D, dtype=torch.float32, device=s.device)
     nbytes = lib.lrs_rmsnorm_bwd_workspace_bytes(R, D)
     ws = _workspace(nbytes, s.device, workspace)
@@ -308,11 +382,14 @@ def logprobs_fwd(logits, target, top: int = 0):
     top_ids, top_logprobs): [N] fp32 three times, [N,top] int64 and fp32 (None
     without)."""
     lib = load()
+    if _several and _elsewhere(logits):
+        with torch.cuda.device(logits.device):
+            return logprobs_fwd(logits, target, top)
     N, V, ld = _logit_rows("logits", logits)
     dev = logits.device
     if target is None:
         raise TypeError("target must be a device tensor")
-    _check_dev("target", target, torch.int64, (N,))
+    _check_dev("target", target, torch.int64, (N,), dev.index)
     if not 0 <= top <= min(64, V):
         raise ValueError("top must be between 0 and 64 and at most the number of logits")
     logprob, entropy, lse = (torch.empty(N, dtype=torch.float32, device=dev) for _ in range(3))
@@ -331,18 +408,23 @@ def logprobs_bwd(logits, target, lse, entropy, grad_logprob, grad_entropy=None, 
     grad_entropy ([N] fp32; the latter None for 0, entropy is then not read).  out may
     be the logits.  Returns grad_logits [N,V]."""
     lib = load()
+    if _several and _elsewhere(logits):
+        with torch.cuda.device(logits.device):
+            return logprobs_bwd(logits, target, lse, entropy, grad_logprob, grad_entropy, out)
     N, V, ld = _logit_rows("logits", logits)
+    index = logits.get_device()
     for name, t, dtype in (("target", target, torch.int64), ("lse", lse, torch.float32),
                            ("grad_logprob", grad_logprob, torch.float32)):
         if t is None:
             raise TypeError(f"{name} must be a device tensor")
-        _check_dev(name, t, dtype, (N,))
-    _check_dev("grad_entropy", grad_entropy, torch.float32, (N,))
-    _check_dev("entropy", entropy, torch.float32, (N,))
+        _check_dev(name, t, dtype, (N,), index)
+    _check_dev("grad_entropy", grad_entropy, torch.float32, (N,), index)
+    _check_dev("entropy", entropy, torch.float32, (N,), index)
     if grad_entropy is not None and entropy is None:
         raise TypeError("entropy must be the tensor that logprobs_fwd returned")
     g = torch.empty((N, V), dtype=logits.dtype, device=logits.device) if out is None else out
     _, _, ld_grad = _logit_rows("out", g, logits)
+    _same_device("out", g, index)
     _call(lib.lrs_logprobs_bwd(logits.data_ptr(), ld, target.data_ptr(), lse.data_ptr(),
                                _ptr(entropy), grad_logprob.data_ptr(), _ptr(grad_entropy),
                                g.data_ptr(), ld_grad, N, V, DTYPES[logits.dtype],
