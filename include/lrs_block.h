@@ -37,8 +37,11 @@ extern "C" {
  *          ld_v apart.  A k of length 1 and a beta in [0,2] keep the state from
  *          growing; neither is asked for.
  * log_decay, beta : [T,B,H] fp32 contiguous (a log_decay under -16384 counts as
- *          -16384: exp of it is 0 either way).
- * reset  : [T,B] bytes, or NULL for none.  state0: [B,H,K,V] fp32, or NULL (zero).
+ *          -16384: exp of it is 0 either way).  A log_decay may be above 0, but where its
+ *          sum over neighbouring steps of a chunk of 64 passes 88 their exp is infinite,
+ *          and gives NaN also for a state of 0.
+ * reset  : [T,B] bytes, or NULL for none; each document in a chunk of 64 steps costs the
+ *          chunk's work again.  state0: [B,H,K,V] fp32, or NULL (zero).
  * o      : [T,B,H,V] contiguous output.  state: [B,H,K,V] fp32 output, the state
  *          after the last step, or NULL; it may be state0's own buffer.
  * checkpoints : fp32 output [lrs_gdr_checkpoint_rows(T), B, H, K + 64, V'], V' = V
@@ -104,6 +107,7 @@ LRS_API int lrs_gdr_step(const void *q, int64_t ld_q, const void *k, int64_t ld_
  *   and is required with a residual (it may be x's or the residual's own
  *   buffer: the residual stream in place), and NULL without.
  * gamma : [D] fp32.  rstd: [R] fp32 output or NULL.  eps >= 0 and finite.
+ * Squares are summed in fp32: where they pass its range rstd is 0, and y with it.
  * Supported while R stays below 2^22, or below 2^26 - 4 where D <= 1024. */
 LRS_API int lrs_rmsnorm_fwd(const void *x, const void *residual, const float *gamma, void *y,
                             void *sum, float *rstd, int64_t R, int64_t D, float eps, int io_dtype,
@@ -153,8 +157,11 @@ LRS_API int lrs_logprobs_fwd(const void *logits, int64_t ld, const int64_t *targ
 
 /* The gradient of logprob and entropy:
  *   grad_l = grad_logprob (onehot - p) - grad_entropy p (log p + entropy),
- * 0 where p is 0, and 0 in a row whose target is ignored and whose grad_entropy
- * is 0, whatever its logits are.  lse, entropy: as lrs_logprobs_fwd wrote them.  grad_logprob,
+ * where a p of 0 adds nothing, and 0 in a row whose target is ignored and whose grad_entropy
+ * is 0, whatever its logits are.  lse, entropy: as lrs_logprobs_fwd wrote them.  With lse as it
+ * was rounded, p is known to some 2^-24 (|lse| + 3 |log p|) of itself, which is also what
+ * onehot - p keeps of a nearly certain target; from |lse| = 256 on the row is summed again
+ * instead (one more reading of it).  grad_logprob,
  * grad_entropy: [N] fp32, the latter NULL for 0 (entropy is then not read).
  * grad_logits: [N,V], I/O type, rows ld_grad apart; it may be the logits' own
  * buffer (with ld_grad = ld). */

@@ -23,15 +23,24 @@
 //                dP = do' u^T, dL = -dR u^T and through them and the states dq, dk and
 //                the decay's gradient.
 // What bounds it.  The bytes of a long prompt take 40 us at 16384 steps of 16 heads (K = V =
-// 128, bf16); it takes 104 us (prep) and 629 us (chain: 2.46 us a chunk, of which a wave
+// 128, bf16); it takes 103 us (prep) and 621 us (chain: 2.42 us a chunk, of which a wave
 // issues for 0.7 us and waits for the others' barriers, LDS and the matrix cores else).
 // Training at 2048 x 8 x 16 heads, 151 us of inputs and outputs, and 1.3 GB more of kept
-// states and operands: prep 130 us, forward and backward, chain 295 us, back 310 us, grads
-// 497 us, issue-bound at eight waves a compute unit.
+// states and operands: prep 124 us in the forward and 126 in the backward, at two waves a SIMD
+// for its LDS; chain 275 us and back 297, where a wave issues for 29 % of its time, is held up by
+// the others' instructions for 32 and waits for 38; grads 477 us at two waves a SIMD (201
+// registers), which issue for 28 % of their time and wait, for memory and the two barriers of
+// every 32 columns, for 58.
+// Two column blocks a wave and two waves a SIMD want more than 256 registers: of the chain
+// 3 (bf16, K > 64) and 28 (fp32, K > 64) go to scratch, of back 15 (bf16, K > 64), 3 (bf16) and
+// 21 (fp32, K <= 64).
 //
 // Restarts.  A chunk is taken apart into its documents' segments: the matrices are made
 // and used a segment at a time, rows outside count as 0 by selection, never by a
 // product, so that nothing of a document reaches another, NaN and infinities included.
+// So each segment costs the work of a chunk, in prep and in both chains: 2048 x 8 x 16 heads
+// bf16, forward / backward in us: without restarts 375 / 850, documents of 128 steps 425 / 950,
+// of 32 589 / 1142, of 10 1042 / 1633, of 4 2038 / 2692, of one 6841 / 7758.
 //
 // Numbers.  Sums, states and decays are fp32 or more.  What a product of the matrix
 // cores takes is split into two fp16 parts, hi + lo = x to 2^-22, scaled by a power of
@@ -1868,6 +1877,8 @@ __global__ __launch_bounds__(256) void k_gdr_step(GdrArgs a, const int32_t* __re
 //   64      110 / 238  107 / 250  119 / 268
 //   96      160 / 356  191 / 412  133 / 353
 //   128     212 / 483  206 / 493  150 / 433
+//
+// The backward follows the forward's rule; at 64 heads it would rather have one, by 5 %.
 template <typename F>
 void chain_shape(const GdrArgs& a, bool most_four, F launch) {
   const int64_t heads = a.B * a.H, cus = device_cus();

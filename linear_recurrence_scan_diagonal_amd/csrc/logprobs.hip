@@ -7,7 +7,10 @@
 //
 // Memory bound: the logits are read once.  A row streams through the 256 (or, where rows
 // are few, 1024) threads of a workgroup, each with a maximum of its own so far and sums
-// relative to it; a larger value rescales them, which is rare after the first few.
+// relative to it, which a larger value rescales.  A thread finds one in its i-th group once in
+// about i rows, so that in nearly every group some of a wave's 64 do (32768 bf16 logits are 16
+// groups a thread): the wave pays for the rescaling, one exponential beside the group's eight,
+// each time.
 //
 // The `top` largest.  Every thread also keeps the place of the first of its largest values;
 // the largest of 64 (or 128) groups of threads are ranked, and the top-th of them is a
@@ -20,12 +23,11 @@
 // more candidates than the LDS holds (many equal values over 1024 threads, or a NaN) are
 // read `top` times again, each time for the largest below the one before.
 //
-// Measured: 8192 x 32768 bf16 with 20 alternatives 150 to 157 us (3.6 TB/s: eight exponentials
-// for 16 bytes, beside the loads); 4099 x 50021 fp32 forward 146 us (5.6 TB/s), backward
-// 306 us (5.4 TB/s);
-// 64 x 32000 bf16 with 8 alternatives 13.9 us: a row's 16 waves' loads, sums, ranks and a
-// second reading one behind the other (12.2 with the row kept in registers, which took up
-// to 193 us at 8192 rows).
+// Measured: 8192 x 32768 bf16 with 20 alternatives 148 to 160 us (3.4 to 3.6 TB/s), in which
+// vector instructions take some 80 % of the SIMDs' cycles; 4099 x 50021 fp32 forward 142 us
+// (5.8 TB/s), backward 308 us (5.3 TB/s); 64 x 32000 bf16 with 8 alternatives 13.7 us: a row's
+// 16 waves' loads, sums, ranks and a second reading one behind the other (12.2 with the row kept
+// in registers, which took up to 193 us at 8192 rows).
 #include "lrs_device.hpp"
 #include "lrs_internal.hpp"
 #include "lrs_rows.hpp"

@@ -13,10 +13,10 @@
 // that is a maximum over 16 (bf16) or 32 (fp32) lanes for groups of 128, and one more sum
 // over the row's threads for a scale a row.
 //
-// Measured: 16384 x 4096 bf16 with residual to 8 bits 84 us (5.6 TB/s); 32768 x 2048 bf16
-// with residual forward 89 us (6.0 TB/s), backward 100 us and 5 us for the column sums, with
-// nontemporal accesses (a copy of 1 GiB reaches 5.1 TB/s); 5003 x 1711 fp32, whose rows do not
-// begin on 16 bytes, 15, 22 and 5.6 us; 64 x 1024 4.1 us.
+// Measured: 16384 x 4096 bf16 with residual to 8 bits 84 to 89 us (5.3 to 5.6 TB/s); 32768 x
+// 2048 bf16 with residual forward 88 us (6.1 TB/s), backward 97 us and 5 us for the column
+// sums, with nontemporal accesses (a copy of 1 GiB reaches 5.1 TB/s); 5003 x 1711 fp32, whose
+// rows do not begin on 16 bytes, 14, 22 and 5.5 us; 64 x 1024 4.2 us.
 #include "lrs_device.hpp"
 #include "lrs_internal.hpp"
 #include "lrs_rows.hpp"
