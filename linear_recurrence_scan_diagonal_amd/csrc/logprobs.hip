@@ -90,18 +90,23 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-// exp(l - m) and its product with l - m, added up over a group.  While there is nothing but
-// -infinity, m is that, and the lowest finite value stands for it.
+// exp(l - m) and its product with l - m, added up over a group, and then to the thread's sums:
+// a sum of n additions is known to n 2^-25 of itself where all of them round one way, as in rows of
+// many equal logits.  While there is nothing but -infinity, m is that, and the lowest finite
+// value stands for it.
 template <int G>
 __device__ __forceinline__ void add_group(const float (&v)[G], float m, float& s, float& t) {
   m = fmaxf(m, kLowest);
+  float gs = 0.0f, gt = 0.0f;
 #pragma unroll
   for (int j = 0; j < G; ++j) {
     const float c = v[j] - m;
     const float x = __builtin_amdgcn_exp2f(c * kLog2eF);
-    s += x;
-    t = __builtin_fmaf(x, fmaxf(c, kFarBelow), t);
+    gs = j == 0 ? x : gs + x;
+    gt = j == 0 ? x * fmaxf(c, kFarBelow) : __builtin_fmaf(x, fmaxf(c, kFarBelow), gt);
   }
+  s += gs;
+  t += gt;
 }
 // A larger maximum: the sums become relative to it.
 __device__ __forceinline__ void raise(float x, float& m, float& s, float& t) {

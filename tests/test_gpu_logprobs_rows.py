@@ -68,3 +68,22 @@ def test_far_from_0_in_pieces(N, V, dtype):
     kind = torch.int32 if dtype == torch.float32 else torch.int16
     nan = torch.isnan(x)
     assert torch.equal(torch.isnan(apart), nan) and torch.equal(apart.view(kind)[~nan], x.view(kind)[~nan])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N", [4, 520])
+def test_flat_wide_rows(N, dtype):
+    """Rows of equal logits below a first few: every addition to a thread's sum rounds the same way.
+    A thread of 256 has 879 groups of fp32, whose sum is known to 879 2^-25 = 2.6e-5 of itself, and lse
+    to as much: 2e-6 of 1 + |lse|, which is 14."""
+    V = 900001
+    x = torch.zeros(N, V, dtype=dtype, device=DEV)
+    target = torch.zeros(N, dtype=torch.int64, device=DEV)
+    for low in (-0.3, -0.7, -1.0, -1.3, -2.1):
+        x[:, 8192:] = low
+        ref = R.logprobs(x[:1].cpu().double(), target[:1].cpu())
+        logprob, entropy, lse, _, _ = lrs.logprobs_fwd(x, target)
+        for name, got in (("logprob", logprob), ("entropy", entropy), ("lse", lse)):
+            assert (got == got[0]).all()
+            off = abs(float(got[0]) - float(ref[name][0])) / (1 + abs(float(ref[name][0])))
+            assert off <= 2e-6, (name, low, off)
